@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libdsa.so")
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA = 0, 1, 2, 3
 DSA_ERR_WORKSPACE, DSA_ERR_TIMEOUT, DSA_ERR_BAD_INPUT = 4, 5, 6
 DSA_BF16, DSA_FP8_E4M3_ROWSCALE, DSA_FP8_DS_MLA, DSA_NVFP4 = 0, 1, 2, 3
+DSA_ROPE_PAIRS, DSA_ROPE_HALVES = 0, 1
 EXPORTS = ("dsa_workspace_size", "dsa_index_scores", "dsa_topk", "sparse_mla_decode", "dsa_decode_layer",
            "dsa_decode_layer_launches", "dsa_decode_layer_launches_for", "sparse_mla_decode_noalloc",
            "dsa_last_error_string", "dsa_status_string", "dsa_version")
@@ -27,6 +28,18 @@ EXPORTS = ("dsa_workspace_size", "dsa_index_scores", "dsa_topk", "sparse_mla_dec
 class DcpShard(ctypes.Structure):
     """dsa_dcp_shard: token t lives on rank (t // interleave) % world."""
     _fields_ = [("world", ctypes.c_int32), ("rank", ctypes.c_int32), ("interleave", ctypes.c_int32)]
+
+
+class GqaShape(ctypes.Structure):
+    """dsa_gqa_shape: heads, head width, cache dtype and row strides (elements;
+    0: contiguous) of the dense attention calls."""
+    _fields_ = [("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("kv_dtype", ctypes.c_int), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
+
+    def __init__(self, num_heads: int, num_kv_heads: int, head_dim: int, kv_dtype: int = DSA_BF16, *,
+                 q_stride: int = 0, k_stride: int = 0, v_stride: int = 0):
+        super().__init__(num_heads, num_kv_heads, head_dim, kv_dtype, q_stride, k_stride, v_stride)
 
 
 class DsaError(RuntimeError):
@@ -96,6 +109,14 @@ def load(path: str = LIB_PATH):
         L.dsa_lse_combine.argtypes = [P, P, I32, I32, P, P, P]
         L.dsa_dcp_shard_seqs.argtypes = [S, I32, SH, P, P, P, I32, ctypes.POINTER(I32), P, P]
         L.dsa_block_topk.argtypes = [P, I64, S, I32, I32, I32, P, P, P, P]
+        G = ctypes.POINTER(GqaShape)
+        L.dsa_kv_insert.argtypes = [G, P, I64, P, I64, P, I64, P, P, I32, P, I32, ctypes.c_int, P, P, P, P, I64, P, P,
+                                    P]
+        L.dense_gqa_workspace_size.argtypes = [G, S, I32, ctypes.POINTER(SZ)]
+        L.dense_gqa_decode.argtypes = [G, P, P, P, P, P, S, I32, F, P, P, P, SZ, P, P]
+        L.dense_gqa_prefill.argtypes = L.dense_gqa_decode.argtypes
+        for f in ("dsa_kv_insert", "dense_gqa_workspace_size", "dense_gqa_decode", "dense_gqa_prefill"):
+            getattr(L, f).restype = ctypes.c_int
         L.dsa_decode_layer_launches.restype = ctypes.c_int32
         for f in ("dsa_workspace_size", "dsa_index_scores", "dsa_topk", "sparse_mla_decode", "dsa_decode_layer"):
             getattr(L, f).restype = ctypes.c_int
@@ -327,3 +348,37 @@ def dsa_block_topk(scores, ld: int, seqs: Seqs, num_q: int, block: int, nsel: in
     sc = seqs.c()
     _check(load().dsa_block_topk(_p(scores), ld, ctypes.byref(sc), num_q, block, nsel, _p(idx), _p(topk_len),
                                  _p(d_status), _stream(stream)))
+
+
+# ---- dense attention with grouped heads (include/dsa.h)
+def dsa_kv_insert(shape: GqaShape, k, v, q, pos, slot, n: int, inv_freq, rot_dims: int, layout: int, k_cache, v_cache,
+                  k_scale, v_scale, num_rows: int, q_out, *, k_stride: int = 0, v_stride: int = 0, q_stride: int = 0,
+                  d_status=None, stream=None):
+    """``k_stride``, ``v_stride``, ``q_stride``: elements between the new
+    tokens (0: contiguous); the caches' and q_out's are the shape's."""
+    _check(load().dsa_kv_insert(ctypes.byref(shape), _p(k), k_stride, _p(v), v_stride, _p(q), q_stride, _p(pos),
+                                _p(slot), n, _p(inv_freq), rot_dims, layout, _p(k_cache), _p(v_cache), _p(k_scale),
+                                _p(v_scale), num_rows, _p(q_out), _p(d_status), _stream(stream)))
+
+
+def dense_gqa_workspace_size(shape: GqaShape, seqs: Seqs, num_q: int) -> int:
+    n = ctypes.c_size_t()
+    sc = seqs.c()
+    _check(load().dense_gqa_workspace_size(ctypes.byref(shape), ctypes.byref(sc), num_q, ctypes.byref(n)))
+    return int(n.value)
+
+
+def dense_gqa_decode(shape: GqaShape, q, k_cache, v_cache, k_scale, v_scale, seqs: Seqs, num_q: int, sm_scale: float,
+                     out, lse, workspace, workspace_bytes: int, d_status=None, stream=None):
+    sc = seqs.c()
+    _check(load().dense_gqa_decode(ctypes.byref(shape), _p(q), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
+                                   ctypes.byref(sc), num_q, sm_scale, _p(out), _p(lse), _p(workspace),
+                                   workspace_bytes, _p(d_status), _stream(stream)))
+
+
+def dense_gqa_prefill(shape: GqaShape, q, k_cache, v_cache, k_scale, v_scale, seqs: Seqs, num_q: int, sm_scale: float,
+                      out, lse, workspace, workspace_bytes: int, d_status=None, stream=None):
+    sc = seqs.c()
+    _check(load().dense_gqa_prefill(ctypes.byref(shape), _p(q), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
+                                    ctypes.byref(sc), num_q, sm_scale, _p(out), _p(lse), _p(workspace),
+                                    workspace_bytes, _p(d_status), _stream(stream)))

@@ -153,6 +153,17 @@ int64_t dcp_owned_tokens(int64_t n, int world, int rank, int inter);
 cudaError_t launch_dcp_shard_seqs(const dsa_seqs& s, int num_q, int world, int rank, int inter, int32_t* lctx,
                                   int32_t* lpos, int32_t* ltable, int lmax_pages, int32_t* d_status,
                                   cudaStream_t stream);
+cudaError_t launch_kv_insert(const dsa_gqa_shape& sh, const void* k, int64_t k_in, const void* v, int64_t v_in,
+                             const void* q, int64_t q_in, const int32_t* pos, const int64_t* slot, int32_t n,
+                             const float* inv_freq, int32_t rot, bool halves, void* k_cache, void* v_cache,
+                             float* k_scale, float* v_scale, int64_t num_rows, void* q_out, int32_t* d_status,
+                             cudaStream_t stream);
+namespace gqa {
+size_t decode_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s);
+cudaError_t launch_decode(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v, const float* k_scale,
+                          const float* v_scale, const dsa_seqs& s, int num_q, float sm_scale, void* out, float* lse,
+                          void* workspace, int32_t* d_status, cudaStream_t stream);
+}  // namespace gqa
 size_t block_topk_smem(int max_ctx, int block, int nsel);
 cudaError_t launch_block_topk(const float* scores, int64_t ld, const dsa_seqs& s, int num_q, int block, int nsel,
                               int32_t* idx, int32_t* topk_len, int32_t* d_status, cudaStream_t stream,
@@ -321,6 +332,167 @@ dsa_status dsa_latent_insert(const void* c_kv, const void* k_pe, const int32_t* 
     return cuda_status(launch_latent_insert(c_kv, k_pe, pos, inv_freq, slot, n, latent,
                                             latent_dtype == DSA_FP8_DS_MLA, num_rows, d_status, stream),
                        "dsa_latent_insert launch");
+}
+
+// ---- dense attention with grouped heads
+
+// The shape, checked, with its strides filled in
+static dsa_gqa_shape check_shape(Check& c, const dsa_gqa_shape* in) {
+    c.need(in != nullptr, DSA_ERR_INVALID_ARG, "shape is NULL");
+    if (!in) return dsa_gqa_shape{};
+    dsa_gqa_shape sh = *in;
+    c.need(sh.num_kv_heads >= 1 && sh.num_kv_heads <= 65535, DSA_ERR_INVALID_ARG,
+           "num_kv_heads %d outside [1, 65535]", sh.num_kv_heads);
+    c.need(sh.num_heads >= 1 && sh.num_heads <= 65535, DSA_ERR_INVALID_ARG, "num_heads %d outside [1, 65535]",
+           sh.num_heads);
+    c.need(sh.head_dim == 64 || sh.head_dim == 128, DSA_ERR_UNSUPPORTED, "head_dim %d is neither 64 nor 128",
+           sh.head_dim);
+    c.need(sh.kv_dtype == DSA_BF16 || sh.kv_dtype == DSA_FP8_E4M3_ROWSCALE, DSA_ERR_UNSUPPORTED,
+           "kv_dtype %d is neither DSA_BF16 nor DSA_FP8_E4M3_ROWSCALE", (int)sh.kv_dtype);
+    if (c.st != DSA_OK) return sh;
+    c.need(sh.num_heads % sh.num_kv_heads == 0, DSA_ERR_INVALID_ARG, "num_heads %d is not a multiple of num_kv_heads %d",
+           sh.num_heads, sh.num_kv_heads);
+    c.need(sh.num_heads / sh.num_kv_heads <= DSA_GQA_MAX_GROUP, DSA_ERR_UNSUPPORTED, "%d query heads on a key head exceed %d",
+           sh.num_heads / sh.num_kv_heads, DSA_GQA_MAX_GROUP);
+    const int64_t qw = (int64_t)sh.num_heads * sh.head_dim, kw = (int64_t)sh.num_kv_heads * sh.head_dim;
+    if (sh.q_stride == 0) sh.q_stride = qw;
+    if (sh.k_stride == 0) sh.k_stride = kw;
+    if (sh.v_stride == 0) sh.v_stride = kw;
+    const int64_t unit = sh.kv_dtype == DSA_BF16 ? 8 : 16;
+    const int64_t most = (int64_t)1 << 32;  // elements; a row of any cache is far shorter
+    c.need(sh.q_stride >= qw && sh.q_stride % 8 == 0 && sh.q_stride <= most, DSA_ERR_INVALID_ARG,
+           "q_stride %lld is not a multiple of 8 in [%lld, 2^32]", (long long)sh.q_stride, (long long)qw);
+    c.need(sh.k_stride >= kw && sh.k_stride % unit == 0 && sh.k_stride <= most, DSA_ERR_INVALID_ARG,
+           "k_stride %lld is not a multiple of %lld in [%lld, 2^32]", (long long)sh.k_stride, (long long)unit,
+           (long long)kw);
+    c.need(sh.v_stride >= kw && sh.v_stride % unit == 0 && sh.v_stride <= most, DSA_ERR_INVALID_ARG,
+           "v_stride %lld is not a multiple of %lld in [%lld, 2^32]", (long long)sh.v_stride, (long long)unit,
+           (long long)kw);
+    return sh;
+}
+
+static int64_t check_in_stride(Check& c, const char* name, int64_t stride, int64_t width) {
+    if (stride == 0) return width;
+    c.need(stride >= width && stride % 8 == 0, DSA_ERR_INVALID_ARG, "%s %lld is not a multiple of 8 of at least %lld",
+           name, (long long)stride, (long long)width);
+    return stride;
+}
+
+dsa_status dsa_kv_insert(const dsa_gqa_shape* shape, const void* k, int64_t k_in, const void* v, int64_t v_in,
+                         const void* q, int64_t q_in, const int32_t* pos, const int64_t* slot, int32_t n,
+                         const float* inv_freq, int32_t rot_dims, dsa_rope_layout layout, void* k_cache,
+                         void* v_cache, float* k_scale, float* v_scale, int64_t num_rows, void* q_out,
+                         int32_t* d_status, cudaStream_t stream) {
+    Check c;
+    const dsa_gqa_shape sh = check_shape(c, shape);
+    c.need(n >= 0, DSA_ERR_INVALID_ARG, "n %d < 0", n);
+    c.need(num_rows >= 1, DSA_ERR_INVALID_ARG, "num_rows %lld < 1", (long long)num_rows);
+    c.need(layout == DSA_ROPE_PAIRS || layout == DSA_ROPE_HALVES, DSA_ERR_UNSUPPORTED,
+           "rotation layout %d is neither DSA_ROPE_PAIRS nor DSA_ROPE_HALVES", (int)layout);
+    if (inv_freq)
+        c.need(rot_dims >= 16 && rot_dims % 16 == 0 && (c.st != DSA_OK || rot_dims <= sh.head_dim), DSA_ERR_UNSUPPORTED,
+               "rot_dims %d is not a multiple of 16 in [16, head_dim]", rot_dims);
+    else
+        c.need(rot_dims == 0, DSA_ERR_INVALID_ARG, "rot_dims %d without inv_freq", rot_dims);
+    int64_t ks = k_in, vs = v_in, qs = q_in;
+    if (c.st == DSA_OK) {
+        const int64_t kw = (int64_t)sh.num_kv_heads * sh.head_dim;
+        ks = check_in_stride(c, "k_in", k_in, kw);
+        vs = check_in_stride(c, "v_in", v_in, kw);
+        if (q) qs = check_in_stride(c, "q_in", q_in, (int64_t)sh.num_heads * sh.head_dim);
+    }
+    if (n > 0) {
+        c.ptr(k, "k");
+        c.ptr(v, "v");
+        c.ptr(pos, "pos", 4);
+        c.ptr(slot, "slot", 8);
+        c.ptr(k_cache, "k_cache");
+        c.ptr(v_cache, "v_cache");
+        if (inv_freq) c.ptr(inv_freq, "inv_freq", 4);
+        if (q) {
+            c.ptr(q, "q");
+            c.ptr(q_out, "q_out");
+            c.need(q_out != q || qs == sh.q_stride, DSA_ERR_INVALID_ARG, "q_out is q with another stride");
+        }
+        if (c.st == DSA_OK && sh.kv_dtype == DSA_FP8_E4M3_ROWSCALE) {
+            c.ptr(k_scale, "k_scale", 4);
+            c.ptr(v_scale, "v_scale", 4);
+        }
+    }
+    dsa_status st = c.done();
+    if (st != DSA_OK || n == 0) return st;
+    return cuda_status(launch_kv_insert(sh, k, ks, v, vs, q, qs, pos, slot, n, inv_freq, rot_dims,
+                                        layout == DSA_ROPE_HALVES, k_cache, v_cache, k_scale, v_scale, num_rows,
+                                        q_out, d_status, stream),
+                       "dsa_kv_insert launch");
+}
+
+static size_t gqa_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s) { return gqa::decode_workspace(sh, s); }
+
+static void check_gqa_sizes(Check& c, const dsa_gqa_shape& sh, const dsa_seqs* s) {
+    if (c.st != DSA_OK) return;
+    c.need(s->num_rows <= INT32_MAX, DSA_ERR_UNSUPPORTED, "num_rows %lld exceeds 2^31 - 1", (long long)s->num_rows);
+    c.need((int64_t)s->max_q_per_seq * (sh.num_heads / sh.num_kv_heads) * sh.num_kv_heads < ((int64_t)1 << 31),
+           DSA_ERR_UNSUPPORTED, "max_q_per_seq %d of %d heads exceeds 2^31 rows", s->max_q_per_seq, sh.num_heads);
+}
+
+dsa_status dense_gqa_workspace_size(const dsa_gqa_shape* shape, const dsa_seqs* seqs, int32_t num_q, size_t* bytes) {
+    Check c;
+    const dsa_gqa_shape sh = check_shape(c, shape);
+    check_seqs(c, seqs, num_q);
+    check_gqa_sizes(c, sh, seqs);
+    c.need(bytes != nullptr, DSA_ERR_INVALID_ARG, "bytes is NULL");
+    dsa_status st = c.done();
+    if (st != DSA_OK) return st;
+    *bytes = gqa_workspace(sh, *seqs);
+    return DSA_OK;
+}
+
+static dsa_status dense_gqa(bool prefill, const dsa_gqa_shape* shape, const void* q, const void* k_cache,
+                            const void* v_cache, const float* k_scale, const float* v_scale, const dsa_seqs* seqs,
+                            int32_t num_q, float sm_scale, void* out, float* lse, void* workspace,
+                            size_t workspace_bytes, int32_t* d_status, cudaStream_t stream) {
+    Check c;
+    const dsa_gqa_shape sh = check_shape(c, shape);
+    check_seqs(c, seqs, num_q);
+    check_gqa_sizes(c, sh, seqs);
+    c.need(sm_scale > -INFINITY && sm_scale < INFINITY, DSA_ERR_INVALID_ARG, "sm_scale is not finite");
+    c.ptr(q, "q");
+    c.ptr(k_cache, "k_cache");
+    c.ptr(v_cache, "v_cache");
+    c.ptr(out, "out");
+    if (lse) c.ptr(lse, "lse", 4);
+    if (shape && shape->kv_dtype == DSA_FP8_E4M3_ROWSCALE) {
+        c.ptr(k_scale, "k_scale", 4);
+        c.ptr(v_scale, "v_scale", 4);
+    }
+    if (c.st == DSA_OK) {
+        const size_t need = gqa_workspace(sh, *seqs);
+        c.need(workspace != nullptr || need == 0, DSA_ERR_WORKSPACE, "workspace is NULL");
+        c.need(workspace == nullptr || aligned(workspace, 256), DSA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+        c.need(workspace_bytes >= need, DSA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    }
+    dsa_status st = c.done();
+    if (st != DSA_OK || num_q == 0) return st;
+    return cuda_status(gqa::launch_decode(sh, q, k_cache, v_cache, k_scale, v_scale, *seqs, num_q, sm_scale, out, lse,
+                                          workspace, d_status, stream),
+                       prefill ? "dense_gqa_prefill launch" : "dense_gqa_decode launch");
+}
+
+dsa_status dense_gqa_decode(const dsa_gqa_shape* shape, const void* q, const void* k_cache, const void* v_cache,
+                            const float* k_scale, const float* v_scale, const dsa_seqs* seqs, int32_t num_q,
+                            float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                            int32_t* d_status, cudaStream_t stream) {
+    return dense_gqa(false, shape, q, k_cache, v_cache, k_scale, v_scale, seqs, num_q, sm_scale, out, lse, workspace,
+                     workspace_bytes, d_status, stream);
+}
+
+dsa_status dense_gqa_prefill(const dsa_gqa_shape* shape, const void* q, const void* k_cache, const void* v_cache,
+                             const float* k_scale, const float* v_scale, const dsa_seqs* seqs, int32_t num_q,
+                             float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                             int32_t* d_status, cudaStream_t stream) {
+    return dense_gqa(true, shape, q, k_cache, v_cache, k_scale, v_scale, seqs, num_q, sm_scale, out, lse, workspace,
+                     workspace_bytes, d_status, stream);
 }
 
 dsa_status dsa_mla_q_prep(const void* q, const float* ssmax_s, const float* ssmax_b, const float* inv_freq,

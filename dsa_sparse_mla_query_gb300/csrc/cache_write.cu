@@ -379,6 +379,158 @@ __global__ void __launch_bounds__(128) mla_q_prep_kernel(const __nv_bfloat16* __
     reinterpret_cast<uint32_t*>(qo + kMV)[lane] = pack_bf16x2(x0 * f, x1 * f);
 }
 
+// ---------------------------------------------------------------------------
+// K and V rows of new tokens into caches with heads, and the queries: rows of
+// D dims, D / 8 lanes per row with 8 dims (16 bytes) each.  A token's cosines
+// and sines serve all its query and key heads, so a CTA takes `tb` tokens at a
+// time, computes their tables once in shared memory and then walks the
+// tokens' rows (query heads, key heads, value heads).
+constexpr int kKvThreads = 256;
+constexpr int kKvMaxTokens = 8;  // tokens per CTA pass
+constexpr int kKvUnroll = 4;     // rows a thread has in flight
+
+struct KvInsert {
+    const __nv_bfloat16 *k, *v, *q;
+    int64_t k_in, v_in, q_in;  // elements between tokens
+    const int32_t* pos;
+    const int64_t* slot;
+    const float* inv_freq;
+    void *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+    __nv_bfloat16* q_out;
+    int64_t k_stride, v_stride, q_stride;  // elements between rows of the destinations
+    int64_t num_rows;
+    int32_t n, hq, hkv, rot;  // hq: 0 when there are no queries; rot: 0 for no rotation
+    int32_t tb;
+};
+
+template <int D, bool FP8, bool HALVES>
+__global__ void __launch_bounds__(kKvThreads) kv_insert_kernel(const __grid_constant__ KvInsert a, int32_t* d_status) {
+    constexpr int kLanes = D / 8;  // lanes per row
+    __shared__ float2 cs[kKvMaxTokens][D / 2];
+    pdl_enter();
+    const int rows = a.hq + 2 * a.hkv;
+    const int half = a.rot / 2;
+    const int li = threadIdx.x % kLanes;
+    for (int64_t t0 = (int64_t)blockIdx.x * a.tb; t0 < a.n; t0 += (int64_t)gridDim.x * a.tb) {
+        const int nt = (int)min((int64_t)a.tb, a.n - t0);
+        const int items = nt * rows;
+        for (int i0 = threadIdx.x / kLanes; i0 - (int)(threadIdx.x / kLanes) < items;
+             i0 += kKvUnroll * (kKvThreads / kLanes)) {
+            // item: (token, row) with the row fastest
+            uint4 x[kKvUnroll];
+            int tok[kKvUnroll], row[kKvUnroll];
+#pragma unroll
+            for (int u = 0; u < kKvUnroll; ++u) {
+                const int it = i0 + u * (kKvThreads / kLanes);
+                row[u] = it < items ? it % rows : -1;
+                tok[u] = it < items ? it / rows : 0;
+                x[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (row[u] >= 0) {
+                    const int64_t t = t0 + tok[u];
+                    const int r = row[u];
+                    const __nv_bfloat16* src = r < a.hq           ? a.q + t * a.q_in + (int64_t)r * D
+                                               : r < a.hq + a.hkv ? a.k + t * a.k_in + (int64_t)(r - a.hq) * D
+                                                                  : a.v + t * a.v_in + (int64_t)(r - a.hq - a.hkv) * D;
+                    x[u] = __ldcs(reinterpret_cast<const uint4*>(src) + li);
+                }
+            }
+            if (i0 == (int)(threadIdx.x / kLanes)) {
+                // the tokens' rotation tables, while the first rows are in flight
+                __syncthreads();  // the previous tokens' tables are no longer read
+                for (int i = threadIdx.x; i < nt * half; i += kKvThreads) {
+                    const int t = i / half, f = i - t * half;
+                    const int p = __ldg(a.pos + t0 + t);
+                    float c = 1.f, s = 0.f;
+                    if (p >= 0) rope_cs(p, __ldg(a.inv_freq + f), c, s);
+                    cs[t][f] = make_float2(c, s);
+                }
+                __syncthreads();
+            }
+#pragma unroll
+            for (int u = 0; u < kKvUnroll; ++u) {
+                const int r = row[u];
+                const bool is_q = r >= 0 && r < a.hq, is_k = r >= a.hq && r < a.hq + a.hkv;
+                float v[8];
+                unpack_bf16x8(x[u], v);
+                if (a.rot) {
+                    const float2* tab = cs[tok[u]];
+                    if (HALVES) {
+                        // chunk li holds dims 8 li .. 8 li + 7; its pairs' other halves are rot / 16 lanes away
+                        const int step = a.rot / 16;
+                        const bool first = li < step, second = li >= step && li < 2 * step;
+                        const int lane = threadIdx.x & 31;
+                        const int from = first ? lane + step : second ? lane - step : lane;
+                        uint4 y;
+                        y.x = __shfl_sync(0xffffffffu, x[u].x, from);
+                        y.y = __shfl_sync(0xffffffffu, x[u].y, from);
+                        y.z = __shfl_sync(0xffffffffu, x[u].z, from);
+                        y.w = __shfl_sync(0xffffffffu, x[u].w, from);
+                        if ((is_q || is_k) && (first || second)) {
+                            float o[8];
+                            unpack_bf16x8(y, o);
+                            const int f0 = (first ? li : li - step) * 8;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float2 w = tab[f0 + e];
+                                v[e] = first ? fmaf(v[e], w.x, -o[e] * w.y) : fmaf(o[e], w.y, v[e] * w.x);
+                            }
+                        }
+                    } else if ((is_q || is_k) && 8 * li < a.rot) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 w = tab[4 * li + e];
+                            const float x0 = v[2 * e], x1 = v[2 * e + 1];
+                            v[2 * e] = fmaf(x0, w.x, -x1 * w.y);
+                            v[2 * e + 1] = fmaf(x0, w.y, x1 * w.x);
+                        }
+                    }
+                }
+                float m = 0.f;
+                if (FP8) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+#pragma unroll
+                    for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                }
+                if (r < 0) continue;  // after the shuffles
+                const int64_t t = t0 + tok[u];
+                const int p = __ldg(a.pos + t);
+                const int64_t sl = __ldg(a.slot + t);
+                if (is_q) {
+                    if (p < 0 || sl >= a.num_rows) continue;  // the key heads report it
+                    uint4* dst = reinterpret_cast<uint4*>(a.q_out + t * a.q_stride + (int64_t)r * D);
+                    dst[li] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                         pack_bf16x2(v[6], v[7]));
+                    continue;
+                }
+                if (sl < 0) continue;
+                if (sl >= a.num_rows || p < 0) {
+                    if (li == 0) report(d_status, DSA_ERR_BAD_INPUT);
+                    continue;
+                }
+                const int h = is_k ? r - a.hq : r - a.hq - a.hkv;
+                const int64_t at = sl * (is_k ? a.k_stride : a.v_stride) + (int64_t)h * D;
+                if (FP8) {
+                    // a row below 448 * 2^-126 takes the smallest normal scale: 1 / scale stays finite
+                    const float scale = m > 0.f ? fmaxf(m / 448.f, 0x1p-126f) : 1.f;
+                    const float rs = 1.f / scale;
+                    uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_k ? a.k_cache : a.v_cache) + at);
+                    dst[li] = make_uint2(pack_e4m3x4(v[0] * rs, v[1] * rs, v[2] * rs, v[3] * rs),
+                                         pack_e4m3x4(v[4] * rs, v[5] * rs, v[6] * rs, v[7] * rs));
+                    if (li == 0) (is_k ? a.k_scale : a.v_scale)[sl * a.hkv + h] = scale;
+                } else {
+                    uint4* dst =
+                        reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_k ? a.k_cache : a.v_cache) + at);
+                    dst[li] = is_k ? make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]))
+                                   : x[u];
+                }
+            }
+        }
+    }
+}
+
 constexpr int kTokensPerCta = kWarpsPerCta;
 
 // a grid of a few waves of CTAs (16 per SM) walking the items (keys in groups
@@ -433,6 +585,51 @@ cudaError_t launch_mla_q_prep(const void* q, const float* ssmax_s, const float* 
     const dim3 grid((unsigned)(((int64_t)num_q * kMH + kTokensPerCta - 1) / kTokensPerCta));
     return launch_pdl(mla_q_prep_kernel, grid, dim3(128), 0, stream, 1, static_cast<const __nv_bfloat16*>(q), ssmax_s,
                       ssmax_b, inv_freq, q_pos, num_q, static_cast<__nv_bfloat16*>(q_out), d_status);
+}
+
+cudaError_t launch_kv_insert(const dsa_gqa_shape& sh, const void* k, int64_t k_in, const void* v, int64_t v_in,
+                             const void* q, int64_t q_in, const int32_t* pos, const int64_t* slot, int32_t n,
+                             const float* inv_freq, int32_t rot, bool halves, void* k_cache, void* v_cache,
+                             float* k_scale, float* v_scale, int64_t num_rows, void* q_out, int32_t* d_status,
+                             cudaStream_t stream) {
+    if (n <= 0) return cudaSuccess;
+    KvInsert a;
+    a.k = static_cast<const __nv_bfloat16*>(k);
+    a.v = static_cast<const __nv_bfloat16*>(v);
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.k_in = k_in;
+    a.v_in = v_in;
+    a.q_in = q_in;
+    a.pos = pos;
+    a.slot = slot;
+    a.inv_freq = inv_freq;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.q_out = static_cast<__nv_bfloat16*>(q_out);
+    a.k_stride = sh.k_stride;
+    a.v_stride = sh.v_stride;
+    a.q_stride = sh.q_stride;
+    a.num_rows = num_rows;
+    a.n = n;
+    a.hq = q ? sh.num_heads : 0;
+    a.hkv = sh.num_kv_heads;
+    a.rot = inv_freq ? rot : 0;
+    // tokens per CTA pass: a pass of all its threads' unrolled rows, as long as
+    // the tokens still give every SM several CTAs
+    const int rows = a.hq + 2 * a.hkv;
+    const int per_pass = kKvUnroll * (kKvThreads * 8 / sh.head_dim);
+    a.tb = std::max(1, std::min(kKvMaxTokens, per_pass / rows));
+    while (a.tb > 1 && n / a.tb < 152 * 8) a.tb /= 2;
+    const dim3 grid(insert_grid(((int64_t)n + a.tb - 1) / a.tb * kTokensPerCta));
+    const bool fp8 = sh.kv_dtype == DSA_FP8_E4M3_ROWSCALE;
+    auto go = [&](auto kern) { return launch_pdl(kern, grid, dim3(kKvThreads), 0, stream, 1, a, d_status); };
+    if (sh.head_dim == 64)
+        return fp8 ? (halves ? go(kv_insert_kernel<64, true, true>) : go(kv_insert_kernel<64, true, false>))
+                   : (halves ? go(kv_insert_kernel<64, false, true>) : go(kv_insert_kernel<64, false, false>));
+    return fp8 ? (halves ? go(kv_insert_kernel<128, true, true>) : go(kv_insert_kernel<128, true, false>))
+               : (halves ? go(kv_insert_kernel<128, false, true>) : go(kv_insert_kernel<128, false, false>));
 }
 
 }  // namespace dsa

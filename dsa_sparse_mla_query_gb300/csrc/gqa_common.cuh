@@ -1,0 +1,60 @@
+// gqa_common.cuh -- pieces shared by the dense grouped-head attention kernels
+// (gqa_decode.cu, gqa_prefill.cu): the workspace plan and the tensor maps.
+#pragma once
+
+#include "indexer_common.cuh"
+
+namespace dsa {
+namespace gqa {
+
+constexpr int kPlanSms = 152;  // GB300's SMs: sizes that the host alone has to know are planned for them
+
+// A sequence's counts, checked: queries [q0, q0 + nq) over `ctx` tokens.
+struct Seq {
+    int ctx, q0, nq;
+    bool ok;
+};
+__device__ __forceinline__ Seq load_seq(const dsa_seqs& s, int b, int num_q) {
+    Seq r;
+    r.ctx = __ldg(s.ctx_len + b);
+    r.q0 = __ldg(s.q_start + b);
+    const int qe = __ldg(s.q_start + b + 1);
+    r.nq = qe - r.q0;
+    r.ok = r.ctx >= 0 && r.ctx <= s.max_ctx && r.q0 >= 0 && qe >= r.q0 && qe <= num_q && r.nq <= s.max_q_per_seq;
+    return r;
+}
+
+// Tensor map over a cache [rows, heads, d] whose rows lie `stride` elements
+// apart: dimensions (128 bytes of a head's row, rows, the row's 128-byte
+// pieces, heads), so that a box of R rows lands in shared memory as one
+// [R][128 B] swizzled block per piece (all of a row's pieces, or one).  A
+// head row of 64 bytes (e4m3, d = 64) is one piece of 64 bytes.
+inline cudaError_t cache_map(CUtensorMap* m, bool bytes, const void* base, int heads, int d, int64_t stride,
+                             int64_t rows, int box_rows, bool all_pieces) {
+    auto enc = tmap_encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const uint64_t el = bytes ? 1 : 2;
+    const uint64_t piece = std::min<uint64_t>(128, d * el);
+    cuuint64_t dims[4] = {piece / el, (cuuint64_t)rows, d * el / piece, (cuuint64_t)heads};
+    cuuint64_t strides[3] = {(cuuint64_t)stride * el, piece, d * el};
+    cuuint32_t box[4] = {(cuuint32_t)(piece / el), (cuuint32_t)box_rows,
+                         all_pieces ? (cuuint32_t)(d * el / piece) : 1u, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    const CUresult r = enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                           const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           piece == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
+}
+
+}  // namespace gqa
+}  // namespace dsa

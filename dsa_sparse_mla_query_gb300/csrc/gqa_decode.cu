@@ -1,0 +1,964 @@
+// gqa_decode.cu -- dense attention of a few new tokens per sequence over a
+// long K/V cache with grouped heads (sm_103a), split over the cache and joined.
+//
+//   s_j = sm_scale * q_h . k_j,  p = softmax over j <= pos,  out = sum_j p_j v_j
+//
+// One pass over the keys with a running reference m (in log2 units) and sum l
+// per query row: p_j = 2^(x_j - m), x_j = s_j log2 e, l and the output
+// accumulators rescaled when a row's maximum passes m by more than 8 (so a
+// weight stays below 2^8).  Partial results (m, l, O) of pieces of a row's
+// keys combine exactly: M = max m, weights 2^(m - M).
+//
+// What bounds it: the cache is read once, 2 (G T) / 2 flop a byte (G query
+// heads a key head, T new tokens): HBM.  So the products run on the warp-level
+// matrix instruction straight from shared memory (8 columns wide: no padding
+// of a group of 8), which leaves the accumulators in registers and the
+// issue slots mostly idle, and everything else serves the stream of loads:
+// - A CTA owns a contiguous piece of the space (lane = key head x row chunk,
+//   sequence, 64-key tile), balanced over the tiles that exist, and CTAs of
+//   neighbouring lanes walk the same keys at the same time, so a token's heads
+//   (256 or 512 bytes apart) are read from the same DRAM pages together.
+// - One warp loads: TMA boxes of whole pages (or 64 rows) into a ring of
+//   stages; four warps (eight for more than 16 rows) take 16 keys of each tile,
+//   each with its own softmax state, and meet only at the end of a sequence.
+// - A sequence cut by CTA borders leaves one partial per CTA, which a second
+//   kernel joins in a fixed order.
+#include <type_traits>
+
+#include "gqa_common.cuh"
+
+namespace dsa {
+namespace gqa {
+namespace {
+
+constexpr int kTile = 64;  // keys per tile
+constexpr int kTagDecode = 6;
+constexpr float kLazy = 8.f;  // a row's reference moves when its maximum passes it by 2^8
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D, bool FP8, int NT, int RG>
+struct Cfg {
+    static constexpr int kRows = 8 * NT * RG;  // query rows per chunk
+    static constexpr int kThreads = 32 * (4 * RG + 1);
+    static constexpr int kOcc = RG == 1 ? 2 : 1;  // CTAs per SM
+    static constexpr int kHeadBytes = D * (FP8 ? 1 : 2);
+    static constexpr int kHalf = kTile * kHeadBytes;  // K or V of a stage
+    static constexpr int kStage = 2 * kHalf;
+    static constexpr int kScaleBytes = FP8 ? 2 * kTile * 4 : 0;
+    static constexpr int kScratch = RG * 4 * 8 * D * 4;  // the four key slices' outputs of 8 rows
+    static constexpr int kMl = RG * 4 * 8 * NT * 8;
+    static constexpr int kMisc = 256;
+    static constexpr int kBudget = (RG == 1 ? 115712 : 232448) - kScratch - kMl - kMisc;
+    static constexpr int kFit = kBudget / (kStage + kScaleBytes);
+    static constexpr int kStages = kFit < 8 ? kFit : 8;
+    static constexpr int kSmem = kStages * (kStage + kScaleBytes) + kScratch + kMl + kMisc;
+    static_assert(kStages >= 3, "a ring of at least three stages");
+};
+
+struct Args {
+    const __nv_bfloat16* q;
+    const float *k_scale, *v_scale;
+    __nv_bfloat16* out;
+    float* lse;
+    float* part_o;   // [2 grid][rows][D]
+    float2* part_ml; // [2 grid][rows]
+    int4* desc;      // [grid]: {parts, q0, nq, lane} of the cut sequence that the CTA is the second of
+    dsa_seqs s;
+    int64_t q_stride;
+    int32_t* d_status;
+    float scale_log2;
+    int32_t num_q, group, hkv, lanes, hl, parts;  // hl: lanes side by side; parts: CTAs per lane column
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void lds128(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void lds64(uint32_t (&r)[2], uint32_t addr) {
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ void bar_sync(int id, int n) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ float warp_max_all(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+// byte address of 16-byte chunk `c` of a tile's row in the layout TMA wrote
+// (128-byte pieces of 64 rows, 128-byte swizzle; a 64-byte head row: 64-byte
+// swizzle)
+template <int HB>
+__device__ __forceinline__ uint32_t chunk_addr(uint32_t base, int row, int c) {
+    if (HB == 64) return base + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+    return base + (c >> 3) * (kTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+}
+
+__device__ __forceinline__ int tiles_of(const Seq& q) {
+    return q.ok && q.nq > 0 ? max(1, (q.ctx + kTile - 1) / kTile) : 0;
+}
+
+// The walk over a CTA's pieces: each call of next() gives a run of tiles
+// [i0, i1) of one (lane, sequence).  Every warp of the CTA walks alike.
+struct Piece {
+    int lane, b, i0, i1;
+    Seq q;
+    bool front, back;        // cut by the border before / after this CTA
+    int row0, tok0, ntok;    // chunk's first row, first token and tokens
+    int limit;               // keys that some query of the chunk sees
+    int64_t base;            // first row of a contiguous sequence
+};
+
+struct Walk {
+    int64_t r0, left, sum, total;
+    int u, b, i;
+    __device__ __forceinline__ void init(const Args& a) {
+        const int lane = threadIdx.x & 31;
+        const int B = a.s.num_seqs;
+        const int c = blockIdx.x / a.hl;
+        const int units = a.lanes / a.hl;
+        // every lane a run of sequences: their tiles, then a scan over the lanes
+        const int per = (B + 31) / 32;
+        int64_t mine = 0;
+        for (int k = 0; k < per; k += 4) {
+            int v[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int bb = lane * per + k + x;
+                v[x] = 0;
+                if (k + x < per && bb < B) {
+                    const Seq q = load_seq(a.s, bb, a.num_q);
+                    v[x] = tiles_of(q);
+                    if (!q.ok && blockIdx.x == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
+                }
+            }
+            mine += v[0] + v[1] + v[2] + v[3];
+        }
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        sum = __shfl_sync(0xffffffffu, incl, 31);
+        total = sum * units;
+        const int64_t p = min((int64_t)a.parts, total);
+        left = 0;
+        u = b = i = 0;
+        r0 = 0;
+        if (c >= p) return;  // fewer tiles than CTAs
+        r0 = total * c / p;
+        left = total * (c + 1) / p - r0;
+        u = (int)(r0 / sum);
+        const int64_t rem = r0 - u * sum;
+        const uint32_t hit = __ballot_sync(0xffffffffu, rem >= incl - mine && rem < incl);
+        const int l = __ffs(hit) - 1;
+        int64_t off = rem - __shfl_sync(0xffffffffu, incl - mine, l);
+        // within that lane's run
+        for (int k0 = 0; k0 < per; k0 += 32) {
+            const int bb = l * per + k0 + lane;
+            int v = 0;
+            if (k0 + lane < per && bb < B) v = tiles_of(load_seq(a.s, bb, a.num_q));
+            int in = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, in, o);
+                if (lane >= o) in += y;
+            }
+            const uint32_t h = __ballot_sync(0xffffffffu, off >= in - v && off < in);
+            if (h) {
+                const int x = __ffs(h) - 1;
+                b = l * per + k0 + x;
+                i = (int)(off - __shfl_sync(0xffffffffu, in - v, x));
+                break;
+            }
+            off -= __shfl_sync(0xffffffffu, in, 31);
+        }
+    }
+    template <int ROWS>
+    __device__ __forceinline__ bool next(const Args& a, Piece& p) {
+        while (left > 0) {
+            if (b == a.s.num_seqs) {
+                b = 0;
+                ++u;
+            }
+            const Seq q = load_seq(a.s, b, a.num_q);
+            const int cnt = tiles_of(q);
+            if (cnt == 0) {
+                ++b;
+                continue;
+            }
+            const int take = (int)min((int64_t)(cnt - i), left);
+            p.lane = blockIdx.x % a.hl + a.hl * u;
+            p.b = b;
+            p.i0 = i;
+            p.i1 = i + take;
+            p.q = q;
+            p.front = i > 0;
+            p.back = i + take < cnt;
+            left -= take;
+            i = 0;
+            ++b;
+            p.row0 = p.lane / a.hkv * ROWS;
+            const int64_t rows = (int64_t)q.nq * a.group;
+            if (p.row0 >= rows) continue;  // fewer queries than the longest sequence's
+            p.tok0 = p.row0 / a.group;
+            const int last = (int)min((int64_t)p.row0 + ROWS, rows) - 1;
+            p.ntok = last / a.group - p.tok0 + 1;
+            // keys that the chunk's queries see (at most ROWS <= 32 tokens)
+            int pos = -1;
+            const int lane = threadIdx.x & 31;
+            if (lane < p.ntok) {
+                pos = __ldg(a.s.q_pos + q.q0 + p.tok0 + lane);
+                if (pos < -1 || pos >= q.ctx) pos = -1;
+            }
+            p.limit = __reduce_max_sync(0xffffffffu, pos) + 1;
+            p.base = a.s.page_table ? 0 : __ldg(a.s.seq_base + p.b);
+            return true;
+        }
+        return false;
+    }
+};
+
+template <int D, bool FP8, int NT, int RG>
+__global__ void __launch_bounds__(Cfg<D, FP8, NT, RG>::kThreads, Cfg<D, FP8, NT, RG>::kOcc)
+    gqa_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                      const __grid_constant__ Args a) {
+    using C = Cfg<D, FP8, NT, RG>;
+    constexpr int HB = C::kHeadBytes;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* ring = smem;
+    float* ring_scale = reinterpret_cast<float*>(smem + C::kStages * C::kStage);
+    float* scratch = reinterpret_cast<float*>(smem + C::kStages * (C::kStage + C::kScaleBytes));
+    float2* ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(scratch) + C::kScratch);
+    uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ml) + C::kMl);
+    uint64_t* empty = full + C::kStages;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + C::kStages);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kConsumers = 4 * RG;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            ptx::mbar_init(full + i, FP8 ? 33 : 1);
+            ptx::mbar_init(empty + i, kConsumers);
+        }
+        abort_flag[0] = 0;
+        abort_flag[1] = kTagDecode;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&kmap);
+        ptx::prefetch_tmap(&vmap);
+    }
+    __syncthreads();
+    pdl_enter();
+
+    Walk w;
+    w.init(a);
+    Piece p;
+
+    if (warp == kConsumers) {
+        // ---- the loading warp: a lane per TMA box of a 32-box window of the page table
+        const int R = a.s.page_table ? min(a.s.page_size, kTile) : kTile;  // rows per box
+        const int nbox = kTile / R;
+        const int shift = 31 - __clz(R);
+        int it = 0;
+        bool ok = true;
+        while (ok && w.next<C::kRows>(a, p)) {
+            const int kvh = p.lane % a.hkv;
+            const int end = min(p.i1, (p.limit + kTile - 1) / kTile);
+            auto row_of = [&](int box) -> int {  // physical row of the box's first token, -1: none
+                const int64_t j = (int64_t)box << shift;
+                if (j >= p.limit) return -1;
+                int64_t row;
+                if (a.s.page_table) {
+                    row = phys_row(a.s, p.b, j);
+                    if (row >= 0 && row + R > a.s.num_rows) row = -1;  // a page past the cache
+                } else {
+                    row = p.base + j;
+                    const int64_t last = p.base + min(j + R, (int64_t)p.limit);
+                    if (row < 0 || last > a.s.num_rows) row = -1;
+                }
+                if (row < 0) report(a.d_status, DSA_ERR_BAD_INPUT);
+                return (int)row;
+            };
+            int w0 = p.i0 * nbox;
+            int cur = p.i0 < end ? row_of(w0 + lane) : -1, nxt = p.i0 < end ? row_of(w0 + 32 + lane) : -1;
+            for (int i = p.i0; i < end && ok; ++i, ++it) {
+                const int st = it % C::kStages;
+                if (i * nbox >= w0 + 32) {
+                    w0 += 32;
+                    cur = nxt;
+                    nxt = row_of(w0 + 32 + lane);
+                }
+                if (it >= C::kStages) {
+                    ok = ptx::mbar_wait(empty + st, (it / C::kStages - 1) & 1, abort_flag, a.d_status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                }
+                uint8_t* kd = ring + st * C::kStage;
+                uint8_t* vd = kd + C::kHalf;
+                const int l = i * nbox - w0;  // window lane of the tile's first box
+                const uint32_t have = __ballot_sync(0xffffffffu, cur >= 0 && lane >= l && lane < l + nbox);
+                if (lane == 0) ptx::mbar_expect_tx(full + st, (uint32_t)__popc(have) * 2u * R * HB);
+                __syncwarp();
+                if ((have >> lane) & 1) {
+                    const int x = lane - l;
+                    constexpr int PB = HB < 128 ? HB : 128;
+                    if (HB <= 128 || nbox == 1) {
+                        tma_load_4d(kd + x * R * PB, &kmap, 0, cur, 0, kvh, full + st);
+                        tma_load_4d(vd + x * R * PB, &vmap, 0, cur, 0, kvh, full + st);
+                    } else {
+                        // two 128-byte pieces, each a block of 64 rows: a smaller box is one piece
+                        for (int h = 0; h < HB / 128; ++h) {
+                            tma_load_4d(kd + h * (kTile * 128) + x * R * 128, &kmap, 0, cur, h, kvh, full + st);
+                            tma_load_4d(vd + h * (kTile * 128) + x * R * 128, &vmap, 0, cur, h, kvh, full + st);
+                        }
+                    }
+                }
+                if (FP8) {
+                    float* sd = ring_scale + st * (C::kScaleBytes / 4);
+#pragma unroll
+                    for (int h = 0; h < kTile / 32; ++h) {
+                        const int x = h * 32 + lane;
+                        const int row = __shfl_sync(0xffffffffu, cur, l + (x >> shift));
+                        const int64_t at = ((int64_t)row + (x & (R - 1))) * a.hkv + kvh;
+                        if (row >= 0 && (int64_t)i * kTile + x < p.limit) {
+                            ptx::cp_async4(sd + x, a.k_scale + at);
+                            ptx::cp_async4(sd + kTile + x, a.v_scale + at);
+                        }
+                    }
+                    ptx::cp_async_arrive_noinc(full + st);
+                }
+            }
+        }
+        if (!ok) {
+            // after an abort: let the copies in flight land before the CTA ends
+            for (int k = max(0, it - C::kStages); k < it; ++k)
+                ptx::mbar_drain(full + k % C::kStages, (k / C::kStages) & 1);
+        }
+        return;
+    }
+
+    // ---- the computing warps: key slice ks of every tile for row group rg
+    const int ks = warp & 3, rg = warp >> 2;
+    const int g = lane >> 2, t = lane & 3;
+    constexpr int KK = D / 16;  // k-steps of q.k, and 16-dim tiles of the output
+    const uint32_t ring_u = smem_u32(ring);
+    int it = 0;
+    bool ok = true;
+    int4 join = make_int4(0, 0, 0, 0);
+    while (w.next<C::kRows>(a, p)) {
+        const int kvh = p.lane % a.hkv;
+        const int end = min(p.i1, (p.limit + kTile - 1) / kTile);
+        // queries of this thread's fragment rows (column g of each 8-row tile)
+        uint32_t qf[NT][KK][2];
+        float qfac[NT][2];  // FP8: 2^-e of the columns' scaled queries
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int f = p.row0 + (rg * NT + n) * 8 + g;
+            const int tok = f / a.group, head = f - tok * a.group;
+            const bool live = tok < p.q.nq;
+            const __nv_bfloat16* src =
+                a.q + (int64_t)(p.q.q0 + tok) * a.q_stride + (int64_t)(kvh * a.group + head) * D;
+            if (!FP8) {
+#pragma unroll
+                for (int k = 0; k < KK; ++k) {
+                    const uint32_t* s32 = reinterpret_cast<const uint32_t*>(src + k * 16 + 2 * t);
+                    qf[n][k][0] = live ? __ldg(s32) : 0u;
+                    qf[n][k][1] = live ? __ldg(s32 + 4) : 0u;
+                }
+            } else {
+                // dims (D/4) t .. + D/4 - 1: k-step k takes 4 of them.  f16 after an
+                // exact power-of-two scaling of the row to [2^14, 2^15): only values
+                // 2^28 below the row's largest lose bits.
+                float v[D / 4];
+                float top = 0.f;
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(src + (D / 4) * t) + k)
+                                         : make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[8 * k + 2 * e] = __uint_as_float(xs[e] << 16);
+                        v[8 * k + 2 * e + 1] = __uint_as_float(xs[e] & 0xFFFF0000u);
+                        top = fmaxf(top, fmaxf(fabsf(v[8 * k + 2 * e]), fabsf(v[8 * k + 2 * e + 1])));
+                    }
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // the row times 2^(14 - e), e = exponent of its largest; in two factors, each a normal
+                const int e = top > 0.f && top < INFINITY ? ilogbf(top) : 14;
+                const int sh = min(14 - e, 126);  // a row below 2^-112 keeps its size
+                const float up = __int_as_float((127 + sh) << 23);
+#pragma unroll
+                for (int k = 0; k < KK; ++k) {
+                    qf[n][k][0] = pack_f16(v[4 * k] * up, v[4 * k + 1] * up);
+                    qf[n][k][1] = pack_f16(v[4 * k + 2] * up, v[4 * k + 3] * up);
+                }
+                const float down = sh <= 126 && sh >= -126 ? __int_as_float((127 - sh) << 23) : 0.f;
+                qfac[n][0] = __shfl_sync(0xffffffffu, down, (2 * t) * 4) * a.scale_log2;
+                qfac[n][1] = __shfl_sync(0xffffffffu, down, (2 * t + 1) * 4) * a.scale_log2;
+            }
+        }
+        // the columns' positions (rows 2t and 2t+1 of each 8-row tile); -2: not to be written
+        int cpos[NT][2];
+        int minpos = 0x7FFFFFFF;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int tok = (p.row0 + (rg * NT + n) * 8 + 2 * t + c) / a.group;
+                int pos = -2;
+                if (tok < p.q.nq) {
+                    pos = __ldg(a.s.q_pos + p.q.q0 + tok);
+                    if (pos < -1 || pos >= p.q.ctx) {
+                        if (!p.front) report(a.d_status, DSA_ERR_BAD_INPUT);
+                        pos = -2;
+                    }
+                    minpos = min(minpos, pos);
+                }
+                cpos[n][c] = pos;
+            }
+        minpos = __reduce_min_sync(0xffffffffu, minpos);
+
+        float o[NT][KK][4];
+        float m[NT][2], l[NT][2];
+        float vref = 0x1p-126f, vinv = 0x1p126f;  // FP8: V scales are held relative to vref, a power of two
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int k = 0; k < KK; ++k) o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
+        }
+
+        for (int i = p.i0; i < end; ++i, ++it) {
+            const int st = it % C::kStages;
+            ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(full + st, (it / C::kStages) & 1, abort_flag, a.d_status));
+            if (!ok) continue;  // keep to the walk, so that the slices still meet at its barriers
+            const uint32_t kb = ring_u + st * C::kStage, vb = kb + C::kHalf;
+            const int r0 = ks * 16;                // this warp's first key within the tile
+            const int j0 = i * kTile + r0;         // and its position
+            const bool edge = j0 + 16 > p.limit;   // rows past the last key that is seen
+            if (edge) {
+                // whatever lies there must not reach the products: its weights are 0, but 0 * inf is not
+                uint8_t* vrow = ring + st * C::kStage + C::kHalf;
+                for (int x = lane; x < 16 * (HB / 16); x += 32) {
+                    const int row = r0 + x / (HB / 16), c = x % (HB / 16);
+                    if (i * kTile + row >= p.limit)
+                        *reinterpret_cast<uint4*>(vrow + (chunk_addr<HB>(0u, row, c))) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+            }
+            // S^T = K Q^T: 16 keys x 8 rows per tile
+            float s[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            float s2[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s2[n][0] = s2[n][1] = s2[n][2] = s2[n][3] = 0.f;
+            if (!FP8) {
+#pragma unroll
+                for (int k = 0; k < KK; ++k) {
+                    uint32_t af[4];
+                    ldsm4(af, chunk_addr<HB>(kb, r0 + (lane & 15), 2 * k + (lane >> 4)));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma16816<false>(k & 1 ? s2[n] : s[n], af, qf[n][k][0], qf[n][k][1]);
+                }
+            } else {
+                uint32_t x0[D / 16], x1[D / 16];  // rows g and g + 8: the thread's D / 4 dims
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t y[4];
+                    lds128(y, chunk_addr<HB>(kb, r0 + g, (D / 64) * t + c));
+                    x0[4 * c] = y[0], x0[4 * c + 1] = y[1], x0[4 * c + 2] = y[2], x0[4 * c + 3] = y[3];
+                    lds128(y, chunk_addr<HB>(kb, r0 + g + 8, (D / 64) * t + c));
+                    x1[4 * c] = y[0], x1[4 * c + 1] = y[1], x1[4 * c + 2] = y[2], x1[4 * c + 3] = y[3];
+                }
+#pragma unroll
+                for (int k = 0; k < KK; ++k) {
+                    const uint32_t af[4] = {e4m3x2_to_f16x2((uint16_t)x0[k]), e4m3x2_to_f16x2((uint16_t)x1[k]),
+                                            e4m3x2_to_f16x2((uint16_t)(x0[k] >> 16)),
+                                            e4m3x2_to_f16x2((uint16_t)(x1[k] >> 16))};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma16816<true>(k & 1 ? s2[n] : s[n], af, qf[n][k][0], qf[n][k][1]);
+                }
+            }
+            // scores in log2 units, masked
+            float fk0 = 1.f, fk1 = 1.f, fv0 = 1.f, fv1 = 1.f;
+            if (FP8) {
+                const float* sd = ring_scale + st * (C::kScaleBytes / 4);
+                fk0 = sd[r0 + g], fk1 = sd[r0 + g + 8];
+                fv0 = j0 + g < p.limit ? sd[kTile + r0 + g] : 0.f;
+                fv1 = j0 + g + 8 < p.limit ? sd[kTile + r0 + g + 8] : 0.f;
+            }
+            const bool masked = j0 + 15 > minpos;
+            float mx[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float f = FP8 ? qfac[n][c] : a.scale_log2;
+                    float x0 = (s[n][c] + s2[n][c]) * (FP8 ? f * fk0 : f);
+                    float x1 = (s[n][2 + c] + s2[n][2 + c]) * (FP8 ? f * fk1 : f);
+                    if (masked) {
+                        x0 = j0 + g <= cpos[n][c] ? x0 : -INFINITY;
+                        x1 = j0 + g + 8 <= cpos[n][c] ? x1 : -INFINITY;
+                    }
+                    s[n][c] = x0;
+                    s[n][2 + c] = x1;
+                    mx[n][c] = fmaxf(x0, x1);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    mx[n][c] = fmaxf(mx[n][c], __shfl_xor_sync(0xffffffffu, mx[n][c], 4));
+                    mx[n][c] = fmaxf(mx[n][c], __shfl_xor_sync(0xffffffffu, mx[n][c], 8));
+                    mx[n][c] = fmaxf(mx[n][c], __shfl_xor_sync(0xffffffffu, mx[n][c], 16));
+                }
+            bool move = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) move = move || mx[n][0] > m[n][0] + kLazy || mx[n][1] > m[n][1] + kLazy;
+            float vtop = 0.f;
+            if (FP8) {
+                vtop = fmaxf(fv0, fv1);
+                move = move || vtop > vref;
+            }
+            if (__any_sync(0xffffffffu, move)) {
+                float fv = 1.f;
+                if (FP8) {
+                    vtop = warp_max_all(vtop);
+                    if (vtop > vref) {
+                        // the next power of two (the largest finite one for an infinite scale)
+                        const float nref = __uint_as_float(
+                            min((__float_as_uint(vtop) & 0x7F800000u) + 0x00800000u, 0x7E800000u));
+                        fv = vref * (1.f / nref);
+                        vref = nref;
+                        vinv = 1.f / nref;
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float al[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float mn = fmaxf(m[n][c], mx[n][c]);
+                        al[c] = mn == m[n][c] ? 1.f : fast_exp2(m[n][c] - mn);
+                        m[n][c] = mn;
+                        l[n][c] *= al[c];
+                        al[c] *= fv;
+                    }
+#pragma unroll
+                    for (int k = 0; k < KK; ++k) {
+                        o[n][k][0] *= al[0];
+                        o[n][k][1] *= al[1];
+                        o[n][k][2] *= al[0];
+                        o[n][k][3] *= al[1];
+                    }
+                }
+            }
+            // weights, as the B operand of O^T = V^T P^T (two 8x8 transposes per tile)
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float w0[2], w1[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float mm = m[n][c] == -INFINITY ? 0.f : m[n][c];
+                    w0[c] = fast_exp2(s[n][c] - mm);
+                    w1[c] = fast_exp2(s[n][2 + c] - mm);
+                    l[n][c] += w0[c] + w1[c];
+                    if (FP8) {
+                        w0[c] *= fv0 * vinv;
+                        w1[c] *= fv1 * vinv;
+                    }
+                }
+                // bf16 rounds a weight by up to 2^-9 of itself, f16 by 2^-12 (or 2^-25 of the largest)
+                pf[n][0] = movm_t(FP8 ? pack_f16(w0[0], w0[1]) : pack_bf16(w0[0], w0[1]));
+                pf[n][1] = movm_t(FP8 ? pack_f16(w1[0], w1[1]) : pack_bf16(w1[0], w1[1]));
+            }
+            if (!FP8) {
+#pragma unroll
+                for (int k = 0; k < KK; ++k) {
+                    uint32_t af[4];
+                    ldsm4t(af, chunk_addr<HB>(vb, r0 + ((lane >> 4) << 3) + (lane & 7), 2 * k + ((lane >> 3) & 1)));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16816<false>(o[n][k], af, pf[n][0], pf[n][1]);
+                }
+            } else {
+                // keys 2t, 2t+1, 2t+8, 2t+9 of the thread's D / 8 dims (D/8) g ..; a 16-dim
+                // tile takes two of them: rows g and g + 8 of tile k are dims (D/8) g + 2k, + 1
+                uint32_t x[4][D / 32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int row = r0 + 2 * t + (c & 1) + ((c >> 1) << 3);
+                    if (D == 128) {
+                        uint32_t y[4];
+                        lds128(y, chunk_addr<HB>(vb, row, g));
+#pragma unroll
+                        for (int e = 0; e < D / 32; ++e) x[c][e] = y[e];
+                    } else {
+                        uint32_t y[2];
+                        lds64(y, chunk_addr<HB>(vb, row, g >> 1) + ((g & 1) << 3));
+#pragma unroll
+                        for (int e = 0; e < D / 32; ++e) x[c][e] = y[e];
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < KK; ++k) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        h[c] = e4m3x2_to_f16x2((uint16_t)(k & 1 ? x[c][k >> 1] >> 16 : x[c][k >> 1]));
+                    const uint32_t af[4] = {__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[0], h[1], 0x7632),
+                                            __byte_perm(h[2], h[3], 0x5410), __byte_perm(h[2], h[3], 0x7632)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16816<true>(o[n][k], af, pf[n][0], pf[n][1]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(empty + st);
+        }
+
+        // ---- the four key slices meet
+        float2* mlg = ml + rg * 4 * 8 * NT;  // [4][8 NT]
+        float* sc = scratch + rg * (4 * 8 * D);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float x = l[n][c];
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                x += __shfl_xor_sync(0xffffffffu, x, 8);
+                x += __shfl_xor_sync(0xffffffffu, x, 16);
+                if (g == 0) mlg[ks * 8 * NT + n * 8 + 2 * t + c] = make_float2(m[n][c], x);
+            }
+        bar_sync(1 + rg, 128);
+        const int x = threadIdx.x & 127;
+        const int hr = x >> 4;  // row of the 8 that this thread sums
+        const bool cut = p.front || p.back;
+        const int64_t slot = (int64_t)blockIdx.x * 2 + (p.front ? 0 : 1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int col = n * 8 + 2 * t + c;
+                float mm = mlg[col].x;
+#pragma unroll
+                for (int y = 1; y < 4; ++y) mm = fmaxf(mm, mlg[y * 8 * NT + col].x);
+                const float f = (m[n][c] == -INFINITY ? 0.f : fast_exp2(m[n][c] - mm)) * (FP8 ? vref : 1.f);
+                // [key slice][8 rows][D], the dims of rows 2t and 2t + 1 turned by 8 t: no bank conflicts
+                float* dst = sc + (ks * 8 + 2 * t + c) * D;
+#pragma unroll
+                for (int k = 0; k < KK; ++k) {
+                    const int d0 = FP8 ? (D / 8) * g + 2 * k : 16 * k + g;
+                    const int d1 = FP8 ? d0 + 1 : d0 + 8;
+                    dst[d0 ^ (t << 3)] = o[n][k][c] * f;
+                    dst[d1 ^ (t << 3)] = o[n][k][2 + c] * f;
+                }
+            }
+            bar_sync(1 + rg, 128);
+            {
+                const int col = n * 8 + hr;
+                float mm = mlg[col].x;
+#pragma unroll
+                for (int y = 1; y < 4; ++y) mm = fmaxf(mm, mlg[y * 8 * NT + col].x);
+                float sum = 0.f;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float2 v = mlg[y * 8 * NT + col];
+                    sum += v.x == -INFINITY ? 0.f : v.y * fast_exp2(v.x - mm);
+                }
+                float v[D / 16];
+                const int d0 = (x & 15) * (D / 16);
+#pragma unroll
+                for (int e = 0; e < D / 16; e += 4) {
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const float4 z = *reinterpret_cast<const float4*>(
+                            sc + (y * 8 + hr) * D + ((d0 + e) ^ (((hr >> 1) & 3) << 3)));
+                        acc.x += z.x, acc.y += z.y, acc.z += z.z, acc.w += z.w;
+                    }
+                    v[e] = acc.x, v[e + 1] = acc.y, v[e + 2] = acc.z, v[e + 3] = acc.w;
+                }
+                const int r = (rg * NT + n) * 8 + hr;
+                const int f = p.row0 + r;
+                const int tok = f / a.group, head = f - tok * a.group;
+                bool write = tok < p.q.nq && ok;
+                if (write) {
+                    const int pos = __ldg(a.s.q_pos + p.q.q0 + tok);
+                    write = pos >= -1 && pos < p.q.ctx;
+                }
+                if (cut) {
+                    float* dst = a.part_o + (slot * C::kRows + r) * D + d0;
+#pragma unroll
+                    for (int e = 0; e < D / 16; e += 4)
+                        *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    // a sum of -1: a row that is not to be written
+                    if ((x & 15) == 0) a.part_ml[slot * C::kRows + r] = make_float2(mm, write ? sum : -1.f);
+                } else if (write) {
+                    const int64_t at = (int64_t)(p.q.q0 + tok) * (a.hkv * a.group) + kvh * a.group + head;
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * D + d0);
+                    if (D == 128)
+                        *reinterpret_cast<uint4*>(dst) =
+                            make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
+                                       pack_bf16(v[D / 16 - 4] * inv, v[D / 16 - 3] * inv),
+                                       pack_bf16(v[D / 16 - 2] * inv, v[D / 16 - 1] * inv));
+                    else
+                        *reinterpret_cast<uint2*>(dst) =
+                            make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
+                    if (a.lse && (x & 15) == 0) a.lse[at] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * kLn2;
+                }
+            }
+            bar_sync(1 + rg, 128);
+        }
+        // the first CTA behind a cut tells the joining kernel what to join
+        if (p.front) {
+            const int64_t c = blockIdx.x / a.hl;
+            const int64_t np = min((int64_t)a.parts, w.total);
+            const int64_t s0 = w.r0 - p.i0, s1 = s0 + tiles_of(p.q);
+            if (s0 >= w.total * (c - 1) / np)
+                join = make_int4((int)((s1 * np - 1) / w.total - c + 2), p.q.q0, p.q.nq, p.lane);
+        }
+    }
+    if (threadIdx.x == 0) a.desc[blockIdx.x] = join;
+}
+
+// Joins the partials of one cut (lane, sequence), a CTA per row: its four
+// warps take every fourth part.  Weights 2^(m_i - M), in the parts' order.
+constexpr int kJoinParts = 2 * kPlanSms + 8;  // parts of one sequence: at most the CTAs of a lane column
+
+template <int D>
+__global__ void __launch_bounds__(128) gqa_join_kernel(const __grid_constant__ Args a, int rows) {
+    __shared__ float weight[kJoinParts];
+    __shared__ float red[4][D];
+    __shared__ float sums[4], tops[4];
+    pdl_enter();
+    const int4 d = a.desc[blockIdx.x];
+    const int n = d.x;
+    if (n == 0) return;
+    const int r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int f = d.w / a.hkv * rows + r;
+    const int tok = f / a.group, head = f - tok * a.group;
+    if (tok >= d.z) return;
+    // part i: CTA blockIdx.x + (i - 1) hl; the first one's sequence is cut behind it, the others' before
+    auto slot = [&](int i) -> int64_t {
+        return ((int64_t)blockIdx.x + (int64_t)(i - 1) * a.hl) * 2 + (i == 0 ? 1 : 0);
+    };
+    float top = -INFINITY;
+    bool skip = false;
+    float2 v[(kJoinParts + 127) / 128];
+#pragma unroll
+    for (int k = 0; k < (kJoinParts + 127) / 128; ++k) {
+        const int i = k * 128 + threadIdx.x;
+        v[k] = i < n ? a.part_ml[slot(i) * rows + r] : make_float2(-INFINITY, 0.f);
+        skip = skip || v[k].y == -1.f;
+        top = fmaxf(top, v[k].x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) tops[warp] = top;
+    if (__syncthreads_or(skip)) return;
+    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < (kJoinParts + 127) / 128; ++k) {
+        const int i = k * 128 + threadIdx.x;
+        const float w = v[k].x == -INFINITY ? 0.f : fast_exp2(v[k].x - top);
+        if (i < n) weight[i] = w;
+        sum = fmaf(w, v[k].y, sum);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) sums[warp] = sum;
+    __syncthreads();
+    sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    constexpr int E = D / 32;
+    float acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 8
+    for (int i = warp; i < n; i += 4) {
+        const float* src = a.part_o + (slot(i) * rows + r) * D + lane * E;
+        const float w = weight[i];
+        if (E == 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+            acc[0] = fmaf(w, x.x, acc[0]);
+            acc[1] = fmaf(w, x.y, acc[1]);
+            acc[E - 2] = fmaf(w, x.z, acc[E - 2]);
+            acc[E - 1] = fmaf(w, x.w, acc[E - 1]);
+        } else {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+            acc[0] = fmaf(w, x.x, acc[0]);
+            acc[1] = fmaf(w, x.y, acc[1]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) red[warp][lane * E + e] = acc[e];
+    __syncthreads();
+    const int64_t at = (int64_t)(d.y + tok) * (a.hkv * a.group) + d.w % a.hkv * a.group + head;
+    if (threadIdx.x < D / 2) {
+        const int e = 2 * threadIdx.x;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float x0 = (red[0][e] + red[1][e]) + (red[2][e] + red[3][e]);
+        const float x1 = (red[0][e + 1] + red[1][e + 1]) + (red[2][e + 1] + red[3][e + 1]);
+        reinterpret_cast<uint32_t*>(a.out + at * D)[threadIdx.x] = pack_bf16(x0 * inv, x1 * inv);
+    }
+    if (a.lse && threadIdx.x == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------
+// host side
+struct Plan {
+    int nt, rg, rows, chunks, lanes, hl, parts, grid;
+    size_t o_bytes, ml_bytes, desc_bytes;
+};
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s) {
+    Plan p;
+    const int group = sh.num_heads / sh.num_kv_heads;
+    const int64_t rows = (int64_t)s.max_q_per_seq * group;
+    // 8, 16 or 32 query rows a chunk; more than 16 take a CTA of eight computing
+    // warps with an SM to itself (its accumulators need the registers)
+    p.nt = rows <= 8 ? 1 : 2;
+    p.rg = rows <= 16 ? 1 : 2;
+    p.rows = 8 * p.nt * p.rg;
+    p.chunks = (int)((rows + p.rows - 1) / p.rows);
+    p.lanes = sh.num_kv_heads * p.chunks;
+    // lanes side by side: a divisor of the lanes that leaves few CTAs idle, the
+    // largest such (its lanes' rows are neighbours in memory)
+    const int n = kPlanSms * (p.rg == 1 ? 2 : 1);
+    int best = 0;
+    p.hl = 1;
+    for (int d = 1; d <= p.lanes && d <= n; ++d)
+        if (p.lanes % d == 0) {
+            const int used = n / d * d;
+            if (used * 32 >= best * 31) p.hl = d;
+            best = std::max(best, used);
+        }
+    const int64_t tiles = std::max<int64_t>(1, ((int64_t)s.max_ctx + kTile - 1) / kTile);
+    p.parts = (int)std::min<int64_t>(n / p.hl, (int64_t)(p.lanes / p.hl) * s.num_seqs * tiles);
+    p.grid = p.parts * p.hl;
+    const size_t slots = (size_t)2 * p.grid;
+    p.o_bytes = up256(slots * p.rows * sh.head_dim * 4);
+    p.ml_bytes = up256(slots * p.rows * 8);
+    p.desc_bytes = up256((size_t)p.grid * 16);
+    return p;
+}
+
+template <int D, bool FP8, int NT, int RG>
+cudaError_t launch_one(const CUtensorMap& km, const CUtensorMap& vm, const Args& a, int grid, cudaStream_t stream) {
+    using C = Cfg<D, FP8, NT, RG>;
+    auto kern = gqa_decode_kernel<D, FP8, NT, RG>;
+    // per device: the attribute belongs to the current device's copy of the kernel
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(grid), dim3(C::kThreads), C::kSmem, stream, 1, km, vm, a);
+}
+
+}  // namespace
+
+size_t decode_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s) {
+    const Plan p = make_plan(sh, s);
+    return p.o_bytes + p.ml_bytes + p.desc_bytes;
+}
+
+cudaError_t launch_decode(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v, const float* k_scale,
+                          const float* v_scale, const dsa_seqs& s, int num_q, float sm_scale, void* out, float* lse,
+                          void* workspace, int32_t* d_status, cudaStream_t stream) {
+    const Plan p = make_plan(sh, s);
+    const bool fp8 = sh.kv_dtype == DSA_FP8_E4M3_ROWSCALE;
+    const int box = s.page_table ? std::min(s.page_size, kTile) : kTile;
+    CUtensorMap km, vm;
+    cudaError_t e = cache_map(&km, fp8, k, sh.num_kv_heads, sh.head_dim, sh.k_stride, s.num_rows, box, box == kTile);
+    if (e == cudaSuccess)
+        e = cache_map(&vm, fp8, v, sh.num_kv_heads, sh.head_dim, sh.v_stride, s.num_rows, box, box == kTile);
+    if (e != cudaSuccess) return e;
+    Args a;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.lse = lse;
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    a.part_o = reinterpret_cast<float*>(w);
+    a.part_ml = reinterpret_cast<float2*>(w + p.o_bytes);
+    a.desc = reinterpret_cast<int4*>(w + p.o_bytes + p.ml_bytes);
+    a.s = s;
+    a.q_stride = sh.q_stride;
+    a.d_status = d_status;
+    a.scale_log2 = sm_scale * 1.4426950408889634f;
+    a.num_q = num_q;
+    a.group = sh.num_heads / sh.num_kv_heads;
+    a.hkv = sh.num_kv_heads;
+    a.lanes = p.lanes;
+    a.hl = p.hl;
+    a.parts = p.parts;
+    auto by_rows = [&](auto d, auto f8) {
+        constexpr int D = decltype(d)::value;
+        constexpr bool F = decltype(f8)::value;
+        if (p.rg == 2) return launch_one<D, F, 2, 2>(km, vm, a, p.grid, stream);
+        return p.nt == 2 ? launch_one<D, F, 2, 1>(km, vm, a, p.grid, stream)
+                         : launch_one<D, F, 1, 1>(km, vm, a, p.grid, stream);
+    };
+    using std::integral_constant;
+    if (sh.head_dim == 64)
+        e = fp8 ? by_rows(integral_constant<int, 64>(), std::true_type())
+                : by_rows(integral_constant<int, 64>(), std::false_type());
+    else
+        e = fp8 ? by_rows(integral_constant<int, 128>(), std::true_type())
+                : by_rows(integral_constant<int, 128>(), std::false_type());
+    if (e != cudaSuccess || p.parts == 1) return e;
+    auto join = sh.head_dim == 64 ? gqa_join_kernel<64> : gqa_join_kernel<128>;
+    return launch_pdl(join, dim3(p.grid, p.rows), dim3(128), 0, stream, 1, a, p.rows);
+}
+
+}  // namespace gqa
+}  // namespace dsa

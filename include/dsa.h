@@ -11,6 +11,8 @@
  * the cache-write side (new indexer keys and latent rows into their caches,
  * the attention query's RoPE + SSMax) and one rank's compute steps of decode
  * context parallelism (top-k candidates, their merge, compaction, LSE combine).
+ * Beside it: dense attention with grouped heads for the layers without an
+ * indexer (K/V cache writes, decode, prompts).
  *
  * Sources (web pages, cited by title and section):
  *   [vLLM-ML4] "Day 0 support for Mistral Large 4" (vLLM blog), Implementation
@@ -45,7 +47,8 @@
  *     (1 indexer scan, 2 attention, 3 attention over fp8_ds_mla, 4 attention
  *     over NVFP4 latent rows, 5 indexer scan over NVFP4 keys) and bits
  *     16-30 the wait (its mbarrier's shared-memory offset / 8, or 0x7FFF for
- *     the attention's issue loop).
+ *     the attention's issue loop).  Kernel 6 is dense_gqa_decode, 7
+ *     dense_gqa_prefill.
  *   - Indices are logical token positions within a sequence.  The page table or
  *     seq_base maps them to physical cache rows.
  */
@@ -366,6 +369,99 @@ dsa_status dsa_dcp_shard_seqs(const dsa_seqs* seqs, int32_t num_q, const dsa_dcp
  * Weights and sums in fp32, out rounded to bf16 (nearest even). */
 dsa_status dsa_lse_combine(const void* const* o_parts, const float* const* lse_parts, int32_t num_parts,
                            int32_t num_q, void* out, float* lse, cudaStream_t stream);
+
+/* ---- dense attention with grouped heads: the layers beside the sparse ones ----
+ * Layers without an indexer (the full-attention layers that a hybrid stack
+ * keeps, dense draft models) attend over every causal key, with num_heads
+ * query heads in groups of G = num_heads / num_kv_heads on a key/value head:
+ *   query t of sequence b, head h, g = h / G, keys 0 <= j <= q_pos[t]:
+ *   s_j = sm_scale * q[t][h] . k_j[g],  p = softmax(s),
+ *   out[t][h] = sum_j p_j v_j[g],  lse[t][h] = ln sum_j exp(s_j).
+ * dsa_kv_insert writes new tokens' keys and values into the caches,
+ * dense_gqa_decode serves a few new tokens per sequence (one, or a draft to
+ * verify) and dense_gqa_prefill whole prompts; the last two take the same
+ * arguments and give the same results within rounding.  Sequences are dsa_seqs
+ * as above: paged, or contiguous from seq_base (freshly projected, packed
+ * prompts: seq_base[b] = q_start[b], ctx_len[b] = their length).  q_rope_pos
+ * is not read. */
+typedef enum {
+    DSA_ROPE_PAIRS = 0, /* pair i of the first rot_dims dims: (2i, 2i+1) */
+    DSA_ROPE_HALVES = 1 /* pair i: (i, i + rot_dims/2) */
+} dsa_rope_layout;
+
+typedef struct {
+    int32_t num_heads;    /* query heads, a multiple of num_kv_heads */
+    int32_t num_kv_heads; /* key/value heads >= 1, num_heads / num_kv_heads <= DSA_GQA_MAX_GROUP */
+    int32_t head_dim;     /* 64 or 128 */
+    dsa_dtype kv_dtype;   /* DSA_BF16: K and V [rows, num_kv_heads, head_dim] bf16;
+                             DSA_FP8_E4M3_ROWSCALE: e4m3 codes of that shape and fp32 scales
+                             [rows, num_kv_heads] each: value = scale * code */
+    int64_t q_stride;     /* elements between consecutive rows of q, of K and of V (a token's heads are */
+    int64_t k_stride;     /* contiguous); 0: heads * head_dim.  Whole multiples of 16 bytes, so that K and */
+    int64_t v_stride;     /* V may share one cache, and q, k, v one projection's output */
+} dsa_gqa_shape;
+#define DSA_GQA_MAX_GROUP 64
+
+/* K and V of n new tokens into their caches, rotated on the way, and the
+ * queries' rotation with them:
+ *   y = x with pair i < rot_dims/2 of every head rotated by pos * inv_freq[i]
+ *   (x0 cos - x1 sin, x0 sin + x1 cos), dims >= rot_dims as they are;
+ *   K row slot[i] = y(k[i]), V row slot[i] = v[i] (not rotated), as bf16 or as
+ *   e4m3 with one fp32 scale per row and head (storage rounding and scales as
+ *   the other cache writes);  q_out[i] = y(q[i]), bf16.
+ *   k, v  bf16 [n, num_kv_heads, head_dim], k_in / v_in elements between tokens
+ *   q     bf16 [n, num_heads, head_dim], q_in elements between tokens, or NULL:
+ *         no queries; q_out: rows shape->q_stride apart; may be q itself when
+ *         the strides are the same
+ *         (an input stride of 0: contiguous)
+ *   pos int32 [n]; slot int64 [n], no physical row twice; inv_freq fp32
+ *   [rot_dims/2] (rot_dims a multiple of 16 in [16, head_dim]), or NULL with
+ *   rot_dims 0: no rotation
+ *   k_cache, v_cache, k_scale, v_scale, num_rows: shape's caches
+ * slot < 0: the token's K and V are not stored (padding, or another rank's
+ * token); its query is rotated all the same unless pos < 0, which leaves its
+ * q_out row unwritten.  slot >= num_rows, or pos < 0 with slot >= 0:
+ * DSA_ERR_BAD_INPUT, the token skipped.  Alignment: k, v, q, q_out and the
+ * caches 16 bytes, their strides whole multiples of 16 bytes. */
+dsa_status dsa_kv_insert(const dsa_gqa_shape* shape, const void* k, int64_t k_in, const void* v, int64_t v_in,
+                         const void* q, int64_t q_in, const int32_t* pos, const int64_t* slot, int32_t n,
+                         const float* inv_freq, int32_t rot_dims, dsa_rope_layout layout, void* k_cache,
+                         void* v_cache, float* k_scale, float* v_scale, int64_t num_rows, void* q_out,
+                         int32_t* d_status, cudaStream_t stream);
+
+/* Bytes of workspace that dense_gqa_decode and dense_gqa_prefill need for
+ * these sizes (host only; one workspace sized for the largest call serves all
+ * calls that do not overlap). */
+dsa_status dense_gqa_workspace_size(const dsa_gqa_shape* shape, const dsa_seqs* seqs, int32_t num_q, size_t* bytes);
+
+/* Attention of a few new tokens per sequence over its cached keys (their own
+ * among them), the work split over the caches' length.
+ *   q    bf16 [num_q, num_heads, head_dim], rows shape->q_stride apart
+ *   k_cache, v_cache (and k_scale, v_scale for DSA_FP8_E4M3_ROWSCALE, else
+ *        NULL): shape's caches, seqs->num_rows rows
+ *   out  bf16 [num_q, num_heads, head_dim] contiguous; lse fp32
+ *        [num_q, num_heads] or NULL
+ * q_pos[t] = -1 sees no key: out = 0, lse = -inf.  Cache rows that no query of
+ * a call may see are not used, whatever they hold; a non-finite key or value
+ * that one query of a sequence sees can reach the sequence's other queries.
+ * DSA_ERR_BAD_INPUT in *d_status: a position outside [-1, ctx_len) (its row is
+ * left unwritten), a malformed sequence (its rows are left unwritten), a page
+ * or row outside the cache (not read; the outputs of the sequence's queries
+ * that see it are undefined).  Rows of out past q_start[num_seqs] are left as
+ * they were.  Alignment: q, k_cache, v_cache and out 16 bytes, workspace 256. */
+dsa_status dense_gqa_decode(const dsa_gqa_shape* shape, const void* q, const void* k_cache, const void* v_cache,
+                            const float* k_scale, const float* v_scale, const dsa_seqs* seqs, int32_t num_q,
+                            float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                            int32_t* d_status, cudaStream_t stream);
+
+/* The same attention for prompts: many new tokens per sequence (a whole
+ * prompt, or a chunk of one behind the tokens that the cache already holds),
+ * packed sequences of any lengths.  Arguments, results and errors as
+ * dense_gqa_decode. */
+dsa_status dense_gqa_prefill(const dsa_gqa_shape* shape, const void* q, const void* k_cache, const void* v_cache,
+                             const float* k_scale, const float* v_scale, const dsa_seqs* seqs, int32_t num_q,
+                             float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                             int32_t* d_status, cudaStream_t stream);
 
 /* One decode layer: dsa_index_scores -> dsa_topk -> sparse_mla_decode on one
  * stream, with the scores kept in the workspace.  reuse_idx != 0 is a
