@@ -1,0 +1,689 @@
+// gqa_prefill.cu -- dense causal attention of whole prompts with grouped heads
+// over packed or paged sequences (sm_103a, tcgen05).
+//
+//   s_j = sm_scale * q_h . k_j,  p = softmax over j <= pos,  out = sum_j p_j v_j
+//
+// A 128-row tile holds 128 / G tokens x the G query heads of one key head, so
+// that every key and value tile is read once for the whole group, and a
+// prompt of few tokens still fills its rows.  An item is two such tiles; both
+// run over the same keys (128 at a time), one's softmax under the other's
+// products:
+//   S = Q K^T (tcgen05, Q and K by TMA in shared memory, S in TMEM),
+//   one pass with a running reference m and sum l per row (a thread per row):
+//   p = 2^(x - m), the weights below 2^8 because O is rescaled only when a
+//   row's maximum passes m by more than 8,
+//   O += P V (P from TMEM as bf16, V in shared memory, O in TMEM).
+// Bound by the tensor cores: 4 D flop a visible (query, key) pair.
+//
+// Roles (12 warps, one CTA per SM, persistent): two warpgroups of softmax (one
+// per tile, each also writes its tile's output), and one warp each that issues
+// the products, loads, clears the rows behind the last key, and walks the
+// items.  Items go longest first, dealt to the CTAs in turn, back and forth.
+#include "gqa_common.cuh"
+
+namespace dsa {
+namespace gqa {
+namespace {
+
+constexpr int kTagPrefill = 7;
+constexpr int kKeys = 128;  // keys per tile
+constexpr int kThreads = 384;
+constexpr float kLazy = 8.f;  // a row's reference moves when its maximum passes it by 2^8
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kItemSlots = 2;
+constexpr int kItemReaders = 11;  // warps that read an item: softmax, issuer, loader, clearer
+
+template <int D>
+struct Cfg {
+    static constexpr int kHalves = D / 64;                   // 128-byte pieces of a head row
+    static constexpr int kQTile = 128 * D * 2;               // bytes
+    static constexpr int kStage = kKeys * D * 2;             // a K or a V tile
+    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr int kSmem = 2 * kQTile + kStages * kStage + 1024;
+    // TMEM columns: S of both tiles, then O; P takes the place of its tile's S
+    // (O leaves room beside it for d = 64)
+    static constexpr uint32_t kO = 256;
+    static constexpr uint32_t p_col(int x) { return D == 128 ? x * 128 : 384 + x * 64; }
+};
+
+struct Item {
+    int n;       // key tiles (0: no key is seen; -1: no more items)
+    int limit;   // keys that some query sees
+    int b, kvh;
+    int q0;      // first query row
+    int ntok;    // tokens from there to the sequence's end (may exceed the item)
+    int ctx;
+    int pad;
+    int64_t base;
+};
+
+struct Args {
+    __nv_bfloat16* out;
+    float* lse;
+    dsa_seqs s;
+    int32_t* d_status;
+    float scale_log2;  // > 0
+    int32_t neg;       // the scale's sign
+    int32_t num_q, group, hkv, tpt;  // tpt: tokens per tile
+};
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Walks the items of this CTA, longest first: item y of the order is the one
+// with the y-th largest level, level = item index within the sequence plus the
+// items' worth of tokens before its first query.  Whole warp.
+struct Schedule {
+    static constexpr int kKept = 4;  // sequences per lane held in registers
+    int n[kKept], p[kKept];
+    int64_t total;
+    int top;
+    __device__ __forceinline__ void get(const Args& a, int b, int& nn, int& pp, bool report_errors) const {
+        nn = pp = 0;
+        if (b >= a.s.num_seqs) return;
+        const Seq q = load_seq(a.s, b, a.num_q);
+        if (!q.ok) {
+            if (report_errors) report(a.d_status, DSA_ERR_BAD_INPUT);
+            return;
+        }
+        const int per = 2 * a.tpt;
+        nn = (q.nq + per - 1) / per;
+        pp = nn ? max(q.ctx - q.nq, 0) / per : 0;
+    }
+    __device__ __forceinline__ void pair(const Args& a, int g, int& nn, int& pp) const {
+        if (g >= kKept) {
+            get(a, g * 32 + (threadIdx.x & 31), nn, pp, false);
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < kKept; ++k)
+            if (g == k) nn = n[k], pp = p[k];
+    }
+    // items at this level or above
+    __device__ __forceinline__ int64_t above(const Args& a, int level) const {
+        int64_t c = 0;
+        for (int g = 0; g * 32 < a.s.num_seqs; ++g) {
+            int nn = 0, pp = 0;
+            pair(a, g, nn, pp);
+            c += __reduce_add_sync(0xffffffffu, (unsigned)min(max(nn + pp - level, 0), nn));
+        }
+        return c;
+    }
+    __device__ __forceinline__ void init(const Args& a) {
+        const int lane = threadIdx.x & 31;
+        int t = 0;
+        for (int g = 0; g * 32 < a.s.num_seqs; ++g) {
+            int nn, pp;
+            get(a, g * 32 + lane, nn, pp, blockIdx.x == 0);
+#pragma unroll
+            for (int k = 0; k < kKept; ++k)
+                if (g == k) n[k] = nn, p[k] = pp;
+            t = max(t, nn + pp);
+        }
+#pragma unroll
+        for (int k = 0; k < kKept; ++k)
+            if (k * 32 >= a.s.num_seqs) n[k] = p[k] = 0;
+        top = __reduce_max_sync(0xffffffffu, t);
+        total = above(a, 0) * a.hkv;
+    }
+    // item f of the order (f < total)
+    __device__ __forceinline__ Item find(const Args& a, int64_t f) const {
+        const int lane = threadIdx.x & 31;
+        const int64_t y = f / a.hkv;
+        int lo = 0, hi = top - 1;  // the largest level with above(level) > y
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (above(a, mid) > y) lo = mid; else hi = mid - 1;
+        }
+        int64_t z = y - above(a, lo + 1);  // place among the level's items
+        Item it;
+        it.kvh = (int)(f - y * a.hkv);
+        it.b = 0;
+        int tile = 0;
+        for (int g = 0; g * 32 < a.s.num_seqs; ++g) {
+            int nn = 0, pp = 0;
+            pair(a, g, nn, pp);
+            const bool in = pp <= lo && lo < pp + nn;
+            const uint32_t m = __ballot_sync(0xffffffffu, in);
+            if (z < __popc(m)) {
+                const int l = __fns(m, 0, (int)z + 1);
+                it.b = g * 32 + l;
+                tile = lo - __shfl_sync(0xffffffffu, pp, l);
+                break;
+            }
+            z -= __popc(m);
+        }
+        const Seq q = load_seq(a.s, it.b, a.num_q);
+        const int tok = tile * 2 * a.tpt;
+        it.q0 = q.q0 + tok;
+        it.ntok = q.nq - tok;
+        it.ctx = q.ctx;
+        it.base = a.s.page_table ? 0 : __ldg(a.s.seq_base + it.b);
+        int pos = -1;
+        for (int i = lane; i < min(2 * a.tpt, it.ntok); i += 32) {
+            const int x = __ldg(a.s.q_pos + it.q0 + i);
+            if (x < q.ctx) pos = max(pos, x);
+        }
+        it.limit = max(0, __reduce_max_sync(0xffffffffu, pos) + 1);
+        it.n = (it.limit + kKeys - 1) / kKeys;
+        it.pad = 0;
+        return it;
+    }
+};
+
+struct Shared {
+    Item item[kItemSlots];
+    uint64_t item_full[kItemSlots], item_empty[kItemSlots];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t kv_full[10], kv_empty[10], tail_full[10];
+    uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2];
+    uint64_t drain;
+    int abort_flag[2];
+    uint32_t tmem;
+};
+static_assert(sizeof(Shared) <= 1024, "the barriers' page");
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    gqa_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a) {
+    using C = Cfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* qs = smem;
+    uint8_t* ring = smem + 2 * C::kQTile;
+    Shared& sh = *reinterpret_cast<Shared*>(smem + 2 * C::kQTile + C::kStages * C::kStage);
+    volatile int* abort_flag = sh.abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (warp == 8) {
+        ptx::tmem_alloc(&sh.tmem, 512);
+        ptx::tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kItemSlots; ++i) {
+            ptx::mbar_init(sh.item_full + i, 1);
+            ptx::mbar_init(sh.item_empty + i, kItemReaders);
+        }
+        for (int i = 0; i < C::kStages; ++i) {
+            ptx::mbar_init(sh.kv_full + i, 1);
+            ptx::mbar_init(sh.kv_empty + i, 1);
+            ptx::mbar_init(sh.tail_full + i, 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            ptx::mbar_init(sh.q_full + x, 1);
+            ptx::mbar_init(sh.q_empty + x, 1);
+            ptx::mbar_init(sh.s_full + x, 1);
+            ptx::mbar_init(&sh.p_full[x][0], 128);
+            ptx::mbar_init(&sh.p_full[x][1], 128);
+            ptx::mbar_init(sh.o_full + x, 1);
+            ptx::mbar_init(sh.o_empty + x, 128);
+        }
+        ptx::mbar_init(&sh.drain, 1);
+        abort_flag[0] = 0;
+        abort_flag[1] = kTagPrefill;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&qmap);
+        ptx::prefetch_tmap(&kmap);
+        ptx::prefetch_tmap(&vmap);
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
+    pdl_enter();
+
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_wait(bar, parity & 1, abort_flag, a.d_status); };
+    // the next item, read by a whole warp; false at the end or after an abort
+    int item_no = 0;
+    auto next_item = [&](Item& it) -> bool {
+        const int sl = item_no % kItemSlots;
+        const bool ok = wait(sh.item_full + sl, item_no / kItemSlots);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        it = sh.item[sl];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(sh.item_empty + sl);
+        ++item_no;
+        return it.n >= 0;
+    };
+
+    if (warp >= 8) {
+        reg_dec<88>();
+        if (warp == 11) {
+            // ------------------------------------------------------------ walks the items
+            Schedule sc;
+            sc.init(a);
+            bool ok = true;
+            int64_t k = 0;
+            for (;; ++k) {
+                const int64_t f = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                Item it;
+                it.n = -1;
+                if (f < sc.total) it = sc.find(a, f);
+                const int sl = (int)(k % kItemSlots);
+                if (k >= kItemSlots) {
+                    ok = wait(sh.item_empty + sl, (uint32_t)(k / kItemSlots) - 1);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                }
+                if (lane == 0) {
+                    sh.item[sl] = it;
+                    ptx::mbar_arrive(sh.item_full + sl);
+                }
+                __syncwarp();
+                if (it.n < 0) break;  // every later round's item lies past the end too
+            }
+        } else if (warp == 10) {
+            // ------------------------------------------------------------ clears V's rows behind the last key
+            // whatever lies there must not reach the products: its weights are 0, but 0 * inf is not
+            Item it;
+            uint32_t phases = 0;
+            int64_t c = 0;  // ring position
+            while (next_item(it)) {
+                if (it.n > 0 && it.limit % kKeys) {
+                    const int st = (int)((c + 2 * it.n - 1) % C::kStages);
+                    const bool ok = wait(sh.tail_full + st, (phases >> st) & 1);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    phases ^= 1u << st;
+                    const int r0 = it.limit % kKeys;
+                    for (int h = 0; h < C::kHalves; ++h) {
+                        uint4* dst = reinterpret_cast<uint4*>(ring + st * C::kStage + h * (kKeys * 128));
+                        for (int i = r0 * 8 + lane; i < kKeys * 8; i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(sh.kv_full + st);
+                }
+                c += 2 * it.n;
+            }
+        } else if (warp == 9) {
+            // ------------------------------------------------------------ loads
+            const int R = a.s.page_table ? min(a.s.page_size, kKeys) : kKeys;  // rows per box
+            const int nbox = kKeys / R;
+            const int shift = 31 - __clz(R);
+            Item it;
+            int64_t c = 0;
+            int uses[2] = {0, 0};  // Q loads per tile
+            bool ok = true;
+            uint32_t tails = 0;    // stages whose last load goes to tail_full
+            uint32_t tail_phase = 0;
+            while (ok && next_item(it)) {
+                if (it.n == 0) continue;
+                const int tiles_q = it.ntok > a.tpt ? 2 : 1;
+                auto row_of = [&](int box) -> int {
+                    const int64_t j = (int64_t)box << shift;
+                    if (j >= it.limit) return -1;
+                    int64_t row;
+                    if (a.s.page_table) {
+                        row = phys_row(a.s, it.b, j);
+                        if (row >= 0 && row + R > a.s.num_rows) row = -1;
+                    } else {
+                        row = it.base + j;
+                        if (row < 0 || it.base + min(j + R, (int64_t)it.limit) > a.s.num_rows) row = -1;
+                    }
+                    if (row < 0) report(a.d_status, DSA_ERR_BAD_INPUT);
+                    return (int)row;
+                };
+                int w0 = 0;
+                int cur = row_of(lane), nxt = row_of(32 + lane);
+                auto load = [&](const CUtensorMap* map, int i, bool tail) -> bool {
+                    const int st = (int)(c % C::kStages);
+                    if (c >= C::kStages) {
+                        const bool free = wait(sh.kv_empty + st, (uint32_t)(c / C::kStages) - 1);
+                        if (!__all_sync(0xffffffffu, free)) return false;
+                    }
+                    ++c;
+                    uint64_t* bar = tail ? sh.tail_full + st : sh.kv_full + st;
+                    if (tail) tails |= 1u << st, tail_phase ^= 1u << st;
+                    else tails &= ~(1u << st);
+                    const int l = i * nbox - w0;
+                    const uint32_t have = __ballot_sync(0xffffffffu, cur >= 0 && lane >= l && lane < l + nbox);
+                    if (lane == 0) ptx::mbar_expect_tx(bar, (uint32_t)__popc(have) * R * D * 2);
+                    __syncwarp();
+                    if ((have >> lane) & 1) {
+                        uint8_t* dst = ring + st * C::kStage + (lane - l) * R * 128;
+                        if (C::kHalves == 1 || nbox == 1)
+                            tma_load_4d(dst, map, 0, cur, 0, it.kvh, bar);
+                        else
+                            for (int h = 0; h < C::kHalves; ++h)
+                                tma_load_4d(dst + h * (kKeys * 128), map, 0, cur, h, it.kvh, bar);
+                    }
+                    return true;
+                };
+                for (int i = 0; ok && i < it.n; ++i) {
+                    if (i * nbox >= w0 + 32) {
+                        w0 += 32;
+                        cur = nxt;
+                        nxt = row_of(w0 + 32 + lane);
+                    }
+                    ok = load(&kmap, i, false);
+                    if (ok && i == 0) {
+                        for (int x = 0; ok && x < tiles_q; ++x) {
+                            if (uses[x] > 0) ok = __all_sync(0xffffffffu, wait(sh.q_empty + x, uses[x] - 1));
+                            if (!ok) break;
+                            if (lane == 0) {
+                                const int rows = a.group * a.tpt;
+                                ptx::mbar_expect_tx(sh.q_full + x, (uint32_t)rows * D * 2);
+                                for (int h = 0; h < C::kHalves; ++h)
+                                    tma_load_4d(qs + x * C::kQTile + h * (128 * 128), &qmap, 0, it.kvh * a.group,
+                                                it.q0 + x * a.tpt, h, sh.q_full + x);
+                            }
+                            __syncwarp();
+                            ++uses[x];
+                        }
+                    }
+                    if (ok) ok = load(&vmap, i, i + 1 == it.n && it.limit % kKeys);
+                }
+            }
+            if (abort_flag[0] && lane == 0) {
+                // after an abort: let the copies in flight land before the CTA ends
+                for (int64_t k = c > C::kStages ? c - C::kStages : 0; k < c; ++k) {
+                    const int st = (int)(k % C::kStages);
+                    if ((tails >> st) & 1) ptx::mbar_drain(sh.tail_full + st, ((tail_phase >> st) & 1) ^ 1);
+                    else ptx::mbar_drain(sh.kv_full + st, (uint32_t)(k / C::kStages) & 1);
+                }
+                for (int x = 0; x < 2; ++x)
+                    if (uses[x]) ptx::mbar_drain(sh.q_full + x, (uses[x] - 1) & 1);
+            }
+        } else {
+            // ------------------------------------------------------------ issues the products
+            constexpr uint32_t idesc_s = ptx::idesc_f16(128, kKeys, true);
+            constexpr uint32_t idesc_o = ptx::idesc_f16(128, D, true, false, true);
+            const uint32_t qb = smem_u32(qs), rb = smem_u32(ring);
+            Item it;
+            int64_t c = 0;
+            uint32_t q_use[2] = {0, 0}, p_use[2] = {0, 0}, o_use[2] = {0, 0};
+            bool ok = true;
+            while (ok && next_item(it)) {
+                if (it.n == 0) continue;
+                const int nx = it.ntok > a.tpt ? 2 : 1;
+                if (lane == 0) {
+                    auto kv_wait = [&](int64_t at) { return wait(sh.kv_full + at % C::kStages, (uint32_t)(at / C::kStages)); };
+                    auto scores = [&](int x, int64_t at) {
+                        const uint32_t kb = rb + (uint32_t)(at % C::kStages) * C::kStage;
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
+                            ptx::mma_ss(tmem + x * 128, ptx::sdesc_sw128(qb + x * C::kQTile + off),
+                                        ptx::sdesc_sw128(kb + off), idesc_s, k > 0 ? 1u : 0u);
+                        }
+                        ptx::mma_commit(sh.s_full + x);
+                    };
+                    ok = kv_wait(c);
+                    for (int x = 0; ok && x < nx; ++x) {
+                        ok = wait(sh.q_full + x, q_use[x]);
+                        if (!ok) break;
+                        ++q_use[x];
+                        ptx::tc_fence_after();
+                        scores(x, c);
+                    }
+                    if (ok) ptx::mma_commit(sh.kv_empty + c % C::kStages);
+                    for (int i = 0; ok && i < it.n; ++i) {
+                        const int64_t vc = c + 2 * i + 1, kc = vc + 1;
+                        const bool more = i + 1 < it.n;
+                        ok = kv_wait(vc) && (!more || kv_wait(kc));
+                        const uint32_t vb = rb + (uint32_t)(vc % C::kStages) * C::kStage;
+                        for (int x = 0; ok && x < nx; ++x) {
+                            if (i == 0) {
+                                if (o_use[x] > 0) ok = wait(sh.o_empty + x, o_use[x] - 1);
+                                ++o_use[x];
+                            }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                ok = ok && wait(&sh.p_full[x][h], p_use[x]);
+                                if (!ok) break;
+                                ptx::tc_fence_after();
+#pragma unroll
+                                for (int k = 4 * h; k < 4 * h + 4; ++k)
+                                    ptx::mma_ts(tmem + C::kO + x * D, tmem + C::p_col(x) + k * 8,
+                                                ptx::sdesc_sw128_mn(vb + k * 2048, kKeys * 128, 1024), idesc_o,
+                                                i > 0 || k > 0 ? 1u : 0u);
+                            }
+                            if (!ok) break;
+                            ++p_use[x];
+                            if (x + 1 == nx) ptx::mma_commit(sh.kv_empty + vc % C::kStages);
+                            if (more) scores(x, kc);
+                            else ptx::mma_commit(sh.o_full + x);
+                            if (i + 2 == it.n || it.n == 1) ptx::mma_commit(sh.q_empty + x);
+                        }
+                        if (ok && more) ptx::mma_commit(sh.kv_empty + kc % C::kStages);
+                    }
+                    c += 2 * it.n;
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+            }
+            if (lane == 0 && abort_flag[0]) {
+                ptx::mma_commit(&sh.drain);
+                ptx::mbar_drain(&sh.drain, 0);
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax: a row per thread
+        reg_inc<208>();
+        const int x = warp >> 2;
+        const int r = threadIdx.x & 127;
+        const int tok = r / a.group, head = r - tok * a.group;
+        const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, lane in bits 16..
+        const uint32_t ts = tmem + lane_base + x * 128;
+        const uint32_t tp = tmem + lane_base + C::p_col(x);
+        const uint32_t to = tmem + lane_base + C::kO + x * D;
+        Item it;
+        uint32_t s_use = 0, o_use = 0;
+        bool ok = true;
+        while (ok && next_item(it)) {
+            if (x == 1 && it.ntok <= a.tpt) continue;
+            const int t = x * a.tpt + tok;  // token within the item
+            bool live = tok < a.tpt && t < it.ntok;
+            int pos = 0x7FFFFFFF;  // unused rows: no mask, no output
+            if (live) {
+                pos = __ldg(a.s.q_pos + it.q0 + t);
+                if (pos < -1 || pos >= it.ctx) {
+                    report(a.d_status, DSA_ERR_BAD_INPUT);
+                    live = false;
+                    pos = -1;
+                }
+            }
+            float m = -INFINITY;
+            uint64_t l2a = 0ull, l2b = 0ull;  // two pairs of fp32 sums
+            for (int i = 0; i < it.n; ++i) {
+                ok = __all_sync(0xffffffffu, wait(sh.s_full + x, s_use));
+                if (!ok) break;
+                ++s_use;
+                ptx::tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) ptx::tmem_ld32_async(ts + 32 * k, s[k]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) ptx::tmem_wait_ld32(s[k]);
+                if (a.neg) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[k][e] ^= 0x80000000u;
+                }
+                const int lim = pos - i * kKeys;  // the tile's last key that the row sees
+                if (__any_sync(0xffffffffu, lim < kKeys - 1)) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * k + e > lim) s[k][e] = 0xFF800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    mx[k] = __uint_as_float(s[k][0]);
+#pragma unroll
+                    for (int e = 1; e < 32; ++e) mx[k] = fmaxf(mx[k], __uint_as_float(s[k][e]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                const bool move = top > m + kLazy;
+                if (__any_sync(0xffffffffu, move)) {
+                    const float mn = move ? top : m;
+                    const float al = move ? fast_exp2(m - mn) : 1.f;
+                    m = mn;
+                    const uint64_t al2 = pack2(al, al);
+                    l2a = fma2(l2a, al2, 0ull);
+                    l2b = fma2(l2b, al2, 0ull);
+                    if (i > 0) {
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) {
+                            float o[32];
+                            ptx::tmem_ld32(to + 32 * k, o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= al;
+                            ptx::tmem_st32(to + 32 * k, o);
+                        }
+                    }
+                }
+                const float mm = m == -INFINITY ? 0.f : -m;
+                const uint64_t sc2 = pack2(a.scale_log2, a.scale_log2), nm2 = pack2(mm, mm);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const uint64_t v = fma2(pack2(__uint_as_float(s[2 * h + k][e]), __uint_as_float(s[2 * h + k][e + 1])),
+                                                    sc2, nm2);
+                            float p0, p1;
+                            unpack2(v, p0, p1);
+                            p0 = fast_exp2(p0);
+                            p1 = fast_exp2(p1);
+                            if (k == 0) l2a = add2(l2a, pack2(p0, p1));
+                            else l2b = add2(l2b, pack2(p0, p1));
+                            // a weight rounded to bf16 is off by up to 2^-9 of itself; the sum keeps fp32
+                            pk[16 * k + e / 2] = pack_bf16(p0, p1);
+                        }
+                    ptx::tmem_st32_nowait(tp + 32 * h, pk);
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(&sh.p_full[x][h]);
+                }
+            }
+            if (!ok) break;
+            float la, lb, lc, ld;
+            unpack2(l2a, la, lb);
+            unpack2(l2b, lc, ld);
+            const float l = (la + lb) + (lc + ld);
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const int64_t at = (int64_t)(it.q0 + t) * (a.hkv * a.group) + it.kvh * a.group + head;
+            if (it.n > 0) {
+                ok = __all_sync(0xffffffffu, wait(sh.o_full + x, o_use));
+                if (!ok) break;
+                ++o_use;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    float o[32];
+                    ptx::tmem_ld32(to + 32 * k, o);
+                    if (live) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + 32 * k);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float v[8];
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) v[y] = l == 0.f ? 0.f : o[8 * e + y] * inv;
+                            dst[e] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                                pack_bf16(v[6], v[7]));
+                        }
+                    }
+                }
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(sh.o_empty + x);
+            } else if (live) {
+                uint4* dst = reinterpret_cast<uint4*>(a.out + at * D);
+#pragma unroll
+                for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (live && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side: Q [num_q, heads, d] with rows `stride` elements apart, a box of
+// `tokens` x `group` heads x 64 dims
+cudaError_t query_map(CUtensorMap* m, const void* q, int heads, int d, int64_t stride, int num_q, int group, int tokens) {
+    auto enc = tmap_encoder();
+    if (!enc) return cudaErrorNotSupported;
+    cuuint64_t dims[4] = {64, (cuuint64_t)heads, (cuuint64_t)num_q, (cuuint64_t)d / 64};
+    cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2, 128};
+    cuuint32_t box[4] = {64, (cuuint32_t)group, (cuuint32_t)tokens, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D>
+cudaError_t launch_one(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const Args& a, int grid,
+                       cudaStream_t stream) {
+    auto kern = gqa_prefill_kernel<D>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, stream, 1, qm, km, vm, a);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v, const dsa_seqs& s,
+                           int num_q, float sm_scale, void* out, float* lse, int32_t* d_status, cudaStream_t stream) {
+    Args a;
+    a.group = sh.num_heads / sh.num_kv_heads;
+    a.hkv = sh.num_kv_heads;
+    a.tpt = 128 / a.group;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.lse = lse;
+    a.s = s;
+    a.d_status = d_status;
+    a.num_q = num_q;
+    a.neg = sm_scale < 0.f;
+    // a scale of 0 stays a tiny positive one: masked scores are -inf before the scaling
+    a.scale_log2 = std::max(std::fabs(sm_scale) * 1.4426950408889634f, 1e-30f);
+    const int box = s.page_table ? std::min(s.page_size, kKeys) : kKeys;
+    CUtensorMap qm, km, vm;
+    cudaError_t e = query_map(&qm, q, sh.num_heads, sh.head_dim, sh.q_stride, num_q, a.group, a.tpt);
+    if (e == cudaSuccess)
+        e = cache_map(&km, false, k, sh.num_kv_heads, sh.head_dim, sh.k_stride, s.num_rows, box, box == kKeys);
+    if (e == cudaSuccess)
+        e = cache_map(&vm, false, v, sh.num_kv_heads, sh.head_dim, sh.v_stride, s.num_rows, box, box == kKeys);
+    if (e != cudaSuccess) return e;
+    const int64_t items = ((int64_t)num_q / (2 * a.tpt) + s.num_seqs) * a.hkv;  // at most
+    const int grid = (int)std::min<int64_t>(num_sms(), items);
+    return sh.head_dim == 64 ? launch_one<64>(qm, km, vm, a, grid, stream)
+                             : launch_one<128>(qm, km, vm, a, grid, stream);
+}
+
+}  // namespace gqa
+}  // namespace dsa
