@@ -476,7 +476,8 @@ static dsa_status dense_gqa(bool prefill, const dsa_gqa_shape* shape, const void
     }
     dsa_status st = c.done();
     if (st != DSA_OK || num_q == 0) return st;
-    if (prefill && sh.kv_dtype == DSA_BF16)
+    // a negative scale turns the row maxima around: the split kernel scales first
+    if (prefill && sh.kv_dtype == DSA_BF16 && sm_scale >= 0.f)
         return cuda_status(gqa::launch_prefill(sh, q, k_cache, v_cache, *seqs, num_q, sm_scale, out, lse, d_status,
                                                stream),
                            "dense_gqa_prefill launch");

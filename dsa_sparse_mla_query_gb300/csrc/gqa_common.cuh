@@ -47,6 +47,16 @@ inline cudaError_t cache_map(CUtensorMap* m, bool bytes, const void* base, int h
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// mbar_wait for waits that are short as a rule: several hardware-timed probes
+// before the first read of the timer, which takes longer than a probe.
+__device__ __forceinline__ bool quick_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                           int32_t* d_status) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+    return ptx::mbar_wait(bar, parity, abort_flag, d_status);
+}
+
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
                                             uint64_t* bar) {
     asm volatile(

@@ -6,19 +6,24 @@
 // A 128-row tile holds 128 / G tokens x the G query heads of one key head, so
 // that every key and value tile is read once for the whole group, and a
 // prompt of few tokens still fills its rows.  An item is two such tiles; both
-// run over the same keys (128 at a time), one's softmax under the other's
-// products:
+// run over the same keys, 64 at a time:
 //   S = Q K^T (tcgen05, Q and K by TMA in shared memory, S in TMEM),
 //   one pass with a running reference m and sum l per row (a thread per row):
 //   p = 2^(x - m), the weights below 2^8 because O is rescaled only when a
 //   row's maximum passes m by more than 8,
 //   O += P V (P from TMEM as bf16, V in shared memory, O in TMEM).
-// Bound by the tensor cores: 4 D flop a visible (query, key) pair.
+// Bound by the tensor cores: 4 D flop a visible (query, key) pair.  A thread's
+// softmax of a step is a chain far longer than the step's products (TMEM load,
+// maximum, exponentials, TMEM store and two hand-overs), so each tile has two
+// buffers of S: the scores of step j + 1 are made while step j's weights are
+// computed, and the products wait for neither.  (Steps of 128 keys with one
+// buffer: the two tiles' chains alone left the tensor cores idle half the
+// time, 1,083 TFLOP/s on 16,384 tokens, 64/8 heads of 128.)
 //
-// Roles (12 warps, one CTA per SM, persistent): two warpgroups of softmax (one
-// per tile, each also writes its tile's output), and one warp each that issues
-// the products, loads, clears the rows behind the last key, and walks the
-// items.  Items go longest first, dealt to the CTAs in turn, back and forth.
+// Roles (one CTA per SM, persistent): two warpgroups of softmax (one per tile,
+// each also writes its tile's output), two warps that issue the products (one
+// per tile), and one warp each that loads, clears the rows behind the last
+// key, and walks the items.  Items go longest first, dealt to the CTAs in turn, back and forth.
 #include "gqa_common.cuh"
 
 namespace dsa {
@@ -26,12 +31,14 @@ namespace gqa {
 namespace {
 
 constexpr int kTagPrefill = 7;
-constexpr int kKeys = 128;  // keys per tile
-constexpr int kThreads = 384;
+constexpr int kKeys = 128;  // keys per stage of the ring
+constexpr int kStep = 64;   // keys per step of the products
+constexpr int kThreads = 512;
+constexpr int kIssueWarp = 8, kLoadWarp = 10, kClearWarp = 11, kWalkWarp = 12;  // then idle ones
 constexpr float kLazy = 8.f;  // a row's reference moves when its maximum passes it by 2^8
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kItemSlots = 2;
-constexpr int kItemReaders = 11;  // warps that read an item: softmax, issuer, loader, clearer
+constexpr int kItemReaders = 12;  // warps that read an item: softmax, issuers, loader, clearer
 
 template <int D>
 struct Cfg {
@@ -40,20 +47,19 @@ struct Cfg {
     static constexpr int kStage = kKeys * D * 2;             // a K or a V tile
     static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr int kSmem = 2 * kQTile + kStages * kStage + 1024;
-    // TMEM columns: S of both tiles, then O; P takes the place of its tile's S
-    // (O leaves room beside it for d = 64)
+    // TMEM columns: two buffers of S per tile, then O; P takes the place of its S
     static constexpr uint32_t kO = 256;
-    static constexpr uint32_t p_col(int x) { return D == 128 ? x * 128 : 384 + x * 64; }
+    static constexpr uint32_t s_col(int x, int buf) { return x * 128 + buf * kStep; }
 };
 
 struct Item {
-    int n;       // key tiles (0: no key is seen; -1: no more items)
+    int n;       // stages of keys (0: no key is seen; -1: no more items)
     int limit;   // keys that some query sees
+    int steps[2];// steps of either tile (0: the tile sees no key, or has no query)
     int b, kvh;
     int q0;      // first query row
     int ntok;    // tokens from there to the sequence's end (may exceed the item)
     int ctx;
-    int pad;
     int64_t base;
 };
 
@@ -63,7 +69,6 @@ struct Args {
     dsa_seqs s;
     int32_t* d_status;
     float scale_log2;  // > 0
-    int32_t neg;       // the scale's sign
     int32_t num_q, group, hkv, tpt;  // tpt: tokens per tile
 };
 
@@ -85,6 +90,21 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+// Shared-memory matrix descriptors as a low word, which holds the address and
+// the leading stride, and the high word they share (8-row groups 1024 bytes
+// apart, 128-byte swizzle)
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) {
+    return ((addr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t make_desc(uint32_t lo) {
+    constexpr uint64_t hi = (uint64_t)(1024 >> 4) | ((uint64_t)1 << 14) | ((uint64_t)2 << 29);
+    return (hi << 32) | lo;
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
+}
 template <int N>
 __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -93,6 +113,22 @@ template <int N>
 __device__ __forceinline__ void reg_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
+
+// A place in the ring of N stages: the stage and the parity of its use.  (A
+// 64-bit remainder for every stage held the issuing thread for longer than a
+// step's products take.)
+template <int N>
+struct Cursor {
+    int st = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void move(int by) {
+        st += by;
+        if (st >= N) {
+            st -= N;
+            ph ^= 1u;
+        }
+    }
+};
 
 // Walks the items of this CTA, longest first: item y of the order is the one
 // with the y-th largest level, level = item index within the sequence plus the
@@ -183,14 +219,22 @@ struct Schedule {
         it.ntok = q.nq - tok;
         it.ctx = q.ctx;
         it.base = a.s.page_table ? 0 : __ldg(a.s.seq_base + it.b);
-        int pos = -1;
+        int pos[2] = {-1, -1};
         for (int i = lane; i < min(2 * a.tpt, it.ntok); i += 32) {
             const int x = __ldg(a.s.q_pos + it.q0 + i);
-            if (x < q.ctx) pos = max(pos, x);
+            if (x < q.ctx) {
+                if (i < a.tpt) pos[0] = max(pos[0], x);
+                else pos[1] = max(pos[1], x);
+            }
         }
-        it.limit = max(0, __reduce_max_sync(0xffffffffu, pos) + 1);
+        it.limit = 0;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int lim = max(0, __reduce_max_sync(0xffffffffu, pos[x]) + 1);
+            it.steps[x] = (lim + kStep - 1) / kStep;
+            it.limit = max(it.limit, lim);
+        }
         it.n = (it.limit + kKeys - 1) / kKeys;
-        it.pad = 0;
         return it;
     }
 };
@@ -200,8 +244,8 @@ struct Shared {
     uint64_t item_full[kItemSlots], item_empty[kItemSlots];
     uint64_t q_full[2], q_empty[2];
     uint64_t kv_full[10], kv_empty[10], tail_full[10];
-    uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2];
-    uint64_t drain;
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_full[2], o_empty[2];
+    uint64_t drain[2];
     int abort_flag[2];
     uint32_t tmem;
 };
@@ -230,19 +274,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < C::kStages; ++i) {
             ptx::mbar_init(sh.kv_full + i, 1);
-            ptx::mbar_init(sh.kv_empty + i, 1);
+            ptx::mbar_init(sh.kv_empty + i, 2);
             ptx::mbar_init(sh.tail_full + i, 1);
         }
         for (int x = 0; x < 2; ++x) {
             ptx::mbar_init(sh.q_full + x, 1);
             ptx::mbar_init(sh.q_empty + x, 1);
-            ptx::mbar_init(sh.s_full + x, 1);
-            ptx::mbar_init(&sh.p_full[x][0], 128);
-            ptx::mbar_init(&sh.p_full[x][1], 128);
+            for (int b = 0; b < 2; ++b) {
+                ptx::mbar_init(&sh.s_full[x][b], 1);
+                ptx::mbar_init(&sh.p_full[x][b], 4);
+            }
+            ptx::mbar_init(sh.pv_done + x, 1);
             ptx::mbar_init(sh.o_full + x, 1);
-            ptx::mbar_init(sh.o_empty + x, 128);
+            ptx::mbar_init(sh.o_empty + x, 4);
         }
-        ptx::mbar_init(&sh.drain, 1);
+        ptx::mbar_init(sh.drain, 1);
+        ptx::mbar_init(sh.drain + 1, 1);
         abort_flag[0] = 0;
         abort_flag[1] = kTagPrefill;
         ptx::fence_mbar_init();
@@ -256,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
     pdl_enter();
 
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_wait(bar, parity & 1, abort_flag, a.d_status); };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return quick_wait(bar, parity & 1, abort_flag, a.d_status); };
     // the next item, read by a whole warp; false at the end or after an abort
     int item_no = 0;
     auto next_item = [&](Item& it) -> bool {
@@ -271,8 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp >= 8) {
-        reg_dec<88>();
-        if (warp == 11) {
+        reg_dec<64>();
+        if (warp == kWalkWarp) {
             // ------------------------------------------------------------ walks the items
             Schedule sc;
             sc.init(a);
@@ -295,15 +342,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (it.n < 0) break;  // every later round's item lies past the end too
             }
-        } else if (warp == 10) {
+        } else if (warp == kClearWarp) {
             // ------------------------------------------------------------ clears V's rows behind the last key
             // whatever lies there must not reach the products: its weights are 0, but 0 * inf is not
             Item it;
             uint32_t phases = 0;
-            int64_t c = 0;  // ring position
+            int c = 0;  // the item's first stage
             while (next_item(it)) {
                 if (it.n > 0 && it.limit % kKeys) {
-                    const int st = (int)((c + 2 * it.n - 1) % C::kStages);
+                    const int st = (c + 2 * it.n - 1) % C::kStages;
                     const bool ok = wait(sh.tail_full + st, (phases >> st) & 1);
                     if (!__all_sync(0xffffffffu, ok)) break;
                     phases ^= 1u << st;
@@ -316,22 +363,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(sh.kv_full + st);
                 }
-                c += 2 * it.n;
+                c = (c + 2 * it.n) % C::kStages;
             }
-        } else if (warp == 9) {
+        } else if (warp == kLoadWarp) {
             // ------------------------------------------------------------ loads
             const int R = a.s.page_table ? min(a.s.page_size, kKeys) : kKeys;  // rows per box
             const int nbox = kKeys / R;
             const int shift = 31 - __clz(R);
             Item it;
-            int64_t c = 0;
+            Cursor<C::kStages> c;
+            bool lap = false;      // every stage has been used
             int uses[2] = {0, 0};  // Q loads per tile
             bool ok = true;
             uint32_t tails = 0;    // stages whose last load goes to tail_full
             uint32_t tail_phase = 0;
             while (ok && next_item(it)) {
                 if (it.n == 0) continue;
-                const int tiles_q = it.ntok > a.tpt ? 2 : 1;
                 auto row_of = [&](int box) -> int {
                     const int64_t j = (int64_t)box << shift;
                     if (j >= it.limit) return -1;
@@ -349,12 +396,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int w0 = 0;
                 int cur = row_of(lane), nxt = row_of(32 + lane);
                 auto load = [&](const CUtensorMap* map, int i, bool tail) -> bool {
-                    const int st = (int)(c % C::kStages);
-                    if (c >= C::kStages) {
-                        const bool free = wait(sh.kv_empty + st, (uint32_t)(c / C::kStages) - 1);
+                    const int st = c.st;
+                    if (lap) {
+                        const bool free = wait(sh.kv_empty + st, c.ph ^ 1u);
                         if (!__all_sync(0xffffffffu, free)) return false;
                     }
-                    ++c;
+                    c.move(1);
+                    lap = lap || c.st == 0;
                     uint64_t* bar = tail ? sh.tail_full + st : sh.kv_full + st;
                     if (tail) tails |= 1u << st, tail_phase ^= 1u << st;
                     else tails &= ~(1u << st);
@@ -380,7 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     ok = load(&kmap, i, false);
                     if (ok && i == 0) {
-                        for (int x = 0; ok && x < tiles_q; ++x) {
+                        for (int x = 0; ok && x < 2; ++x) {
+                            if (it.steps[x] == 0) continue;
                             if (uses[x] > 0) ok = __all_sync(0xffffffffu, wait(sh.q_empty + x, uses[x] - 1));
                             if (!ok) break;
                             if (lane == 0) {
@@ -399,102 +448,127 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (abort_flag[0] && lane == 0) {
                 // after an abort: let the copies in flight land before the CTA ends
-                for (int64_t k = c > C::kStages ? c - C::kStages : 0; k < c; ++k) {
-                    const int st = (int)(k % C::kStages);
+                for (int st = 0; st < C::kStages; ++st) {
+                    if (!lap && st >= c.st) break;
                     if ((tails >> st) & 1) ptx::mbar_drain(sh.tail_full + st, ((tail_phase >> st) & 1) ^ 1);
-                    else ptx::mbar_drain(sh.kv_full + st, (uint32_t)(k / C::kStages) & 1);
+                    else ptx::mbar_drain(sh.kv_full + st, st < c.st ? c.ph : c.ph ^ 1u);
                 }
                 for (int x = 0; x < 2; ++x)
                     if (uses[x]) ptx::mbar_drain(sh.q_full + x, (uses[x] - 1) & 1);
             }
-        } else {
-            // ------------------------------------------------------------ issues the products
-            constexpr uint32_t idesc_s = ptx::idesc_f16(128, kKeys, true);
+        } else if (warp < kLoadWarp) {
+            // ------------------------------------------------------------ issue a tile's products
+            // The whole warp walks and waits, on values broadcast from lane 0, and
+            // one elected lane issues: descriptors then stay in uniform registers.
+            // An issue blocks until the tensor cores take it and a wait costs over
+            // 100 cycles even when its phase is over, so each tile has a warp of its
+            // own: one waits while the other's products run.  (One warp for both
+            // tiles: 836 TFLOP/s; one lane of it doing everything: 660.)
+            const int x = __shfl_sync(0xffffffffu, warp, 0) - kIssueWarp;
+            constexpr uint32_t idesc_s = ptx::idesc_f16(128, kStep, true);
             constexpr uint32_t idesc_o = ptx::idesc_f16(128, D, true, false, true);
-            const uint32_t qb = smem_u32(qs), rb = smem_u32(ring);
+            const uint32_t qd = desc_lo(smem_u32(qs) + x * C::kQTile, 16), k_lo = desc_lo(smem_u32(ring), 16);
+            const uint32_t v_lo = desc_lo(smem_u32(ring), kKeys * 128);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t t_s = tm + C::s_col(x, 0), t_o = tm + C::kO + x * D;
+            auto all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
             Item it;
-            int64_t c = 0;
-            uint32_t q_use[2] = {0, 0}, p_use[2] = {0, 0}, o_use[2] = {0, 0};
+            Cursor<C::kStages> kc, vc;  // the stages of the next scores' keys and of the next product's values
+            vc.move(1);
+            uint32_t items = 0, s_no = 0, p_no = 0;  // the tile's items, scores and products so far
             bool ok = true;
             while (ok && next_item(it)) {
-                if (it.n == 0) continue;
-                const int nx = it.ntok > a.tpt ? 2 : 1;
-                if (lane == 0) {
-                    auto kv_wait = [&](int64_t at) { return wait(sh.kv_full + at % C::kStages, (uint32_t)(at / C::kStages)); };
-                    auto scores = [&](int x, int64_t at) {
-                        const uint32_t kb = rb + (uint32_t)(at % C::kStages) * C::kStage;
+                const int n = __shfl_sync(0xffffffffu, it.steps[x], 0), stages = __shfl_sync(0xffffffffu, it.n, 0);
+                auto release = [&](int st) {
+                    if (elect_one()) ptx::mma_commit(sh.kv_empty + st);
+                    __syncwarp();
+                };
+                auto scores = [&](int j) -> bool {
+                    if ((j & 1) == 0 && !all(sh.kv_full + kc.st, kc.ph)) return false;
+                    ptx::tc_fence_after();
+                    const uint32_t kd = k_lo + ((kc.st * C::kStage + (j & 1) * (kStep * 128)) >> 4);
+                    const int buf = s_no & 1;
+                    if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
-                            ptx::mma_ss(tmem + x * 128, ptx::sdesc_sw128(qb + x * C::kQTile + off),
-                                        ptx::sdesc_sw128(kb + off), idesc_s, k > 0 ? 1u : 0u);
+                            const uint32_t off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+                            ptx::mma_ss(t_s + buf * kStep, make_desc(qd + off), make_desc(kd + off), idesc_s,
+                                        k > 0 ? 1u : 0u);
                         }
-                        ptx::mma_commit(sh.s_full + x);
-                    };
-                    ok = kv_wait(c);
-                    for (int x = 0; ok && x < nx; ++x) {
-                        ok = wait(sh.q_full + x, q_use[x]);
+                        ptx::mma_commit(&sh.s_full[x][buf]);
+                        if (j + 1 == n) ptx::mma_commit(sh.q_empty + x);
+                    }
+                    __syncwarp();
+                    ++s_no;
+                    if ((j & 1) || j + 1 == n) {
+                        release(kc.st);
+                        kc.move(2);
+                    }
+                    return true;
+                };
+                if (n > 0) {
+                    ok = all(sh.q_full + x, items) && scores(0);
+                    for (int j = 0; ok && j < n; ++j) {
+                        if (j + 1 < n) ok = scores(j + 1);
+                        if (ok && (j & 1) == 0) ok = all(sh.kv_full + vc.st, vc.ph);
+                        if (ok && j == 0 && items > 0) ok = all(sh.o_empty + x, items - 1);
+                        const int buf = p_no & 1;
+                        ok = ok && all(&sh.p_full[x][buf], p_no >> 1);
                         if (!ok) break;
-                        ++q_use[x];
                         ptx::tc_fence_after();
-                        scores(x, c);
-                    }
-                    if (ok) ptx::mma_commit(sh.kv_empty + c % C::kStages);
-                    for (int i = 0; ok && i < it.n; ++i) {
-                        const int64_t vc = c + 2 * i + 1, kc = vc + 1;
-                        const bool more = i + 1 < it.n;
-                        ok = kv_wait(vc) && (!more || kv_wait(kc));
-                        const uint32_t vb = rb + (uint32_t)(vc % C::kStages) * C::kStage;
-                        for (int x = 0; ok && x < nx; ++x) {
-                            if (i == 0) {
-                                if (o_use[x] > 0) ok = wait(sh.o_empty + x, o_use[x] - 1);
-                                ++o_use[x];
-                            }
+                        const uint32_t vd = v_lo + ((vc.st * C::kStage + (j & 1) * (kStep * 128)) >> 4);
+                        if (elect_one()) {
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                ok = ok && wait(&sh.p_full[x][h], p_use[x]);
-                                if (!ok) break;
-                                ptx::tc_fence_after();
-#pragma unroll
-                                for (int k = 4 * h; k < 4 * h + 4; ++k)
-                                    ptx::mma_ts(tmem + C::kO + x * D, tmem + C::p_col(x) + k * 8,
-                                                ptx::sdesc_sw128_mn(vb + k * 2048, kKeys * 128, 1024), idesc_o,
-                                                i > 0 || k > 0 ? 1u : 0u);
-                            }
-                            if (!ok) break;
-                            ++p_use[x];
-                            if (x + 1 == nx) ptx::mma_commit(sh.kv_empty + vc % C::kStages);
-                            if (more) scores(x, kc);
-                            else ptx::mma_commit(sh.o_full + x);
-                            if (i + 2 == it.n || it.n == 1) ptx::mma_commit(sh.q_empty + x);
+                            for (int k = 0; k < kStep / 16; ++k)
+                                ptx::mma_ts(t_o, t_s + buf * kStep + k * 8, make_desc(vd + ((k * 2048) >> 4)), idesc_o,
+                                            k > 0 ? 1u : (j > 0 ? 1u : 0u));
+                            ptx::mma_commit(sh.pv_done + x);
+                            if (j + 1 == n) ptx::mma_commit(sh.o_full + x);
                         }
-                        if (ok && more) ptx::mma_commit(sh.kv_empty + kc % C::kStages);
+                        __syncwarp();
+                        ++p_no;
+                        if ((j & 1) || j + 1 == n) {
+                            release(vc.st);
+                            vc.move(2);
+                        }
                     }
-                    c += 2 * it.n;
+                    ++items;
                 }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
+                // stages that only the other tile reads
+                for (int i = (n + 1) / 2; ok && i < stages; ++i) {
+                    ok = all(sh.kv_full + kc.st, kc.ph) && all(sh.kv_full + vc.st, vc.ph);
+                    if (ok && lane == 0) {
+                        ptx::mbar_arrive(sh.kv_empty + kc.st);
+                        ptx::mbar_arrive(sh.kv_empty + vc.st);
+                    }
+                    __syncwarp();
+                    kc.move(2);
+                    vc.move(2);
+                }
             }
-            if (lane == 0 && abort_flag[0]) {
-                ptx::mma_commit(&sh.drain);
-                ptx::mbar_drain(&sh.drain, 0);
+            if (abort_flag[0]) {
+                if (elect_one()) {
+                    ptx::mma_commit(sh.drain + x);
+                    ptx::mbar_drain(sh.drain + x, 0);
+                }
+                __syncwarp();
             }
         }
     } else {
         // ---------------------------------------------------------------- softmax: a row per thread
-        reg_inc<208>();
+        reg_inc<192>();
         const int x = warp >> 2;
         const int r = threadIdx.x & 127;
         const int tok = r / a.group, head = r - tok * a.group;
         const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, lane in bits 16..
-        const uint32_t ts = tmem + lane_base + x * 128;
-        const uint32_t tp = tmem + lane_base + C::p_col(x);
         const uint32_t to = tmem + lane_base + C::kO + x * D;
         Item it;
-        uint32_t s_use = 0, o_use = 0;
+        uint32_t no = 0, o_use = 0;  // steps so far (buffer no & 1), outputs
         bool ok = true;
+        const uint64_t sc2 = pack2(a.scale_log2, a.scale_log2);
         while (ok && next_item(it)) {
-            if (x == 1 && it.ntok <= a.tpt) continue;
             const int t = x * a.tpt + tok;  // token within the item
+            if (x == 1 && it.ntok <= a.tpt) continue;
             bool live = tok < a.tpt && t < it.ntok;
             int pos = 0x7FFFFFFF;  // unused rows: no mask, no output
             if (live) {
@@ -505,28 +579,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pos = -1;
                 }
             }
+            const int n = it.steps[x];
             float m = -INFINITY;
-            uint64_t l2a = 0ull, l2b = 0ull;  // two pairs of fp32 sums
-            for (int i = 0; i < it.n; ++i) {
-                ok = __all_sync(0xffffffffu, wait(sh.s_full + x, s_use));
+            uint64_t l2[2] = {0ull, 0ull};  // two pairs of fp32 sums
+            for (int j = 0; j < n; ++j, ++no) {
+                const int buf = no & 1;
+                ok = __all_sync(0xffffffffu, wait(&sh.s_full[x][buf], no >> 1));
                 if (!ok) break;
-                ++s_use;
                 ptx::tc_fence_after();
-                uint32_t s[4][32];
+                const uint32_t ts = tmem + lane_base + C::s_col(x, buf);
+                uint32_t s[2][32];
+                ptx::tmem_ld32_async(ts, s[0]);
+                ptx::tmem_ld32_async(ts + 32, s[1]);
+                ptx::tmem_wait_ld32(s[0]);
+                ptx::tmem_wait_ld32(s[1]);
+                const int lim = pos - j * kStep;  // the step's last key that the row sees
+                if (__any_sync(0xffffffffu, lim < kStep - 1)) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) ptx::tmem_ld32_async(ts + 32 * k, s[k]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) ptx::tmem_wait_ld32(s[k]);
-                if (a.neg) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) s[k][e] ^= 0x80000000u;
-                }
-                const int lim = pos - i * kKeys;  // the tile's last key that the row sees
-                if (__any_sync(0xffffffffu, lim < kKeys - 1)) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 2; ++k)
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (32 * k + e > lim) s[k][e] = 0xFF800000u;
@@ -534,9 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float mx[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    mx[k] = __uint_as_float(s[k][0]);
+                    mx[k] = __uint_as_float(s[k >> 1][16 * (k & 1)]);
 #pragma unroll
-                    for (int e = 1; e < 32; ++e) mx[k] = fmaxf(mx[k], __uint_as_float(s[k][e]));
+                    for (int e = 1; e < 16; ++e) mx[k] = fmaxf(mx[k], __uint_as_float(s[k >> 1][16 * (k & 1) + e]));
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
                 const bool move = top > m + kLazy;
@@ -545,9 +615,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float al = move ? fast_exp2(m - mn) : 1.f;
                     m = mn;
                     const uint64_t al2 = pack2(al, al);
-                    l2a = fma2(l2a, al2, 0ull);
-                    l2b = fma2(l2b, al2, 0ull);
-                    if (i > 0) {
+                    l2[0] = fma2(l2[0], al2, 0ull);
+                    l2[1] = fma2(l2[1], al2, 0ull);
+                    if (j > 0) {
+                        // O is at rest once the last step's product is done (the one before it is: this
+                        // step's scores followed it) and until this step's weights are handed over
+                        ok = __all_sync(0xffffffffu, wait(sh.pv_done + x, no - 1));
+                        if (!ok) break;
+                        ptx::tc_fence_after();
 #pragma unroll
                         for (int k = 0; k < D / 32; ++k) {
                             float o[32];
@@ -559,39 +634,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float mm = m == -INFINITY ? 0.f : -m;
-                const uint64_t sc2 = pack2(a.scale_log2, a.scale_log2), nm2 = pack2(mm, mm);
+                const uint64_t nm2 = pack2(mm, mm);
+                uint32_t pk[32];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pk[32];
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const uint64_t v = fma2(pack2(__uint_as_float(s[2 * h + k][e]), __uint_as_float(s[2 * h + k][e + 1])),
-                                                    sc2, nm2);
-                            float p0, p1;
-                            unpack2(v, p0, p1);
-                            p0 = fast_exp2(p0);
-                            p1 = fast_exp2(p1);
-                            if (k == 0) l2a = add2(l2a, pack2(p0, p1));
-                            else l2b = add2(l2b, pack2(p0, p1));
-                            // a weight rounded to bf16 is off by up to 2^-9 of itself; the sum keeps fp32
-                            pk[16 * k + e / 2] = pack_bf16(p0, p1);
-                        }
-                    ptx::tmem_st32_nowait(tp + 32 * h, pk);
-                    ptx::tmem_wait_st();
-                    ptx::tc_fence_before();
-                    ptx::mbar_arrive(&sh.p_full[x][h]);
-                }
+                    for (int e = 0; e < 32; e += 2) {
+                        const uint64_t v =
+                            fma2(pack2(__uint_as_float(s[k][e]), __uint_as_float(s[k][e + 1])), sc2, nm2);
+                        float p0, p1;
+                        unpack2(v, p0, p1);
+                        p0 = fast_exp2(p0);
+                        p1 = fast_exp2(p1);
+                        l2[(e >> 1) & 1] = add2(l2[(e >> 1) & 1], pack2(p0, p1));
+                        // a weight rounded to bf16 is off by up to 2^-9 of itself; the sum keeps fp32
+                        pk[16 * k + e / 2] = pack_bf16(p0, p1);
+                    }
+                ptx::tmem_st32_nowait(ts, pk);
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sh.p_full[x][buf]);
             }
             if (!ok) break;
             float la, lb, lc, ld;
-            unpack2(l2a, la, lb);
-            unpack2(l2b, lc, ld);
+            unpack2(l2[0], la, lb);
+            unpack2(l2[1], lc, ld);
             const float l = (la + lb) + (lc + ld);
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const int64_t at = (int64_t)(it.q0 + t) * (a.hkv * a.group) + it.kvh * a.group + head;
-            if (it.n > 0) {
+            if (n > 0) {
+                // its own barrier: two of pv_done's phases may be open or closed by now, and a
+                // parity tells one from the next only
                 ok = __all_sync(0xffffffffu, wait(sh.o_full + x, o_use));
                 if (!ok) break;
                 ++o_use;
@@ -613,7 +687,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 ptx::tc_fence_before();
-                ptx::mbar_arrive(sh.o_empty + x);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(sh.o_empty + x);
             } else if (live) {
                 uint4* dst = reinterpret_cast<uint4*>(a.out + at * D);
 #pragma unroll
@@ -668,9 +743,8 @@ cudaError_t launch_prefill(const dsa_gqa_shape& sh, const void* q, const void* k
     a.s = s;
     a.d_status = d_status;
     a.num_q = num_q;
-    a.neg = sm_scale < 0.f;
     // a scale of 0 stays a tiny positive one: masked scores are -inf before the scaling
-    a.scale_log2 = std::max(std::fabs(sm_scale) * 1.4426950408889634f, 1e-30f);
+    a.scale_log2 = std::max(sm_scale * 1.4426950408889634f, 1e-30f);
     const int box = s.page_table ? std::min(s.page_size, kKeys) : kKeys;
     CUtensorMap qm, km, vm;
     cudaError_t e = query_map(&qm, q, sh.num_heads, sh.head_dim, sh.q_stride, num_q, a.group, a.tpt);

@@ -275,15 +275,16 @@ def test_large_scores(call):
 
 
 @pytest.mark.parametrize("call", list(CALLS))
-def test_without_lse_and_zero_scale(call):
+def test_without_lse_and_other_scales(call):
     c = Case([300, 90], [2, 90], 8, 2, 128, page=64)
     c.run(call).check()
     want = c.out.clone()
     c.run(call, lse=False)
     torch.cuda.synchronize()
     assert torch.equal(want, c.out) and bool((c.lse == 7).all())
-    c.sm_scale = 0.0
-    c.run(call).check()
+    for scale in (0.0, -0.3, 1e-9):
+        c.sm_scale = scale
+        c.run(call).check()
 
 
 @pytest.mark.parametrize("call", list(CALLS))
