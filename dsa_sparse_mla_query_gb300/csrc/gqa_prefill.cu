@@ -21,9 +21,9 @@
 // time, 1,083 TFLOP/s on 16,384 tokens, 64/8 heads of 128.)
 //
 // Roles (one CTA per SM, persistent): two warpgroups of softmax (one per tile,
-// each also writes its tile's output), two warps that issue the products (one
-// per tile), and one warp each that loads, clears the rows behind the last
-// key, and walks the items.  Items go longest first, dealt to the CTAs in turn, back and forth.
+// each also writes its tile's output), four warps that issue the products (a
+// tile's scores, its outputs), and one warp each that loads, clears the rows
+// behind the last key, and walks the items.  Items go longest first, dealt to the CTAs in turn, back and forth.
 #include "gqa_common.cuh"
 
 namespace dsa {
@@ -34,11 +34,11 @@ constexpr int kTagPrefill = 7;
 constexpr int kKeys = 128;  // keys per stage of the ring
 constexpr int kStep = 64;   // keys per step of the products
 constexpr int kThreads = 512;
-constexpr int kIssueWarp = 8, kLoadWarp = 10, kClearWarp = 11, kWalkWarp = 12;  // then idle ones
+constexpr int kIssueWarp = 8, kLoadWarp = 12, kClearWarp = 13, kWalkWarp = 14;  // then an idle one
 constexpr float kLazy = 8.f;  // a row's reference moves when its maximum passes it by 2^8
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kItemSlots = 2;
-constexpr int kItemReaders = 12;  // warps that read an item: softmax, issuers, loader, clearer
+constexpr int kItemReaders = 14;  // warps that read an item: softmax, issuers, loader, clearer
 
 template <int D>
 struct Cfg {
@@ -244,8 +244,8 @@ struct Shared {
     uint64_t item_full[kItemSlots], item_empty[kItemSlots];
     uint64_t q_full[2], q_empty[2];
     uint64_t kv_full[10], kv_empty[10], tail_full[10];
-    uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_full[2], o_empty[2];
-    uint64_t drain[2];
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], o_empty[2];
+    uint64_t drain[4];
     int abort_flag[2];
     uint32_t tmem;
 };
@@ -283,13 +283,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int b = 0; b < 2; ++b) {
                 ptx::mbar_init(&sh.s_full[x][b], 1);
                 ptx::mbar_init(&sh.p_full[x][b], 4);
+                ptx::mbar_init(&sh.pv_done[x][b], 1);
             }
-            ptx::mbar_init(sh.pv_done + x, 1);
             ptx::mbar_init(sh.o_full + x, 1);
             ptx::mbar_init(sh.o_empty + x, 4);
         }
-        ptx::mbar_init(sh.drain, 1);
-        ptx::mbar_init(sh.drain + 1, 1);
+        for (int i = 0; i < 4; ++i) ptx::mbar_init(sh.drain + i, 1);
         abort_flag[0] = 0;
         abort_flag[1] = kTagPrefill;
         ptx::fence_mbar_init();
@@ -457,99 +456,93 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (uses[x]) ptx::mbar_drain(sh.q_full + x, (uses[x] - 1) & 1);
             }
         } else if (warp < kLoadWarp) {
-            // ------------------------------------------------------------ issue a tile's products
+            // ------------------------------------------------------------ issue the products
             // The whole warp walks and waits, on values broadcast from lane 0, and
             // one elected lane issues: descriptors then stay in uniform registers.
-            // An issue blocks until the tensor cores take it and a wait costs over
-            // 100 cycles even when its phase is over, so each tile has a warp of its
-            // own: one waits while the other's products run.  (One warp for both
-            // tiles: 836 TFLOP/s; one lane of it doing everything: 660.)
-            const int x = __shfl_sync(0xffffffffu, warp, 0) - kIssueWarp;
+            // An issue blocks until the tensor cores take it and a wait costs a few
+            // hundred cycles even when its phase is over (the products keep shared
+            // memory busy), so each tile has a warp for its scores and one for its
+            // outputs: one waits while the others' products run.  (Two warps, one
+            // per tile: 1,320 TFLOP/s; one for both: 836; one lane of it: 660.)
+            const int role = __shfl_sync(0xffffffffu, warp, 0) - kIssueWarp;
+            const int x = role & 1;
             constexpr uint32_t idesc_s = ptx::idesc_f16(128, kStep, true);
             constexpr uint32_t idesc_o = ptx::idesc_f16(128, D, true, false, true);
-            const uint32_t qd = desc_lo(smem_u32(qs) + x * C::kQTile, 16), k_lo = desc_lo(smem_u32(ring), 16);
-            const uint32_t v_lo = desc_lo(smem_u32(ring), kKeys * 128);
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const uint32_t t_s = tm + C::s_col(x, 0), t_o = tm + C::kO + x * D;
             auto all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
             Item it;
-            Cursor<C::kStages> kc, vc;  // the stages of the next scores' keys and of the next product's values
-            vc.move(1);
-            uint32_t items = 0, s_no = 0, p_no = 0;  // the tile's items, scores and products so far
+            Cursor<C::kStages> c;        // the next stage of keys, or of values
+            uint32_t items = 0, no = 0;  // the tile's items and steps so far: buffer no & 1
             bool ok = true;
+            auto release = [&]() {
+                if (elect_one()) ptx::mma_commit(sh.kv_empty + c.st);
+                __syncwarp();
+                c.move(2);
+            };
+            if (role >= 2) c.move(1);
             while (ok && next_item(it)) {
                 const int n = __shfl_sync(0xffffffffu, it.steps[x], 0), stages = __shfl_sync(0xffffffffu, it.n, 0);
-                auto release = [&](int st) {
-                    if (elect_one()) ptx::mma_commit(sh.kv_empty + st);
-                    __syncwarp();
-                };
-                auto scores = [&](int j) -> bool {
-                    if ((j & 1) == 0 && !all(sh.kv_full + kc.st, kc.ph)) return false;
-                    ptx::tc_fence_after();
-                    const uint32_t kd = k_lo + ((kc.st * C::kStage + (j & 1) * (kStep * 128)) >> 4);
-                    const int buf = s_no & 1;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
-                            ptx::mma_ss(t_s + buf * kStep, make_desc(qd + off), make_desc(kd + off), idesc_s,
-                                        k > 0 ? 1u : 0u);
-                        }
-                        ptx::mma_commit(&sh.s_full[x][buf]);
-                        if (j + 1 == n) ptx::mma_commit(sh.q_empty + x);
-                    }
-                    __syncwarp();
-                    ++s_no;
-                    if ((j & 1) || j + 1 == n) {
-                        release(kc.st);
-                        kc.move(2);
-                    }
-                    return true;
-                };
-                if (n > 0) {
-                    ok = all(sh.q_full + x, items) && scores(0);
-                    for (int j = 0; ok && j < n; ++j) {
-                        if (j + 1 < n) ok = scores(j + 1);
-                        if (ok && (j & 1) == 0) ok = all(sh.kv_full + vc.st, vc.ph);
-                        if (ok && j == 0 && items > 0) ok = all(sh.o_empty + x, items - 1);
-                        const int buf = p_no & 1;
-                        ok = ok && all(&sh.p_full[x][buf], p_no >> 1);
+                if (n > 0 && role < 2) {
+                    const uint32_t qd = desc_lo(smem_u32(qs) + x * C::kQTile, 16), k_lo = desc_lo(smem_u32(ring), 16);
+                    ok = all(sh.q_full + x, items);
+                    for (int j = 0; ok && j < n; ++j, ++no) {
+                        const int buf = no & 1;
+                        if ((j & 1) == 0) ok = all(sh.kv_full + c.st, c.ph);
+                        // the buffer's last weights have been used
+                        if (ok && no >= 2) ok = all(&sh.pv_done[x][buf], (no >> 1) - 1);
                         if (!ok) break;
                         ptx::tc_fence_after();
-                        const uint32_t vd = v_lo + ((vc.st * C::kStage + (j & 1) * (kStep * 128)) >> 4);
+                        const uint32_t kd = k_lo + ((c.st * C::kStage + (j & 1) * (kStep * 128)) >> 4);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+                                ptx::mma_ss(t_s + buf * kStep, make_desc(qd + off), make_desc(kd + off), idesc_s,
+                                            k > 0 ? 1u : 0u);
+                            }
+                            ptx::mma_commit(&sh.s_full[x][buf]);
+                            if (j + 1 == n) ptx::mma_commit(sh.q_empty + x);
+                        }
+                        __syncwarp();
+                        if ((j & 1) || j + 1 == n) release();
+                    }
+                    ++items;
+                } else if (n > 0) {
+                    const uint32_t v_lo = desc_lo(smem_u32(ring), kKeys * 128);
+                    if (items > 0) ok = all(sh.o_empty + x, items - 1);
+                    for (int j = 0; ok && j < n; ++j, ++no) {
+                        const int buf = no & 1;
+                        if ((j & 1) == 0) ok = all(sh.kv_full + c.st, c.ph);
+                        ok = ok && all(&sh.p_full[x][buf], no >> 1);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        const uint32_t vd = v_lo + ((c.st * C::kStage + (j & 1) * (kStep * 128)) >> 4);
                         if (elect_one()) {
 #pragma unroll
                             for (int k = 0; k < kStep / 16; ++k)
                                 ptx::mma_ts(t_o, t_s + buf * kStep + k * 8, make_desc(vd + ((k * 2048) >> 4)), idesc_o,
                                             k > 0 ? 1u : (j > 0 ? 1u : 0u));
-                            ptx::mma_commit(sh.pv_done + x);
+                            ptx::mma_commit(&sh.pv_done[x][buf]);
                             if (j + 1 == n) ptx::mma_commit(sh.o_full + x);
                         }
                         __syncwarp();
-                        ++p_no;
-                        if ((j & 1) || j + 1 == n) {
-                            release(vc.st);
-                            vc.move(2);
-                        }
+                        if ((j & 1) || j + 1 == n) release();
                     }
                     ++items;
                 }
                 // stages that only the other tile reads
                 for (int i = (n + 1) / 2; ok && i < stages; ++i) {
-                    ok = all(sh.kv_full + kc.st, kc.ph) && all(sh.kv_full + vc.st, vc.ph);
-                    if (ok && lane == 0) {
-                        ptx::mbar_arrive(sh.kv_empty + kc.st);
-                        ptx::mbar_arrive(sh.kv_empty + vc.st);
-                    }
+                    ok = all(sh.kv_full + c.st, c.ph);
+                    if (ok && lane == 0) ptx::mbar_arrive(sh.kv_empty + c.st);
                     __syncwarp();
-                    kc.move(2);
-                    vc.move(2);
+                    c.move(2);
                 }
             }
             if (abort_flag[0]) {
                 if (elect_one()) {
-                    ptx::mma_commit(sh.drain + x);
-                    ptx::mbar_drain(sh.drain + x, 0);
+                    ptx::mma_commit(sh.drain + role);
+                    ptx::mbar_drain(sh.drain + role, 0);
                 }
                 __syncwarp();
             }
@@ -619,8 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l2[1] = fma2(l2[1], al2, 0ull);
                     if (j > 0) {
                         // O is at rest once the last step's product is done (the one before it is: this
-                        // step's scores followed it) and until this step's weights are handed over
-                        ok = __all_sync(0xffffffffu, wait(sh.pv_done + x, no - 1));
+                        // step's scores waited for it) and until this step's weights are handed over
+                        ok = __all_sync(0xffffffffu, wait(&sh.pv_done[x][buf ^ 1], (no - 1) >> 1));
                         if (!ok) break;
                         ptx::tc_fence_after();
 #pragma unroll
@@ -664,8 +657,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const int64_t at = (int64_t)(it.q0 + t) * (a.hkv * a.group) + it.kvh * a.group + head;
             if (n > 0) {
-                // its own barrier: two of pv_done's phases may be open or closed by now, and a
-                // parity tells one from the next only
                 ok = __all_sync(0xffffffffu, wait(sh.o_full + x, o_use));
                 if (!ok) break;
                 ++o_use;
