@@ -381,13 +381,21 @@ __global__ void __launch_bounds__(128) mla_q_prep_kernel(const __nv_bfloat16* __
 
 // ---------------------------------------------------------------------------
 // K and V rows of new tokens into caches with heads, and the queries: rows of
-// D dims, D / 8 lanes per row with 8 dims (16 bytes) each.  A token's cosines
-// and sines serve all its query and key heads, so a CTA takes `tb` tokens at a
-// time, computes their tables once in shared memory and then walks the
-// tokens' rows (query heads, key heads, value heads).
-constexpr int kKvThreads = 256;
-constexpr int kKvMaxTokens = 8;  // tokens per CTA pass
-constexpr int kKvUnroll = 4;     // rows a thread has in flight
+// D dims, D / 8 lanes per row with 8 dims (16 bytes) each.  A warp takes a
+// token and one or more chunks of its rows (query heads, key heads, value
+// heads), kKvUnroll accesses each.  A lane holds the same dims of every row,
+// so its cosines and sines stay in registers for the whole token:
+//   y_d = C_d x_d + S_d x_d',  d' the pair's other dim, S_d = -sin for its
+//   first dim and +sin for its second.
+// They are computed once per token, one angle per lane at a time, through
+// shared memory, while the first chunk's loads are in flight.
+//
+// Bound by HBM, close to the issue slots with many query heads.  131,072
+// tokens' K and V (8 heads of 128, bf16): 170 us, 6.3 TB/s; 8,191 tokens with
+// 64 query heads into e4m3 caches: 61 us, 5.2 TB/s (a CTA per token with its
+// table in shared memory for every access: 268 and 130 us; eight accesses in
+// flight and fewer warps: 174 and 76).
+constexpr int kKvUnroll = 4;  // accesses per chunk: 8 rows of 128 dims
 
 struct KvInsert {
     const __nv_bfloat16 *k, *v, *q;
@@ -401,130 +409,157 @@ struct KvInsert {
     int64_t k_stride, v_stride, q_stride;  // elements between rows of the destinations
     int64_t num_rows;
     int32_t n, hq, hkv, rot;  // hq: 0 when there are no queries; rot: 0 for no rotation
-    int32_t tb;
+    int32_t span, spans;      // chunks per item, items per token
 };
 
+__device__ __forceinline__ uint64_t f32x2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+// c x + s o of two bf16 each (fp32), rounded to bf16
+__device__ __forceinline__ uint64_t turn2(uint32_t x, uint32_t o, uint64_t c, uint64_t s) {
+    uint64_t r;
+    asm("{\n .reg .b64 t;\n mul.rn.f32x2 t, %1, %2;\n fma.rn.f32x2 %0, %3, %4, t;\n}\n"
+        : "=l"(r)
+        : "l"(f32x2(bf16_lo(x), bf16_hi(x))), "l"(c), "l"(f32x2(bf16_lo(o), bf16_hi(o))), "l"(s));
+    return r;
+}
+
 template <int D, bool FP8, bool HALVES>
-__global__ void __launch_bounds__(kKvThreads) kv_insert_kernel(const __grid_constant__ KvInsert a, int32_t* d_status) {
-    constexpr int kLanes = D / 8;  // lanes per row
-    __shared__ float2 cs[kKvMaxTokens][D / 2];
+__global__ void __launch_bounds__(128, FP8 ? 7 : 8) kv_insert_kernel(const __grid_constant__ KvInsert a, int32_t* d_status) {
+    constexpr int kLanes = D / 8;        // lanes per row
+    constexpr int kGroup = 32 / kLanes;  // rows per warp access
+    __shared__ __align__(16) float cos_t[kWarpsPerCta][D], sin_t[kWarpsPerCta][D];
     pdl_enter();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rows = a.hq + 2 * a.hkv;
     const int half = a.rot / 2;
-    const int li = threadIdx.x % kLanes;
-    for (int64_t t0 = (int64_t)blockIdx.x * a.tb; t0 < a.n; t0 += (int64_t)gridDim.x * a.tb) {
-        const int nt = (int)min((int64_t)a.tb, a.n - t0);
-        const int items = nt * rows;
-        for (int i0 = threadIdx.x / kLanes; i0 - (int)(threadIdx.x / kLanes) < items;
-             i0 += kKvUnroll * (kKvThreads / kLanes)) {
-            // item: (token, row) with the row fastest
+    const int li = lane % kLanes, sub = lane / kLanes;
+    const bool turned = 8 * li < a.rot;  // rot is a multiple of 16: all of the lane's dims or none
+    const int step = a.rot / 16;         // HALVES: lanes between a pair's dims
+    const int from = !turned ? lane : li < step ? lane + step : lane - step;
+    const int64_t items = (int64_t)a.n * a.spans;
+    for (int64_t it = (int64_t)blockIdx.x * kWarpsPerCta + warp; it < items;
+         it += (int64_t)gridDim.x * kWarpsPerCta) {
+        const int64_t t = it / a.spans;
+        const int row0 = (int)(it - t * a.spans) * a.span * (kKvUnroll * kGroup);
+        const int row1 = min(rows, row0 + a.span * (kKvUnroll * kGroup));
+        const int p = __ldg(a.pos + t);
+        const int64_t sl = __ldg(a.slot + t);
+        // pos < 0 or a slot past the cache: nothing of the token is written
+        const bool bad = sl >= a.num_rows || (p < 0 && sl >= 0);
+        if (bad && lane == 0) report(d_status, DSA_ERR_BAD_INPUT);
+        const bool write_q = !bad && p >= 0, write_kv = !bad && sl >= 0;
+        uint64_t c2[4], s2[4];
+        for (int c0 = row0; c0 < row1; c0 += kKvUnroll * kGroup) {
+            // a chunk of query rows only: no choices per row
+            const bool only_q = c0 + kKvUnroll * kGroup <= min(a.hq, row1);
             uint4 x[kKvUnroll];
-            int tok[kKvUnroll], row[kKvUnroll];
+            if (only_q) {
 #pragma unroll
-            for (int u = 0; u < kKvUnroll; ++u) {
-                const int it = i0 + u * (kKvThreads / kLanes);
-                row[u] = it < items ? it % rows : -1;
-                tok[u] = it < items ? it / rows : 0;
-                x[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (row[u] >= 0) {
-                    const int64_t t = t0 + tok[u];
-                    const int r = row[u];
-                    const __nv_bfloat16* src = r < a.hq           ? a.q + t * a.q_in + (int64_t)r * D
-                                               : r < a.hq + a.hkv ? a.k + t * a.k_in + (int64_t)(r - a.hq) * D
-                                                                  : a.v + t * a.v_in + (int64_t)(r - a.hq - a.hkv) * D;
-                    x[u] = __ldcs(reinterpret_cast<const uint4*>(src) + li);
-                }
-            }
-            if (i0 == (int)(threadIdx.x / kLanes)) {
-                // the tokens' rotation tables, while the first rows are in flight
-                __syncthreads();  // the previous tokens' tables are no longer read
-                for (int i = threadIdx.x; i < nt * half; i += kKvThreads) {
-                    const int t = i / half, f = i - t * half;
-                    const int p = __ldg(a.pos + t0 + t);
-                    float c = 1.f, s = 0.f;
-                    if (p >= 0) rope_cs(p, __ldg(a.inv_freq + f), c, s);
-                    cs[t][f] = make_float2(c, s);
-                }
-                __syncthreads();
-            }
+                for (int u = 0; u < kKvUnroll; ++u)
+                    x[u] = __ldcs(reinterpret_cast<const uint4*>(a.q + t * a.q_in + (c0 + sub) * D + 8 * li) + u * 32);
+            } else {
 #pragma unroll
-            for (int u = 0; u < kKvUnroll; ++u) {
-                const int r = row[u];
-                const bool is_q = r >= 0 && r < a.hq, is_k = r >= a.hq && r < a.hq + a.hkv;
-                float v[8];
-                unpack_bf16x8(x[u], v);
-                if (a.rot) {
-                    const float2* tab = cs[tok[u]];
-                    if (HALVES) {
-                        // chunk li holds dims 8 li .. 8 li + 7; its pairs' other halves are rot / 16 lanes away
-                        const int step = a.rot / 16;
-                        const bool first = li < step, second = li >= step && li < 2 * step;
-                        const int lane = threadIdx.x & 31;
-                        const int from = first ? lane + step : second ? lane - step : lane;
-                        uint4 y;
-                        y.x = __shfl_sync(0xffffffffu, x[u].x, from);
-                        y.y = __shfl_sync(0xffffffffu, x[u].y, from);
-                        y.z = __shfl_sync(0xffffffffu, x[u].z, from);
-                        y.w = __shfl_sync(0xffffffffu, x[u].w, from);
-                        if ((is_q || is_k) && (first || second)) {
-                            float o[8];
-                            unpack_bf16x8(y, o);
-                            const int f0 = (first ? li : li - step) * 8;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float2 w = tab[f0 + e];
-                                v[e] = first ? fmaf(v[e], w.x, -o[e] * w.y) : fmaf(o[e], w.y, v[e] * w.x);
-                            }
-                        }
-                    } else if ((is_q || is_k) && 8 * li < a.rot) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 w = tab[4 * li + e];
-                            const float x0 = v[2 * e], x1 = v[2 * e + 1];
-                            v[2 * e] = fmaf(x0, w.x, -x1 * w.y);
-                            v[2 * e + 1] = fmaf(x0, w.y, x1 * w.x);
-                        }
+                for (int u = 0; u < kKvUnroll; ++u) {
+                    const int r = c0 + sub + u * kGroup;
+                    x[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < row1) {
+                        const __nv_bfloat16* src = r < a.hq           ? a.q + t * a.q_in
+                                                   : r < a.hq + a.hkv ? a.k + t * a.k_in - a.hq * D
+                                                                      : a.v + t * a.v_in - (a.hq + a.hkv) * D;
+                        x[u] = __ldcs(reinterpret_cast<const uint4*>(src + r * D + 8 * li));
                     }
                 }
+            }
+            if (c0 == row0 && a.rot && row0 < a.hq + a.hkv) {
+                __syncwarp();  // the last token's table is no longer read
+                for (int f = lane; f < half; f += 32) {
+                    float c = 1.f, s = 0.f;
+                    if (p >= 0) rope_cs(p, __ldg(a.inv_freq + f), c, s);
+                    const int d0 = HALVES ? f : 2 * f, d1 = HALVES ? f + half : 2 * f + 1;
+                    cos_t[warp][d0] = cos_t[warp][d1] = c;
+                    sin_t[warp][d0] = -s;
+                    sin_t[warp][d1] = s;
+                }
+                __syncwarp();
+                const ulonglong2* ct = reinterpret_cast<const ulonglong2*>(&cos_t[warp][8 * li]);
+                const ulonglong2* st = reinterpret_cast<const ulonglong2*>(&sin_t[warp][8 * li]);
+                c2[0] = ct[0].x, c2[1] = ct[0].y, c2[2] = ct[1].x, c2[3] = ct[1].y;
+                s2[0] = st[0].x, s2[1] = st[0].y, s2[2] = st[1].x, s2[3] = st[1].y;
+            }
+            if (only_q) {
+                if (!write_q) continue;
+                uint4* dst = reinterpret_cast<uint4*>(a.q_out + t * a.q_stride + (c0 + sub) * D) + li;
+#pragma unroll
+                for (int u = 0; u < kKvUnroll; ++u) {
+                    uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[e] = HALVES ? __shfl_sync(0xffffffffu, xs[e], from) : __byte_perm(xs[e], 0u, 0x1032);
+                    if (turned) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint64_t y = turn2(xs[e], o[e], c2[e], s2[e]);
+                            xs[e] = pack_bf16x2(__uint_as_float((uint32_t)y), __uint_as_float((uint32_t)(y >> 32)));
+                        }
+                    }
+                    dst[u * 32] = make_uint4(xs[0], xs[1], xs[2], xs[3]);
+                }
+                continue;
+            }
+#pragma unroll
+            for (int u = 0; u < kKvUnroll; ++u) {
+                const int r = c0 + sub + u * kGroup;
+                const bool is_q = r < a.hq, is_k = !is_q && r < a.hq + a.hkv;
+                const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[e] = HALVES ? __shfl_sync(0xffffffffu, xs[e], from) : __byte_perm(xs[e], 0u, 0x1032);
+                float v[8];
+                if (turned && (is_q || is_k)) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint64_t y = turn2(xs[e], o[e], c2[e], s2[e]);
+                        v[2 * e] = __uint_as_float((uint32_t)y);
+                        v[2 * e + 1] = __uint_as_float((uint32_t)(y >> 32));
+                    }
+                } else {
+                    unpack_bf16x8(x[u], v);
+                }
                 float m = 0.f;
-                if (FP8) {
+                if (FP8 && c0 + (u + 1) * kGroup > a.hq) {  // the same for the whole warp
 #pragma unroll
                     for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
 #pragma unroll
-                    for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    for (int w = kLanes / 2; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
                 }
-                if (r < 0) continue;  // after the shuffles
-                const int64_t t = t0 + tok[u];
-                const int p = __ldg(a.pos + t);
-                const int64_t sl = __ldg(a.slot + t);
+                if (r >= row1) continue;  // after the shuffles
                 if (is_q) {
-                    if (p < 0 || sl >= a.num_rows) continue;  // the key heads report it
-                    uint4* dst = reinterpret_cast<uint4*>(a.q_out + t * a.q_stride + (int64_t)r * D);
-                    dst[li] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                         pack_bf16x2(v[6], v[7]));
+                    if (write_q)
+                        *reinterpret_cast<uint4*>(a.q_out + t * a.q_stride + (int64_t)r * D + 8 * li) =
+                            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                       pack_bf16x2(v[6], v[7]));
                     continue;
                 }
-                if (sl < 0) continue;
-                if (sl >= a.num_rows || p < 0) {
-                    if (li == 0) report(d_status, DSA_ERR_BAD_INPUT);
-                    continue;
-                }
+                if (!write_kv) continue;
+                void* cache = is_k ? a.k_cache : a.v_cache;
                 const int h = is_k ? r - a.hq : r - a.hq - a.hkv;
-                const int64_t at = sl * (is_k ? a.k_stride : a.v_stride) + (int64_t)h * D;
+                const int64_t at = sl * (is_k ? a.k_stride : a.v_stride) + h * D + 8 * li;
                 if (FP8) {
                     // a row below 448 * 2^-126 takes the smallest normal scale: 1 / scale stays finite
                     const float scale = m > 0.f ? fmaxf(m / 448.f, 0x1p-126f) : 1.f;
                     const float rs = 1.f / scale;
-                    uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_k ? a.k_cache : a.v_cache) + at);
-                    dst[li] = make_uint2(pack_e4m3x4(v[0] * rs, v[1] * rs, v[2] * rs, v[3] * rs),
-                                         pack_e4m3x4(v[4] * rs, v[5] * rs, v[6] * rs, v[7] * rs));
+                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + at) =
+                        make_uint2(pack_e4m3x4(v[0] * rs, v[1] * rs, v[2] * rs, v[3] * rs),
+                                   pack_e4m3x4(v[4] * rs, v[5] * rs, v[6] * rs, v[7] * rs));
                     if (li == 0) (is_k ? a.k_scale : a.v_scale)[sl * a.hkv + h] = scale;
                 } else {
-                    uint4* dst =
-                        reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_k ? a.k_cache : a.v_cache) + at);
-                    dst[li] = is_k ? make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]))
-                                   : x[u];
+                    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + at) =
+                        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                   pack_bf16x2(v[6], v[7]));
                 }
             }
         }
@@ -616,15 +651,15 @@ cudaError_t launch_kv_insert(const dsa_gqa_shape& sh, const void* k, int64_t k_i
     a.hq = q ? sh.num_heads : 0;
     a.hkv = sh.num_kv_heads;
     a.rot = inv_freq ? rot : 0;
-    // tokens per CTA pass: a pass of all its threads' unrolled rows, as long as
-    // the tokens still give every SM several CTAs
-    const int rows = a.hq + 2 * a.hkv;
-    const int per_pass = kKvUnroll * (kKvThreads * 8 / sh.head_dim);
-    a.tb = std::max(1, std::min(kKvMaxTokens, per_pass / rows));
-    while (a.tb > 1 && n / a.tb < 152 * 8) a.tb /= 2;
-    const dim3 grid(insert_grid(((int64_t)n + a.tb - 1) / a.tb * kTokensPerCta));
+    // a warp takes a token's rows as far as the tokens fill the GPU: with fewer
+    // tokens than that, a chunk of them
+    const int per = kKvUnroll * 256 / sh.head_dim;  // rows per chunk
+    const int chunks = (a.hq + 2 * a.hkv + per - 1) / per;
+    a.span = (int)std::max<int64_t>(1, std::min<int64_t>(chunks, (int64_t)n * chunks / (152 * 128)));
+    a.spans = (chunks + a.span - 1) / a.span;
+    const dim3 grid(insert_grid((int64_t)n * a.spans));
     const bool fp8 = sh.kv_dtype == DSA_FP8_E4M3_ROWSCALE;
-    auto go = [&](auto kern) { return launch_pdl(kern, grid, dim3(kKvThreads), 0, stream, 1, a, d_status); };
+    auto go = [&](auto kern) { return launch_pdl(kern, grid, dim3(32 * kWarpsPerCta), 0, stream, 1, a, d_status); };
     if (sh.head_dim == 64)
         return fp8 ? (halves ? go(kv_insert_kernel<64, true, true>) : go(kv_insert_kernel<64, true, false>))
                    : (halves ? go(kv_insert_kernel<64, false, true>) : go(kv_insert_kernel<64, false, false>));
