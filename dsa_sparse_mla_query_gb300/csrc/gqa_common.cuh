@@ -47,6 +47,16 @@ inline cudaError_t cache_map(CUtensorMap* m, bool bytes, const void* base, int h
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// A warpgroup's registers per thread, from those that the CTA was launched with
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // mbar_wait for waits that are short as a rule: several hardware-timed probes
 // before the first read of the timer, which takes longer than a probe.
 __device__ __forceinline__ bool quick_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,

@@ -18,9 +18,11 @@
 //   sequence, 64-key tile), balanced over the tiles that exist, and CTAs of
 //   neighbouring lanes walk the same keys at the same time, so a token's heads
 //   (256 or 512 bytes apart) are read from the same DRAM pages together.
-// - One warp loads: TMA boxes of whole pages (or 64 rows) into a ring of
-//   stages; four warps (eight for more than 16 rows) take 16 keys of each tile,
-//   each with its own softmax state, and meet only at the end of a sequence.
+// - One warp loads: TMA boxes of whole pages (or of a tile) into a ring of
+//   stages; the computing warps take 16 keys of each tile, each with its own
+//   softmax state, and meet only at the end of a sequence.  Up to 8 query rows:
+//   four of them, two CTAs per SM.  Up to 32 rows (drafts to verify): eight
+//   that hold all the rows each, so that a key is read and converted once.
 // - A sequence cut by CTA borders leaves one partial per CTA, which a second
 //   kernel joins in a fixed order.
 #include <type_traits>
@@ -31,27 +33,32 @@ namespace dsa {
 namespace gqa {
 namespace {
 
-constexpr int kTile = 64;  // keys per tile
 constexpr int kTagDecode = 6;
 constexpr float kLazy = 8.f;  // a row's reference moves when its maximum passes it by 2^8
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int D, bool FP8, int NT, int RG>
+// NT: 8-row tiles of query rows; KS: computing warps, 16 keys of a tile each
+template <int D, bool FP8, int NT, int KS>
 struct Cfg {
-    static constexpr int kRows = 8 * NT * RG;  // query rows per chunk
-    static constexpr int kThreads = 32 * (4 * RG + 1);
-    static constexpr int kOcc = RG == 1 ? 2 : 1;  // CTAs per SM
+    static constexpr int kRows = 8 * NT;     // query rows per chunk
+    static constexpr int kTile = 16 * KS;    // keys per tile
+    static constexpr bool kSplitRegs = KS == 8;  // three warpgroups, the registers given to the computing two
+    static constexpr int kThreads = kSplitRegs ? 384 : 32 * (KS + 1);
+    static constexpr int kOcc = KS == 8 ? 1 : 2;  // CTAs per SM
     static constexpr int kHeadBytes = D * (FP8 ? 1 : 2);
     static constexpr int kHalf = kTile * kHeadBytes;  // K or V of a stage
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kScaleBytes = FP8 ? 2 * kTile * 4 : 0;
-    static constexpr int kScratch = RG * 4 * 8 * D * 4;  // the four key slices' outputs of 8 rows
-    static constexpr int kMl = RG * 4 * 8 * NT * 8;
-    static constexpr int kMisc = 256;
-    static constexpr int kBudget = (RG == 1 ? 115712 : 232448) - kScratch - kMl - kMisc;
+    static constexpr int kScratch = 4 * 8 * D * 4;  // four key slices' outputs of 8 rows
+    static constexpr int kMl = KS * kRows * 8;
+    static constexpr bool kQShared = NT > 2;        // query fragments in shared memory, else in registers
+    static constexpr int kQBytes = kQShared ? (D / 16) * NT * 32 * 8 : 0;
+    static constexpr int kMisc = 256 + kRows * 8;
+    static constexpr int kFixed = kScratch + kMl + kQBytes + kMisc;
+    static constexpr int kBudget = (kOcc == 2 ? 115712 : 232448) - kFixed;
     static constexpr int kFit = kBudget / (kStage + kScaleBytes);
     static constexpr int kStages = kFit < 8 ? kFit : 8;
-    static constexpr int kSmem = kStages * (kStage + kScaleBytes) + kScratch + kMl + kMisc;
+    static constexpr int kSmem = kStages * (kStage + kScaleBytes) + kFixed;
     static_assert(kStages >= 3, "a ring of at least three stages");
 };
 
@@ -110,6 +117,12 @@ __device__ __forceinline__ void lds128(uint32_t (&r)[4], uint32_t addr) {
 __device__ __forceinline__ void lds64(uint32_t (&r)[2], uint32_t addr) {
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
 }
+// four e4m3 codes (low byte first) -> two f16x2, exact
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
@@ -124,16 +137,17 @@ __device__ __forceinline__ float warp_max_all(float x) {
 }
 
 // byte address of 16-byte chunk `c` of a tile's row in the layout TMA wrote
-// (128-byte pieces of 64 rows, 128-byte swizzle; a 64-byte head row: 64-byte
-// swizzle)
-template <int HB>
+// (128-byte pieces of a tile's rows, 128-byte swizzle; a 64-byte head row:
+// 64-byte swizzle)
+template <int HB, int TILE>
 __device__ __forceinline__ uint32_t chunk_addr(uint32_t base, int row, int c) {
     if (HB == 64) return base + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-    return base + (c >> 3) * (kTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+    return base + (c >> 3) * (TILE * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
 }
 
+template <int TILE>
 __device__ __forceinline__ int tiles_of(const Seq& q) {
-    return q.ok && q.nq > 0 ? max(1, (q.ctx + kTile - 1) / kTile) : 0;
+    return q.ok && q.nq > 0 ? max(1, (q.ctx + TILE - 1) / TILE) : 0;
 }
 
 // The walk over a CTA's pieces: each call of next() gives a run of tiles
@@ -147,6 +161,7 @@ struct Piece {
     int64_t base;            // first row of a contiguous sequence
 };
 
+template <int TILE, int ROWS>
 struct Walk {
     int64_t r0, left, sum, total;
     int u, b, i;
@@ -166,7 +181,7 @@ struct Walk {
                 v[x] = 0;
                 if (k + x < per && bb < B) {
                     const Seq q = load_seq(a.s, bb, a.num_q);
-                    v[x] = tiles_of(q);
+                    v[x] = tiles_of<TILE>(q);
                     if (!q.ok && blockIdx.x == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
                 }
             }
@@ -196,7 +211,7 @@ struct Walk {
         for (int k0 = 0; k0 < per; k0 += 32) {
             const int bb = l * per + k0 + lane;
             int v = 0;
-            if (k0 + lane < per && bb < B) v = tiles_of(load_seq(a.s, bb, a.num_q));
+            if (k0 + lane < per && bb < B) v = tiles_of<TILE>(load_seq(a.s, bb, a.num_q));
             int in = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -213,7 +228,6 @@ struct Walk {
             off -= __shfl_sync(0xffffffffu, in, 31);
         }
     }
-    template <int ROWS>
     __device__ __forceinline__ bool next(const Args& a, Piece& p) {
         while (left > 0) {
             if (b == a.s.num_seqs) {
@@ -221,7 +235,7 @@ struct Walk {
                 ++u;
             }
             const Seq q = load_seq(a.s, b, a.num_q);
-            const int cnt = tiles_of(q);
+            const int cnt = tiles_of<TILE>(q);
             if (cnt == 0) {
                 ++b;
                 continue;
@@ -258,27 +272,29 @@ struct Walk {
     }
 };
 
-template <int D, bool FP8, int NT, int RG>
-__global__ void __launch_bounds__(Cfg<D, FP8, NT, RG>::kThreads, Cfg<D, FP8, NT, RG>::kOcc)
+template <int D, bool FP8, int NT, int KS>
+__global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT, KS>::kOcc)
     gqa_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ Args a) {
-    using C = Cfg<D, FP8, NT, RG>;
-    constexpr int HB = C::kHeadBytes;
+    using C = Cfg<D, FP8, NT, KS>;
+    constexpr int HB = C::kHeadBytes, kTile = C::kTile;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem;
     float* ring_scale = reinterpret_cast<float*>(smem + C::kStages * C::kStage);
     float* scratch = reinterpret_cast<float*>(smem + C::kStages * (C::kStage + C::kScaleBytes));
     float2* ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(scratch) + C::kScratch);
-    uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ml) + C::kMl);
+    uint8_t* q_sh = reinterpret_cast<uint8_t*>(ml) + C::kMl;  // [D / 16][NT / 2][lane] two tiles' fragments
+    float* fac_sh = reinterpret_cast<float*>(q_sh + C::kQBytes);  // [rows]
+    int* pos_sh = reinterpret_cast<int*>(fac_sh + C::kRows);      // [rows]
+    uint64_t* full = reinterpret_cast<uint64_t*>(pos_sh + C::kRows);
     uint64_t* empty = full + C::kStages;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + C::kStages);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kConsumers = 4 * RG;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             ptx::mbar_init(full + i, FP8 ? 33 : 1);
-            ptx::mbar_init(empty + i, kConsumers);
+            ptx::mbar_init(empty + i, KS);
         }
         abort_flag[0] = 0;
         abort_flag[1] = kTagDecode;
@@ -289,18 +305,20 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, RG>::kThreads, Cfg<D, FP8, NT,
     __syncthreads();
     pdl_enter();
 
-    Walk w;
-    w.init(a);
+    Walk<kTile, C::kRows> w;
     Piece p;
 
-    if (warp == kConsumers) {
+    if (warp >= KS) {
+        if (C::kSplitRegs) reg_dec<72>();
+        if (warp > KS) return;
+        w.init(a);
         // ---- the loading warp: a lane per TMA box of a 32-box window of the page table
         const int R = a.s.page_table ? min(a.s.page_size, kTile) : kTile;  // rows per box
         const int nbox = kTile / R;
         const int shift = 31 - __clz(R);
         int it = 0;
         bool ok = true;
-        while (ok && w.next<C::kRows>(a, p)) {
+        while (ok && w.next(a, p)) {
             const int kvh = p.lane % a.hkv;
             const int end = min(p.i1, (p.limit + kTile - 1) / kTile);
             auto row_of = [&](int box) -> int {  // physical row of the box's first token, -1: none
@@ -345,7 +363,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, RG>::kThreads, Cfg<D, FP8, NT,
                         tma_load_4d(kd + x * R * PB, &kmap, 0, cur, 0, kvh, full + st);
                         tma_load_4d(vd + x * R * PB, &vmap, 0, cur, 0, kvh, full + st);
                     } else {
-                        // two 128-byte pieces, each a block of 64 rows: a smaller box is one piece
+                        // two 128-byte pieces, each a block of the tile's rows: a smaller box is one piece
                         for (int h = 0; h < HB / 128; ++h) {
                             tma_load_4d(kd + h * (kTile * 128) + x * R * 128, &kmap, 0, cur, h, kvh, full + st);
                             tma_load_4d(vd + h * (kTile * 128) + x * R * 128, &vmap, 0, cur, h, kvh, full + st);
@@ -376,33 +394,47 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, RG>::kThreads, Cfg<D, FP8, NT,
         return;
     }
 
-    // ---- the computing warps: key slice ks of every tile for row group rg
-    const int ks = warp & 3, rg = warp >> 2;
+    // ---- the computing warps: key slice ks of every tile
+    if (C::kSplitRegs) reg_inc<216>();
+    w.init(a);
+    const int ks = warp;
     const int g = lane >> 2, t = lane & 3;
     constexpr int KK = D / 16;  // k-steps of q.k, and 16-dim tiles of the output
-    const uint32_t ring_u = smem_u32(ring);
+    constexpr int NQ = C::kQShared ? 1 : NT;
+    const uint32_t ring_u = smem_u32(ring), q_u = smem_u32(q_sh);
     int it = 0;
     bool ok = true;
     int4 join = make_int4(0, 0, 0, 0);
-    while (w.next<C::kRows>(a, p)) {
+    while (w.next(a, p)) {
         const int kvh = p.lane % a.hkv;
         const int end = min(p.i1, (p.limit + kTile - 1) / kTile);
-        // queries of this thread's fragment rows (column g of each 8-row tile)
-        uint32_t qf[NT][KK][2];
-        float qfac[NT][2];  // FP8: 2^-e of the columns' scaled queries
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int f = p.row0 + (rg * NT + n) * 8 + g;
+        // the rows' positions; -2: not to be written
+        if (threadIdx.x < C::kRows) {
+            const int tok = (p.row0 + (int)threadIdx.x) / a.group;
+            int pos = -2;
+            if (tok < p.q.nq) {
+                pos = __ldg(a.s.q_pos + p.q.q0 + tok);
+                if (pos < -1 || pos >= p.q.ctx) {
+                    if (!p.front) report(a.d_status, DSA_ERR_BAD_INPUT);
+                    pos = -2;
+                }
+            }
+            pos_sh[threadIdx.x] = pos;
+        }
+        // query fragments: this thread's of row g of 8-row tile n, 2^-e of a scaled row
+        auto fragments = [&](int n, uint32_t (&qf)[KK][2], float& down) {
+            const int f = p.row0 + n * 8 + g;
             const int tok = f / a.group, head = f - tok * a.group;
             const bool live = tok < p.q.nq;
             const __nv_bfloat16* src =
                 a.q + (int64_t)(p.q.q0 + tok) * a.q_stride + (int64_t)(kvh * a.group + head) * D;
+            down = 1.f;
             if (!FP8) {
 #pragma unroll
                 for (int k = 0; k < KK; ++k) {
                     const uint32_t* s32 = reinterpret_cast<const uint32_t*>(src + k * 16 + 2 * t);
-                    qf[n][k][0] = live ? __ldg(s32) : 0u;
-                    qf[n][k][1] = live ? __ldg(s32 + 4) : 0u;
+                    qf[k][0] = live ? __ldg(s32) : 0u;
+                    qf[k][1] = live ? __ldg(s32 + 4) : 0u;
                 }
             } else {
                 // dims (D/4) t .. + D/4 - 1: k-step k takes 4 of them.  f16 after an
@@ -424,40 +456,54 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, RG>::kThreads, Cfg<D, FP8, NT,
                 }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // the row times 2^(14 - e), e = exponent of its largest; in two factors, each a normal
                 const int e = top > 0.f && top < INFINITY ? ilogbf(top) : 14;
-                const int sh = min(14 - e, 126);  // a row below 2^-112 keeps its size
+                const int sh = min(14 - e, 126);  // a row below 2^-112 stays below 2^14
                 const float up = __int_as_float((127 + sh) << 23);
 #pragma unroll
                 for (int k = 0; k < KK; ++k) {
-                    qf[n][k][0] = pack_f16(v[4 * k] * up, v[4 * k + 1] * up);
-                    qf[n][k][1] = pack_f16(v[4 * k + 2] * up, v[4 * k + 3] * up);
+                    qf[k][0] = pack_f16(v[4 * k] * up, v[4 * k + 1] * up);
+                    qf[k][1] = pack_f16(v[4 * k + 2] * up, v[4 * k + 3] * up);
                 }
-                const float down = sh <= 126 && sh >= -126 ? __int_as_float((127 - sh) << 23) : 0.f;
-                qfac[n][0] = __shfl_sync(0xffffffffu, down, (2 * t) * 4) * a.scale_log2;
-                qfac[n][1] = __shfl_sync(0xffffffffu, down, (2 * t + 1) * 4) * a.scale_log2;
+                down = __int_as_float((127 - sh) << 23);
+            }
+        };
+        uint32_t qf[NQ][KK][2];
+        if (C::kQShared) {
+            if (ks < NT) {
+                float down;
+                fragments(ks, qf[0], down);
+#pragma unroll
+                for (int k = 0; k < KK; ++k)
+                    *reinterpret_cast<uint2*>(q_sh + (((k * (NT / 2) + (ks >> 1)) * 32 + lane) * 2 + (ks & 1)) * 8) =
+                        make_uint2(qf[0][k][0], qf[0][k][1]);
+                if (t == 0) fac_sh[ks * 8 + g] = down;
+            }
+        } else {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                float down;
+                fragments(n, qf[n], down);
+                if (ks == 0 && t == 0) fac_sh[n * 8 + g] = down;
             }
         }
-        // the columns' positions (rows 2t and 2t+1 of each 8-row tile); -2: not to be written
-        int cpos[NT][2];
+        bar_sync(1, 32 * KS);
+        int cpos[NQ][2];
+        float qfac[NQ][2];
         int minpos = 0x7FFFFFFF;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int tok = (p.row0 + (rg * NT + n) * 8 + 2 * t + c) / a.group;
-                int pos = -2;
-                if (tok < p.q.nq) {
-                    pos = __ldg(a.s.q_pos + p.q.q0 + tok);
-                    if (pos < -1 || pos >= p.q.ctx) {
-                        if (!p.front) report(a.d_status, DSA_ERR_BAD_INPUT);
-                        pos = -2;
-                    }
-                    minpos = min(minpos, pos);
-                }
-                cpos[n][c] = pos;
-            }
+        for (int r = lane; r < C::kRows; r += 32) {
+            const int pos = pos_sh[r];
+            if (pos >= -1) minpos = min(minpos, pos);
+        }
         minpos = __reduce_min_sync(0xffffffffu, minpos);
+        if (!C::kQShared) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    cpos[n][c] = pos_sh[n * 8 + 2 * t + c];
+                    qfac[n][c] = fac_sh[n * 8 + 2 * t + c] * a.scale_log2;
+                }
+        }
 
         float o[NT][KK][4];
         float m[NT][2], l[NT][2];
@@ -484,7 +530,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, RG>::kThreads, Cfg<D, FP8, NT,
                 for (int x = lane; x < 16 * (HB / 16); x += 32) {
                     const int row = r0 + x / (HB / 16), c = x % (HB / 16);
                     if (i * kTile + row >= p.limit)
-                        *reinterpret_cast<uint4*>(vrow + (chunk_addr<HB>(0u, row, c))) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4*>(vrow + (chunk_addr<HB, kTile>(0u, row, c))) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
@@ -493,36 +539,49 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, RG>::kThreads, Cfg<D, FP8, NT,
             float s[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-            float s2[NT][4];
+            // few tiles: two sums each, for shorter chains of products
+            constexpr int N2 = NT <= 2 ? NT : 1;
+            float s2[N2][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) s2[n][0] = s2[n][1] = s2[n][2] = s2[n][3] = 0.f;
+            for (int n = 0; n < N2; ++n) s2[n][0] = s2[n][1] = s2[n][2] = s2[n][3] = 0.f;
+            auto dot = [&](int k, const uint32_t (&af)[4]) {
+                if (C::kQShared) {
+#pragma unroll
+                    for (int n = 0; n < NT; n += 2) {
+                        uint32_t y[4];
+                        lds128(y, q_u + ((k * (NT / 2) + (n >> 1)) * 32 + lane) * 16);
+                        mma16816<FP8>(s[n], af, y[0], y[1]);
+                        if (n + 1 < NT) mma16816<FP8>(s[n + 1], af, y[2], y[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+                        mma16816<FP8>((k & 1) && N2 == NT ? s2[n < N2 ? n : 0] : s[n], af, qf[n][k][0], qf[n][k][1]);
+                }
+            };
             if (!FP8) {
 #pragma unroll
                 for (int k = 0; k < KK; ++k) {
                     uint32_t af[4];
-                    ldsm4(af, chunk_addr<HB>(kb, r0 + (lane & 15), 2 * k + (lane >> 4)));
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma16816<false>(k & 1 ? s2[n] : s[n], af, qf[n][k][0], qf[n][k][1]);
+                    ldsm4(af, chunk_addr<HB, kTile>(kb, r0 + (lane & 15), 2 * k + (lane >> 4)));
+                    dot(k, af);
                 }
             } else {
                 uint32_t x0[D / 16], x1[D / 16];  // rows g and g + 8: the thread's D / 4 dims
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
                     uint32_t y[4];
-                    lds128(y, chunk_addr<HB>(kb, r0 + g, (D / 64) * t + c));
+                    lds128(y, chunk_addr<HB, kTile>(kb, r0 + g, (D / 64) * t + c));
                     x0[4 * c] = y[0], x0[4 * c + 1] = y[1], x0[4 * c + 2] = y[2], x0[4 * c + 3] = y[3];
-                    lds128(y, chunk_addr<HB>(kb, r0 + g + 8, (D / 64) * t + c));
+                    lds128(y, chunk_addr<HB, kTile>(kb, r0 + g + 8, (D / 64) * t + c));
                     x1[4 * c] = y[0], x1[4 * c + 1] = y[1], x1[4 * c + 2] = y[2], x1[4 * c + 3] = y[3];
                 }
 #pragma unroll
                 for (int k = 0; k < KK; ++k) {
-                    const uint32_t af[4] = {e4m3x2_to_f16x2((uint16_t)x0[k]), e4m3x2_to_f16x2((uint16_t)x1[k]),
-                                            e4m3x2_to_f16x2((uint16_t)(x0[k] >> 16)),
-                                            e4m3x2_to_f16x2((uint16_t)(x1[k] >> 16))};
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma16816<true>(k & 1 ? s2[n] : s[n], af, qf[n][k][0], qf[n][k][1]);
+                    uint32_t af[4];
+                    e4m3x4_to_f16(x0[k], af[0], af[2]);
+                    e4m3x4_to_f16(x1[k], af[1], af[3]);
+                    dot(k, af);
                 }
             }
             // scores in log2 units, masked
@@ -539,12 +598,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, RG>::kThreads, Cfg<D, FP8, NT,
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float f = FP8 ? qfac[n][c] : a.scale_log2;
-                    float x0 = (s[n][c] + s2[n][c]) * (FP8 ? f * fk0 : f);
-                    float x1 = (s[n][2 + c] + s2[n][2 + c]) * (FP8 ? f * fk1 : f);
+                    float f = a.scale_log2;
+                    if (FP8) f = C::kQShared ? f * fac_sh[n * 8 + 2 * t + c] : qfac[n < NQ ? n : 0][c];
+                    float x0 = s[n][c], x1 = s[n][2 + c];
+                    if (N2 == NT) x0 += s2[n < N2 ? n : 0][c], x1 += s2[n < N2 ? n : 0][2 + c];
+                    x0 *= FP8 ? f * fk0 : f;
+                    x1 *= FP8 ? f * fk1 : f;
                     if (masked) {
-                        x0 = j0 + g <= cpos[n][c] ? x0 : -INFINITY;
-                        x1 = j0 + g + 8 <= cpos[n][c] ? x1 : -INFINITY;
+                        const int pos = C::kQShared ? pos_sh[n * 8 + 2 * t + c] : cpos[n < NQ ? n : 0][c];
+                        x0 = j0 + g <= pos ? x0 : -INFINITY;
+                        x1 = j0 + g + 8 <= pos ? x1 : -INFINITY;
                     }
                     s[n][c] = x0;
                     s[n][2 + c] = x1;
@@ -624,7 +687,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, RG>::kThreads, Cfg<D, FP8, NT,
 #pragma unroll
                 for (int k = 0; k < KK; ++k) {
                     uint32_t af[4];
-                    ldsm4t(af, chunk_addr<HB>(vb, r0 + ((lane >> 4) << 3) + (lane & 7), 2 * k + ((lane >> 3) & 1)));
+                    ldsm4t(af, chunk_addr<HB, kTile>(vb, r0 + ((lane >> 4) << 3) + (lane & 7), 2 * k + ((lane >> 3) & 1)));
 #pragma unroll
                     for (int n = 0; n < NT; ++n) mma16816<false>(o[n][k], af, pf[n][0], pf[n][1]);
                 }
@@ -637,35 +700,36 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, RG>::kThreads, Cfg<D, FP8, NT,
                     const int row = r0 + 2 * t + (c & 1) + ((c >> 1) << 3);
                     if (D == 128) {
                         uint32_t y[4];
-                        lds128(y, chunk_addr<HB>(vb, row, g));
+                        lds128(y, chunk_addr<HB, kTile>(vb, row, g));
 #pragma unroll
                         for (int e = 0; e < D / 32; ++e) x[c][e] = y[e];
                     } else {
                         uint32_t y[2];
-                        lds64(y, chunk_addr<HB>(vb, row, g >> 1) + ((g & 1) << 3));
+                        lds64(y, chunk_addr<HB, kTile>(vb, row, g >> 1) + ((g & 1) << 3));
 #pragma unroll
                         for (int e = 0; e < D / 32; ++e) x[c][e] = y[e];
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < KK; ++k) {
-                    uint32_t h[4];
+                for (int e = 0; e < KK / 2; ++e) {
+                    uint32_t h[2][4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        h[c] = e4m3x2_to_f16x2((uint16_t)(k & 1 ? x[c][k >> 1] >> 16 : x[c][k >> 1]));
-                    const uint32_t af[4] = {__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[0], h[1], 0x7632),
-                                            __byte_perm(h[2], h[3], 0x5410), __byte_perm(h[2], h[3], 0x7632)};
+                    for (int c = 0; c < 4; ++c) e4m3x4_to_f16(x[c][e], h[0][c], h[1][c]);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16816<true>(o[n][k], af, pf[n][0], pf[n][1]);
+                    for (int z = 0; z < 2; ++z) {
+                        const uint32_t af[4] = {
+                            __byte_perm(h[z][0], h[z][1], 0x5410), __byte_perm(h[z][0], h[z][1], 0x7632),
+                            __byte_perm(h[z][2], h[z][3], 0x5410), __byte_perm(h[z][2], h[z][3], 0x7632)};
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16816<true>(o[n][2 * e + z], af, pf[n][0], pf[n][1]);
+                    }
                 }
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(empty + st);
         }
 
-        // ---- the four key slices meet
-        float2* mlg = ml + rg * 4 * 8 * NT;  // [4][8 NT]
-        float* sc = scratch + rg * (4 * 8 * D);
+        // ---- the key slices meet
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -674,94 +738,92 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, RG>::kThreads, Cfg<D, FP8, NT,
                 x += __shfl_xor_sync(0xffffffffu, x, 4);
                 x += __shfl_xor_sync(0xffffffffu, x, 8);
                 x += __shfl_xor_sync(0xffffffffu, x, 16);
-                if (g == 0) mlg[ks * 8 * NT + n * 8 + 2 * t + c] = make_float2(m[n][c], x);
+                if (g == 0) ml[ks * C::kRows + n * 8 + 2 * t + c] = make_float2(m[n][c], x);
             }
-        bar_sync(1 + rg, 128);
-        const int x = threadIdx.x & 127;
-        const int hr = x >> 4;  // row of the 8 that this thread sums
+        bar_sync(1, 32 * KS);
+        constexpr int kDims = D / (4 * KS);  // dims per thread of the sum: 8 rows x 4 KS threads
+        const int hr = threadIdx.x / (4 * KS);
+        const int d0 = threadIdx.x % (4 * KS) * kDims;
         const bool cut = p.front || p.back;
         const int64_t slot = (int64_t)blockIdx.x * 2 + (p.front ? 0 : 1);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+            // [key slice][8 rows][D], the dims of rows 2t and 2t + 1 turned by 8 t: no bank conflicts.
+            // Eight slices: the upper four hand theirs to the lower four first.
+            auto place = [&](int c, int k, int y) {
+                const int d = FP8 ? (D / 8) * g + 2 * k + y : 16 * k + g + 8 * y;
+                return ((ks & 3) * 8 + 2 * t + c) * D + (d ^ (t << 3));
+            };
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int col = n * 8 + 2 * t + c;
-                float mm = mlg[col].x;
+                float mm = ml[col].x;
 #pragma unroll
-                for (int y = 1; y < 4; ++y) mm = fmaxf(mm, mlg[y * 8 * NT + col].x);
+                for (int y = 1; y < KS; ++y) mm = fmaxf(mm, ml[y * C::kRows + col].x);
                 const float f = (m[n][c] == -INFINITY ? 0.f : fast_exp2(m[n][c] - mm)) * (FP8 ? vref : 1.f);
-                // [key slice][8 rows][D], the dims of rows 2t and 2t + 1 turned by 8 t: no bank conflicts
-                float* dst = sc + (ks * 8 + 2 * t + c) * D;
 #pragma unroll
                 for (int k = 0; k < KK; ++k) {
-                    const int d0 = FP8 ? (D / 8) * g + 2 * k : 16 * k + g;
-                    const int d1 = FP8 ? d0 + 1 : d0 + 8;
-                    dst[d0 ^ (t << 3)] = o[n][k][c] * f;
-                    dst[d1 ^ (t << 3)] = o[n][k][2 + c] * f;
+                    o[n][k][c] *= f;
+                    o[n][k][2 + c] *= f;
+                    if (KS == 4 || ks >= 4) {
+                        scratch[place(c, k, 0)] = o[n][k][c];
+                        scratch[place(c, k, 1)] = o[n][k][2 + c];
+                    }
                 }
             }
-            bar_sync(1 + rg, 128);
-            {
-                const int col = n * 8 + hr;
-                float mm = mlg[col].x;
+            bar_sync(1, 32 * KS);
+            if (KS == 8) {
+                if (ks < 4)
 #pragma unroll
-                for (int y = 1; y < 4; ++y) mm = fmaxf(mm, mlg[y * 8 * NT + col].x);
-                float sum = 0.f;
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int k = 0; k < KK; ++k) {
+                            scratch[place(c, k, 0)] += o[n][k][c];
+                            scratch[place(c, k, 1)] += o[n][k][2 + c];
+                        }
+                bar_sync(1, 32 * KS);
+            }
+            const int r = n * 8 + hr;
+            float mm = ml[r].x;
+#pragma unroll
+            for (int y = 1; y < KS; ++y) mm = fmaxf(mm, ml[y * C::kRows + r].x);
+            float sum = 0.f;
+#pragma unroll
+            for (int y = 0; y < KS; ++y) {
+                const float2 v = ml[y * C::kRows + r];
+                sum += v.x == -INFINITY ? 0.f : v.y * fast_exp2(v.x - mm);
+            }
+            const int f = p.row0 + r;
+            const int tok = f / a.group, head = f - tok * a.group;
+            const bool write = ok && pos_sh[r] >= -1;
+            const int64_t at = (int64_t)(p.q.q0 + tok) * (a.hkv * a.group) + kvh * a.group + head;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int e = 0; e < kDims; e += 2) {
+                float2 v = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const float2 v = mlg[y * 8 * NT + col];
-                    sum += v.x == -INFINITY ? 0.f : v.y * fast_exp2(v.x - mm);
+                    const float2 z = *reinterpret_cast<const float2*>(scratch + (y * 8 + hr) * D +
+                                                                      ((d0 + e) ^ (((hr >> 1) & 3) << 3)));
+                    v.x += z.x, v.y += z.y;
                 }
-                float v[D / 16];
-                const int d0 = (x & 15) * (D / 16);
-#pragma unroll
-                for (int e = 0; e < D / 16; e += 4) {
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const float4 z = *reinterpret_cast<const float4*>(
-                            sc + (y * 8 + hr) * D + ((d0 + e) ^ (((hr >> 1) & 3) << 3)));
-                        acc.x += z.x, acc.y += z.y, acc.z += z.z, acc.w += z.w;
-                    }
-                    v[e] = acc.x, v[e + 1] = acc.y, v[e + 2] = acc.z, v[e + 3] = acc.w;
-                }
-                const int r = (rg * NT + n) * 8 + hr;
-                const int f = p.row0 + r;
-                const int tok = f / a.group, head = f - tok * a.group;
-                bool write = tok < p.q.nq && ok;
-                if (write) {
-                    const int pos = __ldg(a.s.q_pos + p.q.q0 + tok);
-                    write = pos >= -1 && pos < p.q.ctx;
-                }
-                if (cut) {
-                    float* dst = a.part_o + (slot * C::kRows + r) * D + d0;
-#pragma unroll
-                    for (int e = 0; e < D / 16; e += 4)
-                        *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                    // a sum of -1: a row that is not to be written
-                    if ((x & 15) == 0) a.part_ml[slot * C::kRows + r] = make_float2(mm, write ? sum : -1.f);
-                } else if (write) {
-                    const int64_t at = (int64_t)(p.q.q0 + tok) * (a.hkv * a.group) + kvh * a.group + head;
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * D + d0);
-                    if (D == 128)
-                        *reinterpret_cast<uint4*>(dst) =
-                            make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
-                                       pack_bf16(v[D / 16 - 4] * inv, v[D / 16 - 3] * inv),
-                                       pack_bf16(v[D / 16 - 2] * inv, v[D / 16 - 1] * inv));
-                    else
-                        *reinterpret_cast<uint2*>(dst) =
-                            make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
-                    if (a.lse && (x & 15) == 0) a.lse[at] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * kLn2;
-                }
+                if (cut)
+                    *reinterpret_cast<float2*>(a.part_o + (slot * C::kRows + r) * D + d0 + e) = v;
+                else if (write)
+                    *reinterpret_cast<uint32_t*>(a.out + at * D + d0 + e) = pack_bf16(v.x * inv, v.y * inv);
             }
-            bar_sync(1 + rg, 128);
+            if (d0 == 0) {
+                // a sum of -1: a row that is not to be written
+                if (cut) a.part_ml[slot * C::kRows + r] = make_float2(mm, write ? sum : -1.f);
+                else if (write && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * kLn2;
+            }
+            bar_sync(1, 32 * KS);
         }
         // the first CTA behind a cut tells the joining kernel what to join
         if (p.front) {
             const int64_t c = blockIdx.x / a.hl;
             const int64_t np = min((int64_t)a.parts, w.total);
-            const int64_t s0 = w.r0 - p.i0, s1 = s0 + tiles_of(p.q);
+            const int64_t s0 = w.r0 - p.i0, s1 = s0 + tiles_of<kTile>(p.q);
             if (s0 >= w.total * (c - 1) / np)
                 join = make_int4((int)((s1 * np - 1) / w.total - c + 2), p.q.q0, p.q.nq, p.lane);
         }
@@ -855,7 +917,7 @@ __global__ void __launch_bounds__(128) gqa_join_kernel(const __grid_constant__ A
 // ---------------------------------------------------------------------------
 // host side
 struct Plan {
-    int nt, rg, rows, chunks, lanes, hl, parts, grid;
+    int nt, tile, rows, chunks, lanes, hl, parts, grid;
     size_t o_bytes, ml_bytes, desc_bytes;
 };
 
@@ -865,16 +927,16 @@ Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s) {
     Plan p;
     const int group = sh.num_heads / sh.num_kv_heads;
     const int64_t rows = (int64_t)s.max_q_per_seq * group;
-    // 8, 16 or 32 query rows a chunk; more than 16 take a CTA of eight computing
-    // warps with an SM to itself (its accumulators need the registers)
-    p.nt = rows <= 8 ? 1 : 2;
-    p.rg = rows <= 16 ? 1 : 2;
-    p.rows = 8 * p.nt * p.rg;
+    // 8, 16 or 32 query rows a chunk; more than 8 take a CTA of eight computing
+    // warps with an SM to itself (their accumulators need the registers)
+    p.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    p.rows = 8 * p.nt;
+    p.tile = p.nt == 1 ? 64 : 128;
     p.chunks = (int)((rows + p.rows - 1) / p.rows);
     p.lanes = sh.num_kv_heads * p.chunks;
     // lanes side by side: a divisor of the lanes that leaves few CTAs idle, the
     // largest such (its lanes' rows are neighbours in memory)
-    const int n = kPlanSms * (p.rg == 1 ? 2 : 1);
+    const int n = kPlanSms * (p.nt == 1 ? 2 : 1);
     int best = 0;
     p.hl = 1;
     for (int d = 1; d <= p.lanes && d <= n; ++d)
@@ -883,7 +945,7 @@ Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s) {
             if (used * 32 >= best * 31) p.hl = d;
             best = std::max(best, used);
         }
-    const int64_t tiles = std::max<int64_t>(1, ((int64_t)s.max_ctx + kTile - 1) / kTile);
+    const int64_t tiles = std::max<int64_t>(1, ((int64_t)s.max_ctx + p.tile - 1) / p.tile);
     p.parts = (int)std::min<int64_t>(n / p.hl, (int64_t)(p.lanes / p.hl) * s.num_seqs * tiles);
     p.grid = p.parts * p.hl;
     const size_t slots = (size_t)2 * p.grid;
@@ -893,10 +955,10 @@ Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s) {
     return p;
 }
 
-template <int D, bool FP8, int NT, int RG>
+template <int D, bool FP8, int NT, int KS>
 cudaError_t launch_one(const CUtensorMap& km, const CUtensorMap& vm, const Args& a, int grid, cudaStream_t stream) {
-    using C = Cfg<D, FP8, NT, RG>;
-    auto kern = gqa_decode_kernel<D, FP8, NT, RG>;
+    using C = Cfg<D, FP8, NT, KS>;
+    auto kern = gqa_decode_kernel<D, FP8, NT, KS>;
     // per device: the attribute belongs to the current device's copy of the kernel
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
@@ -915,11 +977,11 @@ cudaError_t launch_decode(const dsa_gqa_shape& sh, const void* q, const void* k,
                           void* workspace, int32_t* d_status, cudaStream_t stream) {
     const Plan p = make_plan(sh, s);
     const bool fp8 = sh.kv_dtype == DSA_FP8_E4M3_ROWSCALE;
-    const int box = s.page_table ? std::min(s.page_size, kTile) : kTile;
+    const int box = s.page_table ? std::min(s.page_size, p.tile) : p.tile;
     CUtensorMap km, vm;
-    cudaError_t e = cache_map(&km, fp8, k, sh.num_kv_heads, sh.head_dim, sh.k_stride, s.num_rows, box, box == kTile);
+    cudaError_t e = cache_map(&km, fp8, k, sh.num_kv_heads, sh.head_dim, sh.k_stride, s.num_rows, box, box == p.tile);
     if (e == cudaSuccess)
-        e = cache_map(&vm, fp8, v, sh.num_kv_heads, sh.head_dim, sh.v_stride, s.num_rows, box, box == kTile);
+        e = cache_map(&vm, fp8, v, sh.num_kv_heads, sh.head_dim, sh.v_stride, s.num_rows, box, box == p.tile);
     if (e != cudaSuccess) return e;
     Args a;
     a.q = static_cast<const __nv_bfloat16*>(q);
@@ -944,9 +1006,9 @@ cudaError_t launch_decode(const dsa_gqa_shape& sh, const void* q, const void* k,
     auto by_rows = [&](auto d, auto f8) {
         constexpr int D = decltype(d)::value;
         constexpr bool F = decltype(f8)::value;
-        if (p.rg == 2) return launch_one<D, F, 2, 2>(km, vm, a, p.grid, stream);
-        return p.nt == 2 ? launch_one<D, F, 2, 1>(km, vm, a, p.grid, stream)
-                         : launch_one<D, F, 1, 1>(km, vm, a, p.grid, stream);
+        return p.nt == 4   ? launch_one<D, F, 4, 8>(km, vm, a, p.grid, stream)
+               : p.nt == 2 ? launch_one<D, F, 2, 8>(km, vm, a, p.grid, stream)
+                           : launch_one<D, F, 1, 4>(km, vm, a, p.grid, stream);
     };
     using std::integral_constant;
     if (sh.head_dim == 64)
