@@ -47,6 +47,47 @@ inline cudaError_t cache_map(CUtensorMap* m, bool bytes, const void* base, int h
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// two fp32 values in one register pair, and arithmetic on both at once
+__device__ __forceinline__ uint64_t f32x2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// A place in the ring of N stages: the stage and the parity of its use.  (A
+// 64-bit remainder for every stage held the issuing thread for longer than a
+// step's products take.)
+template <int N>
+struct Cursor {
+    int st = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void move(int by) {
+        st += by;
+        if (st >= N) {
+            st -= N;
+            ph ^= 1u;
+        }
+    }
+};
+
 // A warpgroup's registers per thread, from those that the CTA was launched with
 template <int N>
 __device__ __forceinline__ void reg_inc() {

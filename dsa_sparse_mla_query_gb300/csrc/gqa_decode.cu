@@ -36,6 +36,7 @@ namespace {
 constexpr int kTagDecode = 6;
 constexpr float kLazy = 8.f;  // a row's reference moves when its maximum passes it by 2^8
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNone = -3e38f;  // the reference of a row that has seen no key (its sum is 0)
 
 // NT: 8-row tiles of query rows; KS: computing warps, 16 keys of a tile each
 template <int D, bool FP8, int NT, int KS>
@@ -316,7 +317,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
         const int R = a.s.page_table ? min(a.s.page_size, kTile) : kTile;  // rows per box
         const int nbox = kTile / R;
         const int shift = 31 - __clz(R);
-        int it = 0;
+        Cursor<C::kStages> c;
+        bool lap = false;  // every stage has been used
         bool ok = true;
         while (ok && w.next(a, p)) {
             const int kvh = p.lane % a.hkv;
@@ -338,18 +340,20 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
             };
             int w0 = p.i0 * nbox;
             int cur = p.i0 < end ? row_of(w0 + lane) : -1, nxt = p.i0 < end ? row_of(w0 + 32 + lane) : -1;
-            for (int i = p.i0; i < end && ok; ++i, ++it) {
-                const int st = it % C::kStages;
+            for (int i = p.i0; i < end && ok; ++i) {
+                const int st = c.st;
                 if (i * nbox >= w0 + 32) {
                     w0 += 32;
                     cur = nxt;
                     nxt = row_of(w0 + 32 + lane);
                 }
-                if (it >= C::kStages) {
-                    ok = ptx::mbar_wait(empty + st, (it / C::kStages - 1) & 1, abort_flag, a.d_status);
+                if (lap) {
+                    ok = ptx::mbar_wait(empty + st, c.ph ^ 1u, abort_flag, a.d_status);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                 }
+                c.move(1);
+                lap = lap || c.st == 0;
                 uint8_t* kd = ring + st * C::kStage;
                 uint8_t* vd = kd + C::kHalf;
                 const int l = i * nbox - w0;  // window lane of the tile's first box
@@ -388,8 +392,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
         }
         if (!ok) {
             // after an abort: let the copies in flight land before the CTA ends
-            for (int k = max(0, it - C::kStages); k < it; ++k)
-                ptx::mbar_drain(full + k % C::kStages, (k / C::kStages) & 1);
+            for (int st = 0; st < C::kStages; ++st)
+                if (lap || st < c.st) ptx::mbar_drain(full + st, st < c.st ? c.ph : c.ph ^ 1u);
         }
         return;
     }
@@ -402,7 +406,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
     constexpr int KK = D / 16;  // k-steps of q.k, and 16-dim tiles of the output
     constexpr int NQ = C::kQShared ? 1 : NT;
     const uint32_t ring_u = smem_u32(ring), q_u = smem_u32(q_sh);
-    int it = 0;
+    Cursor<C::kStages> c;
     bool ok = true;
     int4 join = make_int4(0, 0, 0, 0);
     while (w.next(a, p)) {
@@ -501,36 +505,36 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     cpos[n][c] = pos_sh[n * 8 + 2 * t + c];
-                    qfac[n][c] = fac_sh[n * 8 + 2 * t + c] * a.scale_log2;
+                    qfac[n][c] = fac_sh[n * 8 + 2 * t + c];
                 }
         }
 
         float o[NT][KK][4];
-        float m[NT][2], l[NT][2];
+        float m[NT][2];  // references: far below any score until a key is seen
+        uint64_t l[NT];  // sums of the weights, a pair of columns
         float vref = 0x1p-126f, vinv = 0x1p126f;  // FP8: V scales are held relative to vref, a power of two
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            m[n][0] = m[n][1] = -INFINITY;
-            l[n][0] = l[n][1] = 0.f;
+            m[n][0] = m[n][1] = kNone;
+            l[n] = 0ull;
 #pragma unroll
             for (int k = 0; k < KK; ++k) o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
         }
 
-        for (int i = p.i0; i < end; ++i, ++it) {
-            const int st = it % C::kStages;
-            ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(full + st, (it / C::kStages) & 1, abort_flag, a.d_status));
+        for (int i = p.i0; i < end; ++i, c.move(1)) {
+            ok = ok && __all_sync(0xffffffffu, quick_wait(full + c.st, c.ph, abort_flag, a.d_status));
             if (!ok) continue;  // keep to the walk, so that the slices still meet at its barriers
-            const uint32_t kb = ring_u + st * C::kStage, vb = kb + C::kHalf;
+            const uint32_t kb = ring_u + c.st * C::kStage, vb = kb + C::kHalf;
             const int r0 = ks * 16;                // this warp's first key within the tile
             const int j0 = i * kTile + r0;         // and its position
             const bool edge = j0 + 16 > p.limit;   // rows past the last key that is seen
             if (edge) {
                 // whatever lies there must not reach the products: its weights are 0, but 0 * inf is not
-                uint8_t* vrow = ring + st * C::kStage + C::kHalf;
+                uint8_t* vrow = ring + c.st * C::kStage + C::kHalf;
                 for (int x = lane; x < 16 * (HB / 16); x += 32) {
-                    const int row = r0 + x / (HB / 16), c = x % (HB / 16);
+                    const int row = r0 + x / (HB / 16), ch = x % (HB / 16);
                     if (i * kTile + row >= p.limit)
-                        *reinterpret_cast<uint4*>(vrow + (chunk_addr<HB, kTile>(0u, row, c))) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4*>(vrow + (chunk_addr<HB, kTile>(0u, row, ch))) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
@@ -569,12 +573,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
             } else {
                 uint32_t x0[D / 16], x1[D / 16];  // rows g and g + 8: the thread's D / 4 dims
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
+                for (int e = 0; e < D / 64; ++e) {
                     uint32_t y[4];
-                    lds128(y, chunk_addr<HB, kTile>(kb, r0 + g, (D / 64) * t + c));
-                    x0[4 * c] = y[0], x0[4 * c + 1] = y[1], x0[4 * c + 2] = y[2], x0[4 * c + 3] = y[3];
-                    lds128(y, chunk_addr<HB, kTile>(kb, r0 + g + 8, (D / 64) * t + c));
-                    x1[4 * c] = y[0], x1[4 * c + 1] = y[1], x1[4 * c + 2] = y[2], x1[4 * c + 3] = y[3];
+                    lds128(y, chunk_addr<HB, kTile>(kb, r0 + g, (D / 64) * t + e));
+                    x0[4 * e] = y[0], x0[4 * e + 1] = y[1], x0[4 * e + 2] = y[2], x0[4 * e + 3] = y[3];
+                    lds128(y, chunk_addr<HB, kTile>(kb, r0 + g + 8, (D / 64) * t + e));
+                    x1[4 * e] = y[0], x1[4 * e + 1] = y[1], x1[4 * e + 2] = y[2], x1[4 * e + 3] = y[3];
                 }
 #pragma unroll
                 for (int k = 0; k < KK; ++k) {
@@ -584,56 +588,50 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                     dot(k, af);
                 }
             }
-            // scores in log2 units, masked
+            // scores in log2 units, masked: pairs of columns, keys g and g + 8
             float fk0 = 1.f, fk1 = 1.f, fv0 = 1.f, fv1 = 1.f;
             if (FP8) {
-                const float* sd = ring_scale + st * (C::kScaleBytes / 4);
-                fk0 = sd[r0 + g], fk1 = sd[r0 + g + 8];
+                const float* sd = ring_scale + c.st * (C::kScaleBytes / 4);
+                fk0 = sd[r0 + g] * a.scale_log2, fk1 = sd[r0 + g + 8] * a.scale_log2;
                 fv0 = j0 + g < p.limit ? sd[kTile + r0 + g] : 0.f;
                 fv1 = j0 + g + 8 < p.limit ? sd[kTile + r0 + g + 8] : 0.f;
             }
+            const uint64_t k0 = f32x2(FP8 ? fk0 : a.scale_log2, FP8 ? fk0 : a.scale_log2);
+            const uint64_t k1 = f32x2(FP8 ? fk1 : a.scale_log2, FP8 ? fk1 : a.scale_log2);
             const bool masked = j0 + 15 > minpos;
-            float mx[NT][2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float f = a.scale_log2;
-                    if (FP8) f = C::kQShared ? f * fac_sh[n * 8 + 2 * t + c] : qfac[n < NQ ? n : 0][c];
-                    float x0 = s[n][c], x1 = s[n][2 + c];
-                    if (N2 == NT) x0 += s2[n < N2 ? n : 0][c], x1 += s2[n < N2 ? n : 0][2 + c];
-                    x0 *= FP8 ? f * fk0 : f;
-                    x1 *= FP8 ? f * fk1 : f;
-                    if (masked) {
-                        const int pos = C::kQShared ? pos_sh[n * 8 + 2 * t + c] : cpos[n < NQ ? n : 0][c];
-                        x0 = j0 + g <= pos ? x0 : -INFINITY;
-                        x1 = j0 + g + 8 <= pos ? x1 : -INFINITY;
-                    }
-                    s[n][c] = x0;
-                    s[n][2 + c] = x1;
-                    mx[n][c] = fmaxf(x0, x1);
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    mx[n][c] = fmaxf(mx[n][c], __shfl_xor_sync(0xffffffffu, mx[n][c], 4));
-                    mx[n][c] = fmaxf(mx[n][c], __shfl_xor_sync(0xffffffffu, mx[n][c], 8));
-                    mx[n][c] = fmaxf(mx[n][c], __shfl_xor_sync(0xffffffffu, mx[n][c], 16));
-                }
             bool move = false;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) move = move || mx[n][0] > m[n][0] + kLazy || mx[n][1] > m[n][1] + kLazy;
-            float vtop = 0.f;
-            if (FP8) {
-                vtop = fmaxf(fv0, fv1);
-                move = move || vtop > vref;
+            for (int n = 0; n < NT; ++n) {
+                uint64_t x0 = f32x2(s[n][0], s[n][1]), x1 = f32x2(s[n][2], s[n][3]);
+                if (N2 == NT) {
+                    x0 = add2(x0, f32x2(s2[n < N2 ? n : 0][0], s2[n < N2 ? n : 0][1]));
+                    x1 = add2(x1, f32x2(s2[n < N2 ? n : 0][2], s2[n < N2 ? n : 0][3]));
+                }
+                if (FP8) {
+                    const uint64_t f = C::kQShared ? *reinterpret_cast<const uint64_t*>(fac_sh + n * 8 + 2 * t)
+                                                   : f32x2(qfac[n < NQ ? n : 0][0], qfac[n < NQ ? n : 0][1]);
+                    x0 = mul2(x0, f);
+                    x1 = mul2(x1, f);
+                }
+                unpack2(mul2(x0, k0), s[n][0], s[n][1]);
+                unpack2(mul2(x1, k1), s[n][2], s[n][3]);
+                if (masked) {
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const int pos = C::kQShared ? pos_sh[n * 8 + 2 * t + z] : cpos[n < NQ ? n : 0][z];
+                        s[n][z] = j0 + g <= pos ? s[n][z] : -INFINITY;
+                        s[n][2 + z] = j0 + g + 8 <= pos ? s[n][2 + z] : -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int z = 0; z < 2; ++z) move = move || fmaxf(s[n][z], s[n][2 + z]) > m[n][z] + kLazy;
             }
+            if (FP8) move = move || fmaxf(fv0, fv1) > vref;
             if (__any_sync(0xffffffffu, move)) {
+                // rare: the rows' maxima over the slice's keys, and everything relative to them
                 float fv = 1.f;
                 if (FP8) {
-                    vtop = warp_max_all(vtop);
+                    const float vtop = warp_max_all(fmaxf(fv0, fv1));
                     if (vtop > vref) {
                         // the next power of two (the largest finite one for an infinite scale)
                         const float nref = __uint_as_float(
@@ -647,41 +645,44 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                 for (int n = 0; n < NT; ++n) {
                     float al[2];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float mn = fmaxf(m[n][c], mx[n][c]);
-                        al[c] = mn == m[n][c] ? 1.f : fast_exp2(m[n][c] - mn);
-                        m[n][c] = mn;
-                        l[n][c] *= al[c];
-                        al[c] *= fv;
+                    for (int z = 0; z < 2; ++z) {
+                        float mx = fmaxf(s[n][z], s[n][2 + z]);
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        const float mn = fmaxf(m[n][z], mx);
+                        al[z] = mn == m[n][z] ? 1.f : fast_exp2(m[n][z] - mn);
+                        m[n][z] = mn;
                     }
+                    l[n] = mul2(l[n], f32x2(al[0], al[1]));
 #pragma unroll
                     for (int k = 0; k < KK; ++k) {
-                        o[n][k][0] *= al[0];
-                        o[n][k][1] *= al[1];
-                        o[n][k][2] *= al[0];
-                        o[n][k][3] *= al[1];
+                        o[n][k][0] *= al[0] * fv;
+                        o[n][k][1] *= al[1] * fv;
+                        o[n][k][2] *= al[0] * fv;
+                        o[n][k][3] *= al[1] * fv;
                     }
                 }
             }
             // weights, as the B operand of O^T = V^T P^T (two 8x8 transposes per tile)
+            const uint64_t v0 = f32x2(fv0 * vinv, fv0 * vinv), v1 = f32x2(fv1 * vinv, fv1 * vinv);
             uint32_t pf[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float w0[2], w1[2];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float mm = m[n][c] == -INFINITY ? 0.f : m[n][c];
-                    w0[c] = fast_exp2(s[n][c] - mm);
-                    w1[c] = fast_exp2(s[n][2 + c] - mm);
-                    l[n][c] += w0[c] + w1[c];
-                    if (FP8) {
-                        w0[c] *= fv0 * vinv;
-                        w1[c] *= fv1 * vinv;
-                    }
+                const float w00 = fast_exp2(s[n][0] - m[n][0]), w01 = fast_exp2(s[n][1] - m[n][1]);
+                const float w10 = fast_exp2(s[n][2] - m[n][0]), w11 = fast_exp2(s[n][3] - m[n][1]);
+                uint64_t w0 = f32x2(w00, w01), w1 = f32x2(w10, w11);
+                l[n] = add2(l[n], add2(w0, w1));
+                if (FP8) {
+                    w0 = mul2(w0, v0);
+                    w1 = mul2(w1, v1);
                 }
+                float x, y, u, v;
+                unpack2(w0, x, y);
+                unpack2(w1, u, v);
                 // bf16 rounds a weight by up to 2^-9 of itself, f16 by 2^-12 (or 2^-25 of the largest)
-                pf[n][0] = movm_t(FP8 ? pack_f16(w0[0], w0[1]) : pack_bf16(w0[0], w0[1]));
-                pf[n][1] = movm_t(FP8 ? pack_f16(w1[0], w1[1]) : pack_bf16(w1[0], w1[1]));
+                pf[n][0] = movm_t(FP8 ? pack_f16(x, y) : pack_bf16(x, y));
+                pf[n][1] = movm_t(FP8 ? pack_f16(u, v) : pack_bf16(u, v));
             }
             if (!FP8) {
 #pragma unroll
@@ -696,50 +697,51 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                 // tile takes two of them: rows g and g + 8 of tile k are dims (D/8) g + 2k, + 1
                 uint32_t x[4][D / 32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int row = r0 + 2 * t + (c & 1) + ((c >> 1) << 3);
+                for (int z = 0; z < 4; ++z) {
+                    const int row = r0 + 2 * t + (z & 1) + ((z >> 1) << 3);
                     if (D == 128) {
                         uint32_t y[4];
                         lds128(y, chunk_addr<HB, kTile>(vb, row, g));
 #pragma unroll
-                        for (int e = 0; e < D / 32; ++e) x[c][e] = y[e];
+                        for (int e = 0; e < D / 32; ++e) x[z][e] = y[e];
                     } else {
                         uint32_t y[2];
                         lds64(y, chunk_addr<HB, kTile>(vb, row, g >> 1) + ((g & 1) << 3));
 #pragma unroll
-                        for (int e = 0; e < D / 32; ++e) x[c][e] = y[e];
+                        for (int e = 0; e < D / 32; ++e) x[z][e] = y[e];
                     }
                 }
 #pragma unroll
                 for (int e = 0; e < KK / 2; ++e) {
-                    uint32_t h[2][4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) e4m3x4_to_f16(x[c][e], h[0][c], h[1][c]);
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
-                        const uint32_t af[4] = {
-                            __byte_perm(h[z][0], h[z][1], 0x5410), __byte_perm(h[z][0], h[z][1], 0x7632),
-                            __byte_perm(h[z][2], h[z][3], 0x5410), __byte_perm(h[z][2], h[z][3], 0x7632)};
+                        // a dim's codes of two keys side by side, then both converted at once
+                        uint32_t af[4];
+                        const uint32_t pick = z ? 0x7362 : 0x5140;
+                        e4m3x4_to_f16(__byte_perm(x[0][e], x[1][e], pick), af[0], af[1]);
+                        e4m3x4_to_f16(__byte_perm(x[2][e], x[3][e], pick), af[2], af[3]);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) mma16816<true>(o[n][2 * e + z], af, pf[n][0], pf[n][1]);
                     }
                 }
             }
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(empty + st);
+            if (lane == 0) ptx::mbar_arrive(empty + c.st);
         }
 
         // ---- the key slices meet
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+            float x[2];
+            unpack2(l[n], x[0], x[1]);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float x = l[n][c];
-                x += __shfl_xor_sync(0xffffffffu, x, 4);
-                x += __shfl_xor_sync(0xffffffffu, x, 8);
-                x += __shfl_xor_sync(0xffffffffu, x, 16);
-                if (g == 0) ml[ks * C::kRows + n * 8 + 2 * t + c] = make_float2(m[n][c], x);
+            for (int z = 0; z < 2; ++z) {
+                x[z] += __shfl_xor_sync(0xffffffffu, x[z], 4);
+                x[z] += __shfl_xor_sync(0xffffffffu, x[z], 8);
+                x[z] += __shfl_xor_sync(0xffffffffu, x[z], 16);
+                if (g == 0) ml[ks * C::kRows + n * 8 + 2 * t + z] = make_float2(m[n][z], x[z]);
             }
+        }
         bar_sync(1, 32 * KS);
         constexpr int kDims = D / (4 * KS);  // dims per thread of the sum: 8 rows x 4 KS threads
         const int hr = threadIdx.x / (4 * KS);
@@ -760,7 +762,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                 float mm = ml[col].x;
 #pragma unroll
                 for (int y = 1; y < KS; ++y) mm = fmaxf(mm, ml[y * C::kRows + col].x);
-                const float f = (m[n][c] == -INFINITY ? 0.f : fast_exp2(m[n][c] - mm)) * (FP8 ? vref : 1.f);
+                const float f = fast_exp2(m[n][c] - mm) * (FP8 ? vref : 1.f);
 #pragma unroll
                 for (int k = 0; k < KK; ++k) {
                     o[n][k][c] *= f;
@@ -791,7 +793,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
 #pragma unroll
             for (int y = 0; y < KS; ++y) {
                 const float2 v = ml[y * C::kRows + r];
-                sum += v.x == -INFINITY ? 0.f : v.y * fast_exp2(v.x - mm);
+                sum = fmaf(v.y, fast_exp2(v.x - mm), sum);
             }
             const int f = p.row0 + r;
             const int tok = f / a.group, head = f - tok * a.group;
@@ -852,13 +854,13 @@ __global__ void __launch_bounds__(128) gqa_join_kernel(const __grid_constant__ A
     auto slot = [&](int i) -> int64_t {
         return ((int64_t)blockIdx.x + (int64_t)(i - 1) * a.hl) * 2 + (i == 0 ? 1 : 0);
     };
-    float top = -INFINITY;
+    float top = kNone;
     bool skip = false;
     float2 v[(kJoinParts + 127) / 128];
 #pragma unroll
     for (int k = 0; k < (kJoinParts + 127) / 128; ++k) {
         const int i = k * 128 + threadIdx.x;
-        v[k] = i < n ? a.part_ml[slot(i) * rows + r] : make_float2(-INFINITY, 0.f);
+        v[k] = i < n ? a.part_ml[slot(i) * rows + r] : make_float2(kNone, 0.f);
         skip = skip || v[k].y == -1.f;
         top = fmaxf(top, v[k].x);
     }
@@ -871,7 +873,7 @@ __global__ void __launch_bounds__(128) gqa_join_kernel(const __grid_constant__ A
 #pragma unroll
     for (int k = 0; k < (kJoinParts + 127) / 128; ++k) {
         const int i = k * 128 + threadIdx.x;
-        const float w = v[k].x == -INFINITY ? 0.f : fast_exp2(v[k].x - top);
+        const float w = fast_exp2(v[k].x - top);
         if (i < n) weight[i] = w;
         sum = fmaf(w, v[k].y, sum);
     }

@@ -72,24 +72,6 @@ struct Args {
     int32_t num_q, group, hkv, tpt;  // tpt: tokens per tile
 };
 
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 // Shared-memory matrix descriptors as a low word, which holds the address and
 // the leading stride, and the high word they share (8-row groups 1024 bytes
 // apart, 128-byte swizzle)
@@ -105,22 +87,6 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n" : "=r"(one));
     return one != 0;
 }
-
-// A place in the ring of N stages: the stage and the parity of its use.  (A
-// 64-bit remainder for every stage held the issuing thread for longer than a
-// step's products take.)
-template <int N>
-struct Cursor {
-    int st = 0;
-    uint32_t ph = 0;
-    __device__ __forceinline__ void move(int by) {
-        st += by;
-        if (st >= N) {
-            st -= N;
-            ph ^= 1u;
-        }
-    }
-};
 
 // Walks the items of this CTA, longest first: item y of the order is the one
 // with the y-th largest level, level = item index within the sequence plus the
@@ -550,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item it;
         uint32_t no = 0, o_use = 0;  // steps so far (buffer no & 1), outputs
         bool ok = true;
-        const uint64_t sc2 = pack2(a.scale_log2, a.scale_log2);
+        const uint64_t sc2 = f32x2(a.scale_log2, a.scale_log2);
         while (ok && next_item(it)) {
             const int t = x * a.tpt + tok;  // token within the item
             if (x == 1 && it.ntok <= a.tpt) continue;
@@ -599,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float mn = move ? top : m;
                     const float al = move ? fast_exp2(m - mn) : 1.f;
                     m = mn;
-                    const uint64_t al2 = pack2(al, al);
+                    const uint64_t al2 = f32x2(al, al);
                     l2[0] = fma2(l2[0], al2, 0ull);
                     l2[1] = fma2(l2[1], al2, 0ull);
                     if (j > 0) {
@@ -619,19 +585,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float mm = m == -INFINITY ? 0.f : -m;
-                const uint64_t nm2 = pack2(mm, mm);
+                const uint64_t nm2 = f32x2(mm, mm);
                 uint32_t pk[32];
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         const uint64_t v =
-                            fma2(pack2(__uint_as_float(s[k][e]), __uint_as_float(s[k][e + 1])), sc2, nm2);
+                            fma2(f32x2(__uint_as_float(s[k][e]), __uint_as_float(s[k][e + 1])), sc2, nm2);
                         float p0, p1;
                         unpack2(v, p0, p1);
                         p0 = fast_exp2(p0);
                         p1 = fast_exp2(p1);
-                        l2[(e >> 1) & 1] = add2(l2[(e >> 1) & 1], pack2(p0, p1));
+                        l2[(e >> 1) & 1] = add2(l2[(e >> 1) & 1], f32x2(p0, p1));
                         // a weight rounded to bf16 is off by up to 2^-9 of itself; the sum keeps fp32
                         pk[16 * k + e / 2] = pack_bf16(p0, p1);
                     }
