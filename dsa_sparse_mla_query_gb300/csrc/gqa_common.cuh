@@ -2,6 +2,8 @@
 // (gqa_decode.cu, gqa_prefill.cu): the workspace plan and the tensor maps.
 #pragma once
 
+#include <atomic>
+
 #include "indexer_common.cuh"
 
 namespace dsa {
@@ -116,6 +118,24 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
         : "memory");
 }
+
+// A kernel's attributes, set once on each device that launches it (they belong
+// to the device's own copy of the kernel, and setting them takes longer than
+// the rest of a launch's preparation).
+struct OncePerDevice {
+    std::atomic<uint64_t> done{0};
+    template <typename F>
+    cudaError_t run(F set) {
+        int dev = 0;
+        const cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+        if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+        const cudaError_t r = set();
+        if (r == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+        return r;
+    }
+};
 
 }  // namespace gqa
 }  // namespace dsa

@@ -674,7 +674,9 @@ template <int D>
 cudaError_t launch_one(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const Args& a, int grid,
                        cudaStream_t stream) {
     auto kern = gqa_prefill_kernel<D>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+    static OncePerDevice once;
+    const cudaError_t e = once.run(
+        [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem); });
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, stream, 1, qm, km, vm, a);
 }

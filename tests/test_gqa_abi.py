@@ -6,12 +6,15 @@ from __future__ import annotations
 import ctypes
 
 import pytest
+import torch
 
 from dsa_sparse_mla_query_gb300 import _binding as B
 
 
 @pytest.fixture(scope="module")
 def lib():
+    if torch.cuda.is_available():
+        pytest.skip("host-only checks: with a GPU a call that is not refused would launch on the made-up pointers")
     from dsa_sparse_mla_query_gb300 import build
     build.build()
     return B.load()
@@ -73,12 +76,15 @@ def test_pointers_sizes_and_workspace(lib, name):
     assert rc == B.DSA_ERR_UNSUPPORTED and "num_rows" in msg
     rc, msg = _attend(lib, name, seqs=_seqs(page_table=0x5000, page_size=48, max_pages=4))
     assert rc == B.DSA_ERR_UNSUPPORTED and "page_size 48" in msg
-    s, shape, n = _seqs(), B.GqaShape(16, 2, 128), ctypes.c_size_t()
-    assert lib.dense_gqa_workspace_size(ctypes.byref(shape), ctypes.byref(s), 2, ctypes.byref(n)) == 0
-    rc, msg = _attend(lib, name, ws_bytes=n.value - 1)
+    s, shape, n = _seqs(num_seqs=500), B.GqaShape(16, 2, 128), ctypes.c_size_t()  # more than clusters take
+    assert lib.dense_gqa_workspace_size(ctypes.byref(shape), ctypes.byref(s), 500, ctypes.byref(n)) == 0
+    assert n.value > 0
+    rc, msg = _attend(lib, name, seqs=s, num_q=500, ws_bytes=n.value - 1)
     assert rc == B.DSA_ERR_WORKSPACE and f"needs {n.value}" in msg
-    rc, msg = _attend(lib, name, ws=0x10010)
+    rc, msg = _attend(lib, name, seqs=s, num_q=500, ws=0x10010)
     assert rc == B.DSA_ERR_WORKSPACE and "256-byte aligned" in msg
+    rc, msg = _attend(lib, name, seqs=s, num_q=500, ws=None)
+    assert rc == B.DSA_ERR_WORKSPACE and "workspace is NULL" in msg
     assert _attend(lib, name, num_q=0)[0] == 0
     assert _attend(lib, name, num_q=-1)[0] == B.DSA_ERR_INVALID_ARG
 
