@@ -1111,21 +1111,27 @@ Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s) {
     const int64_t tiles = std::max<int64_t>(1, ((int64_t)s.max_ctx + p.tile - 1) / p.tile);
     p.parts = (int)std::min<int64_t>(n / p.hl, (int64_t)(p.lanes / p.hl) * s.num_seqs * tiles);
     p.grid = p.parts * p.hl;
-    // Clusters where all (lane, sequence)s fit at once and the longest sequence's
-    // CTAs take few more tiles than an even deal's would: what the joining kernel
-    // costs is worth about 10 tiles of a CTA, 8 of e4m3.  (64/8 heads of 128, one
-    // token each: 1 x 4,096 bf16 4 tiles against 2, 12.6 us against 14.8, launch
-    // included; 1 x 16,384 16 against 7, 21.0 against 24.6, e4m3 20.7 against 18.8;
-    // 32 x up to 1,000 16 against 14, 20.8 against 29.4; 4 x 8,000 32 against 14,
-    // the other way 33.3 against 29.1.)  Larger clusters leave room: their CTAs
-    // have to find place in one part of the GPU.
+    // Clusters where all (lane, sequence)s fit at once and an estimate from the
+    // longest sequence says that they are faster: a CTA takes at least tile_ns a
+    // tile (latency), all together no less than the bytes at 6.8 TB/s, and the
+    // joining kernel join_ns.  Larger clusters leave room: their CTAs have to
+    // find place in one part of the GPU.  Clusters against the joining kernel,
+    // launch included (64/8 heads of 128, one token, bf16 where not said):
+    // 1 x 4,096 12.6 us and 14.8; 1 x 32,768 31.0 and 34.6; 8 x 8,000 46.7 and
+    // 52.2, e4m3 32.3 and 41.4; 32 x up to 1,000 20.8 and 29.4; 2 x 4,000 with four
+    // tokens, e4m3, 28.9 and 39.3; and where the estimate chooses the other:
+    // 3 x 30,000 70.8 and 66.7, 3 x up to 9,000 with 32/8 heads of 64 18.7 and 15.1.
     p.cluster = 0;
     const int64_t segs = (int64_t)p.lanes * s.num_seqs;
     if (segs <= n) {
         int c = 1;
         auto room = [&](int size) { return size >= 16 ? n / 2 : size >= 8 ? n * 5 / 8 : n * 7 / 8; };
         while (c < kMaxCluster && segs * 2 * c <= room(2 * c) && 2 * c <= tiles) c *= 2;
-        if ((tiles + c - 1) / c <= segs * tiles / n + (sh.kv_dtype == DSA_BF16 ? 10 : 8)) {
+        const int64_t tile_ns = p.tile == 64 ? 600 : 1200, join_ns = p.nt == 1 ? 4000 : p.nt == 2 ? 6000 : 8000;
+        const int64_t bytes = (int64_t)2 * p.tile * sh.head_dim * (sh.kv_dtype == DSA_BF16 ? 2 : 1);
+        const int64_t with = (tiles + c - 1) / c * std::max(tile_ns, segs * c * bytes / 6800);
+        const int64_t without = std::max(segs * tiles * bytes / 6800, segs * tiles * tile_ns / n) + join_ns;
+        if (with <= without) {
             p.cluster = c;
             p.grid = (int)segs * c;
             p.o_bytes = p.ml_bytes = p.desc_bytes = 0;

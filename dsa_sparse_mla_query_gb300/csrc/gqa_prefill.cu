@@ -38,6 +38,10 @@ constexpr int kIssueWarp = 8, kLoadWarp = 12, kClearWarp = 13, kWalkWarp = 14;  
 constexpr float kLazy = 8.f;  // a row's reference moves when its maximum passes it by 2^8
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kItemSlots = 2;
+// Outputs leave through shared memory, 32 dims of a warp's rows at a time: a
+// thread holds a row, and 32 rows a store took as long as a step's products.
+constexpr int kOutRow = 80;             // 64 bytes of a row, 16 more against bank conflicts
+constexpr int kOutWarp = 32 * kOutRow;
 constexpr int kItemReaders = 14;  // warps that read an item: softmax, issuers, loader, clearer
 
 template <int D>
@@ -45,8 +49,8 @@ struct Cfg {
     static constexpr int kHalves = D / 64;                   // 128-byte pieces of a head row
     static constexpr int kQTile = 128 * D * 2;               // bytes
     static constexpr int kStage = kKeys * D * 2;             // a K or a V tile
-    static constexpr int kStages = D == 128 ? 5 : 10;
-    static constexpr int kSmem = 2 * kQTile + kStages * kStage + 1024;
+    static constexpr int kStages = D == 128 ? 4 : 8;         // (five and ten are no faster)
+    static constexpr int kSmem = 2 * kQTile + kStages * kStage + 8 * kOutWarp + 1024;
     // TMEM columns: two buffers of S per tile, then O; P takes the place of its S
     static constexpr uint32_t kO = 256;
     static constexpr uint32_t s_col(int x, int buf) { return x * 128 + buf * kStep; }
@@ -147,7 +151,7 @@ struct Schedule {
     // item f of the order (f < total)
     __device__ __forceinline__ Item find(const Args& a, int64_t f) const {
         const int lane = threadIdx.x & 31;
-        const int64_t y = f / a.hkv;
+        const int64_t y = f <= 0x7FFFFFFF ? (int64_t)((uint32_t)f / (uint32_t)a.hkv) : f / a.hkv;
         int lo = 0, hi = top - 1;  // the largest level with above(level) > y
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -164,7 +168,7 @@ struct Schedule {
             const bool in = pp <= lo && lo < pp + nn;
             const uint32_t m = __ballot_sync(0xffffffffu, in);
             if (z < __popc(m)) {
-                const int l = __fns(m, 0, (int)z + 1);
+                const int l = __ffs(__ballot_sync(0xffffffffu, in && __popc(m & ((1u << lane) - 1)) == (int)z)) - 1;
                 it.b = g * 32 + l;
                 tile = lo - __shfl_sync(0xffffffffu, pp, l);
                 break;
@@ -217,7 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* qs = smem;
     uint8_t* ring = smem + 2 * C::kQTile;
-    Shared& sh = *reinterpret_cast<Shared*>(smem + 2 * C::kQTile + C::kStages * C::kStage);
+    uint8_t* stage_out = smem + 2 * C::kQTile + C::kStages * C::kStage;
+    Shared& sh = *reinterpret_cast<Shared*>(stage_out + 8 * kOutWarp);
     volatile int* abort_flag = sh.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -574,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = __all_sync(0xffffffffu, wait(&sh.pv_done[x][buf ^ 1], (no - 1) >> 1));
                         if (!ok) break;
                         ptx::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < D / 32; ++k) {
                             float o[32];
                             ptx::tmem_ld32(to + 32 * k, o);
@@ -619,21 +624,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 ++o_use;
                 ptx::tc_fence_after();
+                // row 8 y + lane / 4 of the warp's, 16 bytes of it at lane % 4: where it goes
+                uint8_t* mine = stage_out + warp * kOutWarp;
+                const uint32_t alive = __ballot_sync(0xffffffffu, live);
+                __nv_bfloat16* to_row[4];
 #pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    to_row[y] = a.out + __shfl_sync(0xffffffffu, at, 8 * y + (lane >> 2)) * D + 8 * (lane & 3);
+#pragma unroll 1
                 for (int k = 0; k < D / 32; ++k) {
                     float o[32];
                     ptx::tmem_ld32(to + 32 * k, o);
-                    if (live) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + 32 * k);
+                    if (l == 0.f) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float v[8];
-#pragma unroll
-                            for (int y = 0; y < 8; ++y) v[y] = l == 0.f ? 0.f : o[8 * e + y] * inv;
-                            dst[e] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                                                pack_bf16(v[6], v[7]));
-                        }
+                        for (int e = 0; e < 32; ++e) o[e] = 0.f;  // whatever a row without keys holds
                     }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) v[y] = o[8 * e + y] * inv;
+                        *reinterpret_cast<uint4*>(mine + lane * kOutRow + 16 * e) =
+                            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                       pack_bf16(v[6], v[7]));
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int row = 8 * y + (lane >> 2);
+                        if ((alive >> row) & 1)
+                            *reinterpret_cast<uint4*>(to_row[y] + 32 * k) =
+                                *reinterpret_cast<const uint4*>(mine + row * kOutRow + 16 * (lane & 3));
+                    }
+                    __syncwarp();
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
