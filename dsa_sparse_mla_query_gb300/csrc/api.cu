@@ -5,6 +5,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 #include <string>
 
@@ -164,7 +165,9 @@ cudaError_t launch_decode(const dsa_gqa_shape& sh, const void* q, const void* k,
                           const float* v_scale, const dsa_seqs& s, int num_q, float sm_scale, void* out, float* lse,
                           void* workspace, int32_t* d_status, cudaStream_t stream);
 cudaError_t launch_prefill(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v, const dsa_seqs& s,
-                           int num_q, float sm_scale, void* out, float* lse, int32_t* d_status, cudaStream_t stream);
+                           int num_q, float sm_scale, void* out, float* lse, void* workspace, int32_t* d_status,
+                           cudaStream_t stream);
+size_t prefill_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s, int num_q);
 }  // namespace gqa
 size_t block_topk_smem(int max_ctx, int block, int nsel);
 cudaError_t launch_block_topk(const float* scores, int64_t ld, const dsa_seqs& s, int num_q, int block, int nsel,
@@ -429,7 +432,10 @@ dsa_status dsa_kv_insert(const dsa_gqa_shape* shape, const void* k, int64_t k_in
                        "dsa_kv_insert launch");
 }
 
-static size_t gqa_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s) { return gqa::decode_workspace(sh, s); }
+// for either call: one size serves both
+static size_t gqa_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s, int32_t num_q) {
+    return std::max(gqa::decode_workspace(sh, s), gqa::prefill_workspace(sh, s, num_q));
+}
 
 static void check_gqa_sizes(Check& c, const dsa_gqa_shape& sh, const dsa_seqs* s) {
     if (c.st != DSA_OK) return;
@@ -446,7 +452,7 @@ dsa_status dense_gqa_workspace_size(const dsa_gqa_shape* shape, const dsa_seqs* 
     c.need(bytes != nullptr, DSA_ERR_INVALID_ARG, "bytes is NULL");
     dsa_status st = c.done();
     if (st != DSA_OK) return st;
-    *bytes = gqa_workspace(sh, *seqs);
+    *bytes = gqa_workspace(sh, *seqs, num_q);
     return DSA_OK;
 }
 
@@ -469,7 +475,7 @@ static dsa_status dense_gqa(bool prefill, const dsa_gqa_shape* shape, const void
         c.ptr(v_scale, "v_scale", 4);
     }
     if (c.st == DSA_OK) {
-        const size_t need = gqa_workspace(sh, *seqs);
+        const size_t need = gqa_workspace(sh, *seqs, num_q);
         c.need(workspace != nullptr || need == 0, DSA_ERR_WORKSPACE, "workspace is NULL");
         c.need(workspace == nullptr || aligned(workspace, 256), DSA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
         c.need(workspace_bytes >= need, DSA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
@@ -478,8 +484,8 @@ static dsa_status dense_gqa(bool prefill, const dsa_gqa_shape* shape, const void
     if (st != DSA_OK || num_q == 0) return st;
     // a negative scale turns the row maxima around: the split kernel scales first
     if (prefill && sh.kv_dtype == DSA_BF16 && sm_scale >= 0.f)
-        return cuda_status(gqa::launch_prefill(sh, q, k_cache, v_cache, *seqs, num_q, sm_scale, out, lse, d_status,
-                                               stream),
+        return cuda_status(gqa::launch_prefill(sh, q, k_cache, v_cache, *seqs, num_q, sm_scale, out, lse,
+                                               workspace, d_status, stream),
                            "dense_gqa_prefill launch");
     return cuda_status(gqa::launch_decode(sh, q, k_cache, v_cache, k_scale, v_scale, *seqs, num_q, sm_scale, out, lse,
                                           workspace, d_status, stream),

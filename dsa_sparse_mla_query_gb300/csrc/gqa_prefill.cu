@@ -23,7 +23,9 @@
 // Roles (one CTA per SM, persistent): two warpgroups of softmax (one per tile,
 // each also writes its tile's output), four warps that issue the products (a
 // tile's scores, its outputs), and one warp each that loads, clears the rows
-// behind the last key, and walks the items.  Items go longest first, dealt to the CTAs in turn, back and forth.
+// behind the last key, and walks the items.  Items go longest first, dealt to
+// the CTAs in turn, back and forth.  Where few items leave CTAs idle, each is
+// split into ranges of keys, whose partial results a second kernel joins.
 #include "gqa_common.cuh"
 
 namespace dsa {
@@ -58,8 +60,10 @@ struct Cfg {
 
 struct Item {
     int n;       // stages of keys (0: no key is seen; -1: no more items)
-    int limit;   // keys that some query sees
+    int key0;    // the first stage's first key
+    int limit;   // keys that some query sees, up to the last stage's end
     int steps[2];// steps of either tile (0: the tile sees no key, or has no query)
+    int part;    // which of the key ranges that the call is split into
     int b, kvh;
     int q0;      // first query row
     int ntok;    // tokens from there to the sequence's end (may exceed the item)
@@ -74,6 +78,9 @@ struct Args {
     int32_t* d_status;
     float scale_log2;  // > 0
     int32_t num_q, group, hkv, tpt;  // tpt: tokens per tile
+    int32_t splits;   // key ranges per item; more than one: partial results
+    float* part_o;    // [splits][num_q heads][D]
+    float2* part_ml;  // [splits][num_q heads]
 };
 
 // Shared-memory matrix descriptors as a low word, which holds the address and
@@ -146,11 +153,16 @@ struct Schedule {
         for (int k = 0; k < kKept; ++k)
             if (k * 32 >= a.s.num_seqs) n[k] = p[k] = 0;
         top = __reduce_max_sync(0xffffffffu, t);
-        total = above(a, 0) * a.hkv;
+        total = above(a, 0) * a.hkv * a.splits;
     }
     // item f of the order (f < total)
     __device__ __forceinline__ Item find(const Args& a, int64_t f) const {
         const int lane = threadIdx.x & 31;
+        int part = 0;
+        if (a.splits > 1) {
+            part = (int)(f % a.splits);
+            f /= a.splits;
+        }
         const int64_t y = f <= 0x7FFFFFFF ? (int64_t)((uint32_t)f / (uint32_t)a.hkv) : f / a.hkv;
         int lo = 0, hi = top - 1;  // the largest level with above(level) > y
         while (lo < hi) {
@@ -197,6 +209,17 @@ struct Schedule {
             it.limit = max(it.limit, lim);
         }
         it.n = (it.limit + kKeys - 1) / kKeys;
+        it.key0 = 0;
+        it.part = part;
+        if (a.splits > 1) {
+            const int first = (int)((int64_t)it.n * part / a.splits), last = (int)((int64_t)it.n * (part + 1) / a.splits);
+            it.n = last - first;
+            it.key0 = first * kKeys;
+            it.limit = min(it.limit, last * kKeys);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                it.steps[x] = min(max(it.steps[x] - first * (kKeys / kStep), 0), it.n * (kKeys / kStep));
+        }
         return it;
     }
 };
@@ -355,8 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (row < 0) report(a.d_status, DSA_ERR_BAD_INPUT);
                     return (int)row;
                 };
-                int w0 = 0;
-                int cur = row_of(lane), nxt = row_of(32 + lane);
+                const int b0 = it.key0 >> shift;  // the item's first box
+                int w0 = b0;
+                int cur = row_of(w0 + lane), nxt = row_of(w0 + 32 + lane);
                 auto load = [&](const CUtensorMap* map, int i, bool tail) -> bool {
                     const int st = c.st;
                     if (lap) {
@@ -368,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint64_t* bar = tail ? sh.tail_full + st : sh.kv_full + st;
                     if (tail) tails |= 1u << st, tail_phase ^= 1u << st;
                     else tails &= ~(1u << st);
-                    const int l = i * nbox - w0;
+                    const int l = b0 + i * nbox - w0;
                     const uint32_t have = __ballot_sync(0xffffffffu, cur >= 0 && lane >= l && lane < l + nbox);
                     if (lane == 0) ptx::mbar_expect_tx(bar, (uint32_t)__popc(have) * R * D * 2);
                     __syncwarp();
@@ -383,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return true;
                 };
                 for (int i = 0; ok && i < it.n; ++i) {
-                    if (i * nbox >= w0 + 32) {
+                    if (b0 + i * nbox >= w0 + 32) {
                         w0 += 32;
                         cur = nxt;
                         nxt = row_of(w0 + 32 + lane);
@@ -549,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tmem_ld32_async(ts + 32, s[1]);
                 ptx::tmem_wait_ld32(s[0]);
                 ptx::tmem_wait_ld32(s[1]);
-                const int lim = pos - j * kStep;  // the step's last key that the row sees
+                const int lim = pos - it.key0 - j * kStep;  // the step's last key that the row sees
                 if (__any_sync(0xffffffffu, lim < kStep - 1)) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
@@ -619,6 +643,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float l = (la + lb) + (lc + ld);
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const int64_t at = (int64_t)(it.q0 + t) * (a.hkv * a.group) + it.kvh * a.group + head;
+            if (a.splits > 1) {
+                // a partial result: O as it is, its reference and its sum (0: O is not read)
+                const int64_t row = (int64_t)it.part * a.num_q * (a.hkv * a.group) + at;
+                if (live) a.part_ml[row] = make_float2(m, l);
+                if (n == 0) continue;
+                ok = __all_sync(0xffffffffu, wait(sh.o_full + x, o_use));
+                if (!ok) break;
+                ++o_use;
+                ptx::tc_fence_after();
+#pragma unroll 1
+                for (int k = 0; k < D / 32; ++k) {
+                    float o[32];
+                    ptx::tmem_ld32(to + 32 * k, o);
+                    if (live) {
+                        float4* dst = reinterpret_cast<float4*>(a.part_o + row * D + 32 * k);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(sh.o_empty + x);
+                continue;
+            }
             if (n > 0) {
                 ok = __all_sync(0xffffffffu, wait(sh.o_full + x, o_use));
                 if (!ok) break;
@@ -677,6 +726,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// Joins the partial results of a row (query, head), a warp per row: weights
+// 2^(m_i - M), in the ranges' order.  Rows that no valid query owns stay.
+constexpr int kMaxSplits = 16;
+template <int D>
+__global__ void __launch_bounds__(128) gqa_prefill_join_kernel(const __grid_constant__ Args a) {
+    pdl_enter();
+    const int lane = threadIdx.x & 31;
+    const int heads = a.hkv * a.group;
+    const int64_t rows = (int64_t)a.num_q * heads;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    const int t = (int)(row / heads);
+    const int b = seq_of(a.s.q_start, a.s.num_seqs, t);
+    const Seq q = load_seq(a.s, b, a.num_q);
+    if (!q.ok || t < q.q0 || t >= q.q0 + q.nq) return;
+    const int pos = __ldg(a.s.q_pos + t);
+    if (pos < -1 || pos >= q.ctx) return;
+    float2 v = make_float2(-INFINITY, 0.f);
+    if (lane < a.splits) v = a.part_ml[lane * rows + row];
+    float top = v.y == 0.f ? -INFINITY : v.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float w = v.y == 0.f ? 0.f : fast_exp2(v.x - top);
+    float sum = w * v.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    constexpr int E = D / 32;
+    float acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < a.splits; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        if (__shfl_sync(0xffffffffu, v.y, i) == 0.f) continue;  // nothing was written
+        const float* src = a.part_o + (i * rows + row) * D + lane * E;
+        if (E == 4) {
+            const float4 x = __ldcs(reinterpret_cast<const float4*>(src));
+            acc[0] = fmaf(wi, x.x, acc[0]), acc[1] = fmaf(wi, x.y, acc[1]);
+            acc[E - 2] = fmaf(wi, x.z, acc[E - 2]), acc[E - 1] = fmaf(wi, x.w, acc[E - 1]);
+        } else {
+            const float2 x = __ldcs(reinterpret_cast<const float2*>(src));
+            acc[0] = fmaf(wi, x.x, acc[0]), acc[1] = fmaf(wi, x.y, acc[1]);
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+    if (a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
 // ---------------------------------------------------------------------------
 // host side: Q [num_q, heads, d] with rows `stride` elements apart, a box of
 // `tokens` x `group` heads x 64 dims
@@ -704,11 +804,64 @@ cudaError_t launch_one(const CUtensorMap& qm, const CUtensorMap& km, const CUten
     return launch_pdl(kern, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, stream, 1, qm, km, vm, a);
 }
 
+struct Plan {
+    int splits;
+    size_t o_bytes, ml_bytes;
+};
+
+// Key ranges per item, from the sizes that the host knows: one, unless an
+// estimate gains 15% with more, then the fewest within 2% of the best.  Items of
+// equal length fill the GPU in rounds (512 items over 152 CTAs: four rounds, the
+// last for a third of them); items of many lengths, longest first, even out by
+// themselves.  In steps of 64 keys: six of an item's own start and end, a
+// partial result two more, the join at 6.8 TB/s.  Idle SMs leave the others
+// power, so a smaller gain is none.  Split against not: 720 and 360 tokens
+// behind 25,728, 16/2 heads of 128, 183 us and 308; up to 64 tokens of four
+// sequences behind 4,000, 64/8 heads, 46 and 58; and where the estimate says no:
+// 1,867 tokens behind 18,711, 16/2 heads, 256 and 244; 4,000 from the start 61
+// and 56; 2,048 behind 63,488, 64/8 heads, 2,974 and 2,998.
+Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s, int num_q) {
+    const int group = sh.num_heads / sh.num_kv_heads, per = 2 * (128 / group);
+    const double rows = (double)std::max(num_q, 1) * sh.num_heads;
+    const double items = std::max<double>((num_q + per - 1) / per, std::min(num_q, s.num_seqs)) * sh.num_kv_heads;
+    const double mean = (s.max_ctx - 0.5 * std::min(s.max_q_per_seq, s.max_ctx)) / kStep;
+    const bool even = s.max_q_per_seq < s.max_ctx / 4;
+    double t[kMaxSplits + 1], best = 1e30;
+    int most = 0;
+    for (int n = 1; n <= kMaxSplits; ++n) {
+        if (n > 1 && (mean / n < 8 || rows * n * (sh.head_dim * 4 + 8) > 512.0 * (1 << 20))) break;
+        const double piece = mean / n + (n > 1 ? 8 : 6), work = items * n * piece / kPlanSms;
+        t[n] = items * n >= 8 * kPlanSms ? work : std::ceil(items * n / kPlanSms) * piece;
+        if (!even) t[n] = std::max(work, (double)s.max_ctx / kStep / n + 6);
+        if (n > 1) t[n] += 6 + rows * (n * 2.0 * (sh.head_dim * 4 + 8) + sh.head_dim * 2) / 6.8e6 / 0.7;
+        best = std::min(best, t[n]);
+        most = n;
+    }
+    Plan p{1, 0, 0};
+    if (best < 0.85 * t[1])
+        while (p.splits < most && t[p.splits] > 1.02 * best) ++p.splits;
+    if (p.splits > 1) {
+        p.o_bytes = ((size_t)rows * p.splits * sh.head_dim * 4 + 255) & ~(size_t)255;
+        p.ml_bytes = ((size_t)rows * p.splits * 8 + 255) & ~(size_t)255;
+    }
+    return p;
+}
+
 }  // namespace
 
+size_t prefill_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s, int num_q) {
+    const Plan p = make_plan(sh, s, num_q);
+    return p.o_bytes + p.ml_bytes;
+}
+
 cudaError_t launch_prefill(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v, const dsa_seqs& s,
-                           int num_q, float sm_scale, void* out, float* lse, int32_t* d_status, cudaStream_t stream) {
+                           int num_q, float sm_scale, void* out, float* lse, void* workspace, int32_t* d_status,
+                           cudaStream_t stream) {
+    const Plan p = make_plan(sh, s, num_q);
     Args a;
+    a.splits = p.splits;
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.o_bytes);
     a.group = sh.num_heads / sh.num_kv_heads;
     a.hkv = sh.num_kv_heads;
     a.tpt = 128 / a.group;
@@ -727,10 +880,14 @@ cudaError_t launch_prefill(const dsa_gqa_shape& sh, const void* q, const void* k
     if (e == cudaSuccess)
         e = cache_map(&vm, false, v, sh.num_kv_heads, sh.head_dim, sh.v_stride, s.num_rows, box, box == kKeys);
     if (e != cudaSuccess) return e;
-    const int64_t items = ((int64_t)num_q / (2 * a.tpt) + s.num_seqs) * a.hkv;  // at most
+    const int64_t items = ((int64_t)num_q / (2 * a.tpt) + s.num_seqs) * a.hkv * a.splits;  // at most
     const int grid = (int)std::min<int64_t>(num_sms(), items);
-    return sh.head_dim == 64 ? launch_one<64>(qm, km, vm, a, grid, stream)
-                             : launch_one<128>(qm, km, vm, a, grid, stream);
+    e = sh.head_dim == 64 ? launch_one<64>(qm, km, vm, a, grid, stream)
+                          : launch_one<128>(qm, km, vm, a, grid, stream);
+    if (e != cudaSuccess || a.splits == 1) return e;
+    const int64_t rows = (int64_t)num_q * sh.num_heads;
+    auto join = sh.head_dim == 64 ? gqa_prefill_join_kernel<64> : gqa_prefill_join_kernel<128>;
+    return launch_pdl(join, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, 1, a);
 }
 
 }  // namespace gqa

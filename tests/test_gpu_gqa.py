@@ -182,6 +182,12 @@ PROMPTS = {
     "chunk e4m3 d64": ([700, 1000, 90], [200, 64, 90], 10, 2, 64, True, 16),
     "no tokens among them": ([40, 90, 0, 5], [0, 90, 0, 3], 8, 2, 128, False, 64),
     "long": ([2500], [2500], 8, 2, 128, False, 0),
+    # few tokens far into their sequences: the keys are split and joined
+    "far": ([5000, 3100, 40], [9, 70, 40], 16, 2, 128, False, 64),
+    "far d64 pages of 16": ([5000, 3100, 1], [9, 70, 1], 12, 4, 64, False, 16),
+    "far e4m3": ([5000, 3100, 40], [9, 70, 40], 16, 2, 128, True, 64),
+    "far e4m3 d64": ([5000, 3100, 40], [9, 70, 40], 6, 1, 64, True, 32),
+    "far ungrouped": ([4100], [300], 2, 2, 128, False, 0),
 }
 
 
@@ -245,6 +251,22 @@ def test_bad_positions_and_sequences_are_reported_and_skipped(call):
     c.run(call)
     c.check(seqs=[0, 2], status=6)
     assert bool((c.out[3:5] == 7).all()) and bool((c.lse[3:5] == 7).all())
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_joined_rows_that_see_little_and_bad_ones(call, e4m3):
+    """Where a row's keys are split: rows that see no key, one key, the keys of the first part only;
+    a bad position and rows behind the last sequence stay unwritten; stale rows are not used."""
+    pos = [-1, 0, 300, 2000, 5999, 64, 127, 128]
+    c = Case([6000, 30], [8, 1], 8, 2, 128, e4m3=e4m3, page=64, pos=pos + [29], extra_q=3)
+    c.run(call).check()
+    assert bool((c.out[0] == 0).all()) and bool((c.out[c.nq:] == 7).all()) and bool((c.lse[c.nq:] == 7).all())
+    c.d_pos[4] = 6000
+    c.run(call)
+    c.new[0] = 4
+    c.check(status=6)
+    assert bool((c.out[4] == 7).all()) and bool((c.lse[4] == 7).all())
 
 
 @pytest.mark.parametrize("call", list(CALLS))
