@@ -164,9 +164,9 @@ size_t decode_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s);
 cudaError_t launch_decode(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v, const float* k_scale,
                           const float* v_scale, const dsa_seqs& s, int num_q, float sm_scale, void* out, float* lse,
                           void* workspace, int32_t* d_status, cudaStream_t stream);
-cudaError_t launch_prefill(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v, const dsa_seqs& s,
-                           int num_q, float sm_scale, void* out, float* lse, void* workspace, int32_t* d_status,
-                           cudaStream_t stream);
+cudaError_t launch_prefill(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v,
+                           const float* k_scale, const float* v_scale, const dsa_seqs& s, int num_q, float sm_scale,
+                           void* out, float* lse, void* workspace, int32_t* d_status, cudaStream_t stream);
 size_t prefill_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s, int num_q);
 }  // namespace gqa
 size_t block_topk_smem(int max_ctx, int block, int nsel);
@@ -483,9 +483,9 @@ static dsa_status dense_gqa(bool prefill, const dsa_gqa_shape* shape, const void
     dsa_status st = c.done();
     if (st != DSA_OK || num_q == 0) return st;
     // a negative scale turns the row maxima around: the split kernel scales first
-    if (prefill && sh.kv_dtype == DSA_BF16 && sm_scale >= 0.f)
-        return cuda_status(gqa::launch_prefill(sh, q, k_cache, v_cache, *seqs, num_q, sm_scale, out, lse,
-                                               workspace, d_status, stream),
+    if (prefill && sm_scale >= 0.f)
+        return cuda_status(gqa::launch_prefill(sh, q, k_cache, v_cache, k_scale, v_scale, *seqs, num_q, sm_scale, out,
+                                               lse, workspace, d_status, stream),
                            "dense_gqa_prefill launch");
     return cuda_status(gqa::launch_decode(sh, q, k_cache, v_cache, k_scale, v_scale, *seqs, num_q, sm_scale, out, lse,
                                           workspace, d_status, stream),

@@ -35,8 +35,8 @@ namespace {
 constexpr int kTagPrefill = 7;
 constexpr int kKeys = 128;  // keys per stage of the ring
 constexpr int kStep = 64;   // keys per step of the products
-constexpr int kThreads = 512;
 constexpr int kIssueWarp = 8, kLoadWarp = 12, kClearWarp = 13, kWalkWarp = 14;  // then an idle one
+constexpr int kConvertWarp = 16, kConverters = 4;  // e4m3 caches only
 constexpr float kLazy = 8.f;  // a row's reference moves when its maximum passes it by 2^8
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kItemSlots = 2;
@@ -44,15 +44,27 @@ constexpr int kItemSlots = 2;
 // thread holds a row, and 32 rows a store took as long as a step's products.
 constexpr int kOutRow = 80;             // 64 bytes of a row, 16 more against bank conflicts
 constexpr int kOutWarp = 32 * kOutRow;
-constexpr int kItemReaders = 14;  // warps that read an item: softmax, issuers, loader, clearer
 
-template <int D>
+template <int D, bool FP8>
 struct Cfg {
+    static constexpr int kThreads = FP8 ? 640 : 512;
+    // registers per thread of the softmax warpgroups and of the others, which
+    // together take what the CTA is launched with
+    static constexpr int kSoftRegs = FP8 ? 152 : 192, kOtherRegs = FP8 ? 56 : 64;
+    // warps that read an item: softmax, issuers, loader, and the clearer or the converters
+    static constexpr int kItemReaders = 13 + (FP8 ? kConverters : 1);
     static constexpr int kHalves = D / 64;                   // 128-byte pieces of a head row
     static constexpr int kQTile = 128 * D * 2;               // bytes
     static constexpr int kStage = kKeys * D * 2;             // a K or a V tile
-    static constexpr int kStages = D == 128 ? 4 : 8;         // (five and ten are no faster)
-    static constexpr int kSmem = 2 * kQTile + kStages * kStage + 8 * kOutWarp + 1024;
+    static constexpr int kStages = FP8 ? (D == 128 ? 3 : 5) : (D == 128 ? 4 : 8);  // (five and ten bf16: no faster)
+    // e4m3: tiles as they are in the cache, before their conversion, and the scales of
+    // a stage's keys and values.  Those of stage i + slots are written once the values
+    // of stage i have been used: by then no softmax reads the scales of stage i.
+    static constexpr int kCodeStage = FP8 ? kKeys * D : 0;
+    static constexpr int kScaleSlots = (kStages + 2) / 2;
+    static constexpr int kScaleBytes = FP8 ? kScaleSlots * 2 * kKeys * 4 : 0;
+    static constexpr int kSmem = 2 * kQTile + kStages * kStage + 2 * kCodeStage + 8 * kOutWarp + kScaleBytes + 1024;
+    static_assert(kSmem <= 232448, "a CTA's shared memory");
     // TMEM columns: two buffers of S per tile, then O; P takes the place of its S
     static constexpr uint32_t kO = 256;
     static constexpr uint32_t s_col(int x, int buf) { return x * 128 + buf * kStep; }
@@ -79,9 +91,21 @@ struct Args {
     float scale_log2;  // > 0
     int32_t num_q, group, hkv, tpt;  // tpt: tokens per tile
     int32_t splits;   // key ranges per item; more than one: partial results
+    const float *k_scale, *v_scale;  // e4m3: [rows][hkv]
     float* part_o;    // [splits][num_q heads][D]
     float2* part_ml;  // [splits][num_q heads]
 };
+
+// four e4m3 codes (low byte first) to two bf16 pairs, exactly
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    uint32_t a, b;
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+        : "=r"(a), "=r"(b)
+        : "r"(x));
+    const float2 u = __half22float2(*reinterpret_cast<__half2*>(&a)), v = __half22float2(*reinterpret_cast<__half2*>(&b));
+    lo = pack_bf16(u.x, u.y);
+    hi = pack_bf16(v.x, v.y);
+}
 
 // Shared-memory matrix descriptors as a low word, which holds the address and
 // the leading stride, and the high word they share (8-row groups 1024 bytes
@@ -228,7 +252,7 @@ struct Shared {
     Item item[kItemSlots];
     uint64_t item_full[kItemSlots], item_empty[kItemSlots];
     uint64_t q_full[2], q_empty[2];
-    uint64_t kv_full[10], kv_empty[10], tail_full[10];
+    uint64_t kv_full[10], kv_empty[10], tail_full[10], c_full[2], c_empty[2];
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], o_empty[2];
     uint64_t drain[4];
     int abort_flag[2];
@@ -236,16 +260,18 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= 1024, "the barriers' page");
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, bool FP8>
+__global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     gqa_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a) {
-    using C = Cfg<D>;
+    using C = Cfg<D, FP8>;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* qs = smem;
     uint8_t* ring = smem + 2 * C::kQTile;
-    uint8_t* stage_out = smem + 2 * C::kQTile + C::kStages * C::kStage;
-    Shared& sh = *reinterpret_cast<Shared*>(stage_out + 8 * kOutWarp);
+    uint8_t* codes = ring + C::kStages * C::kStage;
+    uint8_t* stage_out = codes + 2 * C::kCodeStage;
+    float* scales = reinterpret_cast<float*>(stage_out + 8 * kOutWarp);  // [slot][keys, values][kKeys]
+    Shared& sh = *reinterpret_cast<Shared*>(stage_out + 8 * kOutWarp + C::kScaleBytes);
     volatile int* abort_flag = sh.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -256,12 +282,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kItemSlots; ++i) {
             ptx::mbar_init(sh.item_full + i, 1);
-            ptx::mbar_init(sh.item_empty + i, kItemReaders);
+            ptx::mbar_init(sh.item_empty + i, C::kItemReaders);
         }
         for (int i = 0; i < C::kStages; ++i) {
-            ptx::mbar_init(sh.kv_full + i, 1);
+            ptx::mbar_init(sh.kv_full + i, FP8 ? kConverters : 1);
             ptx::mbar_init(sh.kv_empty + i, 2);
             ptx::mbar_init(sh.tail_full + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(sh.c_full + i, 1);
+            ptx::mbar_init(sh.c_empty + i, kConverters);
         }
         for (int x = 0; x < 2; ++x) {
             ptx::mbar_init(sh.q_full + x, 1);
@@ -303,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp >= 8) {
-        reg_dec<64>();
+        reg_dec<C::kOtherRegs>();
         if (warp == kWalkWarp) {
             // ------------------------------------------------------------ walks the items
             Schedule sc;
@@ -327,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (it.n < 0) break;  // every later round's item lies past the end too
             }
-        } else if (warp == kClearWarp) {
+        } else if (!FP8 && warp == kClearWarp) {
             // ------------------------------------------------------------ clears V's rows behind the last key
             // whatever lies there must not reach the products: its weights are 0, but 0 * inf is not
             Item it;
@@ -356,7 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nbox = kKeys / R;
             const int shift = 31 - __clz(R);
             Item it;
-            Cursor<C::kStages> c;
+            constexpr int N = FP8 ? 2 : C::kStages;  // e4m3: into the code stages
+            Cursor<N> c;
             bool lap = false;      // every stage has been used
             int uses[2] = {0, 0};  // Q loads per tile
             bool ok = true;
@@ -384,21 +415,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto load = [&](const CUtensorMap* map, int i, bool tail) -> bool {
                     const int st = c.st;
                     if (lap) {
-                        const bool free = wait(sh.kv_empty + st, c.ph ^ 1u);
+                        const bool free = wait((FP8 ? sh.c_empty : sh.kv_empty) + st, c.ph ^ 1u);
                         if (!__all_sync(0xffffffffu, free)) return false;
                     }
                     c.move(1);
                     lap = lap || c.st == 0;
-                    uint64_t* bar = tail ? sh.tail_full + st : sh.kv_full + st;
+                    uint64_t* bar = FP8 ? sh.c_full + st : tail ? sh.tail_full + st : sh.kv_full + st;
                     if (tail) tails |= 1u << st, tail_phase ^= 1u << st;
                     else tails &= ~(1u << st);
                     const int l = b0 + i * nbox - w0;
                     const uint32_t have = __ballot_sync(0xffffffffu, cur >= 0 && lane >= l && lane < l + nbox);
-                    if (lane == 0) ptx::mbar_expect_tx(bar, (uint32_t)__popc(have) * R * D * 2);
+                    if (lane == 0) ptx::mbar_expect_tx(bar, (uint32_t)__popc(have) * R * D * (FP8 ? 1 : 2));
                     __syncwarp();
                     if ((have >> lane) & 1) {
-                        uint8_t* dst = ring + st * C::kStage + (lane - l) * R * 128;
-                        if (C::kHalves == 1 || nbox == 1)
+                        constexpr int PB = FP8 && D == 64 ? 64 : 128;  // bytes of a row's piece
+                        uint8_t* dst = (FP8 ? codes + st * C::kCodeStage : ring + st * C::kStage) + (lane - l) * R * PB;
+                        if (FP8 || C::kHalves == 1 || nbox == 1)
                             tma_load_4d(dst, map, 0, cur, 0, it.kvh, bar);
                         else
                             for (int h = 0; h < C::kHalves; ++h)
@@ -429,18 +461,91 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ++uses[x];
                         }
                     }
-                    if (ok) ok = load(&vmap, i, i + 1 == it.n && it.limit % kKeys);
+                    if (ok) ok = load(&vmap, i, !FP8 && i + 1 == it.n && it.limit % kKeys);
                 }
             }
             if (abort_flag[0] && lane == 0) {
                 // after an abort: let the copies in flight land before the CTA ends
-                for (int st = 0; st < C::kStages; ++st) {
+                for (int st = 0; st < N; ++st) {
                     if (!lap && st >= c.st) break;
-                    if ((tails >> st) & 1) ptx::mbar_drain(sh.tail_full + st, ((tail_phase >> st) & 1) ^ 1);
+                    if (FP8) ptx::mbar_drain(sh.c_full + st, st < c.st ? c.ph : c.ph ^ 1u);
+                    else if ((tails >> st) & 1) ptx::mbar_drain(sh.tail_full + st, ((tail_phase >> st) & 1) ^ 1);
                     else ptx::mbar_drain(sh.kv_full + st, st < c.st ? c.ph : c.ph ^ 1u);
                 }
                 for (int x = 0; x < 2; ++x)
                     if (uses[x]) ptx::mbar_drain(sh.q_full + x, (uses[x] - 1) & 1);
+            }
+        } else if (FP8 && warp >= kConvertWarp) {
+            // ------------------------------------------------------------ converts e4m3 tiles
+            // Codes to bf16, exactly, in the layout that TMA gives a bf16 tile; their
+            // scales stay apart (a key's goes to its scores, a value's to its weights).
+            // Rows behind the last key become zeros: whatever lies there must not
+            // reach the products, where 0 * inf is not 0.
+            const int tid = threadIdx.x - kConvertWarp * 32;
+            constexpr int kChunks = D / 16;  // 16-code chunks of a row
+            Item it;
+            Cursor<2> cc;
+            Cursor<C::kStages> c;
+            bool lap = false;
+            int slot = 0;
+            bool ok = true;
+            while (ok && next_item(it)) {
+                for (int i = 0; ok && i < 2 * it.n; ++i) {
+                    const int k0 = it.key0 + (i >> 1) * kKeys;
+                    const int rows = min(kKeys, it.limit - k0);
+                    if ((i & 1) == 0) {
+                        // the stage's scales: loaded beside the codes, a key per thread
+                        const int j = k0 + tid;
+                        float ks = 0.f, vs = 0.f;
+                        if (j < it.limit) {
+                            const int64_t row = a.s.page_table ? phys_row(a.s, it.b, j) : it.base + j;
+                            if (row >= 0 && row < a.s.num_rows) {
+                                ks = __ldg(a.k_scale + row * a.hkv + it.kvh) * a.scale_log2;
+                                vs = __ldg(a.v_scale + row * a.hkv + it.kvh);
+                            }
+                        }
+                        // (the stage before this slot's last user has been used: its values' place in the
+                        // ring is waited for below, before the first write of this stage; see Cfg)
+                        if (lap) ok = __all_sync(0xffffffffu, wait(sh.kv_empty + c.st, c.ph ^ 1u));
+                        if (!ok) break;
+                        scales[slot * 2 * kKeys + tid] = ks;
+                        scales[slot * 2 * kKeys + kKeys + tid] = vs;
+                        slot = slot + 1 == C::kScaleSlots ? 0 : slot + 1;
+                    } else if (lap) {
+                        ok = __all_sync(0xffffffffu, wait(sh.kv_empty + c.st, c.ph ^ 1u));
+                    }
+                    ok = ok && __all_sync(0xffffffffu, wait(sh.c_full + cc.st, cc.ph));
+                    if (!ok) break;
+                    const uint8_t* src = codes + cc.st * C::kCodeStage;
+                    uint8_t* dst = ring + c.st * C::kStage;
+#pragma unroll 2
+                    for (int q = tid; q < kKeys * kChunks; q += 32 * kConverters) {
+                        const int row = q / kChunks, ch = q % kChunks;
+                        const int from = D == 128 ? row * 128 + ((ch ^ (row & 7)) << 4)
+                                                  : row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
+                        uint4 x = *reinterpret_cast<const uint4*>(src + from);
+                        if (row >= rows) x = make_uint4(0u, 0u, 0u, 0u);
+                        uint32_t y[8];
+                        e4m3x4_to_bf16(x.x, y[0], y[1]);
+                        e4m3x4_to_bf16(x.y, y[2], y[3]);
+                        e4m3x4_to_bf16(x.z, y[4], y[5]);
+                        e4m3x4_to_bf16(x.w, y[6], y[7]);
+                        uint8_t* to = dst + (ch >> 2) * (kKeys * 128) + row * 128;
+                        const int c16 = (ch & 3) * 2;
+                        *reinterpret_cast<uint4*>(to + ((c16 ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                        *reinterpret_cast<uint4*>(to + (((c16 + 1) ^ (row & 7)) << 4)) =
+                            make_uint4(y[4], y[5], y[6], y[7]);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::mbar_arrive(sh.c_empty + cc.st);
+                        ptx::mbar_arrive(sh.kv_full + c.st);
+                    }
+                    cc.move(1);
+                    c.move(1);
+                    lap = lap || c.st == 0;
+                }
             }
         } else if (warp < kLoadWarp) {
             // ------------------------------------------------------------ issue the products
@@ -536,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---------------------------------------------------------------- softmax: a row per thread
-        reg_inc<192>();
+        reg_inc<C::kSoftRegs>();
         const int x = warp >> 2;
         const int r = threadIdx.x & 127;
         const int tok = r / a.group, head = r - tok * a.group;
@@ -546,8 +651,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t no = 0, o_use = 0;  // steps so far (buffer no & 1), outputs
         bool ok = true;
         const uint64_t sc2 = f32x2(a.scale_log2, a.scale_log2);
+        int slot = 0;  // e4m3: of the item's first scales
         while (ok && next_item(it)) {
             const int t = x * a.tpt + tok;  // token within the item
+            int sl = slot;
+            if (FP8) slot = (slot + it.n) % C::kScaleSlots;
             if (x == 1 && it.ntok <= a.tpt) continue;
             bool live = tok < a.tpt && t < it.ntok;
             int pos = 0x7FFFFFFF;  // unused rows: no mask, no output
@@ -573,6 +681,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tmem_ld32_async(ts + 32, s[1]);
                 ptx::tmem_wait_ld32(s[0]);
                 ptx::tmem_wait_ld32(s[1]);
+                const float* sc = scales + sl * 2 * kKeys + (j & 1) * kStep;  // e4m3: the step's keys' (times log2 e)
+                if (FP8) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(sc + 32 * k + e);
+                            uint32_t* y = s[k] + e;
+                            const uint64_t u = mul2(f32x2(__uint_as_float(y[0]), __uint_as_float(y[1])), f.x);
+                            const uint64_t w = mul2(f32x2(__uint_as_float(y[2]), __uint_as_float(y[3])), f.y);
+                            y[0] = (uint32_t)u, y[1] = (uint32_t)(u >> 32);
+                            y[2] = (uint32_t)w, y[3] = (uint32_t)(w >> 32);
+                        }
+                }
                 const int lim = pos - it.key0 - j * kStep;  // the step's last key that the row sees
                 if (__any_sync(0xffffffffu, lim < kStep - 1)) {
 #pragma unroll
@@ -588,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 1; e < 16; ++e) mx[k] = fmaxf(mx[k], __uint_as_float(s[k >> 1][16 * (k & 1) + e]));
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (FP8 ? 1.f : a.scale_log2);
                 const bool move = top > m + kLazy;
                 if (__any_sync(0xffffffffu, move)) {
                     const float mn = move ? top : m;
@@ -620,16 +742,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const uint64_t v =
-                            fma2(f32x2(__uint_as_float(s[k][e]), __uint_as_float(s[k][e + 1])), sc2, nm2);
+                        uint64_t v = f32x2(__uint_as_float(s[k][e]), __uint_as_float(s[k][e + 1]));
+                        v = FP8 ? add2(v, nm2) : fma2(v, sc2, nm2);
                         float p0, p1;
                         unpack2(v, p0, p1);
                         p0 = fast_exp2(p0);
                         p1 = fast_exp2(p1);
                         l2[(e >> 1) & 1] = add2(l2[(e >> 1) & 1], f32x2(p0, p1));
+                        if (FP8) {
+                            const uint64_t f = *reinterpret_cast<const uint64_t*>(sc + kKeys + 32 * k + e);
+                            unpack2(mul2(f32x2(p0, p1), f), p0, p1);
+                        }
                         // a weight rounded to bf16 is off by up to 2^-9 of itself; the sum keeps fp32
                         pk[16 * k + e / 2] = pack_bf16(p0, p1);
                     }
+                if (FP8 && (j & 1)) sl = sl + 1 == C::kScaleSlots ? 0 : sl + 1;
                 ptx::tmem_st32_nowait(ts, pk);
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
@@ -793,15 +920,16 @@ cudaError_t query_map(CUtensorMap* m, const void* q, int heads, int d, int64_t s
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D>
+template <int D, bool FP8>
 cudaError_t launch_one(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const Args& a, int grid,
                        cudaStream_t stream) {
-    auto kern = gqa_prefill_kernel<D>;
+    using C = Cfg<D, FP8>;
+    auto kern = gqa_prefill_kernel<D, FP8>;
     static OncePerDevice once;
     const cudaError_t e = once.run(
-        [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem); });
+        [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, stream, 1, qm, km, vm, a);
+    return launch_pdl(kern, dim3(grid), dim3(C::kThreads), C::kSmem, stream, 1, qm, km, vm, a);
 }
 
 struct Plan {
@@ -854,12 +982,14 @@ size_t prefill_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s, int num_q) 
     return p.o_bytes + p.ml_bytes;
 }
 
-cudaError_t launch_prefill(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v, const dsa_seqs& s,
-                           int num_q, float sm_scale, void* out, float* lse, void* workspace, int32_t* d_status,
-                           cudaStream_t stream) {
+cudaError_t launch_prefill(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v,
+                           const float* k_scale, const float* v_scale, const dsa_seqs& s, int num_q, float sm_scale,
+                           void* out, float* lse, void* workspace, int32_t* d_status, cudaStream_t stream) {
     const Plan p = make_plan(sh, s, num_q);
     Args a;
     a.splits = p.splits;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
     a.part_o = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.o_bytes);
     a.group = sh.num_heads / sh.num_kv_heads;
@@ -873,17 +1003,20 @@ cudaError_t launch_prefill(const dsa_gqa_shape& sh, const void* q, const void* k
     // a scale of 0 stays a tiny positive one: masked scores are -inf before the scaling
     a.scale_log2 = std::max(sm_scale * 1.4426950408889634f, 1e-30f);
     const int box = s.page_table ? std::min(s.page_size, kKeys) : kKeys;
+    const bool fp8 = sh.kv_dtype == DSA_FP8_E4M3_ROWSCALE;
     CUtensorMap qm, km, vm;
     cudaError_t e = query_map(&qm, q, sh.num_heads, sh.head_dim, sh.q_stride, num_q, a.group, a.tpt);
     if (e == cudaSuccess)
-        e = cache_map(&km, false, k, sh.num_kv_heads, sh.head_dim, sh.k_stride, s.num_rows, box, box == kKeys);
+        e = cache_map(&km, fp8, k, sh.num_kv_heads, sh.head_dim, sh.k_stride, s.num_rows, box, box == kKeys);
     if (e == cudaSuccess)
-        e = cache_map(&vm, false, v, sh.num_kv_heads, sh.head_dim, sh.v_stride, s.num_rows, box, box == kKeys);
+        e = cache_map(&vm, fp8, v, sh.num_kv_heads, sh.head_dim, sh.v_stride, s.num_rows, box, box == kKeys);
     if (e != cudaSuccess) return e;
     const int64_t items = ((int64_t)num_q / (2 * a.tpt) + s.num_seqs) * a.hkv * a.splits;  // at most
     const int grid = (int)std::min<int64_t>(num_sms(), items);
-    e = sh.head_dim == 64 ? launch_one<64>(qm, km, vm, a, grid, stream)
-                          : launch_one<128>(qm, km, vm, a, grid, stream);
+    e = sh.head_dim == 64 ? (fp8 ? launch_one<64, true>(qm, km, vm, a, grid, stream)
+                                 : launch_one<64, false>(qm, km, vm, a, grid, stream))
+                          : (fp8 ? launch_one<128, true>(qm, km, vm, a, grid, stream)
+                                 : launch_one<128, false>(qm, km, vm, a, grid, stream));
     if (e != cudaSuccess || a.splits == 1) return e;
     const int64_t rows = (int64_t)num_q * sh.num_heads;
     auto join = sh.head_dim == 64 ? gqa_prefill_join_kernel<64> : gqa_prefill_join_kernel<128>;
