@@ -36,7 +36,7 @@ constexpr int kTagPrefill = 7;
 constexpr int kKeys = 128;  // keys per stage of the ring
 constexpr int kStep = 64;   // keys per step of the products
 constexpr int kIssueWarp = 8, kLoadWarp = 12, kClearWarp = 13, kWalkWarp = 14;  // then an idle one
-constexpr int kConvertWarp = 16, kConverters = 4;  // e4m3 caches only
+constexpr int kConvertWarp = 16, kConverters = 8;  // e4m3 caches only
 constexpr float kLazy = 8.f;  // a row's reference moves when its maximum passes it by 2^8
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kItemSlots = 2;
@@ -47,10 +47,10 @@ constexpr int kOutWarp = 32 * kOutRow;
 
 template <int D, bool FP8>
 struct Cfg {
-    static constexpr int kThreads = FP8 ? 640 : 512;
+    static constexpr int kThreads = FP8 ? 768 : 512;
     // registers per thread of the softmax warpgroups and of the others, which
     // together take what the CTA is launched with
-    static constexpr int kSoftRegs = FP8 ? 152 : 192, kOtherRegs = FP8 ? 56 : 64;
+    static constexpr int kSoftRegs = FP8 ? 144 : 192, kOtherRegs = FP8 ? 48 : 64;
     // warps that read an item: softmax, issuers, loader, and the clearer or the converters
     static constexpr int kItemReaders = 13 + (FP8 ? kConverters : 1);
     static constexpr int kHalves = D / 64;                   // 128-byte pieces of a head row
@@ -480,7 +480,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             // Codes to bf16, exactly, in the layout that TMA gives a bf16 tile; their
             // scales stay apart (a key's goes to its scores, a value's to its weights).
             // Rows behind the last key become zeros: whatever lies there must not
-            // reach the products, where 0 * inf is not 0.
+            // reach the products, where 0 * inf is not 0.  2,048 tokens behind 30,000,
+            // 64/8 heads of 128: 802 TFLOP/s (four converting warps: 678), bound by the
+            // conversion's turn-around: the ring has room for three converted stages.
             const int tid = threadIdx.x - kConvertWarp * 32;
             constexpr int kChunks = D / 16;  // 16-code chunks of a row
             Item it;
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                     const int rows = min(kKeys, it.limit - k0);
                     if ((i & 1) == 0) {
                         // the stage's scales: loaded beside the codes, a key per thread
-                        const int j = k0 + tid;
+                        const int j = tid < kKeys ? k0 + tid : it.limit;
                         float ks = 0.f, vs = 0.f;
                         if (j < it.limit) {
                             const int64_t row = a.s.page_table ? phys_row(a.s, it.b, j) : it.base + j;
@@ -508,8 +510,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                         // ring is waited for below, before the first write of this stage; see Cfg)
                         if (lap) ok = __all_sync(0xffffffffu, wait(sh.kv_empty + c.st, c.ph ^ 1u));
                         if (!ok) break;
-                        scales[slot * 2 * kKeys + tid] = ks;
-                        scales[slot * 2 * kKeys + kKeys + tid] = vs;
+                        if (tid < kKeys) {
+                            scales[slot * 2 * kKeys + tid] = ks;
+                            scales[slot * 2 * kKeys + kKeys + tid] = vs;
+                        }
                         slot = slot + 1 == C::kScaleSlots ? 0 : slot + 1;
                     } else if (lap) {
                         ok = __all_sync(0xffffffffu, wait(sh.kv_empty + c.st, c.ph ^ 1u));
