@@ -160,14 +160,14 @@ cudaError_t launch_kv_insert(const dsa_gqa_shape& sh, const void* k, int64_t k_i
                              float* k_scale, float* v_scale, int64_t num_rows, void* q_out, int32_t* d_status,
                              cudaStream_t stream);
 namespace gqa {
-size_t decode_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s);
+size_t decode_workspace(const dsa_gqa_shape& sh);
 cudaError_t launch_decode(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v, const float* k_scale,
                           const float* v_scale, const dsa_seqs& s, int num_q, float sm_scale, void* out, float* lse,
                           void* workspace, int32_t* d_status, cudaStream_t stream);
 cudaError_t launch_prefill(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v,
                            const float* k_scale, const float* v_scale, const dsa_seqs& s, int num_q, float sm_scale,
                            void* out, float* lse, void* workspace, int32_t* d_status, cudaStream_t stream);
-size_t prefill_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s, int num_q);
+size_t prefill_workspace(const dsa_gqa_shape& sh, int num_q);
 }  // namespace gqa
 size_t block_topk_smem(int max_ctx, int block, int nsel);
 cudaError_t launch_block_topk(const float* scores, int64_t ld, const dsa_seqs& s, int num_q, int block, int nsel,
@@ -432,9 +432,9 @@ dsa_status dsa_kv_insert(const dsa_gqa_shape* shape, const void* k, int64_t k_in
                        "dsa_kv_insert launch");
 }
 
-// for either call: one size serves both
-static size_t gqa_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s, int32_t num_q) {
-    return std::max(gqa::decode_workspace(sh, s), gqa::prefill_workspace(sh, s, num_q));
+// for either call, with any sequences and no more queries
+static size_t gqa_workspace(const dsa_gqa_shape& sh, int32_t num_q) {
+    return std::max(gqa::decode_workspace(sh), gqa::prefill_workspace(sh, num_q));
 }
 
 static void check_gqa_sizes(Check& c, const dsa_gqa_shape& sh, const dsa_seqs* s) {
@@ -452,7 +452,7 @@ dsa_status dense_gqa_workspace_size(const dsa_gqa_shape* shape, const dsa_seqs* 
     c.need(bytes != nullptr, DSA_ERR_INVALID_ARG, "bytes is NULL");
     dsa_status st = c.done();
     if (st != DSA_OK) return st;
-    *bytes = gqa_workspace(sh, *seqs, num_q);
+    *bytes = gqa_workspace(sh, num_q);
     return DSA_OK;
 }
 
@@ -475,9 +475,9 @@ static dsa_status dense_gqa(bool prefill, const dsa_gqa_shape* shape, const void
         c.ptr(v_scale, "v_scale", 4);
     }
     if (c.st == DSA_OK) {
-        const size_t need = gqa_workspace(sh, *seqs, num_q);
-        c.need(workspace != nullptr || need == 0, DSA_ERR_WORKSPACE, "workspace is NULL");
-        c.need(workspace == nullptr || aligned(workspace, 256), DSA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+        const size_t need = gqa_workspace(sh, num_q);
+        c.need(workspace != nullptr, DSA_ERR_WORKSPACE, "workspace is NULL");
+        c.need(aligned(workspace, 256), DSA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
         c.need(workspace_bytes >= need, DSA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
     }
     dsa_status st = c.done();

@@ -28,6 +28,11 @@
 // - Few and short sequences are bound by latency, and the second kernel alone
 //   takes 4 us: there a cluster of CTAs shares a (lane, sequence) and joins its
 //   partials through distributed shared memory.
+//
+// Measured, 64/8 heads of 128: 64 x 32,768 bf16 1,200 us, 7.1 TB/s (a copy: 6.8);
+// 1 x 524,288 e4m3 169 us, 6.5 TB/s; 128 x 4 tokens over 61 to 16,381 e4m3 605 us,
+// 3.7 TB/s: there 32 rows make 64 products, 64 conversions and 480 instructions of
+// a warp's 16 keys, and two warps a scheduler leave half of its cycles unused.
 #include <type_traits>
 
 #include "gqa_common.cuh"
@@ -1160,9 +1165,10 @@ cudaError_t launch_one(const CUtensorMap& km, const CUtensorMap& vm, const Args&
 
 }  // namespace
 
-size_t decode_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s) {
-    const Plan p = make_plan(sh, s);
-    return p.o_bytes + p.ml_bytes + p.desc_bytes;
+// For any call: two partials of 8, 16 or 32 rows per CTA, of two CTAs per SM with 8.
+size_t decode_workspace(const dsa_gqa_shape& sh) {
+    const size_t rows = (size_t)2 * kPlanSms * 32;
+    return up256(rows * sh.head_dim * 4) + up256(rows * 8) + up256((size_t)2 * kPlanSms * 16);
 }
 
 cudaError_t launch_decode(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v, const float* k_scale,

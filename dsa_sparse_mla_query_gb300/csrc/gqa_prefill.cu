@@ -26,6 +26,12 @@
 // behind the last key, and walks the items.  Items go longest first, dealt to
 // the CTAs in turn, back and forth.  Where few items leave CTAs idle, each is
 // split into ranges of keys, whose partial results a second kernel joins.
+//
+// Measured, 64/8 heads of 128, bf16: 16,384 tokens 1,570 to 1,670 TFLOP/s (the
+// chip at its power cap, as a library matrix product is at 1,700 sustained), a
+// step 1,340 cycles of the 1,280 that its products take; 24 packed prompts of 17
+// to 4,095 tokens 1,200 to 1,330, where an item's start and end are 5,000 cycles
+// of 30,000 to 90,000.
 #include "gqa_common.cuh"
 
 namespace dsa {
@@ -41,7 +47,8 @@ constexpr float kLazy = 8.f;  // a row's reference moves when its maximum passes
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kItemSlots = 2;
 // Outputs leave through shared memory, 32 dims of a warp's rows at a time: a
-// thread holds a row, and 32 rows a store took as long as a step's products.
+// thread holds a row, and 16 bytes of 32 rows a store cost 1% of 24 packed
+// prompts.
 constexpr int kOutRow = 80;             // 64 bytes of a row, 16 more against bank conflicts
 constexpr int kOutWarp = 32 * kOutRow;
 
@@ -58,11 +65,11 @@ struct Cfg {
     static constexpr int kStage = kKeys * D * 2;             // a K or a V tile
     static constexpr int kStages = FP8 ? (D == 128 ? 3 : 5) : (D == 128 ? 4 : 8);  // (five and ten bf16: no faster)
     // e4m3: tiles as they are in the cache, before their conversion, and the scales of
-    // a stage's keys and values.  Those of stage i + slots are written once the values
+    // a stage's keys.  Those of stage i + slots are written once the values
     // of stage i have been used: by then no softmax reads the scales of stage i.
     static constexpr int kCodeStage = FP8 ? kKeys * D : 0;
     static constexpr int kScaleSlots = (kStages + 2) / 2;
-    static constexpr int kScaleBytes = FP8 ? kScaleSlots * 2 * kKeys * 4 : 0;
+    static constexpr int kScaleBytes = FP8 ? (kScaleSlots + 2) * kKeys * 4 : 0;  // and those beside the codes
     static constexpr int kSmem = 2 * kQTile + kStages * kStage + 2 * kCodeStage + 8 * kOutWarp + kScaleBytes + 1024;
     static_assert(kSmem <= 232448, "a CTA's shared memory");
     // TMEM columns: two buffers of S per tile, then O; P takes the place of its S
@@ -96,15 +103,18 @@ struct Args {
     float2* part_ml;  // [splits][num_q heads]
 };
 
-// four e4m3 codes (low byte first) to two bf16 pairs, exactly
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+// f times four e4m3 codes (low byte first) as two bf16 pairs; exact for f = 1
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t x, float f, uint32_t& lo, uint32_t& hi) {
     uint32_t a, b;
     asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
         : "=r"(a), "=r"(b)
         : "r"(x));
     const float2 u = __half22float2(*reinterpret_cast<__half2*>(&a)), v = __half22float2(*reinterpret_cast<__half2*>(&b));
-    lo = pack_bf16(u.x, u.y);
-    hi = pack_bf16(v.x, v.y);
+    float p, q, r, t;
+    unpack2(mul2(f32x2(u.x, u.y), f32x2(f, f)), p, q);
+    unpack2(mul2(f32x2(v.x, v.y), f32x2(f, f)), r, t);
+    lo = pack_bf16(p, q);
+    hi = pack_bf16(r, t);
 }
 
 // Shared-memory matrix descriptors as a low word, which holds the address and
@@ -270,7 +280,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     uint8_t* ring = smem + 2 * C::kQTile;
     uint8_t* codes = ring + C::kStages * C::kStage;
     uint8_t* stage_out = codes + 2 * C::kCodeStage;
-    float* scales = reinterpret_cast<float*>(stage_out + 8 * kOutWarp);  // [slot][keys, values][kKeys]
+    float* scales = reinterpret_cast<float*>(stage_out + 8 * kOutWarp);  // [slot][kKeys]
+    float* code_scales = scales + C::kScaleSlots * kKeys;                // [code stage][kKeys]
     Shared& sh = *reinterpret_cast<Shared*>(stage_out + 8 * kOutWarp + C::kScaleBytes);
     volatile int* abort_flag = sh.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -290,7 +301,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             ptx::mbar_init(sh.tail_full + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(sh.c_full + i, 1);
+            ptx::mbar_init(sh.c_full + i, 33);  // the codes' bytes, and every lane's scales
             ptx::mbar_init(sh.c_empty + i, kConverters);
         }
         for (int x = 0; x < 2; ++x) {
@@ -436,6 +447,18 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                             for (int h = 0; h < C::kHalves; ++h)
                                 tma_load_4d(dst + h * (kKeys * 128), map, 0, cur, h, it.kvh, bar);
                     }
+                    if (FP8) {
+                        const float* from = map == &kmap ? a.k_scale : a.v_scale;
+#pragma unroll
+                        for (int y = 0; y < kKeys / 32; ++y) {
+                            const int key = y * 32 + lane;
+                            const int row = __shfl_sync(0xffffffffu, cur, l + (key >> shift));
+                            if (row >= 0 && it.key0 + i * kKeys + key < it.limit)
+                                ptx::cp_async4(code_scales + st * kKeys + key,
+                                               from + ((int64_t)row + (key & (R - 1))) * a.hkv + it.kvh);
+                        }
+                        ptx::cp_async_arrive_noinc(bar);
+                    }
                     return true;
                 };
                 for (int i = 0; ok && i < it.n; ++i) {
@@ -477,63 +500,53 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             }
         } else if (FP8 && warp >= kConvertWarp) {
             // ------------------------------------------------------------ converts e4m3 tiles
-            // Codes to bf16, exactly, in the layout that TMA gives a bf16 tile; their
-            // scales stay apart (a key's goes to its scores, a value's to its weights).
+            // Codes to bf16, in the layout that TMA gives a bf16 tile: keys' exactly, their
+            // scales go to the scores; values' times their scale, one rounding (by up to 2^-9
+            // of itself, as the weights', for the softmax threads' 64 loads of a scale each
+            // would cost a third of shared memory's rate again).
             // Rows behind the last key become zeros: whatever lies there must not
             // reach the products, where 0 * inf is not 0.  2,048 tokens behind 30,000,
-            // 64/8 heads of 128: 802 TFLOP/s (four converting warps: 678), bound by the
-            // conversion's turn-around: the ring has room for three converted stages.
+            // 64/8 heads of 128: 942 TFLOP/s, bound by the conversion, 2,400 cycles a tile
+            // where a step's products take 2,600 for two (four converting warps: 729; four
+            // for the keys and four for the values: 833).
             const int tid = threadIdx.x - kConvertWarp * 32;
-            constexpr int kChunks = D / 16;  // 16-code chunks of a row
+            constexpr int kChunks = D / 16;                      // 16-code chunks of a row
+            constexpr int kRowsAt = 32 * kConverters / kChunks;  // rows that the warps take at once
             Item it;
             Cursor<2> cc;
             Cursor<C::kStages> c;
-            bool lap = false;
+            bool lap = false;  // every stage has been used
             int slot = 0;
             bool ok = true;
             while (ok && next_item(it)) {
                 for (int i = 0; ok && i < 2 * it.n; ++i) {
-                    const int k0 = it.key0 + (i >> 1) * kKeys;
-                    const int rows = min(kKeys, it.limit - k0);
-                    if ((i & 1) == 0) {
-                        // the stage's scales: loaded beside the codes, a key per thread
-                        const int j = tid < kKeys ? k0 + tid : it.limit;
-                        float ks = 0.f, vs = 0.f;
-                        if (j < it.limit) {
-                            const int64_t row = a.s.page_table ? phys_row(a.s, it.b, j) : it.base + j;
-                            if (row >= 0 && row < a.s.num_rows) {
-                                ks = __ldg(a.k_scale + row * a.hkv + it.kvh) * a.scale_log2;
-                                vs = __ldg(a.v_scale + row * a.hkv + it.kvh);
-                            }
-                        }
-                        // (the stage before this slot's last user has been used: its values' place in the
-                        // ring is waited for below, before the first write of this stage; see Cfg)
-                        if (lap) ok = __all_sync(0xffffffffu, wait(sh.kv_empty + c.st, c.ph ^ 1u));
-                        if (!ok) break;
-                        if (tid < kKeys) {
-                            scales[slot * 2 * kKeys + tid] = ks;
-                            scales[slot * 2 * kKeys + kKeys + tid] = vs;
-                        }
-                        slot = slot + 1 == C::kScaleSlots ? 0 : slot + 1;
-                    } else if (lap) {
-                        ok = __all_sync(0xffffffffu, wait(sh.kv_empty + c.st, c.ph ^ 1u));
-                    }
+                    const int what = i & 1;  // 0: keys, 1: values
+                    const int rows = min(kKeys, it.limit - it.key0 - (i >> 1) * kKeys);
+                    if (lap) ok = __all_sync(0xffffffffu, wait(sh.kv_empty + c.st, c.ph ^ 1u));
                     ok = ok && __all_sync(0xffffffffu, wait(sh.c_full + cc.st, cc.ph));
                     if (!ok) break;
                     const uint8_t* src = codes + cc.st * C::kCodeStage;
                     uint8_t* dst = ring + c.st * C::kStage;
-#pragma unroll 2
-                    for (int q = tid; q < kKeys * kChunks; q += 32 * kConverters) {
-                        const int row = q / kChunks, ch = q % kChunks;
+                    const float* cs = code_scales + cc.st * kKeys;
+                    if (what == 0) {
+                        // this slot's last stage has been used: its values' place in the ring, or a later one,
+                        // is the one that has just been waited for (see Cfg)
+                        if (tid < kKeys) scales[slot * kKeys + tid] = tid < rows ? cs[tid] * a.scale_log2 : 0.f;
+                        slot = slot + 1 == C::kScaleSlots ? 0 : slot + 1;
+                    }
+#pragma unroll
+                    for (int z = 0; z < kKeys / kRowsAt; ++z) {
+                        const int row = z * kRowsAt + tid / kChunks, ch = tid % kChunks;
                         const int from = D == 128 ? row * 128 + ((ch ^ (row & 7)) << 4)
                                                   : row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
                         uint4 x = *reinterpret_cast<const uint4*>(src + from);
                         if (row >= rows) x = make_uint4(0u, 0u, 0u, 0u);
                         uint32_t y[8];
-                        e4m3x4_to_bf16(x.x, y[0], y[1]);
-                        e4m3x4_to_bf16(x.y, y[2], y[3]);
-                        e4m3x4_to_bf16(x.z, y[4], y[5]);
-                        e4m3x4_to_bf16(x.w, y[6], y[7]);
+                        const float f = what == 0 ? 1.f : row < rows ? cs[row] : 0.f;
+                        e4m3x4_to_bf16(x.x, f, y[0], y[1]);
+                        e4m3x4_to_bf16(x.y, f, y[2], y[3]);
+                        e4m3x4_to_bf16(x.z, f, y[4], y[5]);
+                        e4m3x4_to_bf16(x.w, f, y[6], y[7]);
                         uint8_t* to = dst + (ch >> 2) * (kKeys * 128) + row * 128;
                         const int c16 = (ch & 3) * 2;
                         *reinterpret_cast<uint4*>(to + ((c16 ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
@@ -685,7 +698,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 ptx::tmem_ld32_async(ts + 32, s[1]);
                 ptx::tmem_wait_ld32(s[0]);
                 ptx::tmem_wait_ld32(s[1]);
-                const float* sc = scales + sl * 2 * kKeys + (j & 1) * kStep;  // e4m3: the step's keys' (times log2 e)
+                const float* sc = scales + sl * kKeys + (j & 1) * kStep;  // e4m3: the step's keys' (times log2 e)
                 if (FP8) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
@@ -753,10 +766,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                         p0 = fast_exp2(p0);
                         p1 = fast_exp2(p1);
                         l2[(e >> 1) & 1] = add2(l2[(e >> 1) & 1], f32x2(p0, p1));
-                        if (FP8) {
-                            const uint64_t f = *reinterpret_cast<const uint64_t*>(sc + kKeys + 32 * k + e);
-                            unpack2(mul2(f32x2(p0, p1), f), p0, p1);
-                        }
                         // a weight rounded to bf16 is off by up to 2^-9 of itself; the sum keeps fp32
                         pk[16 * k + e / 2] = pack_bf16(p0, p1);
                     }
@@ -860,6 +869,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 // Joins the partial results of a row (query, head), a warp per row: weights
 // 2^(m_i - M), in the ranges' order.  Rows that no valid query owns stay.
 constexpr int kMaxSplits = 16;
+constexpr int kMostPieces = 4 * kPlanSms;  // (item, key range) pairs of a call that is split
 template <int D>
 __global__ void __launch_bounds__(128) gqa_prefill_join_kernel(const __grid_constant__ Args a) {
     pdl_enter();
@@ -961,7 +971,7 @@ Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s, int num_q) {
     double t[kMaxSplits + 1], best = 1e30;
     int most = 0;
     for (int n = 1; n <= kMaxSplits; ++n) {
-        if (n > 1 && (mean / n < 8 || rows * n * (sh.head_dim * 4 + 8) > 512.0 * (1 << 20))) break;
+        if (n > 1 && (mean / n < 8 || items * n > kMostPieces)) break;
         const double piece = mean / n + (n > 1 ? 8 : 6), work = items * n * piece / kPlanSms;
         t[n] = items * n >= 8 * kPlanSms ? work : std::ceil(items * n / kPlanSms) * piece;
         if (!even) t[n] = std::max(work, (double)s.max_ctx / kStep / n + 6);
@@ -981,9 +991,11 @@ Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s, int num_q) {
 
 }  // namespace
 
-size_t prefill_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s, int num_q) {
-    const Plan p = make_plan(sh, s, num_q);
-    return p.o_bytes + p.ml_bytes;
+// For any call of up to num_q queries: an item has at most 256 rows, and at
+// most kMostPieces pieces of items leave partial results.
+size_t prefill_workspace(const dsa_gqa_shape& sh, int num_q) {
+    const size_t rows = std::min((size_t)num_q * sh.num_heads * kMaxSplits, (size_t)kMostPieces * 256);
+    return rows * (sh.head_dim * 4 + 8) + 512;
 }
 
 cudaError_t launch_prefill(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v,

@@ -429,9 +429,10 @@ dsa_status dsa_kv_insert(const dsa_gqa_shape* shape, const void* k, int64_t k_in
                          void* v_cache, float* k_scale, float* v_scale, int64_t num_rows, void* q_out,
                          int32_t* d_status, cudaStream_t stream);
 
-/* Bytes of workspace that dense_gqa_decode and dense_gqa_prefill need for
- * these sizes (host only; one workspace sized for the largest call serves all
- * calls that do not overlap). */
+/* Bytes of workspace that dense_gqa_decode and dense_gqa_prefill need (host
+ * only).  The size depends on the shape and num_q alone and grows with num_q:
+ * a workspace sized for the most queries of a shape serves all of its calls
+ * that do not overlap. */
 dsa_status dense_gqa_workspace_size(const dsa_gqa_shape* shape, const dsa_seqs* seqs, int32_t num_q, size_t* bytes);
 
 /* Attention of a few new tokens per sequence over its cached keys (their own

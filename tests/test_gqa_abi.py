@@ -76,14 +76,14 @@ def test_pointers_sizes_and_workspace(lib, name):
     assert rc == B.DSA_ERR_UNSUPPORTED and "num_rows" in msg
     rc, msg = _attend(lib, name, seqs=_seqs(page_table=0x5000, page_size=48, max_pages=4))
     assert rc == B.DSA_ERR_UNSUPPORTED and "page_size 48" in msg
-    s, shape, n = _seqs(num_seqs=500), B.GqaShape(16, 2, 128), ctypes.c_size_t()  # more than clusters take
-    assert lib.dense_gqa_workspace_size(ctypes.byref(shape), ctypes.byref(s), 500, ctypes.byref(n)) == 0
+    s, shape, n = _seqs(), B.GqaShape(16, 2, 128), ctypes.c_size_t()
+    assert lib.dense_gqa_workspace_size(ctypes.byref(shape), ctypes.byref(s), 2, ctypes.byref(n)) == 0
     assert n.value > 0
-    rc, msg = _attend(lib, name, seqs=s, num_q=500, ws_bytes=n.value - 1)
+    rc, msg = _attend(lib, name, ws_bytes=n.value - 1)
     assert rc == B.DSA_ERR_WORKSPACE and f"needs {n.value}" in msg
-    rc, msg = _attend(lib, name, seqs=s, num_q=500, ws=0x10010)
+    rc, msg = _attend(lib, name, ws=0x10010)
     assert rc == B.DSA_ERR_WORKSPACE and "256-byte aligned" in msg
-    rc, msg = _attend(lib, name, seqs=s, num_q=500, ws=None)
+    rc, msg = _attend(lib, name, ws=None)
     assert rc == B.DSA_ERR_WORKSPACE and "workspace is NULL" in msg
     assert _attend(lib, name, num_q=0)[0] == 0
     assert _attend(lib, name, num_q=-1)[0] == B.DSA_ERR_INVALID_ARG
@@ -120,3 +120,18 @@ def test_insert_refuses(lib, kw, part, status):
 
 def test_insert_of_nothing(lib):
     assert _insert(lib, n=0, k=None, v=None, q=None, kc=None, vc=None)[0] == 0
+
+
+def test_a_workspace_for_the_most_queries_serves_all(lib):
+    """The size grows with num_q and depends on the shape, not on the sequences."""
+    for shape in (B.GqaShape(64, 8, 128), B.GqaShape(5, 5, 64), B.GqaShape(64, 1, 128, B.DSA_FP8_E4M3_ROWSCALE)):
+        last = 0
+        for num_q in (0, 1, 4, 37, 512, 4096, 100000):
+            sizes = set()
+            for seqs in (_seqs(), _seqs(num_seqs=300, max_ctx=1 << 20, max_q_per_seq=64), _seqs(max_q_per_seq=5000)):
+                n = ctypes.c_size_t()
+                assert lib.dense_gqa_workspace_size(ctypes.byref(shape), ctypes.byref(seqs), num_q,
+                                                    ctypes.byref(n)) == 0
+                sizes.add(n.value)
+            assert len(sizes) == 1 and max(sizes) >= last
+            last = max(sizes)
