@@ -30,7 +30,7 @@
 // Measured, 64/8 heads of 128, bf16: 16,384 tokens 1,570 to 1,670 TFLOP/s (the
 // chip at its power cap, as a library matrix product is at 1,700 sustained), a
 // step 1,340 cycles of the 1,280 that its products take; 24 packed prompts of 17
-// to 4,095 tokens 1,200 to 1,330, where an item's start and end are 5,000 cycles
+// to 4,095 tokens 1,200 to 1,330, where an item's start and end are 4,000 cycles
 // of 30,000 to 90,000.
 #include "gqa_common.cuh"
 
@@ -46,11 +46,7 @@ constexpr int kConvertWarp = 16, kConverters = 8;  // e4m3 caches only
 constexpr float kLazy = 8.f;  // a row's reference moves when its maximum passes it by 2^8
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kItemSlots = 2;
-// Outputs leave through shared memory, 32 dims of a warp's rows at a time: a
-// thread holds a row, and 16 bytes of 32 rows a store cost 1% of 24 packed
-// prompts.
-constexpr int kOutRow = 80;             // 64 bytes of a row, 16 more against bank conflicts
-constexpr int kOutWarp = 32 * kOutRow;
+constexpr int kOutWarp = 32 * 128;  // outputs leave through shared memory: 64 dims of a warp's 32 rows at a time
 
 template <int D, bool FP8>
 struct Cfg {
@@ -813,39 +809,50 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 if (!ok) break;
                 ++o_use;
                 ptx::tc_fence_after();
-                // row 8 y + lane / 4 of the warp's, 16 bytes of it at lane % 4: where it goes
+                // 64 dims at a time: a thread's row into the warp's 32 x 128 bytes (16-byte pieces
+                // turned by the row: no bank conflicts), then 4 rows of 128 bytes a store
                 uint8_t* mine = stage_out + warp * kOutWarp;
                 const uint32_t alive = __ballot_sync(0xffffffffu, live);
-                __nv_bfloat16* to_row[4];
+                const uint64_t inv2 = f32x2(inv, inv);
+                __nv_bfloat16* to_row[8];
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    to_row[y] = a.out + __shfl_sync(0xffffffffu, at, 8 * y + (lane >> 2)) * D + 8 * (lane & 3);
+                for (int y = 0; y < 8; ++y)
+                    to_row[y] = a.out + __shfl_sync(0xffffffffu, at, 4 * y + (lane >> 3)) * D + 8 * (lane & 7);
 #pragma unroll 1
-                for (int k = 0; k < D / 32; ++k) {
-                    float o[32];
-                    ptx::tmem_ld32(to + 32 * k, o);
-                    if (l == 0.f) {
+                for (int k = 0; k < D / 64; ++k) {
+                    uint32_t o[2][32];
+                    ptx::tmem_ld32_async(to + 64 * k, o[0]);
+                    ptx::tmem_ld32_async(to + 64 * k + 32, o[1]);
+                    ptx::tmem_wait_ld32(o[0]);
+                    ptx::tmem_wait_ld32(o[1]);
+                    if (l == 0.f) {  // no key: whatever O holds
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0.f;  // whatever a row without keys holds
+                        for (int e = 0; e < 64; ++e) o[e >> 5][e & 31] = 0u;
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v[8];
+                    for (int e = 0; e < 8; ++e) {
+                        uint32_t y[4];
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) v[y] = o[8 * e + y] * inv;
-                        *reinterpret_cast<uint4*>(mine + lane * kOutRow + 16 * e) =
-                            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                                       pack_bf16(v[6], v[7]));
+                        for (int z = 0; z < 4; ++z) {
+                            const uint32_t* w = &o[e >> 2][8 * (e & 3) + 2 * z];
+                            float p, q;
+                            unpack2(mul2(f32x2(__uint_as_float(w[0]), __uint_as_float(w[1])), inv2), p, q);
+                            y[z] = pack_bf16(p, q);
+                        }
+                        *reinterpret_cast<uint4*>(mine + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                            make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                    __syncwarp();
+                    uint4 v[8];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        const int row = 4 * y + (lane >> 3);
+                        v[y] = *reinterpret_cast<const uint4*>(mine + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
                     }
                     __syncwarp();
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const int row = 8 * y + (lane >> 2);
-                        if ((alive >> row) & 1)
-                            *reinterpret_cast<uint4*>(to_row[y] + 32 * k) =
-                                *reinterpret_cast<const uint4*>(mine + row * kOutRow + 16 * (lane & 3));
-                    }
-                    __syncwarp();
+                    for (int y = 0; y < 8; ++y)
+                        if ((alive >> (4 * y + (lane >> 3))) & 1) *reinterpret_cast<uint4*>(to_row[y] + 64 * k) = v[y];
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
