@@ -175,8 +175,8 @@ __device__ __forceinline__ int tiles_of(const Seq& q) {
     return q.ok && q.nq > 0 ? max(1, (q.ctx + TILE - 1) / TILE) : 0;
 }
 
-// The walk over a CTA's pieces: each call of next() gives a run of tiles
-// [i0, i1) of one (lane, sequence).  Every warp of the CTA walks alike.
+// The walk over a CTA's pieces: each begin() gives a run of tiles [i0, i1) of
+// one (lane, sequence).  Every warp of the CTA walks alike.
 struct Piece {
     int lane, b, i0, i1;
     Seq q;
@@ -384,98 +384,98 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
     if (warp >= KS) {
         if (C::kSplitRegs) reg_dec<72>();
         if (warp == KS) {
-        w.init(a);
-        // ---- the loading warp: a lane per TMA box of a 32-box window of the page table
-        const int R = a.s.page_table ? min(a.s.page_size, kTile) : kTile;  // rows per box
-        const int nbox = kTile / R;
-        const int shift = 31 - __clz(R);
-        Cursor<C::kStages> c;
-        bool lap = false;  // every stage has been used
-        bool ok = true;
-        int pos;
-        while (ok && w.begin(a, p, pos)) {
-            const int kvh = p.lane % a.hkv;
-            // physical row of a box's first token among the sequence's, -1: none; its
-            // load goes out before the queries' positions have arrived
-            auto row_of = [&](int box) -> int {
-                const int64_t j = (int64_t)box << shift;
-                if (j >= p.q.ctx) return -1;
-                int64_t row;
-                if (a.s.page_table) {
-                    row = phys_row(a.s, p.b, j);
-                    if (row >= 0 && row + R > a.s.num_rows) row = -1;  // a page past the cache
-                } else {
-                    row = p.base + j;
-                    const int64_t last = p.base + min(j + R, (int64_t)p.q.ctx);
-                    if (row < 0 || last > a.s.num_rows) row = -1;
-                }
-                return (int)row;
-            };
-            auto seen = [&](int row, int box) -> int {
-                const bool in = ((int64_t)box << shift) < p.limit;
-                if (in && row < 0) report(a.d_status, DSA_ERR_BAD_INPUT);
-                return in ? row : -1;
-            };
-            int w0 = p.i0 * nbox;
-            int cur = row_of(w0 + lane), nxt = row_of(w0 + 32 + lane);
-            w.finish(p, pos);
-            const int end = min(p.i1, (p.limit + kTile - 1) / kTile);
-            if (p.i0 < end) cur = seen(cur, w0 + lane);
-            for (int i = p.i0; i < end && ok; ++i) {
-                const int st = c.st;
-                if (i * nbox >= w0 + 32) {
-                    w0 += 32;
-                    cur = seen(nxt, w0 + lane);
-                    nxt = row_of(w0 + 32 + lane);
-                }
-                if (lap) {
-                    ok = ptx::mbar_wait(empty + st, c.ph ^ 1u, abort_flag, a.d_status);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                }
-                c.move(1);
-                lap = lap || c.st == 0;
-                uint8_t* kd = ring + st * C::kStage;
-                uint8_t* vd = kd + C::kHalf;
-                const int l = i * nbox - w0;  // window lane of the tile's first box
-                const uint32_t have = __ballot_sync(0xffffffffu, cur >= 0 && lane >= l && lane < l + nbox);
-                if (lane == 0) ptx::mbar_expect_tx(full + st, (uint32_t)__popc(have) * 2u * R * HB);
-                __syncwarp();
-                if ((have >> lane) & 1) {
-                    const int x = lane - l;
-                    constexpr int PB = HB < 128 ? HB : 128;
-                    if (HB <= 128 || nbox == 1) {
-                        tma_load_4d(kd + x * R * PB, &kmap, 0, cur, 0, kvh, full + st);
-                        tma_load_4d(vd + x * R * PB, &vmap, 0, cur, 0, kvh, full + st);
+            w.init(a);
+            // ---- the loading warp: a lane per TMA box of a 32-box window of the page table
+            const int R = a.s.page_table ? min(a.s.page_size, kTile) : kTile;  // rows per box
+            const int nbox = kTile / R;
+            const int shift = 31 - __clz(R);
+            Cursor<C::kStages> c;
+            bool lap = false;  // every stage has been used
+            bool ok = true;
+            int pos;
+            while (ok && w.begin(a, p, pos)) {
+                const int kvh = p.lane % a.hkv;
+                // physical row of a box's first token among the sequence's, -1: none; its
+                // load goes out before the queries' positions have arrived
+                auto row_of = [&](int box) -> int {
+                    const int64_t j = (int64_t)box << shift;
+                    if (j >= p.q.ctx) return -1;
+                    int64_t row;
+                    if (a.s.page_table) {
+                        row = phys_row(a.s, p.b, j);
+                        if (row >= 0 && row + R > a.s.num_rows) row = -1;  // a page past the cache
                     } else {
-                        // two 128-byte pieces, each a block of the tile's rows: a smaller box is one piece
-                        for (int h = 0; h < HB / 128; ++h) {
-                            tma_load_4d(kd + h * (kTile * 128) + x * R * 128, &kmap, 0, cur, h, kvh, full + st);
-                            tma_load_4d(vd + h * (kTile * 128) + x * R * 128, &vmap, 0, cur, h, kvh, full + st);
+                        row = p.base + j;
+                        const int64_t last = p.base + min(j + R, (int64_t)p.q.ctx);
+                        if (row < 0 || last > a.s.num_rows) row = -1;
+                    }
+                    return (int)row;
+                };
+                auto seen = [&](int row, int box) -> int {
+                    const bool in = ((int64_t)box << shift) < p.limit;
+                    if (in && row < 0) report(a.d_status, DSA_ERR_BAD_INPUT);
+                    return in ? row : -1;
+                };
+                int w0 = p.i0 * nbox;
+                int cur = row_of(w0 + lane), nxt = row_of(w0 + 32 + lane);
+                w.finish(p, pos);
+                const int end = min(p.i1, (p.limit + kTile - 1) / kTile);
+                if (p.i0 < end) cur = seen(cur, w0 + lane);
+                for (int i = p.i0; i < end && ok; ++i) {
+                    const int st = c.st;
+                    if (i * nbox >= w0 + 32) {
+                        w0 += 32;
+                        cur = seen(nxt, w0 + lane);
+                        nxt = row_of(w0 + 32 + lane);
+                    }
+                    if (lap) {
+                        ok = ptx::mbar_wait(empty + st, c.ph ^ 1u, abort_flag, a.d_status);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                    }
+                    c.move(1);
+                    lap = lap || c.st == 0;
+                    uint8_t* kd = ring + st * C::kStage;
+                    uint8_t* vd = kd + C::kHalf;
+                    const int l = i * nbox - w0;  // window lane of the tile's first box
+                    const uint32_t have = __ballot_sync(0xffffffffu, cur >= 0 && lane >= l && lane < l + nbox);
+                    if (lane == 0) ptx::mbar_expect_tx(full + st, (uint32_t)__popc(have) * 2u * R * HB);
+                    __syncwarp();
+                    if ((have >> lane) & 1) {
+                        const int x = lane - l;
+                        constexpr int PB = HB < 128 ? HB : 128;
+                        if (HB <= 128 || nbox == 1) {
+                            tma_load_4d(kd + x * R * PB, &kmap, 0, cur, 0, kvh, full + st);
+                            tma_load_4d(vd + x * R * PB, &vmap, 0, cur, 0, kvh, full + st);
+                        } else {
+                            // two 128-byte pieces, each a block of the tile's rows: a smaller box is one piece
+                            for (int h = 0; h < HB / 128; ++h) {
+                                tma_load_4d(kd + h * (kTile * 128) + x * R * 128, &kmap, 0, cur, h, kvh, full + st);
+                                tma_load_4d(vd + h * (kTile * 128) + x * R * 128, &vmap, 0, cur, h, kvh, full + st);
+                            }
                         }
                     }
-                }
-                if (FP8) {
-                    float* sd = ring_scale + st * (C::kScaleBytes / 4);
+                    if (FP8) {
+                        float* sd = ring_scale + st * (C::kScaleBytes / 4);
 #pragma unroll
-                    for (int h = 0; h < kTile / 32; ++h) {
-                        const int x = h * 32 + lane;
-                        const int row = __shfl_sync(0xffffffffu, cur, l + (x >> shift));
-                        const int64_t at = ((int64_t)row + (x & (R - 1))) * a.hkv + kvh;
-                        if (row >= 0 && (int64_t)i * kTile + x < p.limit) {
-                            ptx::cp_async4(sd + x, a.k_scale + at);
-                            ptx::cp_async4(sd + kTile + x, a.v_scale + at);
+                        for (int h = 0; h < kTile / 32; ++h) {
+                            const int x = h * 32 + lane;
+                            const int row = __shfl_sync(0xffffffffu, cur, l + (x >> shift));
+                            const int64_t at = ((int64_t)row + (x & (R - 1))) * a.hkv + kvh;
+                            if (row >= 0 && (int64_t)i * kTile + x < p.limit) {
+                                ptx::cp_async4(sd + x, a.k_scale + at);
+                                ptx::cp_async4(sd + kTile + x, a.v_scale + at);
+                            }
                         }
+                        ptx::cp_async_arrive_noinc(full + st);
                     }
-                    ptx::cp_async_arrive_noinc(full + st);
                 }
             }
-        }
-        if (!ok) {
-            // after an abort: let the copies in flight land before the CTA ends
-            for (int st = 0; st < C::kStages; ++st)
-                if (lap || st < c.st) ptx::mbar_drain(full + st, st < c.st ? c.ph : c.ph ^ 1u);
-        }
+            if (!ok) {
+                // after an abort: let the copies in flight land before the CTA ends
+                for (int st = 0; st < C::kStages; ++st)
+                    if (lap || st < c.st) ptx::mbar_drain(full + st, st < c.st ? c.ph : c.ph ^ 1u);
+            }
         }
         if (a.cluster > 1) {  // the computing warps' two meetings
             cluster_arrive();
@@ -1102,20 +1102,8 @@ Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s) {
     p.tile = p.nt == 1 ? 64 : 128;
     p.chunks = (int)((rows + p.rows - 1) / p.rows);
     p.lanes = sh.num_kv_heads * p.chunks;
-    // lanes side by side: a divisor of the lanes that leaves few CTAs idle, the
-    // largest such (its lanes' rows are neighbours in memory)
     const int n = kPlanSms * (p.nt == 1 ? 2 : 1);
-    int best = 0;
-    p.hl = 1;
-    for (int d = 1; d <= p.lanes && d <= n; ++d)
-        if (p.lanes % d == 0) {
-            const int used = n / d * d;
-            if (used * 32 >= best * 31) p.hl = d;
-            best = std::max(best, used);
-        }
     const int64_t tiles = std::max<int64_t>(1, ((int64_t)s.max_ctx + p.tile - 1) / p.tile);
-    p.parts = (int)std::min<int64_t>(n / p.hl, (int64_t)(p.lanes / p.hl) * s.num_seqs * tiles);
-    p.grid = p.parts * p.hl;
     // Clusters where all (lane, sequence)s fit at once and an estimate from the
     // longest sequence says that they are faster: a CTA takes at least tile_ns a
     // tile (latency), all together no less than the bytes at 6.8 TB/s, and the
@@ -1139,10 +1127,24 @@ Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s) {
         if (with <= without) {
             p.cluster = c;
             p.grid = (int)segs * c;
+            p.hl = p.parts = 1;  // not used
             p.o_bytes = p.ml_bytes = p.desc_bytes = 0;
             return p;
         }
     }
+    // lanes side by side: a divisor of the lanes that leaves few CTAs idle, the
+    // largest such (its lanes' rows are neighbours in memory)
+    int best = 0;
+    p.hl = p.lanes;
+    if (p.lanes > n || n / p.lanes * p.lanes * 32 < n * 31)
+        for (int d = 1; d <= p.lanes && d <= n; ++d)
+            if (p.lanes % d == 0) {
+                const int used = n / d * d;
+                if (used * 32 >= best * 31) p.hl = d;
+                best = std::max(best, used);
+            }
+    p.parts = (int)std::min<int64_t>(n / p.hl, (int64_t)(p.lanes / p.hl) * s.num_seqs * tiles);
+    p.grid = p.parts * p.hl;
     const size_t slots = (size_t)2 * p.grid;
     p.o_bytes = up256(slots * p.rows * sh.head_dim * 4);
     p.ml_bytes = up256(slots * p.rows * 8);

@@ -131,12 +131,17 @@ __device__ __forceinline__ bool elect_one() {
 
 // Walks the items of this CTA, longest first: item y of the order is the one
 // with the y-th largest level, level = item index within the sequence plus the
-// items' worth of tokens before its first query.  Whole warp.
+// items' worth of tokens before its first query.  With more sequences than a
+// warp holds in registers, the search for a level would take longer than an
+// item: there the order is that of the sequences, each one's longest first, and
+// the walk goes through them once.  Whole warp.
 struct Schedule {
     static constexpr int kKept = 4;  // sequences per lane held in registers
     int n[kKept], p[kKept];
     int64_t total;
     int top;
+    int group;       // many sequences: the 32 that the walk has come to,
+    int64_t before;  // and the items before them
     __device__ __forceinline__ void get(const Args& a, int b, int& nn, int& pp, bool report_errors) const {
         nn = pp = 0;
         if (b >= a.s.num_seqs) return;
@@ -183,10 +188,12 @@ struct Schedule {
         for (int k = 0; k < kKept; ++k)
             if (k * 32 >= a.s.num_seqs) n[k] = p[k] = 0;
         top = __reduce_max_sync(0xffffffffu, t);
+        group = 0;
+        before = 0;
         total = above(a, 0) * a.hkv * a.splits;
     }
     // item f of the order (f < total)
-    __device__ __forceinline__ Item find(const Args& a, int64_t f) const {
+    __device__ __forceinline__ Item find(const Args& a, int64_t f) {
         const int lane = threadIdx.x & 31;
         int part = 0;
         if (a.splits > 1) {
@@ -194,28 +201,52 @@ struct Schedule {
             f /= a.splits;
         }
         const int64_t y = f <= 0x7FFFFFFF ? (int64_t)((uint32_t)f / (uint32_t)a.hkv) : f / a.hkv;
-        int lo = 0, hi = top - 1;  // the largest level with above(level) > y
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (above(a, mid) > y) lo = mid; else hi = mid - 1;
-        }
-        int64_t z = y - above(a, lo + 1);  // place among the level's items
         Item it;
         it.kvh = (int)(f - y * a.hkv);
         it.b = 0;
         int tile = 0;
-        for (int g = 0; g * 32 < a.s.num_seqs; ++g) {
-            int nn = 0, pp = 0;
-            pair(a, g, nn, pp);
-            const bool in = pp <= lo && lo < pp + nn;
-            const uint32_t m = __ballot_sync(0xffffffffu, in);
-            if (z < __popc(m)) {
-                const int l = __ffs(__ballot_sync(0xffffffffu, in && __popc(m & ((1u << lane) - 1)) == (int)z)) - 1;
-                it.b = g * 32 + l;
-                tile = lo - __shfl_sync(0xffffffffu, pp, l);
-                break;
+        if (a.s.num_seqs <= 32 * kKept) {
+            int lo = 0, hi = top - 1;  // the largest level with above(level) > y
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (above(a, mid) > y) lo = mid; else hi = mid - 1;
             }
-            z -= __popc(m);
+            int64_t z = y - above(a, lo + 1);  // place among the level's items
+            for (int g = 0; g * 32 < a.s.num_seqs; ++g) {
+                int nn = 0, pp = 0;
+                pair(a, g, nn, pp);
+                const bool in = pp <= lo && lo < pp + nn;
+                const uint32_t m = __ballot_sync(0xffffffffu, in);
+                if (z < __popc(m)) {
+                    const int l =
+                        __ffs(__ballot_sync(0xffffffffu, in && __popc(m & ((1u << lane) - 1)) == (int)z)) - 1;
+                    it.b = g * 32 + l;
+                    tile = lo - __shfl_sync(0xffffffffu, pp, l);
+                    break;
+                }
+                z -= __popc(m);
+            }
+        } else {
+            for (;; ++group) {  // y only grows from call to call
+                int nn = 0, pp = 0;
+                get(a, group * 32 + lane, nn, pp, false);
+                int in = nn;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, in, o);
+                    if (lane >= o) in += v;
+                }
+                const int z = (int)(y - before);  // place among the group's items
+                const uint32_t m = __ballot_sync(0xffffffffu, z < in);
+                if (m) {
+                    const int l = __ffs(m) - 1;
+                    it.b = group * 32 + l;
+                    tile = __shfl_sync(0xffffffffu, in, l) - 1 - z;
+                    break;
+                }
+                before += __shfl_sync(0xffffffffu, in, 31);
+                if (group * 32 >= a.s.num_seqs) break;  // (not reached: y < total)
+            }
         }
         const Seq q = load_seq(a.s, it.b, a.num_q);
         const int tok = tile * 2 * a.tpt;

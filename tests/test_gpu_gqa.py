@@ -185,6 +185,8 @@ PROMPTS = {
     "no tokens among them": ([40, 90, 0, 5], [0, 90, 0, 3], 8, 2, 128, False, 64),
     "long": ([2500], [2500], 8, 2, 128, False, 0),
     # few tokens far into their sequences: the keys are split and joined
+    "many": ([1 + 53 * i % 211 for i in range(150)], [1 + 53 * i % 211 for i in range(150)], 8, 2, 64, False, 0),
+    "many chunks": ([40 + 97 * i % 500 for i in range(170)], [i % 40 for i in range(170)], 4, 1, 128, False, 16),
     "far": ([5000, 3100, 40], [9, 70, 40], 16, 2, 128, False, 64),
     "far d64 pages of 16": ([5000, 3100, 1], [9, 70, 1], 12, 4, 64, False, 16),
     "far e4m3": ([5000, 3100, 40], [9, 70, 40], 16, 2, 128, True, 64),
