@@ -482,8 +482,9 @@ static dsa_status dense_gqa(bool prefill, const dsa_gqa_shape* shape, const void
     }
     dsa_status st = c.done();
     if (st != DSA_OK || num_q == 0) return st;
-    // a negative scale turns the row maxima around: the split kernel scales first
-    if (prefill && sm_scale >= 0.f)
+    // a negative scale turns the row maxima around, and 0 times a masked score is not
+    // -inf: the split kernel scales first and masks then
+    if (prefill && sm_scale > 0.f)
         return cuda_status(gqa::launch_prefill(sh, q, k_cache, v_cache, k_scale, v_scale, *seqs, num_q, sm_scale, out,
                                                lse, workspace, d_status, stream),
                            "dense_gqa_prefill launch");

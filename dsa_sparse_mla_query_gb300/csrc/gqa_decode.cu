@@ -155,6 +155,10 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, int rank, float2 v) {
         "r"(rank), "f"(v.x), "f"(v.y)
         : "memory");
 }
+// two dims of a row times 1 / sum; a row that sees no key (inv = 0) is 0 beside any values
+__device__ __forceinline__ uint32_t pack_row(float a, float b, float inv) {
+    return inv == 0.f ? 0u : pack_bf16(a * inv, b * inv);
+}
 __device__ __forceinline__ float warp_max_all(float x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
@@ -919,7 +923,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                         st_cluster(ring_u + C::kRows * D * 4 + (rank * C::kRows + r) * 8, own,
                                    make_float2(mm, write ? sum : -1.f));
                 } else if (write)
-                    *reinterpret_cast<uint32_t*>(a.out + at * D + d0 + e) = pack_bf16(v.x * inv, v.y * inv);
+                    *reinterpret_cast<uint32_t*>(a.out + at * D + d0 + e) = pack_row(v.x, v.y, inv);
             }
             if (d0 == 0) {
                 // a sum of -1: a row that is not to be written
@@ -974,7 +978,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
         const int tok = f / a.group, head = f - tok * a.group;
         const int64_t at = (int64_t)(p.q.q0 + tok) * (a.hkv * a.group) + p.lane % a.hkv * a.group + head;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint32_t*>(a.out + at * D + d0) = pack_bf16(acc.x * inv, acc.y * inv);
+        *reinterpret_cast<uint32_t*>(a.out + at * D + d0) = pack_row(acc.x, acc.y, inv);
         if (d0 == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
 }
@@ -1077,7 +1081,7 @@ __global__ void __launch_bounds__(128) gqa_join_kernel(const __grid_constant__ A
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const float x0 = (red[0][e] + red[1][e]) + (red[2][e] + red[3][e]);
         const float x1 = (red[0][e + 1] + red[1][e + 1]) + (red[2][e + 1] + red[3][e + 1]);
-        reinterpret_cast<uint32_t*>(a.out + at * D)[threadIdx.x] = pack_bf16(x0 * inv, x1 * inv);
+        reinterpret_cast<uint32_t*>(a.out + at * D)[threadIdx.x] = pack_row(x0, x1, inv);
     }
     if (a.lse && threadIdx.x == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }

@@ -91,7 +91,7 @@ struct Args {
     float* lse;
     dsa_seqs s;
     int32_t* d_status;
-    float scale_log2;  // > 0
+    float scale_log2;  // > 0: masked scores are -inf before they are scaled
     int32_t num_q, group, hkv, tpt;  // tpt: tokens per tile
     int32_t splits;   // key ranges per item; more than one: partial results
     const float *k_scale, *v_scale;  // e4m3: [rows][hkv]
@@ -1054,8 +1054,7 @@ cudaError_t launch_prefill(const dsa_gqa_shape& sh, const void* q, const void* k
     a.s = s;
     a.d_status = d_status;
     a.num_q = num_q;
-    // a scale of 0 stays a tiny positive one: masked scores are -inf before the scaling
-    a.scale_log2 = std::max(sm_scale * 1.4426950408889634f, 1e-30f);
+    a.scale_log2 = sm_scale * 1.4426950408889634f;
     const int box = s.page_table ? std::min(s.page_size, kKeys) : kKeys;
     const bool fp8 = sh.kv_dtype == DSA_FP8_E4M3_ROWSCALE;
     CUtensorMap qm, km, vm;

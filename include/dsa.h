@@ -442,7 +442,8 @@ dsa_status dense_gqa_workspace_size(const dsa_gqa_shape* shape, const dsa_seqs* 
  *        NULL): shape's caches, seqs->num_rows rows
  *   out  bf16 [num_q, num_heads, head_dim] contiguous; lse fp32
  *        [num_q, num_heads] or NULL
- * q_pos[t] = -1 sees no key: out = 0, lse = -inf.  Cache rows that no query of
+ * q_pos[t] = -1 sees no key: out = 0, lse = -inf, whatever the caches hold.
+ * Cache rows that no query of
  * a call may see are not used, whatever they hold; a non-finite key or value
  * that one query of a sequence sees can reach the sequence's other queries.
  * DSA_ERR_BAD_INPUT in *d_status: a position outside [-1, ctx_len) (its row is

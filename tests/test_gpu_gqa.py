@@ -295,6 +295,28 @@ def test_rows_outside_the_cache_are_reported_and_not_read(call):
 
 
 @pytest.mark.parametrize("call", list(CALLS))
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("many", [False, True])
+def test_rows_that_see_nothing_beside_values_that_are_not_finite(call, e4m3, many):
+    """A row without keys is zeros and -inf, whatever the other rows of its sequence see; so are the
+    sequences beside it what they are."""
+    B = 45 if many else 2
+    ctx, new = [3000] + [70] * (B - 1), [8] + [1] * (B - 1)
+    pos = [-1, 2999, 40, -1, 2000, -1, -1, 64] + [69] * (B - 1)
+    c = Case(ctx, new, 32, 8, 128, e4m3=e4m3, page=64, pos=pos)
+    rows = R.rows_of(c.table, 64, None, 0, 3000)
+    for j in (5, 1999, 2990):
+        if e4m3:
+            c.dv[rows[j]] = 0x7F
+        else:
+            c.dv[rows[j]] = math.nan if j == 5 else math.inf
+    c.run(call).check(seqs=range(1, B))
+    out, lse = c.out.cpu(), c.lse.cpu()
+    for i in (0, 3, 5, 6):
+        assert bool((out[i] == 0).all()) and bool((lse[i] == -math.inf).all())
+
+
+@pytest.mark.parametrize("call", list(CALLS))
 def test_large_scores(call):
     """Scores of hundreds: one key takes all the weight, the reference moves often."""
     Case([700, 90], [2, 90], 8, 2, 128, page=64, amp=60.0).run(call).check()
