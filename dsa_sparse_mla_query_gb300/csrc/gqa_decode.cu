@@ -128,16 +128,6 @@ __device__ __forceinline__ void lds128(uint32_t (&r)[4], uint32_t addr) {
 __device__ __forceinline__ void lds64(uint32_t (&r)[2], uint32_t addr) {
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
 }
-// four e4m3 codes (low byte first) -> two f16x2, exact
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
-    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
-        : "=r"(lo), "=r"(hi)
-        : "r"(x));
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-}
 __device__ __forceinline__ void bar_sync(int id, int n) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
@@ -608,7 +598,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
         float o[NT][KK][4];
         float m[NT][2];  // references: far below any score until a key is seen
         uint64_t l[NT];  // sums of the weights, a pair of columns
-        float vref = 0x1p-126f, vinv = 0x1p126f;  // FP8: V scales are held relative to vref, a power of two
+        // FP8: weights take V's scales along, relative to vref, a power of two, times 2^7: below 2^15 with
+        // the lazy reference, and exact to 11 bits down to 2^-21 of the largest
+        float vref = 0x1p-119f, vinv = 0x1p126f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             m[n][0] = m[n][1] = kNone;
@@ -722,19 +714,35 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
 #pragma unroll
                 for (int z = 0; z < 2; ++z) move = move || fmaxf(s[n][z], s[n][2 + z]) > m[n][z] + kLazy;
             }
-            if (FP8) move = move || fmaxf(fv0, fv1) > vref;
+            if (FP8) move = move || fmaxf(fabsf(fv0), fabsf(fv1)) > vref;
             if (__any_sync(0xffffffffu, move)) {
                 // rare: the rows' maxima over the slice's keys, and everything relative to them
                 float fv = 1.f;
                 if (FP8) {
-                    const float vtop = warp_max_all(fmaxf(fv0, fv1));
+                    // a row of zeros may have any scale (1 as a rule): it does not move the others'
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        uint32_t any = 0;
+#pragma unroll
+                        for (int e = 0; e < D / 64; ++e) {
+                            uint32_t y[4];
+                            lds128(y, chunk_addr<HB, kTile>(vb, r0 + g + 8 * z, (D / 64) * t + e));
+                            any |= y[0] | y[1] | y[2] | y[3];
+                        }
+                        any &= 0x7F7F7F7Fu;
+                        any |= __shfl_xor_sync(0xffffffffu, any, 1);
+                        any |= __shfl_xor_sync(0xffffffffu, any, 2);
+                        float& f = z ? fv1 : fv0;
+                        f = any || fabsf(f) == INFINITY ? f : 0.f;
+                    }
+                    const float vtop = warp_max_all(fmaxf(fabsf(fv0), fabsf(fv1)));
                     if (vtop > vref) {
                         // the next power of two (the largest finite one for an infinite scale)
                         const float nref = __uint_as_float(
                             min((__float_as_uint(vtop) & 0x7F800000u) + 0x00800000u, 0x7E800000u));
                         fv = vref * (1.f / nref);
                         vref = nref;
-                        vinv = 1.f / nref;
+                        vinv = 0x1p7f / nref;
                     }
                 }
 #pragma unroll
@@ -864,7 +872,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                 float mm = ml[col].x;
 #pragma unroll
                 for (int y = 1; y < KS; ++y) mm = fmaxf(mm, ml[y * C::kRows + col].x);
-                const float f = fast_exp2(m[n][c] - mm) * (FP8 ? vref : 1.f);
+                const float f = fast_exp2(m[n][c] - mm) * (FP8 ? vref * 0x1p-7f : 1.f);
 #pragma unroll
                 for (int k = 0; k < KK; ++k) {
                     o[n][k][c] *= f;

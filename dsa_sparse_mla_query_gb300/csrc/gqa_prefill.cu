@@ -46,7 +46,6 @@ constexpr int kConvertWarp = 16, kConverters = 8;  // e4m3 caches only
 constexpr float kLazy = 8.f;  // a row's reference moves when its maximum passes it by 2^8
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kItemSlots = 2;
-constexpr int kOutWarp = 32 * 128;  // outputs leave through shared memory: 64 dims of a warp's 32 rows at a time
 
 template <int D, bool FP8>
 struct Cfg {
@@ -65,7 +64,10 @@ struct Cfg {
     // of stage i have been used: by then no softmax reads the scales of stage i.
     static constexpr int kCodeStage = FP8 ? kKeys * D : 0;
     static constexpr int kScaleSlots = (kStages + 2) / 2;
-    static constexpr int kScaleBytes = FP8 ? (kScaleSlots + 2) * kKeys * 4 : 0;  // and those beside the codes
+    static constexpr int kScaleBytes = FP8 ? (kScaleSlots + 1) * 2 * kKeys * 4 : 0;  // and those beside the codes
+    // outputs leave through shared memory: so many dims of a warp's 32 rows at a time
+    static constexpr int kOutDims = FP8 ? 32 : 64;
+    static constexpr int kOutWarp = 32 * kOutDims * 2;
     static constexpr int kSmem = 2 * kQTile + kStages * kStage + 2 * kCodeStage + 8 * kOutWarp + kScaleBytes + 1024;
     static_assert(kSmem <= 232448, "a CTA's shared memory");
     // TMEM columns: two buffers of S per tile, then O; P takes the place of its S
@@ -99,18 +101,13 @@ struct Args {
     float2* part_ml;  // [splits][num_q heads]
 };
 
-// f times four e4m3 codes (low byte first) as two bf16 pairs; exact for f = 1
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t x, float f, uint32_t& lo, uint32_t& hi) {
+// four e4m3 codes (low byte first) as two bf16 pairs, exact
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t x, uint32_t& lo, uint32_t& hi) {
     uint32_t a, b;
-    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
-        : "=r"(a), "=r"(b)
-        : "r"(x));
+    e4m3x4_to_f16(x, a, b);
     const float2 u = __half22float2(*reinterpret_cast<__half2*>(&a)), v = __half22float2(*reinterpret_cast<__half2*>(&b));
-    float p, q, r, t;
-    unpack2(mul2(f32x2(u.x, u.y), f32x2(f, f)), p, q);
-    unpack2(mul2(f32x2(v.x, v.y), f32x2(f, f)), r, t);
-    lo = pack_bf16(p, q);
-    hi = pack_bf16(r, t);
+    lo = pack_bf16(u.x, u.y);
+    hi = pack_bf16(v.x, v.y);
 }
 
 // Shared-memory matrix descriptors as a low word, which holds the address and
@@ -307,9 +304,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     uint8_t* ring = smem + 2 * C::kQTile;
     uint8_t* codes = ring + C::kStages * C::kStage;
     uint8_t* stage_out = codes + 2 * C::kCodeStage;
-    float* scales = reinterpret_cast<float*>(stage_out + 8 * kOutWarp);  // [slot][kKeys]
-    float* code_scales = scales + C::kScaleSlots * kKeys;                // [code stage][kKeys]
-    Shared& sh = *reinterpret_cast<Shared*>(stage_out + 8 * kOutWarp + C::kScaleBytes);
+    float* scales = reinterpret_cast<float*>(stage_out + 8 * C::kOutWarp);  // [slot][keys', values'][kKeys]
+    float* code_scales = scales + C::kScaleSlots * 2 * kKeys;               // [keys', values'][kKeys]
+    Shared& sh = *reinterpret_cast<Shared*>(stage_out + 8 * C::kOutWarp + C::kScaleBytes);
     volatile int* abort_flag = sh.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -475,15 +472,18 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                                 tma_load_4d(dst + h * (kKeys * 128), map, 0, cur, h, it.kvh, bar);
                     }
                     if (FP8) {
-                        const float* from = map == &kmap ? a.k_scale : a.v_scale;
+                        // both scales come with the keys: the weights take the values' before the values' turn
+                        if (map == &kmap)
 #pragma unroll
-                        for (int y = 0; y < kKeys / 32; ++y) {
-                            const int key = y * 32 + lane;
-                            const int row = __shfl_sync(0xffffffffu, cur, l + (key >> shift));
-                            if (row >= 0 && it.key0 + i * kKeys + key < it.limit)
-                                ptx::cp_async4(code_scales + st * kKeys + key,
-                                               from + ((int64_t)row + (key & (R - 1))) * a.hkv + it.kvh);
-                        }
+                            for (int y = 0; y < kKeys / 32; ++y) {
+                                const int key = y * 32 + lane;
+                                const int row = __shfl_sync(0xffffffffu, cur, l + (key >> shift));
+                                if (row >= 0 && it.key0 + i * kKeys + key < it.limit) {
+                                    const int64_t at = ((int64_t)row + (key & (R - 1))) * a.hkv + it.kvh;
+                                    ptx::cp_async4(code_scales + key, a.k_scale + at);
+                                    ptx::cp_async4(code_scales + kKeys + key, a.v_scale + at);
+                                }
+                            }
                         ptx::cp_async_arrive_noinc(bar);
                     }
                     return true;
@@ -527,15 +527,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             }
         } else if (FP8 && warp >= kConvertWarp) {
             // ------------------------------------------------------------ converts e4m3 tiles
-            // Codes to bf16, in the layout that TMA gives a bf16 tile: keys' exactly, their
-            // scales go to the scores; values' times their scale, one rounding (by up to 2^-9
-            // of itself, as the weights', for the softmax threads' 64 loads of a scale each
-            // would cost a third of shared memory's rate again).
-            // Rows behind the last key become zeros: whatever lies there must not
-            // reach the products, where 0 * inf is not 0.  2,048 tokens behind 30,000,
-            // 64/8 heads of 128: 942 TFLOP/s, bound by the conversion, 2,400 cycles a tile
-            // where a step's products take 2,600 for two (four converting warps: 729; four
-            // for the keys and four for the values: 833).
+            // Codes to bf16, exactly, in the layout that TMA gives a bf16 tile: the keys' scales go
+            // to the scores, the values' to the weights.  Rows behind the last key become zeros: whatever lies there must not
+            // reach the products, where 0 * inf is not 0.
             const int tid = threadIdx.x - kConvertWarp * 32;
             constexpr int kChunks = D / 16;                      // 16-code chunks of a row
             constexpr int kRowsAt = 32 * kConverters / kChunks;  // rows that the warps take at once
@@ -554,11 +548,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                     if (!ok) break;
                     const uint8_t* src = codes + cc.st * C::kCodeStage;
                     uint8_t* dst = ring + c.st * C::kStage;
-                    const float* cs = code_scales + cc.st * kKeys;
                     if (what == 0) {
                         // this slot's last stage has been used: its values' place in the ring, or a later one,
                         // is the one that has just been waited for (see Cfg)
-                        if (tid < kKeys) scales[slot * kKeys + tid] = tid < rows ? cs[tid] * a.scale_log2 : 0.f;
+                        if (tid < kKeys) {
+                            scales[slot * 2 * kKeys + tid] = tid < rows ? code_scales[tid] * a.scale_log2 : 0.f;
+                            scales[slot * 2 * kKeys + kKeys + tid] = tid < rows ? code_scales[kKeys + tid] : 0.f;
+                        }
                         slot = slot + 1 == C::kScaleSlots ? 0 : slot + 1;
                     }
 #pragma unroll
@@ -569,11 +565,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                         uint4 x = *reinterpret_cast<const uint4*>(src + from);
                         if (row >= rows) x = make_uint4(0u, 0u, 0u, 0u);
                         uint32_t y[8];
-                        const float f = what == 0 ? 1.f : row < rows ? cs[row] : 0.f;
-                        e4m3x4_to_bf16(x.x, f, y[0], y[1]);
-                        e4m3x4_to_bf16(x.y, f, y[2], y[3]);
-                        e4m3x4_to_bf16(x.z, f, y[4], y[5]);
-                        e4m3x4_to_bf16(x.w, f, y[6], y[7]);
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) e4m3x4_to_bf16(xs[e], y[2 * e], y[2 * e + 1]);
                         uint8_t* to = dst + (ch >> 2) * (kKeys * 128) + row * 128;
                         const int c16 = (ch & 3) * 2;
                         *reinterpret_cast<uint4*>(to + ((c16 ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
@@ -725,7 +719,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 ptx::tmem_ld32_async(ts + 32, s[1]);
                 ptx::tmem_wait_ld32(s[0]);
                 ptx::tmem_wait_ld32(s[1]);
-                const float* sc = scales + sl * kKeys + (j & 1) * kStep;  // e4m3: the step's keys' (times log2 e)
+                const float* sc = scales + sl * 2 * kKeys + (j & 1) * kStep;  // e4m3: the step's keys' (times log2 e)
                 if (FP8) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
@@ -782,6 +776,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 const float mm = m == -INFINITY ? 0.f : -m;
                 const uint64_t nm2 = f32x2(mm, mm);
                 uint32_t pk[32];
+                ulonglong2 vs = make_ulonglong2(0, 0);
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -793,7 +788,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                         p0 = fast_exp2(p0);
                         p1 = fast_exp2(p1);
                         l2[(e >> 1) & 1] = add2(l2[(e >> 1) & 1], f32x2(p0, p1));
-                        // a weight rounded to bf16 is off by up to 2^-9 of itself; the sum keeps fp32
+                        if (FP8) {
+                            if ((e & 2) == 0) vs = *reinterpret_cast<const ulonglong2*>(sc + kKeys + 32 * k + e);
+                            unpack2(mul2(f32x2(p0, p1), e & 2 ? vs.y : vs.x), p0, p1);
+                        }
+                        // a weight (times its value's scale) rounded to bf16 is off by up to 2^-9 of itself;
+                        // the sum keeps fp32
                         pk[16 * k + e / 2] = pack_bf16(p0, p1);
                     }
                 if (FP8 && (j & 1)) sl = sl + 1 == C::kScaleSlots ? 0 : sl + 1;
@@ -840,28 +840,34 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 if (!ok) break;
                 ++o_use;
                 ptx::tc_fence_after();
-                // 64 dims at a time: a thread's row into the warp's 32 x 128 bytes (16-byte pieces
-                // turned by the row: no bank conflicts), then 4 rows of 128 bytes a store
-                uint8_t* mine = stage_out + warp * kOutWarp;
+                // kOutDims at a time: a thread's row into the warp's 32 rows (16-byte pieces turned by
+                // the row: no bank conflicts), then whole lines of 128 (or 64) bytes a store
+                constexpr int OD = C::kOutDims, kPieces = OD / 8;  // 16-byte pieces of a row
+                constexpr int kAtOnce = 32 / kPieces;              // rows a store
+                uint8_t* mine = stage_out + warp * C::kOutWarp;
+                auto piece = [&](int row, int c) {
+                    return row * OD * 2 + ((c ^ (OD == 64 ? row & 7 : (row >> 1) & 3)) << 4);
+                };
                 const uint32_t alive = __ballot_sync(0xffffffffu, live);
                 const uint64_t inv2 = f32x2(inv, inv);
-                __nv_bfloat16* to_row[8];
+                const int part = lane % kPieces, first = lane / kPieces;
+                __nv_bfloat16* to_row[kPieces];
 #pragma unroll
-                for (int y = 0; y < 8; ++y)
-                    to_row[y] = a.out + __shfl_sync(0xffffffffu, at, 4 * y + (lane >> 3)) * D + 8 * (lane & 7);
+                for (int y = 0; y < kPieces; ++y)
+                    to_row[y] = a.out + __shfl_sync(0xffffffffu, at, kAtOnce * y + first) * D + 8 * part;
 #pragma unroll 1
-                for (int k = 0; k < D / 64; ++k) {
-                    uint32_t o[2][32];
-                    ptx::tmem_ld32_async(to + 64 * k, o[0]);
-                    ptx::tmem_ld32_async(to + 64 * k + 32, o[1]);
-                    ptx::tmem_wait_ld32(o[0]);
-                    ptx::tmem_wait_ld32(o[1]);
+                for (int k = 0; k < D / OD; ++k) {
+                    uint32_t o[OD / 32][32];
+#pragma unroll
+                    for (int z = 0; z < OD / 32; ++z) ptx::tmem_ld32_async(to + OD * k + 32 * z, o[z]);
+#pragma unroll
+                    for (int z = 0; z < OD / 32; ++z) ptx::tmem_wait_ld32(o[z]);
                     if (l == 0.f) {  // no key: whatever O holds
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) o[e >> 5][e & 31] = 0u;
+                        for (int e = 0; e < OD; ++e) o[e >> 5][e & 31] = 0u;
                     }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < kPieces; ++e) {
                         uint32_t y[4];
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
@@ -870,20 +876,17 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                             unpack2(mul2(f32x2(__uint_as_float(w[0]), __uint_as_float(w[1])), inv2), p, q);
                             y[z] = pack_bf16(p, q);
                         }
-                        *reinterpret_cast<uint4*>(mine + lane * 128 + ((e ^ (lane & 7)) << 4)) =
-                            make_uint4(y[0], y[1], y[2], y[3]);
+                        *reinterpret_cast<uint4*>(mine + piece(lane, e)) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                     __syncwarp();
-                    uint4 v[8];
+                    uint4 v[kPieces];
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        const int row = 4 * y + (lane >> 3);
-                        v[y] = *reinterpret_cast<const uint4*>(mine + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
-                    }
+                    for (int y = 0; y < kPieces; ++y)
+                        v[y] = *reinterpret_cast<const uint4*>(mine + piece(kAtOnce * y + first, part));
                     __syncwarp();
 #pragma unroll
-                    for (int y = 0; y < 8; ++y)
-                        if ((alive >> (4 * y + (lane >> 3))) & 1) *reinterpret_cast<uint4*>(to_row[y] + 64 * k) = v[y];
+                    for (int y = 0; y < kPieces; ++y)
+                        if ((alive >> (kAtOnce * y + first)) & 1) *reinterpret_cast<uint4*>(to_row[y] + OD * k) = v[y];
                 }
                 ptx::tc_fence_before();
                 __syncwarp();

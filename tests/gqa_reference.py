@@ -9,7 +9,6 @@ out = sum p_j v_j.  Roundings of the kernels, each at most half a step
   - a score's fp32 sum of D exact products: D 2^-24 scale sum_d |q_d k_d|, and
     a few roundings of it (the scale's, the subtraction of the reference m):
     8 * 2^-24 (|s| + |m|), log2 units; it changes p_j by that much, relatively;
-  - over e4m3 caches a prompt's values, scale * code, to bf16: sum_j 2^-8 p_j |v_j| again;
   - fp32 sums of n weights and of n products: n 2^-24 of the sum, counted as
     n / 16 + 64 additions in a row (a lane adds every 16th key or fewer).
 """
@@ -38,7 +37,7 @@ def values(cache, scale):
     return cache.view(torch.float8_e4m3fn).double() * scale.double()[..., None]
 
 
-def attend(q, k, v, pos, sm_scale, rounded_values=False):
+def attend(q, k, v, pos, sm_scale):
     """q [t, hq, d], k and v [n, hkv, d] in fp64, pos [t] (-1: no key).  Returns out, lse and the
     allowed errors of both."""
     t, hq, d = q.shape
@@ -63,7 +62,7 @@ def attend(q, k, v, pos, sm_scale, rounded_values=False):
             av = p @ vv.abs()
             out[i, h] = p @ vv
             lse[i, h] = top
-            tol[i, h] = 2.0 ** -8 * out[i, h].abs() + ((2.0 ** -7 if rounded_values else 2.0 ** -8) + 2 * score + 2 * adds) * av
+            tol[i, h] = 2.0 ** -8 * out[i, h].abs() + (2.0 ** -8 + 2 * score + 2 * adds) * av
             ltol[i, h] = 2 * score + adds + 8 * eps * (1 + abs(float(top)))
     return out, lse, tol, ltol
 

@@ -111,7 +111,6 @@ class Case:
         return self
 
     def again(self, call, stream=None, lse=True):
-        self.rounded_values = self.e4m3 and call == "prefill"
         CALLS[call](self.shape, self.dq, self.dk, self.dv, self.dks, self.dvs, self.seqs, self.num_q, self.sm_scale,
                     self.out, self.lse if lse else None, self.ws, self.ws_bytes, d_status=self.status, stream=stream)
 
@@ -126,8 +125,7 @@ class Case:
             pick = range(m) if m <= max_rows else sorted({0, 1, m - 2, m - 1} | {i * m // 16 for i in range(16)})
             idx = torch.tensor([self.q_start[b] + i for i in pick], dtype=torch.long)
             pos = [self.pos[int(i)] for i in idx]
-            ref, rl, tol, ltol = R.attend(self.q[idx].double(), k[rows], v[rows], pos, self.sm_scale,
-                                          self.rounded_values)
+            ref, rl, tol, ltol = R.attend(self.q[idx].double(), k[rows], v[rows], pos, self.sm_scale)
             err = (out[idx] - ref).abs()
             assert bool((err <= tol).all()), f"sequence {b}: off by {float((err - tol).max()):.3g} more than allowed"
             for i, p in enumerate(pos):
@@ -314,6 +312,26 @@ def test_rows_that_see_nothing_beside_values_that_are_not_finite(call, e4m3, man
     out, lse = c.out.cpu(), c.lse.cpu()
     for i in (0, 3, 5, 6):
         assert bool((out[i] == 0).all()) and bool((lse[i] == -math.inf).all())
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+@pytest.mark.parametrize("where", ["first", "last", "many"])
+def test_value_scales_far_apart(call, where):
+    """e4m3: rows of zeros with a scale 2^20 times the others', and scales that grow along the sequence:
+    a weight times its scale keeps 11 bits down to 2^-21 of the largest such product."""
+    c = Case([700, 130], [3, 130], 16, 2, 128, e4m3=True, page=64)
+    for b in range(2):
+        rows = R.rows_of(c.table, 64, None, b, c.ctx[b])
+        n = len(rows)
+        c.vs[rows] *= 2.0 ** -20
+        if where == "many":
+            c.vs[rows] *= (2.0 ** (20 * torch.arange(n) // n).float())[:, None]
+        else:
+            at = rows[:2] if where == "first" else rows[n // 2:n // 2 + 2]
+            c.v[at] = 0
+            c.vs[at] = 1.0
+    c.dv, c.dvs = c.v.to(DEV), c.vs.to(DEV)
+    c.run(call).check()
 
 
 @pytest.mark.parametrize("call", list(CALLS))
@@ -593,8 +611,7 @@ def test_prompt_then_tokens(e4m3):
                 rk = R.rotate(xs[b][:done[b], hq:hq + hkv].double(), torch.arange(done[b]).int(), inv, 64, True)
                 _check_rows(k[r], rk, "K")
             m = new[b]
-            ref, rl, tol, ltol = R.attend(q[at:at + m].cpu().double(), k[r], v[r], pos[at:at + m], scale,
-                                          e4m3 and max(new) > 1)
+            ref, rl, tol, ltol = R.attend(q[at:at + m].cpu().double(), k[r], v[r], pos[at:at + m], scale)
             assert bool(((out[at:at + m].cpu().double() - ref).abs() <= tol).all()), (step, b)
             assert bool(((lse[at:at + m].cpu().double() - rl).abs() <= ltol).all()), (step, b)
             at += m
