@@ -61,6 +61,7 @@ struct Cfg {
     static constexpr int kScaleBytes = FP8 ? 2 * kTile * 4 : 0;
     static constexpr int kScratch = 4 * 8 * D * 4;  // four key slices' outputs of 8 rows
     static constexpr int kMl = KS * kRows * 8;
+    static constexpr int kStart = KS == 8 ? 8 : 4;  // what a sequence's start and end cost, in tiles
     static constexpr bool kQShared = NT > 2;        // query fragments in shared memory, else in registers
     static constexpr int kQBytes = kQShared ? (D / 16) * NT * 32 * 8 : 0;
     static constexpr int kMisc = 256 + kRows * 8;
@@ -180,8 +181,9 @@ struct Piece {
     int64_t base;            // first row of a contiguous sequence
 };
 
-// The tiles of all lanes of a column in a row, dealt to its CTAs in pieces of
-// `each`, the first `more` CTAs one more.
+// The tiles of all lanes of a column in a row, before each sequence's START
+// units for what its start and end cost, dealt to the column's CTAs in pieces
+// of `each` units, the first `more` CTAs one more.
 struct Deal {
     int64_t total, each;
     int more;
@@ -196,7 +198,7 @@ struct Deal {
         more = (int)(n - each * p);
     }
     __device__ __forceinline__ int64_t first(int c) const { return each * c + min(c, more); }
-    // the CTA that has tile x
+    // the CTA that has unit x
     __device__ __forceinline__ int owner(int64_t x) const {
         const int64_t big = (each + 1) * more;
         if (x < big) return (int)(x / (each + 1));
@@ -204,11 +206,15 @@ struct Deal {
     }
 };
 
-template <int TILE, int ROWS>
+template <int TILE, int ROWS, int START>
 struct Walk {
     Deal deal;
     int64_t r0, left;
-    int u, b, i;
+    int u, b, i;  // the place in the walk: tile i of sequence b, from -START
+    __device__ __forceinline__ int units_of(const Seq& q) const {
+        const int n = tiles_of<TILE>(q);
+        return n ? n + START : 0;
+    }
     __device__ __forceinline__ void init(const Args& a) {
         const int lane = threadIdx.x & 31;
         const int B = a.s.num_seqs;
@@ -237,7 +243,7 @@ struct Walk {
                 v[x] = 0;
                 if (k + x < per && bb < B) {
                     const Seq q = load_seq(a.s, bb, a.num_q);
-                    v[x] = tiles_of<TILE>(q);
+                    v[x] = units_of(q);
                     if (!q.ok && blockIdx.x == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
                 }
             }
@@ -267,14 +273,14 @@ struct Walk {
         int64_t off = rem - __shfl_sync(0xffffffffu, incl - mine, l);
         if (per == 1) {
             b = l;
-            i = (int)off;
+            i = (int)off - START;
             return;
         }
         // within that lane's run
         for (int k0 = 0; k0 < per; k0 += 32) {
             const int bb = l * per + k0 + lane;
             int v = 0;
-            if (k0 + lane < per && bb < B) v = tiles_of<TILE>(load_seq(a.s, bb, a.num_q));
+            if (k0 + lane < per && bb < B) v = units_of(load_seq(a.s, bb, a.num_q));
             int in = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -285,7 +291,7 @@ struct Walk {
             if (h) {
                 const int x = __ffs(h) - 1;
                 b = l * per + k0 + x;
-                i = (int)(off - __shfl_sync(0xffffffffu, in - v, x));
+                i = (int)(off - __shfl_sync(0xffffffffu, in - v, x)) - START;
                 break;
             }
             off -= __shfl_sync(0xffffffffu, in, 31);
@@ -302,20 +308,24 @@ struct Walk {
             const int cnt = tiles_of<TILE>(q);
             if (cnt == 0) {
                 ++b;
+                i = -START;
                 continue;
             }
             int take = (int)min((int64_t)(cnt - i), left);
+            left -= take;
+            take += min(i, 0);  // the tiles among them
+            i = max(i, 0);
+            if (take <= 0) return false;  // the deal ends before the sequence's first tile
             p.lane = a.cluster ? u : blockIdx.x % a.hl + a.hl * u;
             p.b = b;
             p.q = q;
             p.front = i > 0;
             p.back = i + take < cnt;
-            left -= take;
             // (a cluster's CTA without tiles still has a share of nothing)
             if (a.cluster && (int64_t)cnt * (blockIdx.x % a.cluster + 1) / a.cluster == i) take = 0;
             p.i0 = i;
             p.i1 = i + take;
-            i = 0;
+            i = -START;
             ++b;
             p.row0 = p.lane / a.hkv * ROWS;
             const int64_t rows = (int64_t)q.nq * a.group;
@@ -371,7 +381,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
     __syncthreads();
     pdl_enter();
 
-    Walk<kTile, C::kRows> w;
+    Walk<kTile, C::kRows, C::kStart> w;
     Piece p;
     bool had = false;  // a computing warp had a piece
 
@@ -860,11 +870,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
         if (shared) cluster_wait();  // every CTA's ring is at rest: partials may go there
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            // [key slice][8 rows][D], the dims of rows 2t and 2t + 1 turned by 8 t: no bank conflicts.
-            // Eight slices: the upper four hand theirs to the lower four first.
-            auto place = [&](int c, int k, int y) {
-                const int d = FP8 ? (D / 8) * g + 2 * k + y : 16 * k + g + 8 * y;
-                return ((ks & 3) * 8 + 2 * t + c) * D + (d ^ (t << 3));
+            // [key slice][8 rows][D], a row's dims turned so that a warp's stores meet no bank twice
+            auto turn = [](int row, int d) {  // rows 2t, 2t + 1 alike
+                return FP8 ? (row >> 1) | ((d >> 5) << 2) : (row >> 1) << 3;
             };
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -877,24 +885,41 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                 for (int k = 0; k < KK; ++k) {
                     o[n][k][c] *= f;
                     o[n][k][2 + c] *= f;
-                    if (KS == 4 || ks >= 4) {
-                        scratch[place(c, k, 0)] = o[n][k][c];
-                        scratch[place(c, k, 1)] = o[n][k][2 + c];
-                    }
                 }
             }
-            bar_sync(1, 32 * KS);
             if (KS == 8) {
-                if (ks < 4)
+                // the upper four slices hand theirs to the lower four, lane to lane
+                float4* mine = reinterpret_cast<float4*>(scratch) + (ks & 3) * (KK * 32) + lane;
+                if (ks >= 4) {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int k = 0; k < KK; ++k) {
-                            scratch[place(c, k, 0)] += o[n][k][c];
-                            scratch[place(c, k, 1)] += o[n][k][2 + c];
-                        }
+                    for (int k = 0; k < KK; ++k)
+                        mine[k * 32] = make_float4(o[n][k][0], o[n][k][1], o[n][k][2], o[n][k][3]);
+                }
                 bar_sync(1, 32 * KS);
+                if (ks < 4) {
+                    float4 x[KK];
+#pragma unroll
+                    for (int k = 0; k < KK; ++k) x[k] = mine[k * 32];
+#pragma unroll
+                    for (int k = 0; k < KK; ++k) {
+                        o[n][k][0] += x[k].x, o[n][k][1] += x[k].y;
+                        o[n][k][2] += x[k].z, o[n][k][3] += x[k].w;
+                    }
+                    __syncwarp();
+                }
             }
+            if (ks < 4) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int k = 0; k < KK; ++k)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int row = 2 * t + c, d = FP8 ? (D / 8) * g + 2 * k + y : 16 * k + g + 8 * y;
+                            scratch[(ks * 8 + row) * D + (d ^ turn(row, d))] = o[n][k][2 * y + c];
+                        }
+            }
+            bar_sync(1, 32 * KS);
             const int r = n * 8 + hr;
             float mm = ml[r].x;
 #pragma unroll
@@ -915,9 +940,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                 float2 v = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const float2 z = *reinterpret_cast<const float2*>(scratch + (y * 8 + hr) * D +
-                                                                      ((d0 + e) ^ (((hr >> 1) & 3) << 3)));
-                    v.x += z.x, v.y += z.y;
+                    const int x = turn(hr, d0 + e);
+                    const float2 z =
+                        *reinterpret_cast<const float2*>(scratch + (y * 8 + hr) * D + ((d0 + e) ^ (x & ~1)));
+                    v.x += x & 1 ? z.y : z.x, v.y += x & 1 ? z.x : z.y;
                 }
                 if (cut)
                     *reinterpret_cast<float2*>(a.part_o + (slot * C::kRows + r) * D + d0 + e) = v;
