@@ -64,7 +64,7 @@ struct Cfg {
     static constexpr int kStart = KS == 8 ? 8 : 4;  // what a sequence's start and end cost, in tiles
     static constexpr bool kQShared = NT > 2;        // query fragments in shared memory, else in registers
     static constexpr int kQBytes = kQShared ? (D / 16) * NT * 32 * 8 : 0;
-    static constexpr int kMisc = 256 + kRows * 8;
+    static constexpr int kMisc = 256 + kRows * 24;
     static constexpr int kFixed = kScratch + kMl + kQBytes + kMisc;
     static constexpr int kBudget = (kOcc == 2 ? 115712 : 232448) - kFixed;
     static constexpr int kFit = kBudget / (kStage + kScaleBytes);
@@ -206,11 +206,13 @@ struct Deal {
     }
 };
 
-template <int TILE, int ROWS, int START>
+template <int TILE, int ROWS, int START, bool KEEP>
 struct Walk {
     Deal deal;
     int64_t r0, left;
     int u, b, i;  // the place in the walk: tile i of sequence b, from -START
+    Seq kept;     // of the lane's of the 32 sequences around b
+    int kept_of;
     __device__ __forceinline__ int units_of(const Seq& q) const {
         const int n = tiles_of<TILE>(q);
         return n ? n + START : 0;
@@ -218,6 +220,7 @@ struct Walk {
     __device__ __forceinline__ void init(const Args& a) {
         const int lane = threadIdx.x & 31;
         const int B = a.s.num_seqs;
+        kept_of = -1;
         if (a.cluster) {
             // the cluster's (lane, sequence), this CTA's share of its tiles
             const int seg = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
@@ -297,6 +300,23 @@ struct Walk {
             off -= __shfl_sync(0xffffffffu, in, 31);
         }
     }
+    // sequence b's counts, from those that the lanes hold (whole warp); a CTA that
+    // shares its SM has no registers for them, and another's work to hide the loads
+    __device__ __forceinline__ Seq seq(const Args& a) {
+        if (!KEEP) return load_seq(a.s, b, a.num_q);
+        if (kept_of != b >> 5) {
+            kept_of = b >> 5;
+            const int bb = (b & ~31) + (threadIdx.x & 31);
+            kept = bb < a.s.num_seqs ? load_seq(a.s, bb, a.num_q) : Seq{0, 0, 0, false};
+            if (!kept.ok) kept.nq = 0;
+        }
+        Seq q;
+        q.ctx = __shfl_sync(0xffffffffu, kept.ctx, b & 31);
+        q.q0 = __shfl_sync(0xffffffffu, kept.q0, b & 31);
+        q.nq = __shfl_sync(0xffffffffu, kept.nq, b & 31);
+        q.ok = q.nq > 0;
+        return q;
+    }
     // the next piece, without its limit: `pos` is the lane's share of that
     __device__ __forceinline__ bool begin(const Args& a, Piece& p, int& pos) {
         while (left > 0) {
@@ -304,7 +324,7 @@ struct Walk {
                 b = 0;
                 ++u;
             }
-            const Seq q = load_seq(a.s, b, a.num_q);
+            const Seq q = seq(a);
             const int cnt = tiles_of<TILE>(q);
             if (cnt == 0) {
                 ++b;
@@ -362,9 +382,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
     uint8_t* q_sh = reinterpret_cast<uint8_t*>(ml) + C::kMl;  // [D / 16][NT / 2][lane] two tiles' fragments
     float* fac_sh = reinterpret_cast<float*>(q_sh + C::kQBytes);  // [rows]
     int* pos_sh = reinterpret_cast<int*>(fac_sh + C::kRows);      // [rows]
-    uint64_t* full = reinterpret_cast<uint64_t*>(pos_sh + C::kRows);
+    float2* total = reinterpret_cast<float2*>(pos_sh + C::kRows);   // [rows] reference and sum of all slices
+    int64_t* at_sh = reinterpret_cast<int64_t*>(total + C::kRows);  // [rows] row of out and lse
+    uint64_t* full = reinterpret_cast<uint64_t*>(at_sh + C::kRows);
     uint64_t* empty = full + C::kStages;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + C::kStages);
+    float* vref_sh = reinterpret_cast<float*>(empty + C::kStages + 1);  // [slices] e4m3
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -381,7 +404,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
     __syncthreads();
     pdl_enter();
 
-    Walk<kTile, C::kRows, C::kStart> w;
+    Walk<kTile, C::kRows, C::kStart, C::kOcc == 1> w;
     Piece p;
     bool had = false;  // a computing warp had a piece
 
@@ -574,16 +597,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
         w.finish(p, seen);
         // the rows' positions; -2: not to be written
         if (threadIdx.x < C::kRows) {
-            const int tok = (p.row0 + (int)threadIdx.x) / a.group;
-            int pos = -2;
-            if (tok < p.q.nq) {
-                pos = __ldg(a.s.q_pos + p.q.q0 + tok);
-                if (pos < -1 || pos >= p.q.ctx) {
-                    if (p.i0 == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
-                    pos = -2;
-                }
+            const int f = p.row0 + (int)threadIdx.x, tok = f / a.group;
+            int pos = __shfl_sync(C::kRows >= 32 ? 0xffffffffu : (1u << (C::kRows & 31)) - 1, seen, (tok - p.tok0) & 31);
+            if (tok >= p.q.nq) {
+                pos = -2;
+            } else if (pos < -1 || pos >= p.q.ctx) {
+                if (p.i0 == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
+                pos = -2;
             }
             pos_sh[threadIdx.x] = pos;
+            at_sh[threadIdx.x] = (int64_t)(p.q.q0 + tok) * (a.hkv * a.group) + kvh * a.group + (f - tok * a.group);
         }
         const int end = min(p.i1, (p.limit + kTile - 1) / kTile);
         bar_sync(1, 32 * KS);
@@ -848,48 +871,69 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
             cluster_arrive();  // this warp reads the ring no more
         }
         // ---- the key slices meet
+        {
+            float x[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float x[2];
-            unpack2(l[n], x[0], x[1]);
+            for (int n = 0; n < NT; ++n) unpack2(l[n], x[n][0], x[n][1]);
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                x[z] += __shfl_xor_sync(0xffffffffu, x[z], 4);
-                x[z] += __shfl_xor_sync(0xffffffffu, x[z], 8);
-                x[z] += __shfl_xor_sync(0xffffffffu, x[z], 16);
-                if (g == 0) ml[ks * C::kRows + n * 8 + 2 * t + z] = make_float2(m[n][z], x[z]);
+            for (int y = 4; y < 32; y <<= 1)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) x[n][z] += __shfl_xor_sync(0xffffffffu, x[n][z], y);
+            if (g == 0)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) ml[ks * C::kRows + n * 8 + 2 * t + z] = make_float2(m[n][z], x[n][z]);
+        }
+        if (FP8 && lane == 0) vref_sh[ks] = vref * 0x1p-7f;
+        const bool cut = !a.cluster && (p.front || p.back), shared = a.cluster > 1;
+        const int64_t slot = (int64_t)blockIdx.x * 2 + (p.front ? 0 : 1);
+        const int rank = shared ? blockIdx.x % a.cluster : 0;
+        bar_sync(1, 32 * KS);
+        // a row's reference and sum over the slices, and what each slice's outputs are multiplied by
+        if (threadIdx.x < C::kRows * KS) {
+            const int r = threadIdx.x / KS, y = threadIdx.x % KS;
+            const float2 v = ml[y * C::kRows + r];
+            float mm = v.x;
+#pragma unroll
+            for (int z = 1; z < KS; z <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, z));
+            const float f = fast_exp2(v.x - mm);
+            float sum = f * v.y;
+#pragma unroll
+            for (int z = 1; z < KS; z <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, z);
+            ml[y * C::kRows + r].x = FP8 ? f * vref_sh[y] : f;
+            if (y == 0) {
+                const bool write = ok && pos_sh[r] >= -1;
+                // a sum of -1: a row that is not to be written
+                const float2 tot = make_float2(mm, write ? sum : -1.f);
+                total[r] = tot;
+                if (cut) a.part_ml[slot * C::kRows + r] = tot;
+                else if (!shared && write && a.lse) a.lse[at_sh[r]] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * kLn2;
             }
         }
         bar_sync(1, 32 * KS);
         constexpr int kDims = D / (4 * KS);  // dims per thread of the sum: 8 rows x 4 KS threads
         const int hr = threadIdx.x / (4 * KS);
         const int d0 = threadIdx.x % (4 * KS) * kDims;
-        const bool cut = !a.cluster && (p.front || p.back), shared = a.cluster > 1;
-        const int64_t slot = (int64_t)blockIdx.x * 2 + (p.front ? 0 : 1);
-        const int rank = shared ? blockIdx.x % a.cluster : 0;
         if (shared) cluster_wait();  // every CTA's ring is at rest: partials may go there
+        // [key slice][8 rows][D], a row's dims turned so that a warp's stores meet no bank twice
+        auto turn = [](int row, int d) {  // rows 2t, 2t + 1 alike
+            return FP8 ? (row >> 1) | ((d >> 5) << 2) : (row >> 1) << 3;
+        };
+        float4* mine = reinterpret_cast<float4*>(scratch) + (ks & 3) * (KK * 32) + lane;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            // [key slice][8 rows][D], a row's dims turned so that a warp's stores meet no bank twice
-            auto turn = [](int row, int d) {  // rows 2t, 2t + 1 alike
-                return FP8 ? (row >> 1) | ((d >> 5) << 2) : (row >> 1) << 3;
-            };
+            const int col = n * 8 + 2 * t;
+            const uint64_t f = f32x2(ml[ks * C::kRows + col].x, ml[ks * C::kRows + col + 1].x);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int col = n * 8 + 2 * t + c;
-                float mm = ml[col].x;
-#pragma unroll
-                for (int y = 1; y < KS; ++y) mm = fmaxf(mm, ml[y * C::kRows + col].x);
-                const float f = fast_exp2(m[n][c] - mm) * (FP8 ? vref * 0x1p-7f : 1.f);
-#pragma unroll
-                for (int k = 0; k < KK; ++k) {
-                    o[n][k][c] *= f;
-                    o[n][k][2 + c] *= f;
-                }
+            for (int k = 0; k < KK; ++k) {
+                unpack2(mul2(f32x2(o[n][k][0], o[n][k][1]), f), o[n][k][0], o[n][k][1]);
+                unpack2(mul2(f32x2(o[n][k][2], o[n][k][3]), f), o[n][k][2], o[n][k][3]);
             }
             if (KS == 8) {
                 // the upper four slices hand theirs to the lower four, lane to lane
-                float4* mine = reinterpret_cast<float4*>(scratch) + (ks & 3) * (KK * 32) + lane;
                 if (ks >= 4) {
 #pragma unroll
                     for (int k = 0; k < KK; ++k)
@@ -910,37 +954,27 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
             }
             if (ks < 4) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int k = 0; k < KK; ++k)
 #pragma unroll
-                    for (int k = 0; k < KK; ++k)
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const int row = 2 * t + c, d = FP8 ? (D / 8) * g + 2 * k + y : 16 * k + g + 8 * y;
-                            scratch[(ks * 8 + row) * D + (d ^ turn(row, d))] = o[n][k][2 * y + c];
-                        }
+                    for (int y = 0; y < 2; ++y) {
+                        const int d = FP8 ? (D / 8) * g + 2 * k + y : 16 * k + g + 8 * y;
+                        float* dst = scratch + (ks * 8 + 2 * t) * D + (d ^ turn(2 * t, d));
+                        dst[0] = o[n][k][2 * y];
+                        dst[D] = o[n][k][2 * y + 1];
+                    }
             }
             bar_sync(1, 32 * KS);
             const int r = n * 8 + hr;
-            float mm = ml[r].x;
-#pragma unroll
-            for (int y = 1; y < KS; ++y) mm = fmaxf(mm, ml[y * C::kRows + r].x);
-            float sum = 0.f;
-#pragma unroll
-            for (int y = 0; y < KS; ++y) {
-                const float2 v = ml[y * C::kRows + r];
-                sum = fmaf(v.y, fast_exp2(v.x - mm), sum);
-            }
-            const int f = p.row0 + r;
-            const int tok = f / a.group, head = f - tok * a.group;
-            const bool write = ok && pos_sh[r] >= -1;
-            const int64_t at = (int64_t)(p.q.q0 + tok) * (a.hkv * a.group) + kvh * a.group + head;
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float2 tot = total[r];
+            const bool write = tot.y != -1.f;
+            const float inv = tot.y == 0.f ? 0.f : 1.f / tot.y;
+            __nv_bfloat16* dst = a.out + at_sh[r] * D + d0;
 #pragma unroll
             for (int e = 0; e < kDims; e += 2) {
                 float2 v = make_float2(0.f, 0.f);
+                const int x = turn(hr, d0 + e);
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const int x = turn(hr, d0 + e);
                     const float2 z =
                         *reinterpret_cast<const float2*>(scratch + (y * 8 + hr) * D + ((d0 + e) ^ (x & ~1)));
                     v.x += x & 1 ? z.y : z.x, v.y += x & 1 ? z.x : z.y;
@@ -954,15 +988,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                     const int own = pair / share, at2 = pair % share;
                     st_cluster(ring_u + (rank * share + at2) * 8, own, v);
                     if (at2 % min(share, D / 2) == 0)
-                        st_cluster(ring_u + C::kRows * D * 4 + (rank * C::kRows + r) * 8, own,
-                                   make_float2(mm, write ? sum : -1.f));
+                        st_cluster(ring_u + C::kRows * D * 4 + (rank * C::kRows + r) * 8, own, tot);
                 } else if (write)
-                    *reinterpret_cast<uint32_t*>(a.out + at * D + d0 + e) = pack_row(v.x, v.y, inv);
-            }
-            if (d0 == 0) {
-                // a sum of -1: a row that is not to be written
-                if (cut) a.part_ml[slot * C::kRows + r] = make_float2(mm, write ? sum : -1.f);
-                else if (!shared && write && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * kLn2;
+                    *reinterpret_cast<uint32_t*>(dst + e) = pack_row(v.x, v.y, inv);
             }
             bar_sync(1, 32 * KS);
         }
