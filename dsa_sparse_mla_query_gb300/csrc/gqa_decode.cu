@@ -873,6 +873,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                     }
                 }
             }
+            // The stage's next contents come through the async proxy: without the fence they were
+            // seen to overtake this warp's reads (wrong values of a few keys of e4m3 caches, whenever
+            // the loads were waited for: a different result in each of twenty runs).
+            ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(empty + c.st);
         }

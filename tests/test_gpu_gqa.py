@@ -382,6 +382,56 @@ def test_same_bits_in_any_workspace_stream_or_graph(call, e4m3):
     assert int(c.status.item()) == 0
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("b, ctx, new, d", [(1, 262144, 1, 128), (40, 6000, 1, 128), (40, 6000, 2, 128), (1, 262144, 2, 64),
+                                            (40, 6000, 4, 128), (6, 6000, 1, 128)])
+def test_same_bits_whenever_the_loads_are_waited_for(b, ctx, new, d, e4m3):
+    """Long caches, bound by memory: the same results every time, and those of the formula."""
+    hq, hkv, rows = 64, 8, b * ctx
+    g = torch.Generator(device=DEV).manual_seed(7)
+    if e4m3:
+        k, v = [torch.randint(0, 0x7F, (rows, hkv, d), generator=g, device=DEV, dtype=torch.uint8)
+                | (torch.randint(0, 2, (rows, hkv, d), generator=g, device=DEV, dtype=torch.uint8) << 7) for _ in range(2)]
+        ks, vs = [torch.rand(rows, hkv, generator=g, device=DEV) * 0.004 + 0.004 for _ in range(2)]
+    else:
+        k, v = [torch.randn(rows, hkv, d, generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(2)]
+        ks = vs = None
+    q = torch.randn(b * new, hq, d, generator=g, device=DEV, dtype=torch.bfloat16)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    pos = torch.arange(ctx - new, ctx, **i32).repeat(b)
+    seqs = dsa.Seqs(torch.full((b,), ctx, **i32), torch.arange(0, b * new + 1, new, **i32), pos, max_ctx=ctx,
+                    max_q_per_seq=new, num_rows=rows,
+                    seq_base=torch.arange(0, rows, ctx, dtype=torch.int64, device=DEV))
+    shape = dsa.GqaShape(hq, hkv, d, dsa.DSA_FP8_E4M3_ROWSCALE if e4m3 else dsa.DSA_BF16)
+    nb = dsa.dense_gqa_workspace_size(shape, seqs, b * new)
+    ws = torch.empty(nb, dtype=torch.uint8, device=DEV)
+    status = torch.zeros(1, **i32)
+    scale = 1 / math.sqrt(d)
+
+    def run():
+        out = torch.empty_like(q)
+        lse = torch.empty(b * new, hq, device=DEV)
+        dsa.dense_gqa_decode(shape, q, k, v, ks, vs, seqs, b * new, scale, out, lse, ws, nb, d_status=status)
+        return out, lse
+
+    out, lse = run()
+    for _ in range(20):
+        o, l = run()
+        assert torch.equal(o, out) and torch.equal(l, lse)
+    assert int(status.item()) == 0
+    s, h = b - 1, 3  # one sequence's heads of one key head
+    kk = R.values(k[s * ctx:, h:h + 1], None if ks is None else ks[s * ctx:, h:h + 1])[:, 0]
+    vv = R.values(v[s * ctx:, h:h + 1], None if vs is None else vs[s * ctx:, h:h + 1])[:, 0]
+    for t in range(new):
+        n = ctx - new + t + 1
+        p = torch.softmax(scale * (kk[:n] @ q[s * new + t, h * 8:h * 8 + 8].double().T), 0)
+        ref, av = p.T @ vv[:n], p.T @ vv[:n].abs()
+        # a half step of the result; weights off by a half step each, in no one direction: a
+        # twentieth of the worst case; sums of n / 16 fp32 additions
+        tol = 2.0 ** -8 * ref.abs() + (2.0 ** -8 / 20 + 2.0 ** -24 * (n / 16 + 64) * 2) * av
+        assert bool(((out[s * new + t, h * 8:h * 8 + 8].double() - ref).abs() <= tol).all())
+
+
 @pytest.mark.parametrize("call", list(CALLS))
 def test_two_calls_at_once(call):
     """Two streams, a workspace each."""
