@@ -30,9 +30,10 @@
 //   partials through distributed shared memory.
 //
 // Measured, 64/8 heads of 128: 64 x 32,768 bf16 1,200 us, 7.1 TB/s (a copy: 6.8);
-// 1 x 524,288 e4m3 169 us, 6.5 TB/s; 128 x 4 tokens over 61 to 16,381 e4m3 605 us,
-// 3.7 TB/s: there 32 rows make 64 products, 64 conversions and 480 instructions of
-// a warp's 16 keys, and two warps a scheduler leave half of its cycles unused.
+// 1 x 524,288 e4m3 169 us, 6.5 TB/s; 128 x 4 tokens over 61 to 16,381 e4m3 556 us,
+// 4.0 TB/s: there 32 rows make 64 products, 64 conversions and 480 instructions of
+// a warp's 16 keys, and two warps a scheduler leave half of its cycles unused
+// (the rows split over 16 warps: 699, a key is then converted twice).
 #include <type_traits>
 
 #include "gqa_common.cuh"
@@ -61,7 +62,9 @@ struct Cfg {
     static constexpr int kScaleBytes = FP8 ? 2 * kTile * 4 : 0;
     static constexpr int kScratch = 4 * 8 * D * 4;  // four key slices' outputs of 8 rows
     static constexpr int kMl = KS * kRows * 8;
-    static constexpr int kStart = KS == 8 ? 6 : 3;  // what a sequence's start and end cost, in tiles
+    // What a sequence's start and end cost, in tiles.  (Left out of the deal, the CTA with the most
+    // sequences ended 14% after the average; 128 x 4 tokens over 61 to 16,381: 556 us, with twice these 566.)
+    static constexpr int kStart = KS == 8 ? 6 : 3;
     static constexpr bool kQShared = NT > 2;        // query fragments in shared memory, else in registers
     static constexpr int kQBytes = kQShared ? (D / 16) * NT * 32 * 8 : 0;
     static constexpr int kMisc = 256 + kRows * 24;
@@ -1190,11 +1193,11 @@ Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s) {
     // tile (latency), all together no less than the bytes at 6.8 TB/s, and the
     // joining kernel join_ns.  Larger clusters leave room: their CTAs have to
     // find place in one part of the GPU.  Clusters against the joining kernel,
-    // launch included (64/8 heads of 128, one token, bf16 where not said):
-    // 1 x 4,096 12.6 us and 14.8; 1 x 32,768 31.0 and 34.6; 8 x 8,000 46.7 and
-    // 52.2, e4m3 32.3 and 41.4; 32 x up to 1,000 20.8 and 29.4; 2 x 4,000 with four
-    // tokens, e4m3, 28.9 and 39.3; and where the estimate chooses the other:
-    // 3 x 30,000 70.8 and 66.7, 3 x up to 9,000 with 32/8 heads of 64 18.7 and 15.1.
+    // launch included (64/8 heads of 128, one token, bf16 where not said): 8 x 8,192
+    // 47.7 us and 53.3; 16 x 4,096 48.4 and 54.2; 32 x 8,192 156.7 and 167.5, e4m3
+    // 92.7 and 100; four tokens over e4m3, 2 x 4,000 22.8 and 24.4, 19 x 4,000 50.5
+    // and 57.5; level at 4 x 65,536, 165 and 164; and where the estimate chooses the
+    // other: 3 x 30,000 70.8 and 66.7, 3 x up to 9,000 with 32/8 heads of 64 18.7 and 15.1.
     p.cluster = 0;
     const int64_t segs = (int64_t)p.lanes * s.num_seqs;
     if (segs <= n) {
