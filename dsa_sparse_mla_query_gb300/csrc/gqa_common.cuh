@@ -1,5 +1,6 @@
 // gqa_common.cuh -- pieces shared by the dense grouped-head attention kernels
-// (gqa_decode.cu, gqa_prefill.cu): the workspace plan and the tensor maps.
+// (gqa_decode.cu, gqa_prefill.cu): sequences' counts, tensor maps, paired fp32
+// arithmetic, e4m3 codes, ring places and waits.
 #pragma once
 
 #include <atomic>
