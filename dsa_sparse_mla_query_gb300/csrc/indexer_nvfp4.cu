@@ -405,6 +405,8 @@ __global__ void __launch_bounds__(320, Nv4Cfg<NQ, KP>::ctas_per_sm)
                 cw[k] = *reinterpret_cast<const uint4*>(stg + row * kNvCodeBytes + ((k ^ swz) << 4));
             const uint2 sc = *reinterpret_cast<const uint2*>(stg + C::codes_bytes + rbx * sc_slot +
                                                              (rin + bpar[st * 8 + rbx]) * kNvScaleBytes);
+            // The refill comes through the async proxy: without the fence it may overtake these loads
+            ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(empty + st);  // codes in registers: the stage may refill
             const int b = (int)(c & 1);
