@@ -425,26 +425,22 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
             int pos;
             while (ok && w.begin(a, p, pos)) {
                 const int kvh = p.lane % a.hkv;
-                // physical row of a box's first token among the sequence's, -1: none; its
-                // load goes out before the queries' positions have arrived
+                // physical row of a box's first token among the sequence's, num_rows: outside the
+                // cache, -1: none; its load goes out before the queries' positions have arrived
                 auto row_of = [&](int box) -> int {
                     const int64_t j = (int64_t)box << shift;
                     if (j >= p.q.ctx) return -1;
-                    int64_t row;
-                    if (a.s.page_table) {
-                        row = phys_row(a.s, p.b, j);
-                        if (row >= 0 && row + R > a.s.num_rows) row = -1;  // a page past the cache
-                    } else {
-                        row = p.base + j;
-                        const int64_t last = p.base + min(j + R, (int64_t)p.q.ctx);
-                        if (row < 0 || last > a.s.num_rows) row = -1;
-                    }
+                    int64_t row = a.s.page_table ? phys_row(a.s, p.b, j) : p.base + j;
+                    if (row < 0 || row >= a.s.num_rows) row = a.s.num_rows;
                     return (int)row;
                 };
+                // -1 for a box that no query sees.  Rows outside the cache are loaded as zeros (TMA's fill),
+                // and reported where a query sees one.
                 auto seen = [&](int row, int box) -> int {
-                    const bool in = ((int64_t)box << shift) < p.limit;
-                    if (in && row < 0) report(a.d_status, DSA_ERR_BAD_INPUT);
-                    return in ? row : -1;
+                    const int64_t j = (int64_t)box << shift;
+                    if (j >= p.limit) return -1;
+                    if (row + (min(j + R, (int64_t)p.limit) - j) > a.s.num_rows) report(a.d_status, DSA_ERR_BAD_INPUT);
+                    return row;
                 };
                 int w0 = p.i0 * nbox;
                 int cur = row_of(w0 + lane), nxt = row_of(w0 + 32 + lane);
@@ -504,8 +500,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                             const int row = __shfl_sync(0xffffffffu, cur, l + (x >> shift));
                             const int64_t at = ((int64_t)row + (x & (R - 1))) * a.hkv + kvh;
                             if (row >= 0 && (int64_t)i * kTile + x < p.limit) {
-                                ptx::cp_async4(sd + x, a.k_scale + at);
-                                ptx::cp_async4(sd + kTile + x, a.v_scale + at);
+                                const bool in = (int64_t)row + (x & (R - 1)) < a.s.num_rows;
+                                ptx::cp_async4_or_zero(sd + x, a.k_scale + (in ? at : 0), in);
+                                ptx::cp_async4_or_zero(sd + kTile + x, a.v_scale + (in ? at : 0), in);
                             }
                         }
                         ptx::cp_async_arrive_noinc(full + st);

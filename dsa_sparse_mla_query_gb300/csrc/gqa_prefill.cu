@@ -430,18 +430,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             uint32_t tail_phase = 0;
             while (ok && next_item(it)) {
                 if (it.n == 0) continue;
+                // physical row of a box's first token, -1 for a box that no query sees.  Rows outside the cache
+                // are loaded as zeros (TMA's fill) and reported.
                 auto row_of = [&](int box) -> int {
                     const int64_t j = (int64_t)box << shift;
                     if (j >= it.limit) return -1;
-                    int64_t row;
-                    if (a.s.page_table) {
-                        row = phys_row(a.s, it.b, j);
-                        if (row >= 0 && row + R > a.s.num_rows) row = -1;
-                    } else {
-                        row = it.base + j;
-                        if (row < 0 || it.base + min(j + R, (int64_t)it.limit) > a.s.num_rows) row = -1;
-                    }
-                    if (row < 0) report(a.d_status, DSA_ERR_BAD_INPUT);
+                    int64_t row = a.s.page_table ? phys_row(a.s, it.b, j) : it.base + j;
+                    if (row < 0 || row >= a.s.num_rows) row = a.s.num_rows;
+                    if (row + (min(j + R, (int64_t)it.limit) - j) > a.s.num_rows) report(a.d_status, DSA_ERR_BAD_INPUT);
                     return (int)row;
                 };
                 const int b0 = it.key0 >> shift;  // the item's first box
@@ -479,9 +475,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                                 const int key = y * 32 + lane;
                                 const int row = __shfl_sync(0xffffffffu, cur, l + (key >> shift));
                                 if (row >= 0 && it.key0 + i * kKeys + key < it.limit) {
-                                    const int64_t at = ((int64_t)row + (key & (R - 1))) * a.hkv + it.kvh;
-                                    ptx::cp_async4(code_scales + key, a.k_scale + at);
-                                    ptx::cp_async4(code_scales + kKeys + key, a.v_scale + at);
+                                    const int64_t at = (int64_t)row + (key & (R - 1));
+                                    const bool in = at < a.s.num_rows;
+                                    const int64_t off = in ? at * a.hkv + it.kvh : 0;
+                                    ptx::cp_async4_or_zero(code_scales + key, a.k_scale + off, in);
+                                    ptx::cp_async4_or_zero(code_scales + kKeys + key, a.v_scale + off, in);
                                 }
                             }
                         ptx::cp_async_arrive_noinc(bar);

@@ -139,6 +139,11 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
+// the same, or 4 zero bytes: nothing is read then, but src is still an address of the buffer
+__device__ __forceinline__ void cp_async4_or_zero(void* dst, const void* src, bool copy) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(copy ? 4 : 0)
+                 : "memory");
+}
 // 8-byte asynchronous global -> shared copy (both addresses 8-byte aligned)
 __device__ __forceinline__ void cp_async8(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");

@@ -448,9 +448,10 @@ dsa_status dense_gqa_workspace_size(const dsa_gqa_shape* shape, const dsa_seqs* 
  * that one query of a sequence sees can reach the sequence's other queries.
  * DSA_ERR_BAD_INPUT in *d_status: a position outside [-1, ctx_len) (its row is
  * left unwritten), a malformed sequence (its rows are left unwritten), a page
- * or row outside the cache (not read; the outputs of the sequence's queries
- * that see it are undefined).  Rows of out past q_start[num_seqs] are left as
- * they were.  Alignment: q, k_cache, v_cache and out 16 bytes, workspace 256. */
+ * or row outside the cache that some query sees (not read: its keys and values
+ * count as zeros; nothing changes for queries that do not see it).  A context
+ * or a last page that runs past the cache behind every position is no error.
+ * Rows of out past q_start[num_seqs] are left as they were.  Alignment: q, k_cache, v_cache and out 16 bytes, workspace 256. */
 dsa_status dense_gqa_decode(const dsa_gqa_shape* shape, const void* q, const void* k_cache, const void* v_cache,
                             const float* k_scale, const float* v_scale, const dsa_seqs* seqs, int32_t num_q,
                             float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
