@@ -132,6 +132,11 @@ __device__ __forceinline__ void lds128(uint32_t (&r)[4], uint32_t addr) {
 __device__ __forceinline__ void lds64(uint32_t (&r)[2], uint32_t addr) {
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t r;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+    return r;
+}
 __device__ __forceinline__ void bar_sync(int id, int n) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
@@ -642,9 +647,17 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
         float o[NT][KK][4];
         float m[NT][2];  // references: far below any score until a key is seen
         uint64_t l[NT];  // sums of the weights, a pair of columns
-        // FP8: weights take V's scales along, relative to vref, a power of two, times 2^7: below 2^15 with
-        // the lazy reference, and exact to 11 bits down to 2^-21 of the largest
+        // FP8: weights take V's scales along, relative to vref, a power of two above every scale so far, times
+        // 2^7: below 2^15 with the lazy reference.  f16 rounds such a product by 2^-11 of itself or 2^-25,
+        // which is 2^-32 vref, and a row's largest product is at least its weight of 1 times the least scale.
+        // So while vref stays below 2^span that scale, all of the slice's products that vanish in f16 are
+        // together less than 2^-8 of the largest; beyond it (wide) every 16 keys' products take a
+        // reference of their row's own.  (128 x 4 tokens over 61 to 16,381: 567 us, 1,570 wide; 1 x 524,288:
+        // 170 and 320.  Products of the sequence's large and small scales are kept down to 2^-100 of vref.)
         float vref = 0x1p-119f, vinv = 0x1p126f;
+        uint32_t vlow = 0xFFFFFFFFu;  // bits of a power of two below every scale so far but 0, less 1
+        bool wide = false;
+        const int span = 25 - (32 - __clz(16 * max(1, p.i1 - p.i0) - 1));
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             m[n][0] = m[n][1] = kNone;
@@ -758,12 +771,20 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
 #pragma unroll
                 for (int z = 0; z < 2; ++z) move = move || fmaxf(s[n][z], s[n][2 + z]) > m[n][z] + kLazy;
             }
-            if (FP8) move = move || fmaxf(fabsf(fv0), fabsf(fv1)) > vref;
+            // four dims of keys 2t, 2t+1, 2t+8, 2t+9 as A operands: z-th of the two 16-dim tiles they belong to
+            auto codes = [](const uint32_t (&x)[4], int z, uint32_t (&af)[4]) {
+                const uint32_t pick = z ? 0x7362 : 0x5140;  // a dim's codes of two keys side by side
+                e4m3x4_to_f16(__byte_perm(x[0], x[1], pick), af[0], af[1]);
+                e4m3x4_to_f16(__byte_perm(x[2], x[3], pick), af[2], af[3]);
+            };
+            auto above0 = [](float x) { return (__float_as_uint(x) & 0x7FFFFFFFu) - 1u; };  // 0: none
+            if (FP8)
+                move = move || fmaxf(fabsf(fv0), fabsf(fv1)) > vref || min(above0(fv0), above0(fv1)) < vlow || wide;
             if (__any_sync(0xffffffffu, move)) {
                 // rare: the rows' maxima over the slice's keys, and everything relative to them
                 float fv = 1.f;
                 if (FP8) {
-                    // a row of zeros may have any scale (1 as a rule): it does not move the others'
+                    // a row of zeros may have any scale (1 as a rule): it has no say in the references
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
                         uint32_t any = 0;
@@ -788,6 +809,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                         vref = nref;
                         vinv = 0x1p7f / nref;
                     }
+                    const uint32_t least = __reduce_min_sync(0xffffffffu, min(above0(fv0), above0(fv1)));
+                    if (least < vlow) vlow = max((least + 1u) & 0x7F800000u, 1u) - 1u;
+                    wide = (int)(__float_as_uint(vref) >> 23) - (int)((vlow + 1u) >> 23) > span && vlow != 0xFFFFFFFFu;
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -810,6 +834,55 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                         o[n][k][2] *= al[0] * fv;
                         o[n][k][3] *= al[1] * fv;
                     }
+                }
+                if (FP8 && wide) {
+                    // rare: the products with f16 weights of their own power of two per row, then into O's units
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float w[2][2], up[2], down[2];
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            w[0][z] = fast_exp2(s[n][z] - m[n][z]);
+                            w[1][z] = fast_exp2(s[n][2 + z] - m[n][z]);
+                        }
+                        l[n] = add2(l[n], add2(f32x2(w[0][0], w[0][1]), f32x2(w[1][0], w[1][1])));
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            w[0][z] *= fv0 * vinv;
+                            w[1][z] *= fv1 * vinv;
+                            float top = fmaxf(fabsf(w[0][z]), fabsf(w[1][z]));
+#pragma unroll
+                            for (int y = 4; y < 32; y <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
+                            // the row's largest to [2^14, 2^15), by at most 2^126
+                            const int e = min(127 + 126, 127 + 14 + 127 - (int)(__float_as_uint(top) >> 23));
+                            up[z] = __uint_as_float((uint32_t)e << 23);
+                            down[z] = 1.f / up[z];
+                        }
+                        const uint32_t p0 = movm_t(pack_f16(w[0][0] * up[0], w[0][1] * up[1]));
+                        const uint32_t p1 = movm_t(pack_f16(w[1][0] * up[0], w[1][1] * up[1]));
+#pragma unroll
+                        for (int e = 0; e < KK / 2; ++e) {
+                            __syncwarp();  // keeps later loads behind these products: registers
+                            uint32_t x[4];
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) {
+                                const int at = (D / 8) * g + 4 * e;  // the row's byte
+                                x[z] = lds32(chunk_addr<HB, kTile>(vb, r0 + 2 * t + (z & 1) + ((z >> 1) << 3), at >> 4) + (at & 15));
+                            }
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                uint32_t af[4];
+                                codes(x, z, af);
+                                float y[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma16816<true>(y, af, p0, p1);
+#pragma unroll
+                                for (int d = 0; d < 4; ++d)
+                                    o[n][2 * e + z][d] = fmaf(y[d], down[d & 1], o[n][2 * e + z][d]);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = -INFINITY;  // done
                 }
             }
             // weights, as the B operand of O^T = V^T P^T (two 8x8 transposes per tile)
@@ -863,11 +936,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                 for (int e = 0; e < KK / 2; ++e) {
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
-                        // a dim's codes of two keys side by side, then both converted at once
                         uint32_t af[4];
-                        const uint32_t pick = z ? 0x7362 : 0x5140;
-                        e4m3x4_to_f16(__byte_perm(x[0][e], x[1][e], pick), af[0], af[1]);
-                        e4m3x4_to_f16(__byte_perm(x[2][e], x[3][e], pick), af[2], af[3]);
+                        const uint32_t y[4] = {x[0][e], x[1][e], x[2][e], x[3][e]};
+                        codes(y, z, af);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) mma16816<true>(o[n][2 * e + z], af, pf[n][0], pf[n][1]);
                     }
