@@ -780,6 +780,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 const uint64_t nm2 = f32x2(mm, mm);
                 uint32_t pk[32];
                 ulonglong2 vs = make_ulonglong2(0, 0);
+                uint64_t step[2];  // the step's sums: 16 additions each, and one to the row's
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -790,7 +791,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                         unpack2(v, p0, p1);
                         p0 = fast_exp2(p0);
                         p1 = fast_exp2(p1);
-                        l2[(e >> 1) & 1] = add2(l2[(e >> 1) & 1], f32x2(p0, p1));
+                        uint64_t& sum = step[(e >> 1) & 1];
+                        sum = k == 0 && e < 4 ? f32x2(p0, p1) : add2(sum, f32x2(p0, p1));
                         if (FP8) {
                             if ((e & 2) == 0) vs = *reinterpret_cast<const ulonglong2*>(sc + kKeys + 32 * k + e);
                             unpack2(mul2(f32x2(p0, p1), e & 2 ? vs.y : vs.x), p0, p1);
@@ -799,6 +801,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                         // the sum keeps fp32
                         pk[16 * k + e / 2] = pack_bf16(p0, p1);
                     }
+                l2[0] = add2(l2[0], step[0]);
+                l2[1] = add2(l2[1], step[1]);
                 if (FP8 && (j & 1)) sl = sl + 1 == C::kScaleSlots ? 0 : sl + 1;
                 ptx::tmem_st32_nowait(ts, pk);
                 ptx::tmem_wait_st();
