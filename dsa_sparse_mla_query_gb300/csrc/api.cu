@@ -483,8 +483,11 @@ static dsa_status dense_gqa(bool prefill, const dsa_gqa_shape* shape, const void
     dsa_status st = c.done();
     if (st != DSA_OK || num_q == 0) return st;
     // a negative scale turns the row maxima around, and 0 times a masked score is not
-    // -inf: the split kernel scales first and masks then
-    if (prefill && sm_scale > 0.f)
+    // -inf: the split kernel scales first and masks then.  It also takes contexts past
+    // kPromptCtx: an item of the prompt kernel holds some of its waits for as long as it
+    // takes (2^22 keys 46 to 80 ms), and they give up after a second.
+    constexpr int kPromptCtx = 1 << 22;
+    if (prefill && sm_scale > 0.f && seqs->max_ctx <= kPromptCtx)
         return cuda_status(gqa::launch_prefill(sh, q, k_cache, v_cache, k_scale, v_scale, *seqs, num_q, sm_scale, out,
                                                lse, workspace, d_status, stream),
                            "dense_gqa_prefill launch");
