@@ -27,7 +27,8 @@ def _gpu():
 @pytest.mark.parametrize("shift, amp", [(7, 1.0), (24, 4.0), (34, 4.0), (60, 4.0), (60, 1.0), (100, 4.0)])
 @pytest.mark.parametrize("ctx, new, hq, hkv, d", [([700], [1], 16, 2, 128), ([5000, 70], [1, 1], 8, 8, 64),
                                                   ([3000], [2], 16, 2, 128), ([900, 4000], [4, 3], 16, 2, 128),
-                                                  ([900], [4], 16, 2, 64)])
+                                                  ([900], [4], 16, 2, 64), ([40000], [1], 16, 2, 128),
+                                                  ([30000, 25], [3, 1], 16, 2, 64)])
 def test_large_scales_of_keys_without_weight(call, shift, amp, ctx, new, hq, hkv, d):
     """Every eighth key of the first 256 and a few behind them: scores some 40 amp below the others'
     (for amp 1 a weight of 2^-58 or so), scales 2^shift times the others'."""
