@@ -391,8 +391,8 @@ __global__ void __launch_bounds__(128) mla_q_prep_kernel(const __nv_bfloat16* __
 // shared memory, while the first chunk's loads are in flight.
 //
 // Bound by HBM, close to the issue slots with many query heads.  131,072
-// tokens' K and V (8 heads of 128, bf16): 170 us, 6.3 TB/s; 8,191 tokens with
-// 64 query heads into e4m3 caches: 61 us, 5.2 TB/s (a CTA per token with its
+// tokens' K and V (8 heads of 128, bf16): 168 us, 6.4 TB/s; 8,191 tokens with
+// 64 query heads into e4m3 caches: 58 us, 5.5 TB/s (a CTA per token with its
 // table in shared memory for every access: 268 and 130 us; eight accesses in
 // flight and fewer warps: 174 and 76).
 constexpr int kKvUnroll = 4;  // accesses per chunk: 8 rows of 128 dims

@@ -29,10 +29,10 @@
 //   takes 4 us: there a cluster of CTAs shares a (lane, sequence) and joins its
 //   partials through distributed shared memory.
 //
-// Measured, 64/8 heads of 128: 64 x 32,768 bf16 1,200 us, 7.1 TB/s (a copy: 6.8);
-// 1 x 524,288 e4m3 169 us, 6.5 TB/s; 128 x 4 tokens over 61 to 16,381 e4m3 556 us,
-// 4.0 TB/s: there 32 rows make 64 products, 64 conversions and 480 instructions of
-// a warp's 16 keys, and two warps a scheduler leave half of its cycles unused
+// Measured, 64/8 heads of 128: 64 x 32,768 bf16 1,230 us, 7.0 TB/s (a copy: 6.8);
+// 1 x 524,288 e4m3 170 to 173 us, 6.4 TB/s; 128 x 4 tokens over 61 to 16,381 e4m3 567 us,
+// 3.9 TB/s: there 32 rows make 64 products, 64 conversions and 480 instructions of
+// a warp's 16 keys, and two warps a scheduler leave 62% of its issue slots unused
 // (the rows split over 16 warps: 699, a key is then converted twice).
 #include <type_traits>
 
@@ -63,7 +63,7 @@ struct Cfg {
     static constexpr int kScratch = 4 * 8 * D * 4;  // four key slices' outputs of 8 rows
     static constexpr int kMl = KS * kRows * 8;
     // What a sequence's start and end cost, in tiles.  (Left out of the deal, the CTA with the most
-    // sequences ended 14% after the average; 128 x 4 tokens over 61 to 16,381: 556 us, with twice these 566.)
+    // sequences ended 14% after the average; with twice these 128 x 4 tokens over 61 to 16,381 take 2% longer.)
     static constexpr int kStart = KS == 8 ? 6 : 3;
     static constexpr bool kQShared = NT > 2;        // query fragments in shared memory, else in registers
     static constexpr int kQBytes = kQShared ? (D / 16) * NT * 32 * 8 : 0;
@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                 float x, y, u, v;
                 unpack2(w0, x, y);
                 unpack2(w1, u, v);
-                // bf16 rounds a weight by up to 2^-9 of itself, f16 by 2^-12 (or 2^-25 of the largest)
+                // bf16 rounds a weight by up to 2^-8 of itself, f16 by 2^-11 or 2^-25 (see vref)
                 pf[n][0] = movm_t(FP8 ? pack_f16(x, y) : pack_bf16(x, y));
                 pf[n][1] = movm_t(FP8 ? pack_f16(u, v) : pack_bf16(u, v));
             }

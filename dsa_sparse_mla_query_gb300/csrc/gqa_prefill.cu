@@ -27,11 +27,11 @@
 // the CTAs in turn, back and forth.  Where few items leave CTAs idle, each is
 // split into ranges of keys, whose partial results a second kernel joins.
 //
-// Measured, 64/8 heads of 128, bf16: 16,384 tokens 1,570 to 1,670 TFLOP/s (the
+// Measured, 64/8 heads of 128, bf16: 16,384 tokens 1,540 to 1,590 TFLOP/s (the
 // chip at its power cap, as a library matrix product is at 1,700 sustained), a
-// step 1,340 cycles of the 1,280 that its products take; 24 packed prompts of 17
-// to 4,095 tokens 1,200 to 1,330, where an item's start and end are 4,000 cycles
-// of 30,000 to 90,000.
+// step 1,340 cycles of the 1,280 that its products take; 24 packed prompts of 17 to
+// 4,095 tokens 1,200 to 1,240, where an item's start and end are 4,000 cycles of
+// 30,000 to 90,000.
 #include "gqa_common.cuh"
 
 namespace dsa {
@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                             if ((e & 2) == 0) vs = *reinterpret_cast<const ulonglong2*>(sc + kKeys + 32 * k + e);
                             unpack2(mul2(f32x2(p0, p1), e & 2 ? vs.y : vs.x), p0, p1);
                         }
-                        // a weight (times its value's scale) rounded to bf16 is off by up to 2^-9 of itself;
+                        // a weight (times its value's scale) rounded to bf16 is off by up to 2^-8 of itself;
                         // the sum keeps fp32
                         pk[16 * k + e / 2] = pack_bf16(p0, p1);
                     }

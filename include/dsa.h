@@ -383,7 +383,20 @@ dsa_status dsa_lse_combine(const void* const* o_parts, const float* const* lse_p
  * arguments and give the same results within rounding.  Sequences are dsa_seqs
  * as above: paged, or contiguous from seq_base (freshly projected, packed
  * prompts: seq_base[b] = q_start[b], ctx_len[b] = their length).  q_rope_pos
- * is not read. */
+ * is not read.
+ * Which of the two: with up to 32 query rows per key head (G times a sequence's
+ * new tokens) dense_gqa_decode; with more it reads every key once per 32 rows,
+ * and dense_gqa_prefill is faster over long contexts, from 40 rows over bf16
+ * caches and from some 64 to 128 over e4m3 ones.  Over a few thousand keys of a
+ * sequence or two they take the same time.
+ * Roundings: scores, maxima, sums of weights, outputs before their last step
+ * are fp32; a weight is rounded once for its product with the value, to bf16
+ * (half a step: 2^-8 of it) or, in dense_gqa_decode over e4m3 caches, to f16
+ * (2^-11); over e4m3 caches it carries the value's scale then (scales up to
+ * 2^100 apart); out is rounded once, to bf16.  The tensor cores truncate their
+ * fp32 sums: over n keys of values of one sign a result may fall short by n 2^-26
+ * of itself in dense_gqa_prefill (1% at 2^20 keys) and n 2^-28 in
+ * dense_gqa_decode.  Calls with max_ctx past 2^22 run decode's kernel. */
 typedef enum {
     DSA_ROPE_PAIRS = 0, /* pair i of the first rot_dims dims: (2i, 2i+1) */
     DSA_ROPE_HALVES = 1 /* pair i: (i, i + rot_dims/2) */
@@ -443,15 +456,16 @@ dsa_status dense_gqa_workspace_size(const dsa_gqa_shape* shape, const dsa_seqs* 
  *   out  bf16 [num_q, num_heads, head_dim] contiguous; lse fp32
  *        [num_q, num_heads] or NULL
  * q_pos[t] = -1 sees no key: out = 0, lse = -inf, whatever the caches hold.
- * Cache rows that no query of
- * a call may see are not used, whatever they hold; a non-finite key or value
- * that one query of a sequence sees can reach the sequence's other queries.
+ * Cache rows that no query of a call may see are not used, whatever they hold;
+ * a non-finite key or value that one query of a sequence sees can reach the
+ * sequence's other queries.
  * DSA_ERR_BAD_INPUT in *d_status: a position outside [-1, ctx_len) (its row is
  * left unwritten), a malformed sequence (its rows are left unwritten), a page
  * or row outside the cache that some query sees (not read: its keys and values
  * count as zeros; nothing changes for queries that do not see it).  A context
  * or a last page that runs past the cache behind every position is no error.
- * Rows of out past q_start[num_seqs] are left as they were.  Alignment: q, k_cache, v_cache and out 16 bytes, workspace 256. */
+ * Rows of out past q_start[num_seqs] are left as they were.  Alignment: q,
+ * k_cache, v_cache and out 16 bytes, workspace 256. */
 dsa_status dense_gqa_decode(const dsa_gqa_shape* shape, const void* q, const void* k_cache, const void* v_cache,
                             const float* k_scale, const float* v_scale, const dsa_seqs* seqs, int32_t num_q,
                             float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
