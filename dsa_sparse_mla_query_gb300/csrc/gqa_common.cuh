@@ -81,6 +81,14 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t
         : "=r"(lo), "=r"(hi)
         : "r"(x));
 }
+// four e4m3 codes (low byte first) as two bf16 pairs, exact
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    uint32_t a, b;
+    e4m3x4_to_f16(x, a, b);
+    const float2 u = __half22float2(*reinterpret_cast<__half2*>(&a)), v = __half22float2(*reinterpret_cast<__half2*>(&b));
+    lo = pack_bf16(u.x, u.y);
+    hi = pack_bf16(v.x, v.y);
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);

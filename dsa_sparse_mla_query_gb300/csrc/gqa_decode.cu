@@ -30,7 +30,7 @@
 //   partials through distributed shared memory.
 //
 // Measured, 64/8 heads of 128: 64 x 32,768 bf16 1,230 us, 7.0 TB/s (a copy: 6.8);
-// 1 x 524,288 e4m3 170 to 173 us, 6.4 TB/s; 128 x 4 tokens over 61 to 16,381 e4m3 567 us,
+// 1 x 524,288 e4m3 170 to 173 us, 6.4 TB/s; 128 x 4 tokens over 61 to 16,381 e4m3 566 us,
 // 3.9 TB/s: there 32 rows make 64 products, 64 conversions and 480 instructions of
 // a warp's 16 keys, and two warps a scheduler leave 62% of its issue slots unused
 // (the rows split over 16 warps: 699, a key is then converted twice).
@@ -651,9 +651,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
         // 2^7: below 2^15 with the lazy reference.  f16 rounds such a product by 2^-11 of itself or 2^-25,
         // which is 2^-32 vref, and a row's largest product is at least its weight of 1 times the least scale.
         // So while vref stays below 2^span that scale, all of the slice's products that vanish in f16 are
-        // together less than 2^-8 of the largest; beyond it (wide) every 16 keys' products take a
-        // reference of their row's own.  (128 x 4 tokens over 61 to 16,381: 567 us, 1,570 wide; 1 x 524,288:
-        // 170 and 320.  Products of the sequence's large and small scales are kept down to 2^-100 of vref.)
+        // together less than 2^-8 of the largest; beyond it (wide) weights are rounded to bf16 (2^-8 of
+        // each), which reaches down to 2^-126 of vref.  (128 x 4 tokens over 61 to 16,381: 566 us, 1,300
+        // wide; 1 x 524,288: 173 and 303.  With f16 and a power of two per row and 16 keys, 1,570, dims
+        // that the row's largest product leaves 0 lost the others.)
         float vref = 0x1p-119f, vinv = 0x1p126f;
         uint32_t vlow = 0xFFFFFFFFu;  // bits of a power of two below every scale so far but 0, less 1
         bool wide = false;
@@ -771,12 +772,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
 #pragma unroll
                 for (int z = 0; z < 2; ++z) move = move || fmaxf(s[n][z], s[n][2 + z]) > m[n][z] + kLazy;
             }
-            // four dims of keys 2t, 2t+1, 2t+8, 2t+9 as A operands: z-th of the two 16-dim tiles they belong to
-            auto codes = [](const uint32_t (&x)[4], int z, uint32_t (&af)[4]) {
-                const uint32_t pick = z ? 0x7362 : 0x5140;  // a dim's codes of two keys side by side
-                e4m3x4_to_f16(__byte_perm(x[0], x[1], pick), af[0], af[1]);
-                e4m3x4_to_f16(__byte_perm(x[2], x[3], pick), af[2], af[3]);
-            };
+            // the bytes of two words (keys) that hold the dims of the z-th of two 16-dim tiles, a dim's side by side
+            auto pick_dim = [](int z) { return z ? 0x7362u : 0x5140u; };
             auto above0 = [](float x) { return (__float_as_uint(x) & 0x7FFFFFFFu) - 1u; };  // 0: none
             if (FP8)
                 move = move || fmaxf(fabsf(fv0), fabsf(fv1)) > vref || min(above0(fv0), above0(fv1)) < vlow || wide;
@@ -836,30 +833,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                     }
                 }
                 if (FP8 && wide) {
-                    // rare: the products with f16 weights of their own power of two per row, then into O's units
+                    // rare: the products with bf16 weights, whose exponents suffice, and bf16 codes
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        float w[2][2], up[2], down[2];
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            w[0][z] = fast_exp2(s[n][z] - m[n][z]);
-                            w[1][z] = fast_exp2(s[n][2 + z] - m[n][z]);
-                        }
-                        l[n] = add2(l[n], add2(f32x2(w[0][0], w[0][1]), f32x2(w[1][0], w[1][1])));
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            w[0][z] *= fv0 * vinv;
-                            w[1][z] *= fv1 * vinv;
-                            float top = fmaxf(fabsf(w[0][z]), fabsf(w[1][z]));
-#pragma unroll
-                            for (int y = 4; y < 32; y <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
-                            // the row's largest to [2^14, 2^15), by at most 2^126
-                            const int e = min(127 + 126, 127 + 14 + 127 - (int)(__float_as_uint(top) >> 23));
-                            up[z] = __uint_as_float((uint32_t)e << 23);
-                            down[z] = 1.f / up[z];
-                        }
-                        const uint32_t p0 = movm_t(pack_f16(w[0][0] * up[0], w[0][1] * up[1]));
-                        const uint32_t p1 = movm_t(pack_f16(w[1][0] * up[0], w[1][1] * up[1]));
+                        const float w00 = fast_exp2(s[n][0] - m[n][0]), w01 = fast_exp2(s[n][1] - m[n][1]);
+                        const float w10 = fast_exp2(s[n][2] - m[n][0]), w11 = fast_exp2(s[n][3] - m[n][1]);
+                        l[n] = add2(l[n], add2(f32x2(w00, w01), f32x2(w10, w11)));
+                        const float u0 = fv0 * vinv, u1 = fv1 * vinv;
+                        const uint32_t p0 = movm_t(pack_bf16(w00 * u0, w01 * u0));
+                        const uint32_t p1 = movm_t(pack_bf16(w10 * u1, w11 * u1));
 #pragma unroll
                         for (int e = 0; e < KK / 2; ++e) {
                             __syncwarp();  // keeps later loads behind these products: registers
@@ -872,12 +854,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
 #pragma unroll
                             for (int z = 0; z < 2; ++z) {
                                 uint32_t af[4];
-                                codes(x, z, af);
-                                float y[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma16816<true>(y, af, p0, p1);
-#pragma unroll
-                                for (int d = 0; d < 4; ++d)
-                                    o[n][2 * e + z][d] = fmaf(y[d], down[d & 1], o[n][2 * e + z][d]);
+                                e4m3x4_to_bf16(__byte_perm(x[0], x[1], pick_dim(z)), af[0], af[1]);
+                                e4m3x4_to_bf16(__byte_perm(x[2], x[3], pick_dim(z)), af[2], af[3]);
+                                mma16816<false>(o[n][2 * e + z], af, p0, p1);
                             }
                         }
                     }
@@ -937,8 +916,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
                         uint32_t af[4];
-                        const uint32_t y[4] = {x[0][e], x[1][e], x[2][e], x[3][e]};
-                        codes(y, z, af);
+                        e4m3x4_to_f16(__byte_perm(x[0][e], x[1][e], pick_dim(z)), af[0], af[1]);
+                        e4m3x4_to_f16(__byte_perm(x[2][e], x[3][e], pick_dim(z)), af[2], af[3]);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) mma16816<true>(o[n][2 * e + z], af, pf[n][0], pf[n][1]);
                     }

@@ -101,15 +101,6 @@ struct Args {
     float2* part_ml;  // [splits][num_q heads]
 };
 
-// four e4m3 codes (low byte first) as two bf16 pairs, exact
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t x, uint32_t& lo, uint32_t& hi) {
-    uint32_t a, b;
-    e4m3x4_to_f16(x, a, b);
-    const float2 u = __half22float2(*reinterpret_cast<__half2*>(&a)), v = __half22float2(*reinterpret_cast<__half2*>(&b));
-    lo = pack_bf16(u.x, u.y);
-    hi = pack_bf16(v.x, v.y);
-}
-
 // Shared-memory matrix descriptors as a low word, which holds the address and
 // the leading stride, and the high word they share (8-row groups 1024 bytes
 // apart, 128-byte swizzle)

@@ -392,8 +392,9 @@ dsa_status dsa_lse_combine(const void* const* o_parts, const float* const* lse_p
  * Roundings: scores, maxima, sums of weights, outputs before their last step
  * are fp32; a weight is rounded once for its product with the value, to bf16
  * (half a step: 2^-8 of it) or, in dense_gqa_decode over e4m3 caches, to f16
- * (2^-11); over e4m3 caches it carries the value's scale then (scales up to
- * 2^100 apart); out is rounded once, to bf16.  The tensor cores truncate their
+ * (2^-11; what is lost of small weights is together below 2^-8 of the largest;
+ * where scales lie too far apart for that, bf16); over e4m3 caches it carries
+ * the value's scale then (scales up to 2^100 apart); out is rounded once, to bf16.  The tensor cores truncate their
  * fp32 sums: over n keys of values of one sign a result may fall short by n 2^-26
  * of itself in dense_gqa_prefill (seen: 0.8% at 2^20 keys) and n 2^-28 in
  * dense_gqa_decode.  Calls with max_ctx past 2^22 run decode's kernel. */

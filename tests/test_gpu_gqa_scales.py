@@ -24,14 +24,15 @@ def _gpu():
 
 
 @pytest.mark.parametrize("call", list(CALLS))
-@pytest.mark.parametrize("shift, amp", [(7, 1.0), (24, 4.0), (34, 4.0), (60, 4.0), (60, 1.0), (100, 4.0)])
+@pytest.mark.parametrize("shift, amp", [(7, 1.0), (24, 4.0), (34, 4.0), (60, 4.0), (60, 1.0), (60, 0.5), (100, 4.0)])
 @pytest.mark.parametrize("ctx, new, hq, hkv, d", [([700], [1], 16, 2, 128), ([5000, 70], [1, 1], 8, 8, 64),
                                                   ([3000], [2], 16, 2, 128), ([900, 4000], [4, 3], 16, 2, 128),
                                                   ([900], [4], 16, 2, 64), ([40000], [1], 16, 2, 128),
                                                   ([30000, 25], [3, 1], 16, 2, 64)])
 def test_large_scales_of_keys_without_weight(call, shift, amp, ctx, new, hq, hkv, d):
     """Every eighth key of the first 256 and a few behind them: scores some 40 amp below the others'
-    (for amp 1 a weight of 2^-58 or so), scales 2^shift times the others'."""
+    (for amp 1 a weight of 2^-58 or so), scales 2^shift times the others'.  Their values are 0 in every other
+    dim: there the other keys alone count, however small their products are beside the largest."""
     c = Case(ctx, new, hq, hkv, d, e4m3=True, page=64, seed=shift)
     c.q = (c.q.float().abs() * amp).bfloat16()
     for b, n in enumerate(ctx):
@@ -39,9 +40,10 @@ def test_large_scales_of_keys_without_weight(call, shift, amp, ctx, new, hq, hkv
         at = rows[[j for j in range(n) if (j < 256 and j % 8 == 3) or j % 613 == 600]]
         c.k[at] = 0xFE  # -448
         c.ks[at] = 0.01 if d == 128 else 0.0141
+        c.v[at, :, ::2] = 0
         c.vs[rows] *= 2.0 ** (-shift / 2)
         c.vs[at] *= 2.0 ** shift
-    c.dq, c.dk, c.dks, c.dvs = [x.to(DEV) for x in (c.q, c.k, c.ks, c.vs)]
+    c.dq, c.dk, c.dv, c.dks, c.dvs = [x.to(DEV) for x in (c.q, c.k, c.v, c.ks, c.vs)]
     c.run(call).check()
 
 
