@@ -14,6 +14,7 @@ raises if it is not built.
 from ._binding import (  # noqa: F401
     DSA_BF16,
     DSA_FP8_DS_MLA,
+    DSA_FP8_E4M3_BLOCKSCALE,
     DSA_FP8_E4M3_ROWSCALE,
     DSA_NVFP4,
     DSA_ROPE_HALVES,
@@ -33,10 +34,12 @@ from ._binding import (  # noqa: F401
     dsa_index_k_insert,
     dsa_index_scores,
     dsa_index_scores_nvfp4,
+    dsa_kv_block_insert,
     dsa_kv_insert,
     dsa_latent_insert,
     dsa_lse_combine,
     dsa_mla_q_prep,
+    dsa_step_plan,
     dsa_topk,
     dsa_topk_candidates,
     dsa_topk_compact,
@@ -54,5 +57,5 @@ __all__ = ["Seqs", "DsaError", "dsa_workspace_size", "dsa_index_scores", "dsa_in
            "DcpShard", "dsa_topk_candidates", "dsa_topk_merge", "dsa_topk_compact", "dsa_lse_combine",
            "dsa_block_topk", "dsa_dcp_shard_seqs",
            "GqaShape", "dsa_kv_insert", "dense_gqa_workspace_size", "dense_gqa_decode", "dense_gqa_prefill",
-           "DSA_ROPE_PAIRS", "DSA_ROPE_HALVES",
+           "DSA_ROPE_PAIRS", "DSA_ROPE_HALVES", "DSA_FP8_E4M3_BLOCKSCALE", "dsa_kv_block_insert", "dsa_step_plan",
            "load", "version", "DSA_BF16", "DSA_FP8_E4M3_ROWSCALE", "DSA_FP8_DS_MLA"]

@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libdsa.so")
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA = 0, 1, 2, 3
 DSA_ERR_WORKSPACE, DSA_ERR_TIMEOUT, DSA_ERR_BAD_INPUT = 4, 5, 6
-DSA_BF16, DSA_FP8_E4M3_ROWSCALE, DSA_FP8_DS_MLA, DSA_NVFP4 = 0, 1, 2, 3
+DSA_BF16, DSA_FP8_E4M3_ROWSCALE, DSA_FP8_DS_MLA, DSA_NVFP4, DSA_FP8_E4M3_BLOCKSCALE = 0, 1, 2, 3, 4
 DSA_ROPE_PAIRS, DSA_ROPE_HALVES = 0, 1
 EXPORTS = ("dsa_workspace_size", "dsa_index_scores", "dsa_topk", "sparse_mla_decode", "dsa_decode_layer",
            "dsa_decode_layer_launches", "dsa_decode_layer_launches_for", "sparse_mla_decode_noalloc",
@@ -32,14 +32,15 @@ class DcpShard(ctypes.Structure):
 
 class GqaShape(ctypes.Structure):
     """dsa_gqa_shape: heads, head width, cache dtype and row strides (elements;
-    0: contiguous) of the dense attention calls."""
+    0: contiguous) of the grouped-head attention calls; scale_block: tokens per
+    scale of a DSA_FP8_E4M3_BLOCKSCALE cache."""
     _fields_ = [("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("kv_dtype", ctypes.c_int), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
-                ("v_stride", ctypes.c_int64)]
+                ("v_stride", ctypes.c_int64), ("scale_block", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
     def __init__(self, num_heads: int, num_kv_heads: int, head_dim: int, kv_dtype: int = DSA_BF16, *,
-                 q_stride: int = 0, k_stride: int = 0, v_stride: int = 0):
-        super().__init__(num_heads, num_kv_heads, head_dim, kv_dtype, q_stride, k_stride, v_stride)
+                 q_stride: int = 0, k_stride: int = 0, v_stride: int = 0, scale_block: int = 0):
+        super().__init__(num_heads, num_kv_heads, head_dim, kv_dtype, q_stride, k_stride, v_stride, scale_block, 0)
 
 
 class DsaError(RuntimeError):
@@ -117,6 +118,10 @@ def load(path: str = LIB_PATH):
         L.dense_gqa_workspace_size.argtypes = [G, S, I32, ctypes.POINTER(SZ)]
         L.dense_gqa_decode.argtypes = [G, P, P, P, P, P, S, I32, F, P, P, P, SZ, P, P]
         L.dense_gqa_prefill.argtypes = L.dense_gqa_decode.argtypes
+        L.dsa_kv_block_insert.argtypes = [G, P, I64, P, I64, P, I64, S, I32, P, I32, ctypes.c_int, P, P, P, P, P, P, P]
+        L.dsa_step_plan.argtypes = [P, P, I32, P, I32, P, I32, I32, P, I32, I32, P, P, P, P, P, P, P]
+        for f in ("dsa_kv_block_insert", "dsa_step_plan"):
+            getattr(L, f).restype = ctypes.c_int
         for f in ("dsa_kv_insert", "dense_gqa_workspace_size", "dense_gqa_decode", "dense_gqa_prefill"):
             getattr(L, f).restype = ctypes.c_int
         L.dsa_decode_layer_launches.restype = ctypes.c_int32
@@ -367,6 +372,28 @@ def dsa_kv_insert(shape: GqaShape, k, v, q, pos, slot, n: int, inv_freq, rot_dim
     _check(load().dsa_kv_insert(ctypes.byref(shape), _p(k), k_stride, _p(v), v_stride, _p(q), q_stride, _p(pos),
                                 _p(slot), n, _p(inv_freq), rot_dims, layout, _p(k_cache), _p(v_cache), _p(k_scale),
                                 _p(v_scale), num_rows, _p(q_out), _p(d_status), _stream(stream)))
+
+
+def dsa_kv_block_insert(shape: GqaShape, k, v, q, seqs: Seqs, num_q: int, inv_freq, rot_dims: int, layout: int,
+                        k_cache, v_cache, k_scale, v_scale, q_out, *, k_stride: int = 0, v_stride: int = 0,
+                        q_stride: int = 0, d_status=None, stream=None):
+    """The sequences' new tokens into a cache with a scale per block of tokens
+    and head; strides as dsa_kv_insert."""
+    sc = seqs.c()
+    _check(load().dsa_kv_block_insert(ctypes.byref(shape), _p(k), k_stride, _p(v), v_stride, _p(q), q_stride,
+                                      ctypes.byref(sc), num_q, _p(inv_freq), rot_dims, layout, _p(k_cache),
+                                      _p(v_cache), _p(k_scale), _p(v_scale), _p(q_out), _p(d_status),
+                                      _stream(stream)))
+
+
+def dsa_step_plan(cached_len, new_len, num_seqs: int, free_pages, free_range, page_size: int, num_pages: int,
+                  page_table, num_q: int, ctx_len, q_start, q_pos, slot, next_range, *, d_status=None, stream=None):
+    """A step's page table [num_seqs, max_pages], positions and slots from its
+    requests' lengths; ``free_pages`` and ``page_table`` are tensors."""
+    _check(load().dsa_step_plan(_p(cached_len), _p(new_len), num_seqs, _p(free_pages), int(free_pages.shape[0]),
+                                _p(free_range), page_size, num_pages, _p(page_table), int(page_table.shape[1]), num_q,
+                                _p(ctx_len), _p(q_start), _p(q_pos), _p(slot), _p(next_range), _p(d_status),
+                                _stream(stream)))
 
 
 def dense_gqa_workspace_size(shape: GqaShape, seqs: Seqs, num_q: int) -> int:

@@ -2,6 +2,7 @@
 // every reason listed), workspace carving and the launch sequence.  No entry
 // point allocates, synchronises or reads device memory on the host.
 #include <stdarg.h>
+#include <stddef.h>
 #include <stdio.h>
 #include <string.h>
 
@@ -159,6 +160,15 @@ cudaError_t launch_kv_insert(const dsa_gqa_shape& sh, const void* k, int64_t k_i
                              const float* inv_freq, int32_t rot, bool halves, void* k_cache, void* v_cache,
                              float* k_scale, float* v_scale, int64_t num_rows, void* q_out, int32_t* d_status,
                              cudaStream_t stream);
+cudaError_t launch_kv_block_insert(const dsa_gqa_shape& sh, const void* k, int64_t k_in, const void* v, int64_t v_in,
+                                   const void* q, int64_t q_in, const dsa_seqs& s, int32_t num_q,
+                                   const float* inv_freq, int32_t rot, bool halves, void* k_cache, void* v_cache,
+                                   float* k_scale, float* v_scale, void* q_out, int32_t* d_status,
+                                   cudaStream_t stream);
+cudaError_t launch_step_plan(const int32_t* cached, const int32_t* fresh, int32_t num_seqs, const int32_t* free_pages,
+                             int32_t free_cap, const int32_t* free_range, int32_t page_size, int32_t num_pages,
+                             int32_t* table, int32_t max_pages, int32_t num_q, int32_t* ctx, int32_t* q_start,
+                             int32_t* q_pos, int64_t* slot, int32_t* next, int32_t* d_status, cudaStream_t stream);
 namespace gqa {
 size_t decode_workspace(const dsa_gqa_shape& sh);
 cudaError_t launch_decode(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v, const float* k_scale,
@@ -341,19 +351,29 @@ dsa_status dsa_latent_insert(const void* c_kv, const void* k_pe, const int32_t* 
 
 // ---- dense attention with grouped heads
 
-// The shape, checked, with its strides filled in
+// The shape, checked, with its strides filled in.  scale_block is read for the
+// dtype that has one only: the struct's earlier form ends before it.
 static dsa_gqa_shape check_shape(Check& c, const dsa_gqa_shape* in) {
     c.need(in != nullptr, DSA_ERR_INVALID_ARG, "shape is NULL");
-    if (!in) return dsa_gqa_shape{};
-    dsa_gqa_shape sh = *in;
+    dsa_gqa_shape sh{};
+    if (!in) return sh;
+    memcpy(&sh, in, offsetof(dsa_gqa_shape, scale_block));
+    if (sh.kv_dtype == DSA_FP8_E4M3_BLOCKSCALE) {
+        sh.scale_block = in->scale_block;
+        c.need(sh.scale_block >= 16 && sh.scale_block <= DSA_GQA_MAX_BLOCK &&
+                   (sh.scale_block & (sh.scale_block - 1)) == 0,
+               DSA_ERR_UNSUPPORTED, "scale_block %d is not a power of two in [16, %d]", sh.scale_block,
+               DSA_GQA_MAX_BLOCK);
+    }
     c.need(sh.num_kv_heads >= 1 && sh.num_kv_heads <= 65535, DSA_ERR_INVALID_ARG,
            "num_kv_heads %d outside [1, 65535]", sh.num_kv_heads);
     c.need(sh.num_heads >= 1 && sh.num_heads <= 65535, DSA_ERR_INVALID_ARG, "num_heads %d outside [1, 65535]",
            sh.num_heads);
     c.need(sh.head_dim == 64 || sh.head_dim == 128, DSA_ERR_UNSUPPORTED, "head_dim %d is neither 64 nor 128",
            sh.head_dim);
-    c.need(sh.kv_dtype == DSA_BF16 || sh.kv_dtype == DSA_FP8_E4M3_ROWSCALE, DSA_ERR_UNSUPPORTED,
-           "kv_dtype %d is neither DSA_BF16 nor DSA_FP8_E4M3_ROWSCALE", (int)sh.kv_dtype);
+    c.need(sh.kv_dtype == DSA_BF16 || sh.kv_dtype == DSA_FP8_E4M3_ROWSCALE || sh.kv_dtype == DSA_FP8_E4M3_BLOCKSCALE,
+           DSA_ERR_UNSUPPORTED, "kv_dtype %d is none of DSA_BF16, DSA_FP8_E4M3_ROWSCALE and DSA_FP8_E4M3_BLOCKSCALE",
+           (int)sh.kv_dtype);
     if (c.st != DSA_OK) return sh;
     c.need(sh.num_heads % sh.num_kv_heads == 0, DSA_ERR_INVALID_ARG, "num_heads %d is not a multiple of num_kv_heads %d",
            sh.num_heads, sh.num_kv_heads);
@@ -390,6 +410,8 @@ dsa_status dsa_kv_insert(const dsa_gqa_shape* shape, const void* k, int64_t k_in
                          int32_t* d_status, cudaStream_t stream) {
     Check c;
     const dsa_gqa_shape sh = check_shape(c, shape);
+    c.need(sh.kv_dtype != DSA_FP8_E4M3_BLOCKSCALE, DSA_ERR_UNSUPPORTED,
+           "kv_dtype DSA_FP8_E4M3_BLOCKSCALE: dsa_kv_block_insert writes such caches");
     c.need(n >= 0, DSA_ERR_INVALID_ARG, "n %d < 0", n);
     c.need(num_rows >= 1, DSA_ERR_INVALID_ARG, "num_rows %lld < 1", (long long)num_rows);
     c.need(layout == DSA_ROPE_PAIRS || layout == DSA_ROPE_HALVES, DSA_ERR_UNSUPPORTED,
@@ -439,9 +461,95 @@ static size_t gqa_workspace(const dsa_gqa_shape& sh, int32_t num_q) {
 
 static void check_gqa_sizes(Check& c, const dsa_gqa_shape& sh, const dsa_seqs* s) {
     if (c.st != DSA_OK) return;
+    if (sh.kv_dtype == DSA_FP8_E4M3_BLOCKSCALE && s->page_table)
+        c.need(s->page_size >= sh.scale_block, DSA_ERR_UNSUPPORTED, "page_size %d below scale_block %d", s->page_size,
+               sh.scale_block);
     c.need(s->num_rows <= INT32_MAX, DSA_ERR_UNSUPPORTED, "num_rows %lld exceeds 2^31 - 1", (long long)s->num_rows);
     c.need((int64_t)s->max_q_per_seq * (sh.num_heads / sh.num_kv_heads) * sh.num_kv_heads < ((int64_t)1 << 31),
            DSA_ERR_UNSUPPORTED, "max_q_per_seq %d of %d heads exceeds 2^31 rows", s->max_q_per_seq, sh.num_heads);
+}
+
+dsa_status dsa_kv_block_insert(const dsa_gqa_shape* shape, const void* k, int64_t k_in, const void* v, int64_t v_in,
+                               const void* q, int64_t q_in, const dsa_seqs* seqs, int32_t num_q,
+                               const float* inv_freq, int32_t rot_dims, dsa_rope_layout layout, void* k_cache,
+                               void* v_cache, float* k_scale, float* v_scale, void* q_out, int32_t* d_status,
+                               cudaStream_t stream) {
+    Check c;
+    const dsa_gqa_shape sh = check_shape(c, shape);
+    c.need(!shape || sh.kv_dtype == DSA_FP8_E4M3_BLOCKSCALE, DSA_ERR_UNSUPPORTED,
+           "kv_dtype %d is not DSA_FP8_E4M3_BLOCKSCALE", (int)sh.kv_dtype);
+    check_seqs(c, seqs, num_q);
+    check_gqa_sizes(c, sh, seqs);
+    c.need(layout == DSA_ROPE_PAIRS || layout == DSA_ROPE_HALVES, DSA_ERR_UNSUPPORTED,
+           "rotation layout %d is neither DSA_ROPE_PAIRS nor DSA_ROPE_HALVES", (int)layout);
+    if (inv_freq)
+        c.need(rot_dims >= 16 && rot_dims % 16 == 0 && (c.st != DSA_OK || rot_dims <= sh.head_dim), DSA_ERR_UNSUPPORTED,
+               "rot_dims %d is not a multiple of 16 in [16, head_dim]", rot_dims);
+    else
+        c.need(rot_dims == 0, DSA_ERR_INVALID_ARG, "rot_dims %d without inv_freq", rot_dims);
+    int64_t ks = k_in, vs = v_in, qs = q_in;
+    if (c.st == DSA_OK) {
+        const int64_t kw = (int64_t)sh.num_kv_heads * sh.head_dim;
+        ks = check_in_stride(c, "k_in", k_in, kw);
+        vs = check_in_stride(c, "v_in", v_in, kw);
+        if (q) qs = check_in_stride(c, "q_in", q_in, (int64_t)sh.num_heads * sh.head_dim);
+    }
+    c.ptr(k, "k");
+    c.ptr(v, "v");
+    c.ptr(k_cache, "k_cache");
+    c.ptr(v_cache, "v_cache");
+    c.ptr(k_scale, "k_scale", 4);
+    c.ptr(v_scale, "v_scale", 4);
+    if (inv_freq) c.ptr(inv_freq, "inv_freq", 4);
+    if (q) {
+        c.ptr(q, "q");
+        c.ptr(q_out, "q_out");
+        c.need(q_out != q || qs == sh.q_stride, DSA_ERR_INVALID_ARG, "q_out is q with another stride");
+    }
+    dsa_status st = c.done();
+    if (st != DSA_OK || num_q == 0) return st;
+    return cuda_status(launch_kv_block_insert(sh, k, ks, v, vs, q, qs, *seqs, num_q, inv_freq, rot_dims,
+                                              layout == DSA_ROPE_HALVES, k_cache, v_cache, k_scale, v_scale, q_out,
+                                              d_status, stream),
+                       "dsa_kv_block_insert launch");
+}
+
+dsa_status dsa_step_plan(const int32_t* cached_len, const int32_t* new_len, int32_t num_seqs,
+                         const int32_t* free_pages, int32_t free_cap, const int32_t* free_range, int32_t page_size,
+                         int32_t num_pages, int32_t* page_table, int32_t max_pages, int32_t num_q, int32_t* ctx_len,
+                         int32_t* q_start, int32_t* q_pos, int64_t* slot, int32_t* next_range, int32_t* d_status,
+                         cudaStream_t stream) {
+    Check c;
+    c.need(num_seqs >= 1, DSA_ERR_INVALID_ARG, "num_seqs %d < 1", num_seqs);
+    c.need(num_q >= 0 && num_q <= (1 << 30), DSA_ERR_INVALID_ARG, "num_q %d outside [0, 2^30]", num_q);
+    c.need(free_cap >= 0, DSA_ERR_INVALID_ARG, "free_cap %d < 0", free_cap);
+    c.need(num_pages >= 1, DSA_ERR_INVALID_ARG, "num_pages %d < 1", num_pages);
+    c.need(max_pages >= 1, DSA_ERR_INVALID_ARG, "max_pages %d < 1", max_pages);
+    c.need(page_size >= 16 && (page_size & (page_size - 1)) == 0, DSA_ERR_UNSUPPORTED,
+           "page_size %d is not a power of two >= 16", page_size);
+    c.ptr(cached_len, "cached_len", 4);
+    c.ptr(new_len, "new_len", 4);
+    if (free_cap > 0) c.ptr(free_pages, "free_pages", 4);
+    c.ptr(free_range, "free_range", 4);
+    c.ptr(page_table, "page_table", 4);
+    c.ptr(ctx_len, "ctx_len", 4);
+    c.ptr(q_start, "q_start", 4);
+    if (num_q > 0) {
+        c.ptr(q_pos, "q_pos", 4);
+        c.ptr(slot, "slot", 8);
+    }
+    c.ptr(next_range, "next_range", 4);
+    // every CTA reads the lengths and the range: what they are must not become what they will be
+    const void* out[] = {ctx_len, q_start, q_pos, slot, next_range};
+    for (const void* p : out)
+        c.need(!p || (p != cached_len && p != new_len && p != free_range && p != free_pages && p != page_table),
+               DSA_ERR_INVALID_ARG, "an output is one of the inputs");
+    dsa_status st = c.done();
+    if (st != DSA_OK) return st;
+    return cuda_status(launch_step_plan(cached_len, new_len, num_seqs, free_pages, free_cap, free_range, page_size,
+                                        num_pages, page_table, max_pages, num_q, ctx_len, q_start, q_pos, slot,
+                                        next_range, d_status, stream),
+                       "dsa_step_plan launch");
 }
 
 dsa_status dense_gqa_workspace_size(const dsa_gqa_shape* shape, const dsa_seqs* seqs, int32_t num_q, size_t* bytes) {
@@ -470,7 +578,7 @@ static dsa_status dense_gqa(bool prefill, const dsa_gqa_shape* shape, const void
     c.ptr(v_cache, "v_cache");
     c.ptr(out, "out");
     if (lse) c.ptr(lse, "lse", 4);
-    if (shape && shape->kv_dtype == DSA_FP8_E4M3_ROWSCALE) {
+    if (sh.kv_dtype == DSA_FP8_E4M3_ROWSCALE || sh.kv_dtype == DSA_FP8_E4M3_BLOCKSCALE) {
         c.ptr(k_scale, "k_scale", 4);
         c.ptr(v_scale, "v_scale", 4);
     }

@@ -1,6 +1,7 @@
 // cache_write.cu -- the kernels on either side of the decode path (sm_103a):
 // new tokens into the indexer-key and latent caches, and the attention query's
-// RoPE + SSMax.
+// RoPE + SSMax; keys and values of grouped heads, with a scale per row or per
+// block of tokens.
 //
 // Definitions ([colibri] "Mistral-Large-4 (c/colibri.c)", What differs from
 // GLM-5.2: The indexer (k = LayerNorm(wk(x)), rotated on its first 64 dims on
@@ -18,8 +19,10 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
-#include "dsa_internal.cuh"
+#include "once.cuh"
+#include "segments.cuh"
 
 namespace dsa {
 namespace {
@@ -665,6 +668,300 @@ cudaError_t launch_kv_insert(const dsa_gqa_shape& sh, const void* k, int64_t k_i
                    : (halves ? go(kv_insert_kernel<64, false, true>) : go(kv_insert_kernel<64, false, false>));
     return fp8 ? (halves ? go(kv_insert_kernel<128, true, true>) : go(kv_insert_kernel<128, true, false>))
                : (halves ? go(kv_insert_kernel<128, false, true>) : go(kv_insert_kernel<128, false, false>));
+}
+
+// ---------------------------------------------------------------------------
+// Keys and values into an e4m3 cache with one scale per block of S tokens and
+// head, a power of two:
+//   need = 2^ceil(log2(max |y| / 448)) over the block's new tokens (at least
+//   kLeastScale), scale = need, or the larger of it and the held scale where
+//   older tokens lie in the block; code = y / scale to nearest even.
+// A power of two costs an e4m3 code no precision (its exponent moves), and
+// makes a grown block's older codes exact multiples: they are encoded again
+// without loss but for values below the smallest normal code.
+//
+// HBM-bound: 3 bytes a key or value, 4 a query value.  A CTA takes one block of
+// new tokens at a time: the cosines and sines of its tokens go to shared memory
+// once for all heads; then eight warps of 16 rows each take the heads one after
+// the other (a head's rows in as many warps as it needs), so that a block's
+// maximum is met on the way and every value is read once, held in registers
+// between the maximum and its code.  Few blocks: blockIdx.y shares the heads.
+namespace {
+
+constexpr float kLeastScale = 0x1p-60f;
+constexpr int kBlkThreads = 256, kBlkWarps = kBlkThreads / 32;
+
+struct KvBlockInsert {
+    const __nv_bfloat16 *k, *v, *q;
+    int64_t k_in, v_in, q_in;  // elements between tokens
+    const float* inv_freq;
+    uint8_t *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+    __nv_bfloat16* q_out;
+    int64_t k_stride, v_stride, q_stride;
+    dsa_seqs s;
+    int32_t* d_status;
+    int32_t num_q, hq, hkv, rot, shift;  // hq: 0 without queries; 2^shift tokens per scale
+};
+
+// a row's 8 dims of lane li, rotated: `o` holds the partner dims (HALVES) or the same (PAIRS)
+template <bool HALVES>
+__device__ __forceinline__ void turn8(float (&v)[8], const uint4& x, const uint4& o, bool turned, bool upper,
+                                      const float2* cs) {
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, os[4] = {o.x, o.y, o.z, o.w};
+    if (!turned) {
+        unpack_bf16x8(x, v);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float a = bf16_lo(xs[e]), b = bf16_hi(xs[e]);
+        if (HALVES) {
+            const float2 c0 = cs[2 * e], c1 = cs[2 * e + 1];
+            const float s0 = upper ? c0.y : -c0.y, s1 = upper ? c1.y : -c1.y;
+            v[2 * e] = fmaf(bf16_lo(os[e]), s0, a * c0.x);
+            v[2 * e + 1] = fmaf(bf16_hi(os[e]), s1, b * c1.x);
+        } else {
+            const float2 c = cs[e];
+            v[2 * e] = fmaf(b, -c.y, a * c.x);
+            v[2 * e + 1] = fmaf(a, c.y, b * c.x);
+        }
+    }
+}
+
+template <int D, bool HALVES>
+__global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const __grid_constant__ KvBlockInsert a) {
+    constexpr int kLanes = D / 8;        // lanes per row
+    constexpr int kGroup = 32 / kLanes;  // rows per warp access
+    constexpr int kAcc = 16 / kGroup;    // accesses of a warp's 16 rows
+    extern __shared__ __align__(16) float2 table[];  // [token][rot / 2]: cos, sin
+    __shared__ Pieces<kBlkThreads> pieces;
+    __shared__ float top[2][kBlkWarps];
+    __shared__ bool good[128];
+    pdl_enter();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int half = a.rot / 2;
+    const int li = lane % kLanes, sub = lane / kLanes;
+    const bool turned = 8 * li < a.rot;
+    const int step = a.rot / 16;  // HALVES: lanes between a pair's dims
+    const bool upper = turned && HALVES && li >= step;
+    const int from = !turned || !HALVES ? lane : upper ? lane - step : lane + step;
+    const int f0 = !turned ? 0 : HALVES ? 8 * (upper ? li - step : li) : 4 * li;  // the lane's first frequency
+    const bool lead = blockIdx.y == 0;
+    int64_t before = 0;
+    int turn = 0;
+    for (int c0 = 0; c0 < a.s.num_seqs; c0 += Pieces<kBlkThreads>::kChunk) {
+        const int left = min(Pieces<kBlkThreads>::kChunk, a.s.num_seqs - c0);
+        const int total = pieces.scan(c0, a.s.num_seqs, [&](int b) {
+            const NewTokens n = new_tokens(a.s, b, a.num_q);
+            if (n.bad && blockIdx.x == 0 && lead) report(a.d_status, DSA_ERR_BAD_INPUT);
+            return blocks_touched(n, a.shift);
+        });
+        for (int x = (int)((gridDim.x + blockIdx.x - before % gridDim.x) % gridDim.x); x < total; x += gridDim.x) {
+            const int i = pieces.find(x, left), b = c0 + i;
+            const NewTokens nt = new_tokens(a.s, b, a.num_q);
+            const int blk = (nt.p0 >> a.shift) + (x - pieces.first[i]);
+            const int64_t lo = (int64_t)blk << a.shift;
+            const int pos0 = (int)max(lo, (int64_t)nt.p0);                    // the piece's first new token
+            const int t0 = nt.q0 + (pos0 - nt.p0);
+            const int n = (int)min(lo + (1 << a.shift), (int64_t)nt.p0 + nt.nq) - pos0;
+            const int old = pos0 - (int)lo;                                   // older tokens of the block
+            const int64_t row0 = phys_row(a.s, b, lo);                        // the block's first row
+            const bool there = row0 >= 0 && (row0 & ((1 << a.shift) - 1)) == 0;
+            __syncthreads();  // the last piece's table and tokens are no longer read
+            bool some = false;
+            if ((int)threadIdx.x < n) {
+                const int p = __ldg(a.s.q_pos + t0 + threadIdx.x);
+                const bool ok = p == pos0 + (int)threadIdx.x && p < nt.ctx && there &&
+                                row0 + old + (int)threadIdx.x < a.s.num_rows;
+                if (!ok && p != -1 && lead) report(a.d_status, DSA_ERR_BAD_INPUT);
+                good[threadIdx.x] = ok;
+                some = ok;
+            }
+            for (int y = threadIdx.x; y < n * half; y += kBlkThreads) {
+                const int tok = y / half, f = y - tok * half;
+                float c, sn;
+                rope_cs(pos0 + tok, __ldg(a.inv_freq + f), c, sn);
+                table[y] = make_float2(c, sn);
+            }
+            if (!__syncthreads_or(some)) continue;
+
+            // ---- keys and values: a head's rows in `per` warps
+            const int per = n <= 16 ? 1 : n <= 32 ? 2 : n <= 64 ? 4 : 8;
+            const int heads = kBlkWarps / per;
+            const int rounds = (2 * a.hkv + heads - 1) / heads;
+            for (int r = blockIdx.y; r < rounds; r += gridDim.y) {
+                const int task = r * heads + warp / per, part = warp % per;
+                const bool live = task < 2 * a.hkv;
+                const bool is_k = task < a.hkv;
+                const int h = is_k ? task : task - a.hkv;
+                const __nv_bfloat16* src = is_k ? a.k : a.v;
+                const int64_t in = is_k ? a.k_in : a.v_in;
+                uint8_t* cache = is_k ? a.k_cache : a.v_cache;
+                float* scales = is_k ? a.k_scale : a.v_scale;
+                const int64_t stride = is_k ? a.k_stride : a.v_stride;
+                const int64_t at_scale = (row0 >> a.shift) * a.hkv + h;
+                const float held = live && old ? scales[at_scale] : 0.f;
+                uint4 raw[kAcc];
+#pragma unroll
+                for (int u = 0; u < kAcc; ++u) {
+                    const int tok = part * 16 + u * kGroup + sub;
+                    raw[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (live && tok < n && good[tok])
+                        raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + (int64_t)(t0 + tok) * in + h * D + 8 * li));
+                }
+                float v[kAcc][8];
+                float m = 0.f;
+#pragma unroll
+                for (int u = 0; u < kAcc; ++u) {
+                    const int tok = min(part * 16 + u * kGroup + sub, n - 1);
+                    uint4 o = raw[u];
+                    if (HALVES && a.rot) {
+                        o.x = __shfl_sync(0xffffffffu, o.x, from);
+                        o.y = __shfl_sync(0xffffffffu, o.y, from);
+                        o.z = __shfl_sync(0xffffffffu, o.z, from);
+                        o.w = __shfl_sync(0xffffffffu, o.w, from);
+                    }
+                    turn8<HALVES>(v[u], raw[u], o, turned && is_k, upper, table + tok * half + f0);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float y = fabsf(v[u][e]);
+                        m = fmaxf(m, y < INFINITY ? y : 0.f);  // what is not finite has no say
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                if (lane == 0) top[turn][warp] = m;
+                __syncthreads();
+                for (int w = warp - part; w < warp - part + per; ++w) m = fmaxf(m, top[turn][w]);
+                turn ^= 1;  // (the next round's barrier lies between this reading and the next writing)
+                if (!live) continue;
+                float scale = m > 0.f ? fmaxf(two_to(scale_exponent(m, 8, 0x600000u)), kLeastScale) : kLeastScale;
+                if (old) {
+                    const bool known = held > 0.f && held < INFINITY;
+                    if (!known && lane == 0 && part == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
+                    if (known && held >= scale) {
+                        scale = held;
+                    } else if (known) {
+                        // rare: the older codes in the new scale
+                        const float f = held / scale;
+                        constexpr int kOldLanes = D / 16;
+                        for (int y = part * (32 / kOldLanes) + lane / kOldLanes; y < old; y += per * (32 / kOldLanes)) {
+                            uint4* c = reinterpret_cast<uint4*>(cache + (row0 + y) * stride + h * D) + lane % kOldLanes;
+                            const uint4 z = *c;
+                            uint32_t w[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t l2 = e4m3x2_to_f16x2((uint16_t)w[e]), h2 = e4m3x2_to_f16x2((uint16_t)(w[e] >> 16));
+                                const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&l2));
+                                const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                                w[e] = pack_e4m3x4(p.x * f, p.y * f, q.x * f, q.y * f);
+                            }
+                            *c = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                const float rs = 1.f / scale;
+#pragma unroll
+                for (int u = 0; u < kAcc; ++u) {
+                    const int tok = part * 16 + u * kGroup + sub;
+                    if (tok < n && good[tok])
+                        *reinterpret_cast<uint2*>(cache + (row0 + old + tok) * stride + h * D + 8 * li) =
+                            make_uint2(pack_e4m3x4(v[u][0] * rs, v[u][1] * rs, v[u][2] * rs, v[u][3] * rs),
+                                       pack_e4m3x4(v[u][4] * rs, v[u][5] * rs, v[u][6] * rs, v[u][7] * rs));
+                }
+                if (part == 0 && lane == 0 && scale != held) scales[at_scale] = scale;
+            }
+
+            // ---- queries: 16 (token, head) rows a warp
+            const int rows = n * a.hq;
+            for (int r = ((int)blockIdx.y * kBlkWarps + warp) * 16; r < rows; r += gridDim.y * kBlkWarps * 16) {
+                uint4 raw[kAcc];
+                int tok[kAcc], head[kAcc];
+#pragma unroll
+                for (int u = 0; u < kAcc; ++u) {
+                    const int y = min(r + u * kGroup + sub, rows - 1);
+                    tok[u] = y / a.hq;
+                    head[u] = y - tok[u] * a.hq;
+                    raw[u] = __ldcs(reinterpret_cast<const uint4*>(a.q + (int64_t)(t0 + tok[u]) * a.q_in + head[u] * D +
+                                                                   8 * li));
+                }
+#pragma unroll
+                for (int u = 0; u < kAcc; ++u) {
+                    uint4 o = raw[u];
+                    if (HALVES && a.rot) {
+                        o.x = __shfl_sync(0xffffffffu, o.x, from);
+                        o.y = __shfl_sync(0xffffffffu, o.y, from);
+                        o.z = __shfl_sync(0xffffffffu, o.z, from);
+                        o.w = __shfl_sync(0xffffffffu, o.w, from);
+                    }
+                    float v[8];
+                    turn8<HALVES>(v, raw[u], o, turned, upper, table + tok[u] * half + f0);
+                    if (r + u * kGroup + sub < rows && good[tok[u]])
+                        *reinterpret_cast<uint4*>(a.q_out + (int64_t)(t0 + tok[u]) * a.q_stride + head[u] * D + 8 * li) =
+                            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                       pack_bf16x2(v[6], v[7]));
+                }
+            }
+        }
+        before += total;
+        __syncthreads();  // the chunk's counts are no longer read
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_block_insert(const dsa_gqa_shape& sh, const void* k, int64_t k_in, const void* v, int64_t v_in,
+                                   const void* q, int64_t q_in, const dsa_seqs& s, int32_t num_q,
+                                   const float* inv_freq, int32_t rot, bool halves, void* k_cache, void* v_cache,
+                                   float* k_scale, float* v_scale, void* q_out, int32_t* d_status,
+                                   cudaStream_t stream) {
+    KvBlockInsert a;
+    a.k = static_cast<const __nv_bfloat16*>(k);
+    a.v = static_cast<const __nv_bfloat16*>(v);
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.k_in = k_in;
+    a.v_in = v_in;
+    a.q_in = q_in;
+    a.inv_freq = inv_freq;
+    a.k_cache = static_cast<uint8_t*>(k_cache);
+    a.v_cache = static_cast<uint8_t*>(v_cache);
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.q_out = static_cast<__nv_bfloat16*>(q_out);
+    a.k_stride = sh.k_stride;
+    a.v_stride = sh.v_stride;
+    a.q_stride = sh.q_stride;
+    a.s = s;
+    a.d_status = d_status;
+    a.num_q = num_q;
+    a.hq = q ? sh.num_heads : 0;
+    a.hkv = sh.num_kv_heads;
+    a.rot = inv_freq ? rot : 0;
+    a.shift = 31 - __builtin_clz((unsigned)sh.scale_block);
+    // pieces: at most a block per token, and two more than whole blocks per sequence; the heads
+    // are shared where they do not fill the GPU (eight CTAs per SM in all)
+    const int64_t blocks = std::min<int64_t>(num_q, (num_q >> a.shift) + 2 * (int64_t)s.num_seqs);
+    const int64_t longest = std::min<int64_t>(sh.scale_block, s.max_q_per_seq);
+    const int64_t per = longest <= 16 ? 1 : longest <= 32 ? 2 : longest <= 64 ? 4 : 8;
+    const int64_t work = std::max<int64_t>((2 * sh.num_kv_heads * per + 7) / 8, (longest * a.hq + 127) / 128);
+    const unsigned grid = (unsigned)std::min<int64_t>(blocks, 152 * 8);
+    const unsigned share = (unsigned)std::max<int64_t>(1, std::min<int64_t>(work, 152 * 8 / grid));
+    const size_t smem = (size_t)sh.scale_block * (a.rot / 2) * sizeof(float2);  // up to 64 KB
+    auto go = [&](auto d, auto h) {
+        auto kern = kv_block_insert_kernel<decltype(d)::value, decltype(h)::value>;
+        static OncePerDevice once;
+        const cudaError_t e = once.run(
+            [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 64 * 8); });
+        if (e != cudaSuccess) return e;
+        return launch_pdl(kern, dim3(grid, share), dim3(kBlkThreads), smem, stream, 1, a);
+    };
+    using std::integral_constant;
+    if (sh.head_dim == 64)
+        return halves ? go(integral_constant<int, 64>(), std::true_type())
+                      : go(integral_constant<int, 64>(), std::false_type());
+    return halves ? go(integral_constant<int, 128>(), std::true_type())
+                  : go(integral_constant<int, 128>(), std::false_type());
 }
 
 }  // namespace dsa

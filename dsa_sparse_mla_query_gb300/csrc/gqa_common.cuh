@@ -3,14 +3,18 @@
 // arithmetic, e4m3 codes, ring places and waits.
 #pragma once
 
-#include <atomic>
-
 #include "indexer_common.cuh"
+#include "once.cuh"
 
 namespace dsa {
 namespace gqa {
 
 constexpr int kPlanSms = 152;  // GB300's SMs: sizes that the host alone has to know are planned for them
+
+// rows that share a scale, as a power of two (e4m3: one row, or a block of them)
+inline int scale_shift(const dsa_gqa_shape& sh) {
+    return sh.kv_dtype == DSA_FP8_E4M3_BLOCKSCALE ? 31 - __builtin_clz((unsigned)sh.scale_block) : 0;
+}
 
 // A sequence's counts, checked: queries [q0, q0 + nq) over `ctx` tokens.
 struct Seq {
@@ -138,24 +142,6 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
         : "memory");
 }
-
-// A kernel's attributes, set once on each device that launches it (they belong
-// to the device's own copy of the kernel, and setting them takes longer than
-// the rest of a launch's preparation).
-struct OncePerDevice {
-    std::atomic<uint64_t> done{0};
-    template <typename F>
-    cudaError_t run(F set) {
-        int dev = 0;
-        const cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
-        if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-        const cudaError_t r = set();
-        if (r == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-        return r;
-    }
-};
 
 }  // namespace gqa
 }  // namespace dsa

@@ -90,6 +90,7 @@ struct Args {
     float scale_log2;
     int32_t num_q, group, hkv, lanes, hl, parts;  // hl: lanes side by side; parts: CTAs per lane column
     int32_t cluster;  // > 0: a cluster of this many CTAs per (lane, sequence) instead
+    int32_t scale_shift;  // e4m3: 2^scale_shift rows share a scale
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
                         for (int h = 0; h < kTile / 32; ++h) {
                             const int x = h * 32 + lane;
                             const int row = __shfl_sync(0xffffffffu, cur, l + (x >> shift));
-                            const int64_t at = ((int64_t)row + (x & (R - 1))) * a.hkv + kvh;
+                            const int64_t at = (((int64_t)row + (x & (R - 1))) >> a.scale_shift) * a.hkv + kvh;
                             if (row >= 0 && (int64_t)i * kTile + x < p.limit) {
                                 const bool in = (int64_t)row + (x & (R - 1)) < a.s.num_rows;
                                 ptx::cp_async4_or_zero(sd + x, a.k_scale + (in ? at : 0), in);
@@ -1308,7 +1309,7 @@ cudaError_t launch_decode(const dsa_gqa_shape& sh, const void* q, const void* k,
                           const float* v_scale, const dsa_seqs& s, int num_q, float sm_scale, void* out, float* lse,
                           void* workspace, int32_t* d_status, cudaStream_t stream) {
     const Plan p = make_plan(sh, s);
-    const bool fp8 = sh.kv_dtype == DSA_FP8_E4M3_ROWSCALE;
+    const bool fp8 = sh.kv_dtype != DSA_BF16;
     const int box = s.page_table ? std::min(s.page_size, p.tile) : p.tile;
     CUtensorMap km, vm;
     cudaError_t e = cache_map(&km, fp8, k, sh.num_kv_heads, sh.head_dim, sh.k_stride, s.num_rows, box, box == p.tile);
@@ -1336,6 +1337,7 @@ cudaError_t launch_decode(const dsa_gqa_shape& sh, const void* q, const void* k,
     a.hl = p.hl;
     a.parts = p.parts;
     a.cluster = p.cluster;
+    a.scale_shift = scale_shift(sh);
     auto by_rows = [&](auto d, auto f8) {
         constexpr int D = decltype(d)::value;
         constexpr bool F = decltype(f8)::value;

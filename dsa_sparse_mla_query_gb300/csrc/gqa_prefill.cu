@@ -96,7 +96,8 @@ struct Args {
     float scale_log2;  // > 0: masked scores are -inf before they are scaled
     int32_t num_q, group, hkv, tpt;  // tpt: tokens per tile
     int32_t splits;   // key ranges per item; more than one: partial results
-    const float *k_scale, *v_scale;  // e4m3: [rows][hkv]
+    const float *k_scale, *v_scale;  // e4m3: [rows >> scale_shift][hkv]
+    int32_t scale_shift;
     float* part_o;    // [splits][num_q heads][D]
     float2* part_ml;  // [splits][num_q heads]
 };
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                                 if (row >= 0 && it.key0 + i * kKeys + key < it.limit) {
                                     const int64_t at = (int64_t)row + (key & (R - 1));
                                     const bool in = at < a.s.num_rows;
-                                    const int64_t off = in ? at * a.hkv + it.kvh : 0;
+                                    const int64_t off = in ? (at >> a.scale_shift) * a.hkv + it.kvh : 0;
                                     ptx::cp_async4_or_zero(code_scales + key, a.k_scale + off, in);
                                     ptx::cp_async4_or_zero(code_scales + kKeys + key, a.v_scale + off, in);
                                 }
@@ -1057,7 +1058,8 @@ cudaError_t launch_prefill(const dsa_gqa_shape& sh, const void* q, const void* k
     a.num_q = num_q;
     a.scale_log2 = sm_scale * 1.4426950408889634f;
     const int box = s.page_table ? std::min(s.page_size, kKeys) : kKeys;
-    const bool fp8 = sh.kv_dtype == DSA_FP8_E4M3_ROWSCALE;
+    const bool fp8 = sh.kv_dtype != DSA_BF16;
+    a.scale_shift = scale_shift(sh);
     CUtensorMap qm, km, vm;
     cudaError_t e = query_map(&qm, q, sh.num_heads, sh.head_dim, sh.q_stride, num_q, a.group, a.tpt);
     if (e == cudaSuccess)

@@ -1,0 +1,117 @@
+// segments.cuh -- what a call's new tokens touch, found on the GPU: every CTA
+// scans the sequences' counts and takes its share of the pieces.
+#pragma once
+
+#include "dsa_internal.cuh"
+
+namespace dsa {
+
+// exclusive sum over the CTA's threads; `total` gets the sum of all.  `red` is
+// shared scratch of THREADS / 32 + 1 values; ends in a barrier.
+template <int THREADS, typename T>
+__device__ __forceinline__ T cta_scan(T mine, T* red, T& total) {
+    constexpr int W = THREADS / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    T incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    __syncthreads();  // the last scan's sums are no longer read
+    if (lane == 31) red[warp] = incl;
+    __syncthreads();
+    T before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const T x = red[w];
+        if (w < warp) before += x;
+        total += x;
+    }
+    return before + incl - mine;
+}
+
+// Sequences in pieces, a chunk of them at a time: first[i] pieces lie before
+// sequence i of the chunk.
+template <int THREADS>
+struct Pieces {
+    static constexpr int kPer = 4, kChunk = THREADS * kPer;
+    int first[kChunk + 1];
+    int red[THREADS / 32 + 1];
+    // counts of sequences c0 .. ; count(b) >= 0.  Returns the chunk's pieces.
+    template <typename F>
+    __device__ __forceinline__ int scan(int c0, int num_seqs, F count) {
+        const int left = min(kChunk, num_seqs - c0);
+        const int per = (left + THREADS - 1) / THREADS;
+        int v[kPer];
+        int mine = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int i = (int)threadIdx.x * per + k;
+            v[k] = k < per && i < left ? count(c0 + i) : 0;
+            mine += v[k];
+        }
+        int total;
+        int at = cta_scan<THREADS>(mine, red, total);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int i = (int)threadIdx.x * per + k;
+            if (k < per && i < left) first[i] = at;
+            at += v[k];
+        }
+        if (threadIdx.x == 0) first[left] = total;
+        __syncthreads();
+        return total;
+    }
+    // the sequence of the chunk that piece x lies in
+    __device__ __forceinline__ int find(int x, int left) const {
+        int lo = 0, hi = left - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (first[mid] <= x) lo = mid; else hi = mid - 1;
+        }
+        return lo;
+    }
+};
+
+// Sequence b's new tokens: rows [q0, q0 + nq) at positions p0, p0 + 1, ..;
+// nq = 0 where there is nothing to do (p0 = -1: refused tokens).
+struct NewTokens {
+    int q0, nq, p0, ctx;
+    bool bad;
+};
+__device__ __forceinline__ NewTokens new_tokens(const dsa_seqs& s, int b, int num_q) {
+    NewTokens r;
+    r.ctx = __ldg(s.ctx_len + b);
+    r.q0 = __ldg(s.q_start + b);
+    const int qe = __ldg(s.q_start + b + 1);
+    r.nq = qe - r.q0;
+    r.p0 = -1;
+    r.bad = !(r.ctx >= 0 && r.ctx <= s.max_ctx && r.q0 >= 0 && qe >= r.q0 && qe <= num_q && r.nq <= s.max_q_per_seq);
+    if (r.bad || r.nq == 0) {
+        r.nq = 0;
+        return r;
+    }
+    r.p0 = __ldg(s.q_pos + r.q0);
+    if (r.p0 < 0 || r.p0 >= r.ctx) {
+        r.bad = r.p0 != -1;
+        r.nq = 0;
+    }
+    return r;
+}
+
+// the blocks of 2^shift tokens that they lie in
+__device__ __forceinline__ int blocks_touched(const NewTokens& n, int shift) {
+    return n.nq ? (int)((((int64_t)n.p0 + n.nq - 1) >> shift) - (n.p0 >> shift)) + 1 : 0;
+}
+
+// the least e >= -126 with |x| <= 1.m 2^e max, for max = (1 + limit 2^-23) 2^top: x > 0 finite
+__device__ __forceinline__ int scale_exponent(float x, int top, uint32_t limit) {
+    const uint32_t u = __float_as_uint(x);
+    const int e = (int)(u >> 23) - 127 - top + ((u & 0x7FFFFFu) > limit ? 1 : 0);
+    return (u >> 23) == 0 || e < -126 ? -126 : e;  // (a subnormal x lies below 2^-126)
+}
+__device__ __forceinline__ float two_to(int e) { return __int_as_float((e + 127) << 23); }
+
+}  // namespace dsa

@@ -89,11 +89,13 @@ typedef enum {
     DSA_FP8_DS_MLA = 2,         /* latent: [rows,656] bytes = [0,512) e4m3 latent codes,
                                    [512,528) 4 fp32 scales (one per 128 latent dims),
                                    [528,656) 64 bf16 RoPE dims ([vLLM-ML4] FP8 latent cache) */
-    DSA_NVFP4 = 3               /* latent: codes [rows,288] bytes (576 E2M1 values, value 2i in the low
+    DSA_NVFP4 = 3,              /* latent: codes [rows,288] bytes (576 E2M1 values, value 2i in the low
                                    nibble of byte i) + E4M3 block scales [rows,36] (one per 16 values) +
                                    one fp32 tensor scale g: value = g * scale * code, 4.5 bits/value;
                                    index keys: codes [rows,64] + scales [rows,8] + g (72 B/token)
                                    ("vLLM adds NVFP4 serving for MiniMax M3.1 Flash": NVFP4 caches) */
+    DSA_FP8_E4M3_BLOCKSCALE = 4 /* K and V of grouped heads: e4m3 codes, one fp32 scale per block of tokens
+                                   and head (dsa_gqa_shape) */
 } dsa_dtype;
 
 /* Where tokens live.  Sequence b holds ctx_len[b] tokens; its queries are rows
@@ -409,12 +411,18 @@ typedef struct {
     int32_t head_dim;     /* 64 or 128 */
     dsa_dtype kv_dtype;   /* DSA_BF16: K and V [rows, num_kv_heads, head_dim] bf16;
                              DSA_FP8_E4M3_ROWSCALE: e4m3 codes of that shape and fp32 scales
-                             [rows, num_kv_heads] each: value = scale * code */
+                             [rows, num_kv_heads] each: value = scale * code;
+                             DSA_FP8_E4M3_BLOCKSCALE: such codes and scales [ceil(rows / scale_block),
+                             num_kv_heads]: physical rows [i, i + 1) scale_block share scale i of a head */
     int64_t q_stride;     /* elements between consecutive rows of q, of K and of V (a token's heads are */
     int64_t k_stride;     /* contiguous); 0: heads * head_dim.  Whole multiples of 16 bytes, so that K and */
     int64_t v_stride;     /* V may share one cache, and q, k, v one projection's output */
+    int32_t scale_block;  /* DSA_FP8_E4M3_BLOCKSCALE (not read otherwise): tokens per scale, a power of two in
+                             [16, DSA_GQA_MAX_BLOCK], at most a page's tokens */
+    int32_t reserved;
 } dsa_gqa_shape;
 #define DSA_GQA_MAX_GROUP 64
+#define DSA_GQA_MAX_BLOCK 128
 
 /* K and V of n new tokens into their caches, rotated on the way, and the
  * queries' rotation with them:
@@ -443,6 +451,70 @@ dsa_status dsa_kv_insert(const dsa_gqa_shape* shape, const void* k, int64_t k_in
                          void* v_cache, float* k_scale, float* v_scale, int64_t num_rows, void* q_out,
                          int32_t* d_status, cudaStream_t stream);
 
+/* The same for a cache with one scale per block of tokens and head
+ * (DSA_FP8_E4M3_BLOCKSCALE), which the sequences' new tokens are appended to.
+ * Rows q_start[b] .. of k, v (and q) are sequence b's tokens at positions
+ * q_pos, each one more than the row's before; their physical rows are dsa_seqs'.
+ * Per block of scale_block tokens (of the sequence, and so of the cache), head,
+ * and K or V, with y the block's new values (keys rotated):
+ *   need  = 2^ceil(log2(max |y| / 448)), at least 2^-60 (values that are not
+ *           finite do not count: infinities are stored as 448, NaN as NaN);
+ *   scale = need where the block's tokens are all new, else the larger of need
+ *           and the block's scale so far;
+ *   code  = y / scale to nearest even.
+ * Where the scale grows, codes of the block's older tokens (positions below
+ * the sequence's first new one) are encoded again: a power of two moves an
+ * e4m3 code's exponent, so that only codes that fall below 2^-6 lose bits.
+ * Rows of a block behind its last new token have no meaning afterwards (a
+ * rejected draft's tokens: write the next ones over them).
+ * A sequence whose first position is -1 is skipped, and so is a row with
+ * position -1 (dsa_step_plan writes both); their queries stay unwritten.
+ * DSA_ERR_BAD_INPUT: a position that does not follow its row's before or is
+ * not below ctx_len, a row outside the cache (these tokens are skipped), a
+ * block that does not start at a multiple of scale_block rows (seq_base; its
+ * tokens are skipped), an older scale that is not positive and finite (older
+ * codes are left), a malformed sequence (skipped).  No two sequences with new
+ * tokens may share a block.  q, q_in, q_out, inv_freq, rot_dims, layout and
+ * alignment as above; the queries' positions are the tokens'. */
+dsa_status dsa_kv_block_insert(const dsa_gqa_shape* shape, const void* k, int64_t k_in, const void* v, int64_t v_in,
+                               const void* q, int64_t q_in, const dsa_seqs* seqs, int32_t num_q,
+                               const float* inv_freq, int32_t rot_dims, dsa_rope_layout layout, void* k_cache,
+                               void* v_cache, float* k_scale, float* v_scale, void* q_out, int32_t* d_status,
+                               cudaStream_t stream);
+
+/* A step's page table, positions and cache slots from its requests' lengths,
+ * all on the device (lengths that an earlier step left there, a step captured
+ * into a graph).  Request b has cached_len[b] tokens in its pages and
+ * new_len[b] >= 0 new ones, whose rows follow those of the requests before it:
+ *   ctx_len[b] = cached_len[b] + new_len[b];
+ *   q_start[b] = sum of new_len before b, q_start[num_seqs] = the number of
+ *                rows (both at most num_q);
+ *   q_pos[q_start[b] + i] = cached_len[b] + i;
+ *   page_table[b][c] for ceil(cached_len / page_size) <= c < ceil(ctx_len /
+ *                page_size): the next pages of free_pages[free_range[0] ..
+ *                free_range[1]), in the requests' order;
+ *   slot[row] = page_table[b][pos / page_size] * page_size + pos % page_size;
+ *   next_range = {the first page that was not taken, free_range[1]}.
+ * Rows from the last request's end to num_q are padding: q_pos = slot = -1.
+ * Other entries of page_table are left as they were.  The results are what
+ * dsa_seqs, dsa_kv_insert and dsa_kv_block_insert take.
+ *   cached_len, new_len int32 [num_seqs]; free_pages int32 [free_cap];
+ *   free_range, next_range int32 [2]; page_table int32 [num_seqs, max_pages];
+ *   ctx_len int32 [num_seqs]; q_start int32 [num_seqs + 1]; q_pos int32, slot
+ *   int64 [num_q].  page_size as in dsa_seqs; num_pages: pages in the cache.
+ * No output may be an input's memory.
+ * DSA_ERR_BAD_INPUT in *d_status: a request that cannot be served (a negative
+ * length, more tokens than max_pages pages hold, rows past num_q, not enough
+ * free pages for it and those before it): it takes no pages, ctx_len =
+ * cached_len (0 if that is negative), q_pos = slot = -1 for its rows; a page
+ * outside the cache (the rows in it: -1); a free_range that is not one of
+ * free_pages (counts as empty). */
+dsa_status dsa_step_plan(const int32_t* cached_len, const int32_t* new_len, int32_t num_seqs,
+                         const int32_t* free_pages, int32_t free_cap, const int32_t* free_range, int32_t page_size,
+                         int32_t num_pages, int32_t* page_table, int32_t max_pages, int32_t num_q, int32_t* ctx_len,
+                         int32_t* q_start, int32_t* q_pos, int64_t* slot, int32_t* next_range, int32_t* d_status,
+                         cudaStream_t stream);
+
 /* Bytes of workspace that dense_gqa_decode and dense_gqa_prefill need (host
  * only).  The size depends on the shape and num_q alone and grows with num_q:
  * a workspace sized for the most queries of a shape serves all of its calls
@@ -452,8 +524,8 @@ dsa_status dense_gqa_workspace_size(const dsa_gqa_shape* shape, const dsa_seqs* 
 /* Attention of a few new tokens per sequence over its cached keys (their own
  * among them), the work split over the caches' length.
  *   q    bf16 [num_q, num_heads, head_dim], rows shape->q_stride apart
- *   k_cache, v_cache (and k_scale, v_scale for DSA_FP8_E4M3_ROWSCALE, else
- *        NULL): shape's caches, seqs->num_rows rows
+ *   k_cache, v_cache (and k_scale, v_scale for e4m3 caches, else NULL): shape's
+ *        caches, seqs->num_rows rows
  *   out  bf16 [num_q, num_heads, head_dim] contiguous; lse fp32
  *        [num_q, num_heads] or NULL
  * q_pos[t] = -1 sees no key: out = 0, lse = -inf, whatever the caches hold.
