@@ -3,8 +3,10 @@ absorbed-MLA attention, as hand-written CUDA behind a C ABI (include/dsa.h),
 plus the cache-write side (new indexer keys and latent rows into the caches,
 the attention query's RoPE + SSMax) and one rank's compute steps of decode
 context parallelism (top-k candidates, their merge, compaction, LSE combine),
-and dense attention with grouped heads for the layers without an indexer (K/V
-cache writes with the rotation, decode, prompts).
+and attention with grouped heads for the layers without an indexer (K/V cache
+writes with the rotation, with a scale per row or per block of tokens; dense
+decode and prompts; attention over blocks chosen by a bound of their scores),
+with a step's page tables and slots built on the GPU.
 
 The Python names mirror the C entry points; they only marshal arguments.
 Importing the package loads nothing; the first call loads ``libdsa.so`` and
@@ -23,6 +25,10 @@ from ._binding import (  # noqa: F401
     DsaError,
     GqaShape,
     Seqs,
+    block_gqa_attend,
+    block_gqa_bounds,
+    block_gqa_select,
+    block_gqa_workspace_size,
     dense_gqa_decode,
     dense_gqa_prefill,
     dense_gqa_workspace_size,
@@ -58,4 +64,5 @@ __all__ = ["Seqs", "DsaError", "dsa_workspace_size", "dsa_index_scores", "dsa_in
            "dsa_block_topk", "dsa_dcp_shard_seqs",
            "GqaShape", "dsa_kv_insert", "dense_gqa_workspace_size", "dense_gqa_decode", "dense_gqa_prefill",
            "DSA_ROPE_PAIRS", "DSA_ROPE_HALVES", "DSA_FP8_E4M3_BLOCKSCALE", "dsa_kv_block_insert", "dsa_step_plan",
+           "block_gqa_workspace_size", "block_gqa_bounds", "block_gqa_select", "block_gqa_attend",
            "load", "version", "DSA_BF16", "DSA_FP8_E4M3_ROWSCALE", "DSA_FP8_DS_MLA"]

@@ -120,7 +120,12 @@ def load(path: str = LIB_PATH):
         L.dense_gqa_prefill.argtypes = L.dense_gqa_decode.argtypes
         L.dsa_kv_block_insert.argtypes = [G, P, I64, P, I64, P, I64, S, I32, P, I32, ctypes.c_int, P, P, P, P, P, P, P]
         L.dsa_step_plan.argtypes = [P, P, I32, P, I32, P, I32, I32, P, I32, I32, P, P, P, P, P, P, P]
-        for f in ("dsa_kv_block_insert", "dsa_step_plan"):
+        L.block_gqa_workspace_size.argtypes = [G, S, I32, I32, I32, ctypes.POINTER(SZ)]
+        L.block_gqa_bounds.argtypes = [G, P, P, S, I32, I32, P, P, P, P]
+        L.block_gqa_select.argtypes = [G, P, P, P, S, I32, I32, I32, I32, I32, P, P, P, SZ, P, P]
+        L.block_gqa_attend.argtypes = [G, P, P, P, P, P, S, I32, P, P, I32, I32, F, P, P, P, SZ, P, P]
+        for f in ("dsa_kv_block_insert", "dsa_step_plan", "block_gqa_workspace_size", "block_gqa_bounds",
+                  "block_gqa_select", "block_gqa_attend"):
             getattr(L, f).restype = ctypes.c_int
         for f in ("dsa_kv_insert", "dense_gqa_workspace_size", "dense_gqa_decode", "dense_gqa_prefill"):
             getattr(L, f).restype = ctypes.c_int
@@ -417,3 +422,36 @@ def dense_gqa_prefill(shape: GqaShape, q, k_cache, v_cache, k_scale, v_scale, se
     _check(load().dense_gqa_prefill(ctypes.byref(shape), _p(q), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
                                     ctypes.byref(sc), num_q, sm_scale, _p(out), _p(lse), _p(workspace),
                                     workspace_bytes, _p(d_status), _stream(stream)))
+
+
+# ---- grouped-head attention over selected blocks (include/dsa.h)
+def block_gqa_workspace_size(shape: GqaShape, seqs: Seqs, num_q: int, block: int, nsel: int) -> int:
+    n = ctypes.c_size_t()
+    sc = seqs.c()
+    _check(load().block_gqa_workspace_size(ctypes.byref(shape), ctypes.byref(sc), num_q, block, nsel,
+                                           ctypes.byref(n)))
+    return int(n.value)
+
+
+def block_gqa_bounds(shape: GqaShape, k_cache, k_scale, seqs: Seqs, num_q: int, block: int, bounds, steps, *,
+                     d_status=None, stream=None):
+    sc = seqs.c()
+    _check(load().block_gqa_bounds(ctypes.byref(shape), _p(k_cache), _p(k_scale), ctypes.byref(sc), num_q, block,
+                                   _p(bounds), _p(steps), _p(d_status), _stream(stream)))
+
+
+def block_gqa_select(shape: GqaShape, q, bounds, steps, seqs: Seqs, num_q: int, block: int, nsel: int, num_first: int,
+                     num_local: int, blocks, sel_len, workspace, workspace_bytes: int, *, d_status=None, stream=None):
+    sc = seqs.c()
+    _check(load().block_gqa_select(ctypes.byref(shape), _p(q), _p(bounds), _p(steps), ctypes.byref(sc), num_q, block,
+                                   nsel, num_first, num_local, _p(blocks), _p(sel_len), _p(workspace),
+                                   workspace_bytes, _p(d_status), _stream(stream)))
+
+
+def block_gqa_attend(shape: GqaShape, q, k_cache, v_cache, k_scale, v_scale, seqs: Seqs, num_q: int, blocks, sel_len,
+                     block: int, nsel: int, sm_scale: float, out, lse, workspace, workspace_bytes: int, *,
+                     d_status=None, stream=None):
+    sc = seqs.c()
+    _check(load().block_gqa_attend(ctypes.byref(shape), _p(q), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
+                                   ctypes.byref(sc), num_q, _p(blocks), _p(sel_len), block, nsel, sm_scale, _p(out),
+                                   _p(lse), _p(workspace), workspace_bytes, _p(d_status), _stream(stream)))

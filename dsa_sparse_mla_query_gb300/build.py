@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libdsa.so")
 BUILD_DIR = os.path.join(ROOT, "_build", platform.machine())
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "indexer.cu", "indexer_nvfp4.cu", "topk.cu", "mla.cu", "cache_write.cu", "dcp.cu", "block_topk.cu",
-           "gqa_decode.cu", "gqa_prefill.cu", "step_plan.cu"]
+           "gqa_decode.cu", "gqa_blocks.cu", "gqa_prefill.cu", "block_select.cu", "step_plan.cu"]
 
 
 def nvcc() -> str:

@@ -178,6 +178,16 @@ cudaError_t launch_prefill(const dsa_gqa_shape& sh, const void* q, const void* k
                            const float* k_scale, const float* v_scale, const dsa_seqs& s, int num_q, float sm_scale,
                            void* out, float* lse, void* workspace, int32_t* d_status, cudaStream_t stream);
 size_t prefill_workspace(const dsa_gqa_shape& sh, int num_q);
+cudaError_t launch_bounds(const dsa_gqa_shape& sh, const void* k, const float* k_scale, const dsa_seqs& s, int num_q,
+                          int block, void* bounds, float* steps, int32_t* d_status, cudaStream_t stream);
+size_t select_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s, int num_q, int block);
+cudaError_t launch_select(const dsa_gqa_shape& sh, const void* q, const void* bounds, const float* steps,
+                          const dsa_seqs& s, int num_q, int block, int nsel, int first, int local, int32_t* blocks,
+                          int32_t* len, void* workspace, int32_t* d_status, cudaStream_t stream);
+cudaError_t launch_attend(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v, const float* k_scale,
+                          const float* v_scale, const dsa_seqs& s, int num_q, const int32_t* blocks,
+                          const int32_t* len, int block, int nsel, float sm_scale, void* out, float* lse,
+                          void* workspace, int32_t* d_status, cudaStream_t stream);
 }  // namespace gqa
 size_t block_topk_smem(int max_ctx, int block, int nsel);
 cudaError_t launch_block_topk(const float* scores, int64_t ld, const dsa_seqs& s, int num_q, int block, int nsel,
@@ -618,6 +628,129 @@ dsa_status dense_gqa_prefill(const dsa_gqa_shape* shape, const void* q, const vo
                              int32_t* d_status, cudaStream_t stream) {
     return dense_gqa(true, shape, q, k_cache, v_cache, k_scale, v_scale, seqs, num_q, sm_scale, out, lse, workspace,
                      workspace_bytes, d_status, stream);
+}
+
+// ---- attention over selected blocks
+
+static void check_blocks(Check& c, const dsa_gqa_shape& sh, const dsa_seqs* s, int32_t num_q, int32_t block) {
+    c.need(block >= 16 && block <= DSA_GQA_MAX_BLOCK && (block & (block - 1)) == 0, DSA_ERR_UNSUPPORTED,
+           "block %d is not a power of two in [16, %d]", block, DSA_GQA_MAX_BLOCK);
+    if (c.st != DSA_OK) return;
+    if (s->page_table)
+        c.need(s->page_size >= block, DSA_ERR_UNSUPPORTED, "page_size %d below block %d", s->page_size, block);
+    c.need(((int64_t)s->max_ctx + block - 1) / block <= DSA_GQA_MAX_BLOCKS, DSA_ERR_UNSUPPORTED,
+           "max_ctx %d has more than %d blocks of %d", s->max_ctx, DSA_GQA_MAX_BLOCKS, block);
+    c.need((int64_t)num_q * sh.num_kv_heads <= INT32_MAX / 2, DSA_ERR_UNSUPPORTED,
+           "num_q %d of %d key heads exceeds 2^30 rows", num_q, sh.num_kv_heads);
+}
+
+static void check_nsel(Check& c, int32_t nsel) {
+    c.need(nsel >= 1 && nsel <= DSA_GQA_MAX_NSEL, DSA_ERR_UNSUPPORTED, "nsel %d outside [1, %d]", nsel,
+           DSA_GQA_MAX_NSEL);
+}
+
+static size_t block_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s, int32_t num_q, int32_t block) {
+    return std::max(gqa::decode_workspace(sh), gqa::select_workspace(sh, s, num_q, block));
+}
+
+static void check_block_workspace(Check& c, const dsa_gqa_shape& sh, const dsa_seqs* s, int32_t num_q, int32_t block,
+                                  const void* workspace, size_t bytes) {
+    if (c.st != DSA_OK) return;
+    const size_t need = block_workspace(sh, *s, num_q, block);
+    c.need(workspace != nullptr, DSA_ERR_WORKSPACE, "workspace is NULL");
+    c.need(aligned(workspace, 256), DSA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+    c.need(bytes >= need, DSA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", bytes, need);
+}
+
+dsa_status block_gqa_workspace_size(const dsa_gqa_shape* shape, const dsa_seqs* seqs, int32_t num_q, int32_t block,
+                                    int32_t nsel, size_t* bytes) {
+    Check c;
+    const dsa_gqa_shape sh = check_shape(c, shape);
+    check_seqs(c, seqs, num_q);
+    check_gqa_sizes(c, sh, seqs);
+    check_blocks(c, sh, seqs, num_q, block);
+    check_nsel(c, nsel);
+    c.need(bytes != nullptr, DSA_ERR_INVALID_ARG, "bytes is NULL");
+    dsa_status st = c.done();
+    if (st != DSA_OK) return st;
+    *bytes = block_workspace(sh, *seqs, num_q, block);
+    return DSA_OK;
+}
+
+dsa_status block_gqa_bounds(const dsa_gqa_shape* shape, const void* k_cache, const float* k_scale,
+                            const dsa_seqs* seqs, int32_t num_q, int32_t block, int8_t* bounds, float* steps,
+                            int32_t* d_status, cudaStream_t stream) {
+    Check c;
+    const dsa_gqa_shape sh = check_shape(c, shape);
+    check_seqs(c, seqs, num_q);
+    check_gqa_sizes(c, sh, seqs);
+    check_blocks(c, sh, seqs, num_q, block);
+    c.ptr(k_cache, "k_cache");
+    if (sh.kv_dtype == DSA_FP8_E4M3_ROWSCALE || sh.kv_dtype == DSA_FP8_E4M3_BLOCKSCALE) c.ptr(k_scale, "k_scale", 4);
+    c.ptr(bounds, "bounds");
+    c.ptr(steps, "steps", 4);
+    dsa_status st = c.done();
+    if (st != DSA_OK || num_q == 0) return st;
+    return cuda_status(gqa::launch_bounds(sh, k_cache, k_scale, *seqs, num_q, block, bounds, steps, d_status, stream),
+                       "block_gqa_bounds launch");
+}
+
+dsa_status block_gqa_select(const dsa_gqa_shape* shape, const void* q, const int8_t* bounds, const float* steps,
+                            const dsa_seqs* seqs, int32_t num_q, int32_t block, int32_t nsel, int32_t num_first,
+                            int32_t num_local, int32_t* blocks, int32_t* sel_len, void* workspace,
+                            size_t workspace_bytes, int32_t* d_status, cudaStream_t stream) {
+    Check c;
+    const dsa_gqa_shape sh = check_shape(c, shape);
+    check_seqs(c, seqs, num_q);
+    check_gqa_sizes(c, sh, seqs);
+    check_blocks(c, sh, seqs, num_q, block);
+    check_nsel(c, nsel);
+    c.need(num_first >= 0, DSA_ERR_INVALID_ARG, "num_first %d < 0", num_first);
+    c.need(num_local >= 1, DSA_ERR_INVALID_ARG, "num_local %d < 1", num_local);
+    c.need(nsel < 1 || (int64_t)num_first + num_local <= nsel, DSA_ERR_INVALID_ARG, "num_first %d and num_local %d exceed nsel %d",
+           num_first, num_local, nsel);
+    c.ptr(q, "q");
+    c.ptr(bounds, "bounds");
+    c.ptr(steps, "steps", 4);
+    c.ptr(blocks, "blocks", 4);
+    c.ptr(sel_len, "sel_len", 4);
+    check_block_workspace(c, sh, seqs, num_q, block, workspace, workspace_bytes);
+    dsa_status st = c.done();
+    if (st != DSA_OK || num_q == 0) return st;
+    return cuda_status(gqa::launch_select(sh, q, bounds, steps, *seqs, num_q, block, nsel, num_first, num_local, blocks,
+                                          sel_len, workspace, d_status, stream),
+                       "block_gqa_select launch");
+}
+
+dsa_status block_gqa_attend(const dsa_gqa_shape* shape, const void* q, const void* k_cache, const void* v_cache,
+                            const float* k_scale, const float* v_scale, const dsa_seqs* seqs, int32_t num_q,
+                            const int32_t* blocks, const int32_t* sel_len, int32_t block, int32_t nsel,
+                            float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                            int32_t* d_status, cudaStream_t stream) {
+    Check c;
+    const dsa_gqa_shape sh = check_shape(c, shape);
+    check_seqs(c, seqs, num_q);
+    check_gqa_sizes(c, sh, seqs);
+    check_blocks(c, sh, seqs, num_q, block);
+    check_nsel(c, nsel);
+    c.need(sm_scale > -INFINITY && sm_scale < INFINITY, DSA_ERR_INVALID_ARG, "sm_scale is not finite");
+    c.ptr(q, "q");
+    c.ptr(k_cache, "k_cache");
+    c.ptr(v_cache, "v_cache");
+    if (sh.kv_dtype == DSA_FP8_E4M3_ROWSCALE || sh.kv_dtype == DSA_FP8_E4M3_BLOCKSCALE) {
+        c.ptr(k_scale, "k_scale", 4);
+        c.ptr(v_scale, "v_scale", 4);
+    }
+    c.ptr(blocks, "blocks", 4);
+    c.ptr(sel_len, "sel_len", 4);
+    c.ptr(out, "out");
+    if (lse) c.ptr(lse, "lse", 4);
+    check_block_workspace(c, sh, seqs, num_q, block, workspace, workspace_bytes);
+    dsa_status st = c.done();
+    if (st != DSA_OK || num_q == 0) return st;
+    return cuda_status(gqa::launch_attend(sh, q, k_cache, v_cache, k_scale, v_scale, *seqs, num_q, blocks, sel_len,
+                                          block, nsel, sm_scale, out, lse, workspace, d_status, stream),
+                       "block_gqa_attend launch");
 }
 
 dsa_status dsa_mla_q_prep(const void* q, const float* ssmax_s, const float* ssmax_b, const float* inv_freq,

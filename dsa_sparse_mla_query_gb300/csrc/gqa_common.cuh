@@ -1,5 +1,5 @@
 // gqa_common.cuh -- pieces shared by the dense grouped-head attention kernels
-// (gqa_decode.cu, gqa_prefill.cu): sequences' counts, tensor maps, paired fp32
+// (gqa_decode.cuh, gqa_prefill.cu, block_select.cu): sequences' counts, tensor maps, paired fp32
 // arithmetic, e4m3 codes, ring places and waits.
 #pragma once
 
@@ -29,6 +29,21 @@ __device__ __forceinline__ Seq load_seq(const dsa_seqs& s, int b, int num_q) {
     r.nq = qe - r.q0;
     r.ok = r.ctx >= 0 && r.ctx <= s.max_ctx && r.q0 >= 0 && qe >= r.q0 && qe <= num_q && r.nq <= s.max_q_per_seq;
     return r;
+}
+
+// the sequence of row t, a warp's lanes trying 32 places at once
+__device__ __forceinline__ int warp_seq_of(const int32_t* q_start, int B, int t) {
+    int lo = 0, hi = B;  // q_start[lo] <= t < q_start[hi]
+    const int lane = threadIdx.x & 31;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int at = lo + lane * step;
+        const uint32_t in = __ballot_sync(0xffffffffu, at < hi && (lane == 0 || __ldg(q_start + at) <= t));
+        const int l = 31 - __clz(in);
+        hi = min(hi, lo + (l + 1) * step);
+        lo += l * step;
+    }
+    return lo;
 }
 
 // Tensor map over a cache [rows, heads, d] whose rows lie `stride` elements

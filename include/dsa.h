@@ -11,8 +11,9 @@
  * the cache-write side (new indexer keys and latent rows into their caches,
  * the attention query's RoPE + SSMax) and one rank's compute steps of decode
  * context parallelism (top-k candidates, their merge, compaction, LSE combine).
- * Beside it: dense attention with grouped heads for the layers without an
- * indexer (K/V cache writes, decode, prompts).
+ * Beside it: attention with grouped heads for the layers without an indexer
+ * (K/V cache writes; over all keys: decode, prompts; over blocks chosen by a
+ * bound of their scores), and a step's page tables and slots built on the GPU.
  *
  * Sources (web pages, cited by title and section):
  *   [vLLM-ML4] "Day 0 support for Mistral Large 4" (vLLM blog), Implementation
@@ -47,8 +48,8 @@
  *     (1 indexer scan, 2 attention, 3 attention over fp8_ds_mla, 4 attention
  *     over NVFP4 latent rows, 5 indexer scan over NVFP4 keys) and bits
  *     16-30 the wait (its mbarrier's shared-memory offset / 8, or 0x7FFF for
- *     the attention's issue loop).  Kernel 6 is dense_gqa_decode, 7
- *     dense_gqa_prefill.
+ *     the attention's issue loop).  Kernel 6 is dense_gqa_decode or
+ *     block_gqa_attend, 7 dense_gqa_prefill.
  *   - Indices are logical token positions within a sequence.  The page table or
  *     seq_base maps them to physical cache rows.
  */
@@ -552,6 +553,83 @@ dsa_status dense_gqa_prefill(const dsa_gqa_shape* shape, const void* q, const vo
                              const float* k_scale, const float* v_scale, const dsa_seqs* seqs, int32_t num_q,
                              float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
                              int32_t* d_status, cudaStream_t stream);
+
+/* ---- grouped-head attention over selected blocks ----
+ * Keys in blocks of `block` tokens (a power of two in [16, DSA_GQA_MAX_BLOCK],
+ * at most a page's tokens), block i of a sequence being positions
+ * [i, i + 1) block; every query token and key head chooses nsel of them by a
+ * cheap score and attends over those alone.  shape and seqs as for the dense
+ * calls, any cache dtype; q_rope_pos is not read.
+ *
+ * The score of a block is a bound of the scores of its keys: per block and head
+ *   step = 2^ceil(log2(max |k| / 127)) over its keys and dims (1 if all are 0),
+ *   bounds[0][d] = floor(min k_d / step), bounds[1][d] = ceil(max k_d / step),
+ *   both in [-127, 127] (values that are not finite do not count for the step;
+ *   infinities saturate, NaN widens both bounds);
+ * for query token t and key head g, with its group's query heads h in whole
+ * steps of their own, 2^ceil(log2(max |q| / 127)) for the group (rounded to
+ * nearest even; NaN counts as 0, infinities as 127):
+ *   score(i) = step_i max_h sum_d max(q_h[d] bounds_i[0][d], q_h[d] bounds_i[1][d]),
+ * whole numbers times a power of two: exact, so that the order is the same
+ * everywhere; equal scores go to the smaller block. */
+#define DSA_GQA_MAX_NSEL 1024
+#define DSA_GQA_MAX_BLOCKS 51200 /* blocks of the longest context */
+
+/* Bytes of workspace that block_gqa_select and block_gqa_attend need (host
+ * only): it grows with num_q and max_ctx.  The scores take num_q num_kv_heads
+ * ceil(max_ctx / block) 4 bytes. */
+dsa_status block_gqa_workspace_size(const dsa_gqa_shape* shape, const dsa_seqs* seqs, int32_t num_q, int32_t block,
+                                    int32_t nsel, size_t* bytes);
+
+/* Bounds of the blocks that the sequences' new tokens lie in, from all of the
+ * block's keys up to the last new one; to be called after the keys are in the
+ * cache and before block_gqa_select.  The new tokens are those of
+ * dsa_kv_block_insert: consecutive positions (only the first one is read; -1:
+ * the sequence is skipped).
+ *   bounds int8 [ceil(num_rows / block), num_kv_heads, 2, head_dim], by physical
+ *   row: block i of the cache is rows [i, i + 1) block; steps fp32
+ *   [ceil(num_rows / block), num_kv_heads].  Other blocks' are left as they were.
+ * DSA_ERR_BAD_INPUT: a malformed sequence, a block outside the cache or not at a
+ * multiple of `block` rows (seq_base), new tokens past ctx_len: their blocks
+ * are left.  Alignment: k_cache and bounds 16 bytes. */
+dsa_status block_gqa_bounds(const dsa_gqa_shape* shape, const void* k_cache, const float* k_scale,
+                            const dsa_seqs* seqs, int32_t num_q, int32_t block, int8_t* bounds, float* steps,
+                            int32_t* d_status, cudaStream_t stream);
+
+/* The blocks that each query token and key head attends over, of the n =
+ * q_pos / block + 1 that hold keys it sees: all of them if n <= nsel, else the
+ * first num_first, the last num_local (the query's own among them), and those
+ * of the others with the largest scores.
+ *   q       bf16 [num_q, num_heads, head_dim], rows shape->q_stride apart (as
+ *           the attention takes it)
+ *   blocks  int32 [num_q, num_kv_heads, nsel]: ascending, then -1
+ *   sel_len int32 [num_q, num_kv_heads]: keys that the query sees in them
+ * num_first >= 0, num_local >= 1, num_first + num_local <= nsel <=
+ * DSA_GQA_MAX_NSEL.  q_pos = -1: no blocks, sel_len 0.  DSA_ERR_BAD_INPUT: a
+ * position outside [-1, ctx_len) or a malformed sequence (their rows are left
+ * unwritten), a block outside the cache (its score counts as 0).  Rows past
+ * q_start[num_seqs] are left as they were.  Alignment: q and bounds 16 bytes,
+ * workspace 256. */
+dsa_status block_gqa_select(const dsa_gqa_shape* shape, const void* q, const int8_t* bounds, const float* steps,
+                            const dsa_seqs* seqs, int32_t num_q, int32_t block, int32_t nsel, int32_t num_first,
+                            int32_t num_local, int32_t* blocks, int32_t* sel_len, void* workspace,
+                            size_t workspace_bytes, int32_t* d_status, cudaStream_t stream);
+
+/* Attention of each query token over its listed blocks: the keys of blocks[t][g]
+ * side by side, the first sel_len[t][g] of them (so every listed block but the
+ * last counts whole), with scores, softmax, out and lse as the dense calls.
+ * The lists alone say what a token sees: q_pos is not read, a block listed twice
+ * counts twice.  sel_len = 0: out = 0, lse = -inf.
+ * Arguments, roundings and rows past q_start[num_seqs] as dense_gqa_decode's;
+ * any number of tokens per sequence.  DSA_ERR_BAD_INPUT: sel_len outside
+ * [0, nsel block] (its row is left unwritten), a listed block that is not one of
+ * the sequence's ctx_len tokens', a block outside the cache, a malformed
+ * sequence (their keys and values count as zeros). */
+dsa_status block_gqa_attend(const dsa_gqa_shape* shape, const void* q, const void* k_cache, const void* v_cache,
+                            const float* k_scale, const float* v_scale, const dsa_seqs* seqs, int32_t num_q,
+                            const int32_t* blocks, const int32_t* sel_len, int32_t block, int32_t nsel,
+                            float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                            int32_t* d_status, cudaStream_t stream);
 
 /* One decode layer: dsa_index_scores -> dsa_topk -> sparse_mla_decode on one
  * stream, with the scores kept in the workspace.  reuse_idx != 0 is a

@@ -95,3 +95,51 @@ def plan(cached, new, page, free, free_range, num_pages, table, num_q):
 
 
 rotate = R.rotate
+
+
+# ---- blocks chosen by a bound of their scores
+def step_of(amax: float) -> float:
+    """2^ceil(log2(amax / 127)), at least 2^-126; 1 for 0."""
+    if amax == 0.0:
+        return 1.0
+    m, e = math.frexp(amax)  # amax = m 2^e, m in [0.5, 1); 127 = 0.9921875 2^7
+    return math.ldexp(1.0, max(-126, e - 7 if m <= 0.9921875 else e - 6))
+
+
+def bounds_of(k):
+    """(int8 [heads, 2, d], steps [heads]) of a block's keys [n, heads, d], in fp64."""
+    n, heads, d = k.shape
+    out, steps = torch.zeros(heads, 2, d, dtype=torch.int8), torch.zeros(heads)
+    for h in range(heads):
+        x = k[:, h]
+        finite = x[torch.isfinite(x)]
+        s = step_of(float(finite.abs().max()) if finite.numel() else 0.0)
+        lo = torch.where(torch.isnan(x), torch.full_like(x, -math.inf), x).amin(0)
+        hi = torch.where(torch.isnan(x), torch.full_like(x, math.inf), x).amax(0)
+        out[h, 0] = torch.floor(lo / s).clamp(-127, 127).to(torch.int8)
+        out[h, 1] = torch.ceil(hi / s).clamp(-127, 127).to(torch.int8)
+        steps[h] = s
+    return out, steps
+
+
+def whole(q):
+    """The group's query rows [g, d] (fp64) in whole steps."""
+    finite = q[torch.isfinite(q)]
+    s = step_of(float(finite.abs().max()) if finite.numel() else 0.0)
+    return torch.round(torch.nan_to_num(q, nan=0.0, posinf=math.inf, neginf=-math.inf) / s).clamp(-127, 127)
+
+
+def scores(q, bounds, steps):
+    """q [g, d] in whole steps, bounds [n, 2, d], steps [n]: the blocks' scores (fp64, exact)."""
+    b = bounds.double()
+    x = torch.maximum(q[:, None] * b[None, :, 0], q[:, None] * b[None, :, 1]).sum(-1)  # [g, n]
+    return x.amax(0) * steps.double()
+
+
+def pick(score, n, nsel, first, local):
+    """The ascending list of blocks among the first n."""
+    if n <= nsel:
+        return list(range(n))
+    sure = set(range(first)) | set(range(n - local, n))
+    rest = sorted((i for i in range(n) if i not in sure), key=lambda i: (-float(score[i]), i))
+    return sorted(sure | set(rest[:nsel - len(sure)]))

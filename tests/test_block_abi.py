@@ -114,3 +114,78 @@ def test_names_are_public():
     assert dsa.DSA_FP8_E4M3_BLOCKSCALE == 4
     for name in ("dsa_step_plan", "dsa_kv_block_insert"):
         assert callable(getattr(dsa, name)) and name in dsa.__all__
+
+
+def _sized(**kw):
+    return dict(dict(shape=_shape(), seqs=_seqs(), n=2, block=64, nsel=4), **kw)
+
+
+def _bounds(lib, shape, seqs, n, block, nsel, k=0x100, ks=0x10, bounds=0x200, steps=0x20, **kw):
+    return lib.block_gqa_bounds(ctypes.byref(shape), k, ks, ctypes.byref(seqs), n, block, bounds, steps, None, None)
+
+
+def _select(lib, shape, seqs, n, block, nsel, q=0x100, bounds=0x200, steps=0x20, first=1, local=1, blocks=0x300,
+            length=0x400, ws=0x10000, ws_bytes=1 << 50, **kw):
+    return lib.block_gqa_select(ctypes.byref(shape), q, bounds, steps, ctypes.byref(seqs), n, block, nsel, first,
+                                local, blocks, length, ws, ws_bytes, None, None)
+
+
+def _listed(lib, shape, seqs, n, block, nsel, q=0x100, k=0x200, v=0x300, ks=0x10, vs=0x20, blocks=0x400,
+            length=0x500, scale=0.1, out=0x600, lse=None, ws=0x10000, ws_bytes=1 << 50, **kw):
+    return lib.block_gqa_attend(ctypes.byref(shape), q, k, v, ks, vs, ctypes.byref(seqs), n, blocks, length, block,
+                                nsel, ctypes.c_float(scale), out, lse, ws, ws_bytes, None, None)
+
+
+@pytest.mark.parametrize("call", (_bounds, _select, _listed))
+@pytest.mark.parametrize("kw, part, status", [
+    (dict(block=8), "block 8", B.DSA_ERR_UNSUPPORTED),
+    (dict(block=48), "block 48", B.DSA_ERR_UNSUPPORTED),
+    (dict(block=256), "block 256", B.DSA_ERR_UNSUPPORTED),
+    (dict(seqs=_seqs(page_table=0x5000, page_size=64, max_pages=4), block=128), "page_size 64 below block 128",
+     B.DSA_ERR_UNSUPPORTED),
+    (dict(seqs=_seqs(max_ctx=1 << 24), block=16), "more than 51200 blocks", B.DSA_ERR_UNSUPPORTED),
+    (dict(n=1 << 30), "exceeds 2^30 rows", B.DSA_ERR_UNSUPPORTED),
+    (dict(n=-1), "num_q -1", B.DSA_ERR_INVALID_ARG),
+    (dict(shape=B.GqaShape(16, 2, 96)), "head_dim 96", B.DSA_ERR_UNSUPPORTED),
+    (dict(seqs=_seqs(num_seqs=0)), "num_seqs 0", B.DSA_ERR_INVALID_ARG),
+])
+def test_block_calls_refuse_sizes(lib, call, kw, part, status):
+    rc = call(lib, **_sized(**kw))
+    msg = lib.dsa_last_error_string().decode()
+    assert rc == status and part in msg, (rc, msg)
+
+
+@pytest.mark.parametrize("call, kw, part, status", [
+    (_bounds, dict(k=0x108, ks=None, bounds=0x204, steps=None), "k_cache is not 16-byte aligned; k_scale is NULL; "
+     "bounds is not 16-byte aligned; steps is NULL", B.DSA_ERR_INVALID_ARG),
+    (_select, dict(q=None, bounds=0x204, blocks=0x301, length=None), "q is NULL; bounds is not 16-byte aligned; "
+     "blocks is not 4-byte aligned; sel_len is NULL", B.DSA_ERR_INVALID_ARG),
+    (_select, dict(nsel=0), "nsel 0", B.DSA_ERR_UNSUPPORTED),
+    (_select, dict(nsel=1025), "nsel 1025", B.DSA_ERR_UNSUPPORTED),
+    (_select, dict(local=0), "num_local 0", B.DSA_ERR_INVALID_ARG),
+    (_select, dict(first=-1), "num_first -1", B.DSA_ERR_INVALID_ARG),
+    (_select, dict(first=2, local=3), "num_first 2 and num_local 3 exceed nsel 4", B.DSA_ERR_INVALID_ARG),
+    (_select, dict(ws=None), "workspace is NULL", B.DSA_ERR_WORKSPACE),
+    (_select, dict(ws=0x10010), "256-byte aligned", B.DSA_ERR_WORKSPACE),
+    (_select, dict(ws_bytes=100), "workspace has 100 bytes", B.DSA_ERR_WORKSPACE),
+    (_listed, dict(q=0x108, k=None, vs=0x21, out=0x604, lse=0x2), "q is not 16-byte aligned; k_cache is NULL; v_scale "
+     "is not 4-byte aligned; out is not 16-byte aligned; lse is not 4-byte aligned", B.DSA_ERR_INVALID_ARG),
+    (_listed, dict(nsel=-1), "nsel -1", B.DSA_ERR_UNSUPPORTED),
+    (_listed, dict(scale=float("inf")), "sm_scale", B.DSA_ERR_INVALID_ARG),
+    (_listed, dict(ws_bytes=100), "workspace has 100 bytes", B.DSA_ERR_WORKSPACE),
+])
+def test_block_calls_refuse_arguments(lib, call, kw, part, status):
+    rc = call(lib, **_sized(**kw))
+    msg = lib.dsa_last_error_string().decode()
+    assert rc == status and part in msg, (rc, msg)
+
+
+def test_block_calls_of_nothing_and_their_workspace(lib):
+    for call in (_bounds, _select, _listed):
+        assert call(lib, **_sized(n=0)) == 0
+    shape, n, last = _shape(), ctypes.c_size_t(), 0
+    for num_q, ctx in ((1, 4096), (64, 4096), (64, 65536), (4096, 65536)):
+        s = _seqs(max_ctx=ctx)
+        assert lib.block_gqa_workspace_size(ctypes.byref(shape), ctypes.byref(s), num_q, 64, 4, ctypes.byref(n)) == 0
+        assert n.value >= max(last, num_q * 2 * ctx // 64 * 4)
+        last = n.value
