@@ -10,7 +10,7 @@
 // inputs, and ties are ties.
 //
 // - block_bounds_kernel: minimum and maximum over the keys of the blocks that new
-//   tokens touch, a warp per block and head, keys read once.
+//   tokens touch, four warps per block and head, keys read once.
 // - block_score_kernel: the sums on the warp-level matrix instruction, 16 blocks
 //   by 8 query rows, k-steps over lo with min(q, 0), then over hi with max(q, 0).
 //   A warp holds 16 blocks' bounds as f16 fragments straight from global memory
@@ -42,79 +42,210 @@ struct BoundArgs {
     dsa_seqs s;
     int64_t stride;    // bytes between rows
     int32_t* d_status;
-    int32_t num_q, hkv, shift, scale_shift;
+    int32_t num_q, hkv, shift, scale_shift, page_shift;
 };
 
+// two packed values: f16 (e4m3 codes, converted), or bf16
+template <bool FP8>
+__device__ __forceinline__ uint32_t packed_min(uint32_t x, uint32_t y) {  // NaN if either is
+    if (FP8) {
+        const __half2 r = __hmin2_nan(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+    const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<__nv_bfloat162*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <bool FP8>
+__device__ __forceinline__ uint32_t packed_max(uint32_t x, uint32_t y) {
+    if (FP8) {
+        const __half2 r = __hmax2_nan(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<__nv_bfloat162*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <bool FP8>
+__device__ __forceinline__ float2 packed_floats(uint32_t x) {
+    if (FP8) return __half22float2(*reinterpret_cast<__half2*>(&x));
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+}
+
+// One over the step of values up to `top`, and the step
+__device__ __forceinline__ float step_up(float top, float& step) {
+    const int e = top > 0.f ? scale_exponent(top, 6, 0x7E0000u) : 0;  // 127 = 1.984375 2^6
+    step = two_to(e);
+    return two_to(-e);
+}
+// bounds in whole steps (a product that vanishes still lies below, or above, 0)
+__device__ __forceinline__ uint32_t low_code(float v, float up) {
+    const float x = v * up;
+    return (uint32_t)(int)fmaxf(-127.f, fminf(127.f, x == 0.f && v < 0.f ? -1.f : floorf(x))) & 0xFFu;
+}
+__device__ __forceinline__ uint32_t high_code(float v, float up) {
+    const float x = v * up;
+    return (uint32_t)(int)fmaxf(-127.f, fminf(127.f, x == 0.f && v > 0.f ? 1.f : ceilf(x))) & 0xFFu;
+}
+
+// Four warps take a block and head, its rows among them: minima and maxima as
+// they lie in the cache (pairs of f16 or bf16: exact), converted at the end.
+// Rows with scales of their own, and blocks with values that are not finite,
+// take the long way in fp32, by one warp.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kBoundThreads) block_bounds_kernel(const __grid_constant__ BoundArgs a) {
     constexpr int V = FP8 ? 16 : 8;    // dims per lane
     constexpr int L = D / V;           // lanes per row
     constexpr int R = 32 / L;          // rows per access
+    constexpr int P = V / 2;           // pairs per lane
+    constexpr int kChunk = Pieces<kBoundThreads>::kChunk;
+    constexpr int kParts = 4, kHeads = kBoundThreads / 32 / kParts;
     __shared__ Pieces<kBoundThreads> pieces;
+    __shared__ int4 seq_sh[kChunk];    // first position, tokens, context
+    __shared__ uint32_t ends[kHeads][kParts][2][D / 2];
     pdl_enter();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int part = warp % kParts, slot = warp / kParts;
     const int li = lane % L, sub = lane / L;
     int64_t before = 0;
-    for (int c0 = 0; c0 < a.s.num_seqs; c0 += Pieces<kBoundThreads>::kChunk) {
-        const int left = min(Pieces<kBoundThreads>::kChunk, a.s.num_seqs - c0);
+    for (int c0 = 0; c0 < a.s.num_seqs; c0 += kChunk) {
+        const int left = min(kChunk, a.s.num_seqs - c0);
         const int total = pieces.scan(c0, a.s.num_seqs, [&](int b) {
             const NewTokens n = new_tokens(a.s, b, a.num_q);
             if (n.bad && blockIdx.x == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
+            seq_sh[b - c0] = make_int4(n.p0, n.nq, n.ctx, 0);
             return blocks_touched(n, a.shift);
         });
-        // warps take (block, head) pairs
-        const int64_t tasks = (int64_t)total * a.hkv;
-        const int64_t all = (int64_t)gridDim.x * (kBoundThreads / 32);
-        for (int64_t x = ((int64_t)blockIdx.x * (kBoundThreads / 32) + warp + all - before % all) % all; x < tasks;
-             x += all) {
-            const int piece = (int)(x / a.hkv), h = (int)(x - (int64_t)piece * a.hkv);
+        // CTAs take kHeads heads of a block at a time
+        const int per = (a.hkv + kHeads - 1) / kHeads;
+        const int64_t tasks = (int64_t)total * per;
+        for (int64_t x = (int64_t)((gridDim.x + blockIdx.x - before % gridDim.x) % gridDim.x); x < tasks; x += gridDim.x) {
+            const int piece = (int)((uint64_t)x >> 32 ? x / per : (uint32_t)x / (uint32_t)per);
+            const int h = (int)(x - (int64_t)piece * per) * kHeads + slot;
             const int i = pieces.find(piece, left);
-            const NewTokens nt = new_tokens(a.s, c0 + i, a.num_q);
-            const int64_t first = (int64_t)((nt.p0 >> a.shift) + (piece - pieces.first[i])) << a.shift;
-            const int n = (int)min((int64_t)1 << a.shift, (int64_t)nt.p0 + nt.nq - first);  // its keys
-            const int64_t row0 = phys_row(a.s, c0 + i, first);
-            if (row0 < 0 || (row0 & ((1 << a.shift) - 1)) || row0 + n > a.s.num_rows || nt.p0 + (int64_t)nt.nq > nt.ctx) {
-                if (lane == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
+            const int4 nt = seq_sh[i];
+            const int64_t first = (int64_t)((nt.x >> a.shift) + (piece - pieces.first[i])) << a.shift;
+            const int n = (int)min((int64_t)1 << a.shift, (int64_t)nt.x + nt.y - first);  // its keys
+            const int64_t row0 = row_at(a.s, a.page_shift, c0 + i, first);
+            if (row0 < 0 || (row0 & ((1 << a.shift) - 1)) || row0 + n > a.s.num_rows || nt.x + (int64_t)nt.y > nt.z) {
+                if (threadIdx.x == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
                 continue;
             }
+            const bool live = h < a.hkv;
+            const uint8_t* src = a.k + row0 * a.stride + (int64_t)(live ? h : 0) * (FP8 ? D : 2 * D) + 16 * li;
+            const int64_t at = (row0 >> a.shift) * a.hkv + h;
+            const bool even = !FP8 || a.scale_shift >= a.shift;  // one scale for the block
+            float scale = 1.f;
+            bool odd = !even;
+            if (even) {
+                if (FP8 && live && part == 0) scale = __ldg(a.k_scale + (row0 >> a.scale_shift) * a.hkv + h);
+                uint32_t lo[P], hi[P];
+                // this warp's rows: every fourth access of R rows, the last key again behind the last
+#pragma unroll
+                for (int d = 0; d < P; ++d) lo[d] = hi[d] = 0;
+                for (int r0 = part * R; r0 == part * R || r0 < n; r0 += 4 * kParts * R) {
+                    uint4 z[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        z[u] = __ldg(reinterpret_cast<const uint4*>(src + min(r0 + u * kParts * R + sub, n - 1) * a.stride));
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t w[4] = {z[u].x, z[u].y, z[u].z, z[u].w};
+                        const bool start = u == 0 && r0 == part * R;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t p[2] = {w[e], 0u};
+                            if (FP8) e4m3x4_to_f16(w[e], p[0], p[1]);
+#pragma unroll
+                            for (int y = 0; y < P / 4; ++y) {
+                                const int d = e * (P / 4) + y;
+                                lo[d] = start ? p[y] : packed_min<FP8>(lo[d], p[y]);
+                                hi[d] = start ? p[y] : packed_max<FP8>(hi[d], p[y]);
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int o = L; o < 32; o <<= 1)
+#pragma unroll
+                    for (int d = 0; d < P; ++d) {
+                        lo[d] = packed_min<FP8>(lo[d], __shfl_xor_sync(0xffffffffu, lo[d], o));
+                        hi[d] = packed_max<FP8>(hi[d], __shfl_xor_sync(0xffffffffu, hi[d], o));
+                    }
+                if (sub == 0)
+#pragma unroll
+                    for (int d = 0; d < P; ++d) ends[slot][part][0][li * P + d] = lo[d], ends[slot][part][1][li * P + d] = hi[d];
+                __syncthreads();
+                if (part == 0 && live) {
+                    // D / 64 pairs of dims a lane
+                    float top = 0.f;
+                    float2 l[D / 64], g[D / 64];
+#pragma unroll
+                    for (int y = 0; y < D / 64; ++y) {
+                        const int d = lane * (D / 64) + y;
+                        uint32_t x0 = ends[slot][0][0][d], x1 = ends[slot][0][1][d];
+#pragma unroll
+                        for (int z = 1; z < kParts; ++z) {
+                            x0 = packed_min<FP8>(x0, ends[slot][z][0][d]);
+                            x1 = packed_max<FP8>(x1, ends[slot][z][1][d]);
+                        }
+                        l[y] = packed_floats<FP8>(x0), g[y] = packed_floats<FP8>(x1);
+                        l[y].x *= scale, l[y].y *= scale, g[y].x *= scale, g[y].y *= scale;
+                        const float m = fmaxf(fmaxf(fabsf(l[y].x), fabsf(l[y].y)), fmaxf(fabsf(g[y].x), fabsf(g[y].y)));
+                        // (fmaxf leaves NaN out)
+                        odd = odd || !(m < INFINITY) || l[y].x != l[y].x || l[y].y != l[y].y || g[y].x != g[y].x || g[y].y != g[y].y;
+                        top = fmaxf(top, m);
+                    }
+                    odd = __any_sync(0xffffffffu, odd);
+                    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+                    if (!odd) {
+                        float step;
+                        const float up = step_up(top, step);
+                        uint32_t cl = 0, ch = 0;
+#pragma unroll
+                        for (int y = 0; y < D / 64; ++y) {
+                            cl |= (low_code(l[y].x, up) | low_code(l[y].y, up) << 8) << (16 * y);
+                            ch |= (high_code(g[y].x, up) | high_code(g[y].y, up) << 8) << (16 * y);
+                        }
+                        int8_t* dst = a.bounds + at * (2 * D) + lane * (D / 32);
+                        if (D == 128) {
+                            *reinterpret_cast<uint32_t*>(dst) = cl;
+                            *reinterpret_cast<uint32_t*>(dst + D) = ch;
+                        } else {
+                            *reinterpret_cast<uint16_t*>(dst) = (uint16_t)cl;
+                            *reinterpret_cast<uint16_t*>(dst + D) = (uint16_t)ch;
+                        }
+                        if (lane == 0) a.steps[at] = step;
+                    }
+                }
+                __syncthreads();  // the halves' ends are no longer read
+            }
+            if (!odd || part != 0 || !live) continue;
             float lo[V], hi[V], top = 0.f;
 #pragma unroll
             for (int e = 0; e < V; ++e) lo[e] = INFINITY, hi[e] = -INFINITY;
-            const uint8_t* src = a.k + row0 * a.stride + h * (FP8 ? D : 2 * D) + 16 * li;
-            for (int r0 = 0; r0 < n; r0 += 4 * R) {
-                uint4 z[4];
-                float f[4];
+            for (int r0 = 0; r0 < n; r0 += 2 * R) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int r = min(r0 + u * R + sub, n - 1);  // the last key again behind the last
-                    z[u] = __ldg(reinterpret_cast<const uint4*>(src + r * a.stride));
-                    f[u] = FP8 ? __ldg(a.k_scale + ((row0 + r) >> a.scale_shift) * a.hkv + h) : 1.f;
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint32_t w[4] = {z[u].x, z[u].y, z[u].z, z[u].w};
-                    float v[V];
+                for (int u = 0; u < 2; ++u) {
+                    const int r = min(r0 + u * R + sub, n - 1);
+                    const uint4 z = __ldg(reinterpret_cast<const uint4*>(src + r * a.stride));
+                    const float f = FP8 ? __ldg(a.k_scale + ((row0 + r) >> a.scale_shift) * a.hkv + h) : 1.f;
+                    const uint32_t w[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if (FP8) {
-                            uint32_t p, q;
-                            e4m3x4_to_f16(w[e], p, q);
-                            const float2 x0 = __half22float2(*reinterpret_cast<__half2*>(&p));
-                            const float2 x1 = __half22float2(*reinterpret_cast<__half2*>(&q));
-                            v[4 * e % V] = x0.x * f[u], v[(4 * e + 1) % V] = x0.y * f[u];
-                            v[(4 * e + 2) % V] = x1.x * f[u], v[(4 * e + 3) % V] = x1.y * f[u];
-                        } else {
-                            v[2 * e] = __uint_as_float(w[e] << 16);
-                            v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-                        }
-                    }
+                        uint32_t p[2] = {w[e], 0u};
+                        if (FP8) e4m3x4_to_f16(w[e], p[0], p[1]);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const float m = fabsf(v[e]);
-                        top = fmaxf(top, m < INFINITY ? m : 0.f);
-                        // NaN may be anything
-                        lo[e] = fminf(lo[e], v[e] == v[e] ? v[e] : -INFINITY);
-                        hi[e] = fmaxf(hi[e], v[e] == v[e] ? v[e] : INFINITY);
+                        for (int y = 0; y < P / 4; ++y) {
+                            const float2 v2 = packed_floats<FP8>(p[y]);
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const int d = (e * (P / 4) + y) * 2 + c;
+                                const float v = (c ? v2.y : v2.x) * f, m = fabsf(v);
+                                top = fmaxf(top, m < INFINITY ? m : 0.f);
+                                // NaN may be anything
+                                lo[d] = fminf(lo[d], v == v ? v : -INFINITY);
+                                hi[d] = fmaxf(hi[d], v == v ? v : INFINITY);
+                            }
+                        }
                     }
                 }
             }
@@ -126,30 +257,161 @@ __global__ void __launch_bounds__(kBoundThreads) block_bounds_kernel(const __gri
                     hi[e] = fmaxf(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
                 }
             top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-            // |v| <= 127 steps; 127 = 1.984375 2^6
-            const int e2 = top > 0.f ? scale_exponent(top, 6, 0x7E0000u) : 0;
-            const float up = two_to(-e2 > 127 ? 127 : -e2);
-            uint32_t cl[V / 4], ch[V / 4];
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                // (a product that vanishes still lies below, or above, 0)
-                const float x = lo[e] * up, y = hi[e] * up;
-                const int l = (int)fmaxf(-127.f, fminf(127.f, x == 0.f && lo[e] < 0.f ? -1.f : floorf(x)));
-                const int g = (int)fmaxf(-127.f, fminf(127.f, y == 0.f && hi[e] > 0.f ? 1.f : ceilf(y)));
-                const int sh = 8 * (e & 3);
-                cl[e / 4] = (e & 3 ? cl[e / 4] : 0u) | (uint32_t)(l & 0xFF) << sh;
-                ch[e / 4] = (e & 3 ? ch[e / 4] : 0u) | (uint32_t)(g & 0xFF) << sh;
-            }
-            const int64_t at = (row0 >> a.shift) * a.hkv + h;
+            float step;
+            const float up = step_up(top, step);
             if (sub == 0) {
                 uint32_t* dst = reinterpret_cast<uint32_t*>(a.bounds + at * (2 * D) + V * li);
 #pragma unroll
-                for (int e = 0; e < V / 4; ++e) dst[e] = cl[e], dst[D / 4 + e] = ch[e];
+                for (int e = 0; e < V; e += 4) {
+                    dst[e / 4] = low_code(lo[e], up) | low_code(lo[e + 1], up) << 8 | low_code(lo[e + 2], up) << 16 |
+                                 low_code(lo[e + 3], up) << 24;
+                    dst[D / 4 + e / 4] = high_code(hi[e], up) | high_code(hi[e + 1], up) << 8 |
+                                         high_code(hi[e + 2], up) << 16 | high_code(hi[e + 3], up) << 24;
+                }
             }
-            if (lane == 0) a.steps[at] = two_to(e2);
+            if (lane == 0) a.steps[at] = step;
         }
         before += tasks;
         __syncthreads();  // the chunk's counts are no longer read
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the choice among a row's scores
+constexpr int kBins = 1024;
+
+struct PickArgs {
+    const float* scores;
+    int32_t *blocks, *len;
+    dsa_seqs s;
+    int32_t* d_status;
+    int32_t num_q, hkv, shift, ld, nsel, first, local;
+};
+
+// keys that a query at `pos` sees in its m blocks (the last one its own)
+__device__ __forceinline__ int seen_keys(int pos, int m, int shift) {
+    return pos < 0 ? 0 : ((m - 1) << shift) + (pos & ((1 << shift) - 1)) + 1;
+}
+
+// what a CTA needs to choose among a row's keys
+template <int T>
+struct PickShared {
+    static constexpr int W = T / 32;
+    int hist[kBins];
+    int red[W + 1];
+    uint32_t ends[2][W], names[T], codes[T];
+    int2 sums[W];
+    int found[2], count;
+};
+// an order-preserving code of a score, 1 at least (NaN, of a step that was never written: last)
+__device__ __forceinline__ uint32_t score_code(float s) {
+    const uint32_t u = __float_as_uint(s == 0.f ? 0.f : s);
+    return s != s ? 1u : u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Of the n blocks of a row those in [0, first) and [hi, n), and the `want` with
+// the largest keys in [first, hi): into `out`, ascending.  A CTA; sh.ends holds
+// the warps' least and largest keys, sh.hist zeros, sh.count 0, a barrier behind
+// them.  nsel = the number taken.
+template <int T>
+__device__ __forceinline__ void pick(PickShared<T>& sh, uint32_t* key, int n, int first, int hi, int want, int nsel,
+                                     int32_t* out) {
+    constexpr int W = T / 32, kPer = kBins / T;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t least = 0xFFFFFFFFu, best = 0u;
+#pragma unroll
+    for (int w = 0; w < W; ++w) least = min(least, sh.ends[0][w]), best = max(best, sh.ends[1][w]);
+    // The want-th largest key: bins over the range that is left, until a bin is taken whole, holds few
+    // enough keys to rank each against the others, or is one key.
+    uint32_t low = least, width = best - least;
+    uint32_t cut = 0xFFFFFFFFu;  // keys above are taken, and the first `ties` of those equal
+    int ties = 0;
+    while (want > 0) {
+        const int bits = max(0, 22 - __clz(width | 1));  // width >> bits < kBins
+        for (int i = first + tid; i < hi; i += T) {
+            const uint32_t k = key[i];
+            if (k >= low && k - low <= width) atomicAdd(&sh.hist[(k - low) >> bits], 1);
+        }
+        __syncthreads();
+        // from the top: the thread with the bin where the count passes `want`
+        int h[kPer], mine = 0;
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) {
+            h[y] = tid < kBins / kPer ? sh.hist[kBins - 1 - kPer * tid - y] : 0;
+            mine += h[y];
+        }
+        int all;
+        int c = cta_scan<T>(mine, sh.red, all);
+        if (c < want && c + mine >= want) {
+#pragma unroll
+            for (int y = 0; y < kPer; ++y) {
+                if (c < want && c + h[y] >= want) {
+                    sh.found[0] = kBins - 1 - kPer * tid - y;
+                    sh.found[1] = want - c;
+                }
+                c += h[y];
+            }
+        }
+        __syncthreads();
+        const int bin = sh.found[0], need = sh.found[1], has = sh.hist[bin];
+        low += (uint32_t)bin << bits;
+        width = (1u << bits) - 1;
+        if (need == has && low > 0) {
+            cut = low - 1;
+            break;
+        }
+        if (has <= T) {
+            for (int i = first + tid; i < hi; i += T) {
+                const uint32_t k = key[i];
+                if (k >= low && k - low <= width) {
+                    const int at = atomicAdd(&sh.count, 1);
+                    sh.names[at] = i;
+                    sh.codes[at] = k;
+                }
+            }
+            __syncthreads();
+            if (tid < has) {
+                const uint32_t k = sh.codes[tid], me = sh.names[tid];
+                int rank = 0;
+                for (int y = 0; y < has; ++y) rank += sh.codes[y] > k || (sh.codes[y] == k && sh.names[y] < me);
+                if (rank < need) key[me] = 0xFFFFFFFFu;  // above any score's code
+            }
+            cut = low + width;
+            __syncthreads();
+            break;
+        }
+        if (bits == 0) {
+            cut = low;
+            ties = need;
+            break;
+        }
+        want = need;
+        __syncthreads();
+        for (int i = tid; i < kBins; i += T) sh.hist[i] = 0;
+        __syncthreads();
+    }
+    // in order: a run of blocks per warp, counted, then written
+    const int run = (n + T - 1) / T * 32, i0 = min(n, warp * run), i1 = min(n, i0 + run);
+    int sure = 0, equal = 0;
+    for (int i = i0 + lane; i < i1 + lane; i += 32) {
+        const bool in = i < i1, fix = i < first || i >= hi;
+        sure += __popc(__ballot_sync(0xffffffffu, in && (fix || key[i] > cut)));
+        if (ties) equal += __popc(__ballot_sync(0xffffffffu, in && !fix && key[i] == cut));
+    }
+    if (lane == 0) sh.sums[warp] = make_int2(sure, equal);
+    __syncthreads();
+    int at = 0, eq = 0;
+    for (int w = 0; w < warp; ++w) at += sh.sums[w].x, eq += sh.sums[w].y;
+    const uint32_t under = (1u << lane) - 1;
+    for (int i = i0 + lane; i < i1 + lane; i += 32) {
+        const bool in = i < i1, fix = i < first || i >= hi;
+        const bool yes = in && (fix || key[i] > cut), tie = in && !fix && ties && key[i] == cut;
+        const uint32_t y = __ballot_sync(0xffffffffu, yes), e = __ballot_sync(0xffffffffu, tie);
+        const int rank = eq + __popc(e & under);
+        const int place = at + __popc(y & under) + min(rank, ties);
+        if ((yes || (tie && rank < ties)) && place < nsel) out[place] = i;
+        at += __popc(y);
+        eq += __popc(e);
     }
 }
 
@@ -167,13 +429,344 @@ struct ScoreArgs {
     dsa_seqs s;
     int64_t q_stride;
     int32_t* d_status;
-    int32_t num_q, group, hkv, shift, ld;
+    int32_t num_q, group, hkv, shift, ld, page_shift;
     int32_t pad;     // a token's rows: a power of two of them in one tile, or 8
     int32_t npt;     // tiles per token (1 where pad < 8)
     int32_t tokens;  // per CTA
     int32_t xt;      // CTAs along the blocks
     int32_t direct;  // slot = sequence
 };
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&x)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t below0(uint32_t x) {  // two f16
+    const __half2 v = __hmin2(*reinterpret_cast<__half2*>(&x), __half2half2(__ushort_as_half(0)));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t above0(uint32_t x) {
+    const __half2 v = __hmax2(*reinterpret_cast<__half2*>(&x), __half2half2(__ushort_as_half(0)));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+// four signed bytes as f16: a byte + 128 under the exponent of 1024, less 1152
+__device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    uint32_t x = __byte_perm(u, 0x64646464u, 0x4140), y = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+    const __half2 xh = __hsub2(*reinterpret_cast<__half2*>(&x), bias);
+    const __half2 yh = __hsub2(*reinterpret_cast<__half2*>(&y), bias);
+    lo = *reinterpret_cast<const uint32_t*>(&xh);
+    hi = *reinterpret_cast<const uint32_t*>(&yh);
+}
+
+// a thread's 16 dims, chunk c of its query row: tile j of token tok, column lane / 4
+template <int D>
+__device__ __forceinline__ void load_query(const ScoreArgs& a, int t0, int tok, int n, int kvh, int j, int c, uint4 (&x)[2]) {
+    const int lane = threadIdx.x & 31, col = lane >> 2, t = lane & 3;
+    const int head = min(j * 8 + col % a.pad, a.group - 1);  // a group's last head again behind it
+    const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(t0 + tok) * a.q_stride +
+                                                      (int64_t)(kvh * a.group + head) * D + c * 64 + t * 16);
+    x[0] = tok < n ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);
+    x[1] = tok < n ? __ldg(src + 1) : make_uint4(0u, 0u, 0u, 0u);
+}
+// one over the step of a token's group, for the lanes that hold its rows
+template <int D>
+__device__ __forceinline__ float query_step(const ScoreArgs& a, int t0, int tok, int n, int kvh) {
+    float top = 0.f;
+    for (int j = 0; j < a.npt; ++j)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            uint4 x[2];
+            load_query<D>(a, t0, tok, n, kvh, j, c, x);
+            const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float u = fabsf(__uint_as_float(w[e] << 16)), v = fabsf(__uint_as_float(w[e] & 0xFFFF0000u));
+                top = fmaxf(top, fmaxf(u < INFINITY ? u : 0.f, v < INFINITY ? v : 0.f));
+            }
+        }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    for (int o = 1; o < a.pad; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4 * o));
+    return two_to(top > 0.f ? -scale_exponent(top, 6, 0x7E0000u) : 0);
+}
+__device__ __forceinline__ float whole_steps(float v, float up) {
+    return v == v ? fmaxf(-127.f, fminf(127.f, rintf(v * up))) : 0.f;
+}
+
+// Queries of n tokens from row t0 in whole steps, as fragments: a token's tiles
+// (a tile's tokens where they are several) by one warp, [tile][KS / 2][lane]
+template <int D>
+__device__ __forceinline__ void quantise(const ScoreArgs& a, int t0, int n, int kvh, int warp, int warps, uint4* q_sh) {
+    const int lane = threadIdx.x & 31, col = lane >> 2;
+    const int tpt = 8 / a.pad;  // tokens per tile (npt = 1)
+    const int groups = (n + tpt - 1) / tpt;
+    for (int gu = warp; gu < groups; gu += warps) {
+        const int tok = gu * tpt + col / a.pad;
+        const float up = query_step<D>(a, t0, tok, n, kvh);
+        auto two = [&](uint32_t w) {
+            return pack_f16(whole_steps(__uint_as_float(w << 16), up), whole_steps(__uint_as_float(w & 0xFFFF0000u), up));
+        };
+        for (int j = 0; j < a.npt; ++j)
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                uint4 x[2];
+                load_query<D>(a, t0, tok, n, kvh, j, c, x);
+                uint4* dst = q_sh + ((gu * a.npt + j) * (D / 32) + 2 * c) * 32 + lane;
+                dst[0] = make_uint4(two(x[0].x), two(x[0].y), two(x[0].z), two(x[0].w));
+                dst[32] = make_uint4(two(x[1].x), two(x[1].y), two(x[1].z), two(x[1].w));
+            }
+    }
+}
+
+// the best of a token's heads (columns 2t, 2t + 1 of rows blk and blk + 8) into its rows of scores
+__device__ __forceinline__ void store_scores(const ScoreArgs& a, float (&m)[4], int t0, int n, int kvh, int gu, int blk,
+                                             float step0, float step1) {
+    const int t = threadIdx.x & 3, tpt = 8 / a.pad;
+    if (a.pad >= 2) m[0] = m[1] = fmaxf(m[0], m[1]), m[2] = m[3] = fmaxf(m[2], m[3]);
+    for (int o = 2; o < a.pad; o <<= 1)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], o / 2));
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int c = 2 * t + e;
+        const int tok = gu * tpt + c / a.pad;
+        if (c % a.pad || tok >= n) continue;
+        float* dst = a.scores + ((int64_t)(t0 + tok) * a.hkv + kvh) * a.ld + blk;
+        // (a step above 2^105 overflows to equal scores)
+        if (blk < a.ld) dst[0] = m[e] * step0;
+        if (blk + 8 < a.ld) dst[8] = m[2 + e] * step1;
+    }
+}
+
+// A few query rows a sequence (up to 4 tiles): a CTA of four warps takes a
+// (sequence, key head), or a share of its blocks.  Every warp keeps two tiles of
+// 16 blocks on their way, and the page of a third; bounds are fragments of the
+// 8-bit matrix instruction as they lie in memory, so that a tile of 4 KB takes
+// eight products and few other instructions.  Where (sequence, key head)s alone
+// fill the GPU (PICK) their scores stay in shared memory, and the CTA chooses
+// among them: no second launch.
+constexpr int kFewThreads = 128, kFewWarps = kFewThreads / 32, kFewTiles = 4;
+constexpr int kFewScores = 8192;  // of a CTA's tokens, in shared memory
+
+template <int D, int NT, bool PICK>
+__global__ void __launch_bounds__(kFewThreads, PICK ? 4 : 5)
+    block_score_few_kernel(const __grid_constant__ ScoreArgs a, const __grid_constant__ PickArgs k) {
+    extern __shared__ uint32_t keys[];  // PICK: [token][ld]
+    __shared__ __align__(16) uint32_t q_sh[NT * (D / 32) * 32 * 4];  // [tile][lo, hi][D / 64][lane][4]
+    __shared__ uint32_t top_sh[8 * kFewTiles];                    // largest of a token's queries
+    __shared__ int pos_sh[8 * kFewTiles];
+    __shared__ PickShared<kFewThreads> pick_sh;
+    pdl_enter();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int col = lane >> 2, t = lane & 3;
+    const int kvh = blockIdx.x % a.hkv, rest = blockIdx.x / a.hkv;
+    const int share = rest % a.xt, b = rest / a.xt;
+    if (tid < 8 * kFewTiles) top_sh[tid] = 0;
+    const Seq sq = load_seq(a.s, b, a.num_q);
+    if (!sq.ok) {
+        if (tid == 0 && share == 0 && kvh == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
+        return;
+    }
+    const int n = sq.nq;
+    if (n == 0) return;
+    // places of tile i's blocks (lanes 0 .. 15) among the cache's, by the context; those that no query
+    // sees may lie anywhere
+    auto place = [&](int i) -> int {
+        const int64_t tok = (int64_t)(i * 16 + (lane & 15)) << a.shift;
+        if (tok >= sq.ctx) return -1;
+        const int64_t row = row_at(a.s, a.page_shift, b, tok);
+        return row < 0 || (row & ((1 << a.shift) - 1)) ? -2 : (int)(row >> a.shift);
+    };
+    struct Tile {
+        uint4 x[2][D / 32];
+        float step[2];
+    };
+    const int8_t* bounds = a.bounds + (int64_t)kvh * (2 * D) + 16 * t;
+    auto fetch = [&](int at, Tile& z) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int p = __shfl_sync(0xffffffffu, at, col + 8 * r);
+            const uint4* src = reinterpret_cast<const uint4*>(bounds + (int64_t)max(p, 0) * (a.hkv * 2 * D));
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) z.x[r][c] = p >= 0 ? __ldg(src + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
+            z.step[r] = p >= 0 ? __ldg(a.steps + (int64_t)p * a.hkv + kvh) : 0.f;
+        }
+    };
+    const int stride = a.xt * kFewWarps;
+    int i = share * kFewWarps + warp;
+    int at = place(i), next = place(i + stride);
+    if (tid < n) pos_sh[tid] = __ldg(a.s.q_pos + sq.q0 + tid);
+    // ---- the queries in whole steps: a thread's 16 dims of a row, twice for more than two tiles
+    constexpr int kSets = (NT * 8 * (D / 16) + kFewThreads - 1) / kFewThreads;
+    const int tpt = 8 / a.pad;
+    uint4 raw[kSets][2];
+#pragma unroll
+    for (int y = 0; y < kSets; ++y) {
+        const int x = y * kFewThreads + tid, row = x / (D / 16), c = x % (D / 16);
+        const int j = row >> 3, cl = row & 7;
+        const int tok = a.npt > 1 ? j / a.npt : j * tpt + cl / a.pad;
+        const int head = min(a.npt > 1 ? j % a.npt * 8 + cl : cl % a.pad, a.group - 1);  // the last again behind it
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(sq.q0 + tok) * a.q_stride +
+                                                          (int64_t)(kvh * a.group + head) * D + 16 * c);
+        raw[y][0] = raw[y][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (j < NT && tok < n) raw[y][0] = __ldg(src), raw[y][1] = __ldg(src + 1);
+    }
+    Tile cur;
+    fetch(at, cur);
+    __syncthreads();
+    auto token = [&](int y) {
+        const int row = (y * kFewThreads + tid) / (D / 16);
+        return a.npt > 1 ? (row >> 3) / a.npt : (row >> 3) * tpt + (row & 7) / a.pad;
+    };
+#pragma unroll
+    for (int y = 0; y < kSets; ++y) {
+        const uint32_t w[8] = {raw[y][0].x, raw[y][0].y, raw[y][0].z, raw[y][0].w,
+                               raw[y][1].x, raw[y][1].y, raw[y][1].z, raw[y][1].w};
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float u = fabsf(__uint_as_float(w[e] << 16)), v = fabsf(__uint_as_float(w[e] & 0xFFFF0000u));
+            top = fmaxf(top, fmaxf(u < INFINITY ? u : 0.f, v < INFINITY ? v : 0.f));
+        }
+        if (top > 0.f) atomicMax(&top_sh[token(y)], __float_as_uint(top));
+    }
+    int most = -1;
+    for (int y = 0; y < n; ++y) {
+        const int p = pos_sh[y];
+        if (p >= 0 && p < sq.ctx) most = max(most, p >> a.shift);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int y = 0; y < kSets; ++y) {
+        const int x = y * kFewThreads + tid, row = x / (D / 16), c = x % (D / 16);
+        if (row >= NT * 8) break;
+        const float top = __uint_as_float(top_sh[min(token(y), 8 * kFewTiles - 1)]);
+        float step;
+        const float up = step_up(top, step);
+        const uint32_t w[8] = {raw[y][0].x, raw[y][0].y, raw[y][0].z, raw[y][0].w,
+                               raw[y][1].x, raw[y][1].y, raw[y][1].z, raw[y][1].w};
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            lo[e] = hi[e] = 0;
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const uint32_t u = w[2 * e + z / 2];
+                const int v = (int)whole_steps(__uint_as_float(z & 1 ? u & 0xFFFF0000u : u << 16), up);
+                lo[e] |= (uint32_t)(min(v, 0) & 0xFF) << (8 * z);
+                hi[e] |= (uint32_t)max(v, 0) << (8 * z);
+            }
+        }
+        // dims 16 c ..: chunk c / 4, thread c % 4 of the row's four
+        uint4* dst = reinterpret_cast<uint4*>(q_sh) + ((row >> 3) * (D / 32) + c / 4) * 32 + (row & 7) * 4 + c % 4;
+        dst[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        dst[(D / 64) * 32] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    }
+    __syncthreads();
+    const int groups = (n + tpt - 1) / tpt;
+    const uint4* qf = reinterpret_cast<const uint4*>(q_sh) + lane;
+    bool lost = false;
+    for (; i * 16 <= most; i += stride) {
+        lost = lost || (at == -2 && i * 16 + (lane & 15) <= most);
+        Tile then;
+        fetch(next, then);
+        at = next;
+        next = place(i + 2 * stride);
+        int acc[NT][4], odd[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {  // lo's chunks, hi's
+            const uint4 r0 = cur.x[0][c], r1 = cur.x[1][c];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const uint4 z = qf[(j * (D / 32) + c) * 32];
+                mma_s8(acc[j], r0.x, r1.x, r0.y, r1.y, z.x, z.y);
+                mma_s8(NT == 1 ? odd : acc[j], r0.z, r1.z, r0.w, r1.w, z.z, z.w);
+            }
+        }
+        if (NT == 1)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[0][e] += odd[e];
+        // the best of a token's heads, and its scores of blocks blk and blk + 8
+        const int blk = i * 16 + col;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            if (j % a.npt) continue;
+            int m[4] = {acc[j][0], acc[j][1], acc[j][2], acc[j][3]};
+#pragma unroll
+            for (int z = j + 1; z < NT; ++z)
+                if (z < j + a.npt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m[e] = max(m[e], acc[z][e]);
+            if (a.pad >= 2) m[0] = m[1] = max(m[0], m[1]), m[2] = m[3] = max(m[2], m[3]);
+            for (int o = 2; o < a.pad; o <<= 1)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m[e] = max(m[e], __shfl_xor_sync(0xffffffffu, m[e], o / 2));
+            if (j / a.npt >= groups) continue;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int c = 2 * t + e, tok = j / a.npt * tpt + c / a.pad;
+                if (c % a.pad || tok >= n) continue;
+                // (a step above 2^105 overflows to equal scores)
+                const float s0 = (float)m[e] * cur.step[0], s1 = (float)m[2 + e] * cur.step[1];
+                if (PICK) {
+                    if (blk <= most) keys[tok * a.ld + blk] = score_code(s0);
+                    if (blk + 8 <= most) keys[tok * a.ld + blk + 8] = score_code(s1);
+                } else {
+                    float* dst = a.scores + ((int64_t)(sq.q0 + tok) * a.hkv + kvh) * a.ld + blk;
+                    if (blk < a.ld) dst[0] = s0;
+                    if (blk + 8 < a.ld) dst[8] = s1;
+                }
+            }
+        }
+        cur = then;
+    }
+    if (lost && kvh == 0 && lane < 16) report(a.d_status, DSA_ERR_BAD_INPUT);
+    if (!PICK) return;
+    __syncthreads();
+    for (int tok = 0; tok < n; ++tok) {
+        const int pos = pos_sh[tok];
+        if (pos < -1 || pos >= sq.ctx) {  // left as it was
+            if (tid == 0 && kvh == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
+            continue;
+        }
+        const int64_t row = (int64_t)(sq.q0 + tok) * a.hkv + kvh;
+        const int m = pos < 0 ? 0 : (pos >> a.shift) + 1;
+        int32_t* out = k.blocks + row * k.nsel;
+        if (tid == 0) k.len[row] = seen_keys(pos, min(m, k.nsel), a.shift);
+        if (m <= k.nsel) {
+            for (int x = tid; x < k.nsel; x += kFewThreads) out[x] = x < m ? x : -1;
+            continue;
+        }
+        uint32_t* key = keys + tok * a.ld;
+        const int hi = m - k.local;
+        uint32_t least = 0xFFFFFFFFu, best = 0u;
+        for (int x = k.first + tid; x < hi; x += kFewThreads) {
+            least = min(least, key[x]);
+            best = max(best, key[x]);
+        }
+        least = __reduce_min_sync(0xffffffffu, least);
+        best = __reduce_max_sync(0xffffffffu, best);
+        __syncthreads();  // the last token's choice is made
+        if (lane == 0) pick_sh.ends[0][warp] = least, pick_sh.ends[1][warp] = best;
+        for (int x = tid; x < kBins; x += kFewThreads) pick_sh.hist[x] = 0;
+        if (tid == 0) pick_sh.count = 0;
+        __syncthreads();
+        pick<kFewThreads>(pick_sh, key, m, k.first, hi, k.nsel - k.first - k.local, k.nsel, out);
+    }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __grid_constant__ ScoreArgs a) {
@@ -234,7 +827,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
     const int blk0 = xtile * kScoreBlocks + warp * 16;
     int64_t at = -1;  // the lane's block (lanes 0 .. 15)
     if (blk0 + (lane & 15) <= most) {
-        const int64_t row = phys_row(a.s, b, (int64_t)(blk0 + (lane & 15)) << a.shift);
+        const int64_t row = row_at(a.s, a.page_shift, b, (int64_t)(blk0 + (lane & 15)) << a.shift);
         if (row < 0 || (row & ((1 << a.shift) - 1))) {
             if (kvh == 0 && lane < 16) report(a.d_status, DSA_ERR_BAD_INPUT);
         } else {
@@ -252,58 +845,12 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
     const float step0 = at0 >= 0 ? __ldg(a.steps + at0) : 0.f, step1 = at1 >= 0 ? __ldg(a.steps + at1) : 0.f;
 
     // ---- the queries in whole steps, as fragments
-    const int tpt = 8 / a.pad;  // tokens per tile (npt = 1)
-    const int groups = (n + tpt - 1) / tpt;
-    for (int gu = warp; gu < groups; gu += kScoreWarps) {
-        const int tok = gu * tpt + col / a.pad;
-        const bool live = tok < n;
-        auto load = [&](int j, int c, uint4& x, uint4& y) {
-            const int head = min(j * 8 + col % a.pad, a.group - 1);  // a group's last head again behind it
-            const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(t0 + tok) * a.q_stride +
-                                                              (int64_t)(kvh * a.group + head) * D + c * 64 + t * 16);
-            x = live ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);
-            y = live ? __ldg(src + 1) : make_uint4(0u, 0u, 0u, 0u);
-        };
-        float top = 0.f;
-        for (int j = 0; j < a.npt; ++j)
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                uint4 x, y;
-                load(j, c, x, y);
-                const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float u = fabsf(__uint_as_float(w[e] << 16)), v = fabsf(__uint_as_float(w[e] & 0xFFFF0000u));
-                    top = fmaxf(top, fmaxf(u < INFINITY ? u : 0.f, v < INFINITY ? v : 0.f));
-                }
-            }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        for (int o = 1; o < a.pad; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4 * o));
-        const int e2 = top > 0.f ? scale_exponent(top, 6, 0x7E0000u) : 0;
-        const float up = two_to(-e2 > 127 ? 127 : -e2);
-        auto whole = [&](uint32_t w) {  // two bf16 -> whole steps, f16
-            float u = __uint_as_float(w << 16), v = __uint_as_float(w & 0xFFFF0000u);
-            u = u == u ? fmaxf(-127.f, fminf(127.f, rintf(u * up))) : 0.f;
-            v = v == v ? fmaxf(-127.f, fminf(127.f, rintf(v * up))) : 0.f;
-            return pack_f16(u, v);
-        };
-        for (int j = 0; j < a.npt; ++j)
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                uint4 x, y;
-                load(j, c, x, y);
-                uint4* dst = q_sh + ((gu * a.npt + j) * (KS / 2) + 2 * c) * 32 + lane;
-                dst[0] = make_uint4(whole(x.x), whole(x.y), whole(x.z), whole(x.w));
-                dst[32] = make_uint4(whole(y.x), whole(y.y), whole(y.z), whole(y.w));
-            }
-    }
+    const int tpt = 8 / a.pad, groups = (n + tpt - 1) / tpt;
+    quantise<D>(a, t0, n, kvh, warp, kScoreWarps, q_sh);
     __syncthreads();
     if (blk0 > most) return;
 
-    // bounds to f16 fragments: a byte + 128 under the exponent of 1024
     uint32_t lo[KS][4], hi[KS][4];
-    const __half2 bias = __half2half2(__ushort_as_half(0x6480));
 #pragma unroll
     for (int c = 0; c < D / 32; ++c)
 #pragma unroll
@@ -311,30 +858,11 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
             const uint32_t w[4] = {raw[r][c].x, raw[r][c].y, raw[r][c].z, raw[r][c].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const uint32_t u = w[e] ^ 0x80808080u;
-                uint32_t x = __byte_perm(u, 0x64646464u, 0x4140), y = __byte_perm(u, 0x64646464u, 0x4342);
-                const __half2 xh = __hsub2(*reinterpret_cast<__half2*>(&x), bias);
-                const __half2 yh = __hsub2(*reinterpret_cast<__half2*>(&y), bias);
                 auto& f = c < D / 64 ? lo : hi;
                 const int k = (c % (D / 64)) * 4 + e;
-                f[k][r] = *reinterpret_cast<const uint32_t*>(&xh);
-                f[k][2 + r] = *reinterpret_cast<const uint32_t*>(&yh);
+                bytes_to_f16(w[e], f[k][r], f[k][2 + r]);
             }
         }
-    auto mma = [](float (&d)[4], const uint32_t (&x)[4], uint32_t b0, uint32_t b1) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
-    };
-    auto below = [](uint32_t x) {
-        const __half2 v = __hmin2(*reinterpret_cast<__half2*>(&x), __half2half2(__ushort_as_half(0)));
-        return *reinterpret_cast<const uint32_t*>(&v);
-    };
-    auto above = [](uint32_t x) {
-        const __half2 v = __hmax2(*reinterpret_cast<__half2*>(&x), __half2half2(__ushort_as_half(0)));
-        return *reinterpret_cast<const uint32_t*>(&v);
-    };
     for (int gu = 0; gu < groups; ++gu) {
         float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         for (int j = 0; j < a.npt; ++j) {
@@ -343,161 +871,204 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
 #pragma unroll
             for (int k = 0; k < KS; k += 2) {
                 const uint4 z = src[(k / 2) * 32];
-                mma(x, lo[k], below(z.x), below(z.y));
-                mma(y, hi[k], above(z.x), above(z.y));
-                mma(x, lo[k + 1], below(z.z), below(z.w));
-                mma(y, hi[k + 1], above(z.z), above(z.w));
+                mma_f16(x, lo[k], below0(z.x), below0(z.y));
+                mma_f16(y, hi[k], above0(z.x), above0(z.y));
+                mma_f16(x, lo[k + 1], below0(z.z), below0(z.w));
+                mma_f16(y, hi[k + 1], above0(z.z), above0(z.w));
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], x[e] + y[e]);
         }
-        // the best of a token's heads: columns 2t, 2t + 1 of rows col and col + 8
-        if (a.pad >= 2) m[0] = m[1] = fmaxf(m[0], m[1]), m[2] = m[3] = fmaxf(m[2], m[3]);
-        for (int o = 2; o < a.pad; o <<= 1)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], o / 2));
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int c = 2 * t + e;
-            const int tok = gu * tpt + c / a.pad;
-            if (c % a.pad || tok >= n) continue;
-            float* dst = a.scores + ((int64_t)(t0 + tok) * a.hkv + kvh) * a.ld + blk0 + col;
-            // (a step below 2^-126 / 2^22 of nothing, above 2^105 overflows to equal scores)
-            if (blk0 + col < a.ld) dst[0] = m[e] * step0;
-            if (blk0 + col + 8 < a.ld) dst[8] = m[2 + e] * step1;
-        }
+        store_scores(a, m, t0, n, kvh, gu, blk0 + col, step0, step1);
     }
 }
 
 // ---------------------------------------------------------------------------
 // the best blocks of a row
-constexpr int kPickThreads = 256, kBins = 1024;
+// A warp per row of up to 32 K blocks: the keys stay in registers, and the cut
+// is found by halving their range (counts by a warp's sums, no barrier; it ends
+// when exactly `want` lie above).
+constexpr int kRowsPerCta = 4, kKept = 128;
 
-struct PickArgs {
-    const float* scores;
-    int32_t *blocks, *len;
-    dsa_seqs s;
-    int32_t* d_status;
-    int32_t num_q, hkv, shift, ld, nsel, first, local;
-};
-
-__global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const __grid_constant__ PickArgs a) {
-    extern __shared__ uint32_t key[];
-    __shared__ int hist[kBins];
-    __shared__ int red[kPickThreads / 32 + 1];
-    __shared__ uint32_t range[2];
-    __shared__ int found[2], pos_sh;
+template <int K>
+__global__ void __launch_bounds__(32 * kRowsPerCta) block_pick_row_kernel(const __grid_constant__ PickArgs a) {
+    __shared__ uint32_t kept[kRowsPerCta][2][kKept];
     pdl_enter();
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int t = blockIdx.x / a.hkv, kvh = blockIdx.x - t * a.hkv;
-    if (tid < 32) {
-        const int b = warp_seq_of(a.s.q_start, a.s.num_seqs, t);
-        const Seq sq = load_seq(a.s, b, a.num_q);
-        if (lane == 0) {
-            int pos = __ldg(a.s.q_pos + t);
-            if (t >= sq.q0 + sq.nq || t < sq.q0)
-                pos = -3;  // behind the last sequence
-            else if (!sq.ok || pos < -1 || pos >= sq.ctx)
-                pos = -2;
-            pos_sh = pos;
-            range[0] = 0xFFFFFFFFu;
-            range[1] = 0u;
-        }
-    }
-    __syncthreads();
-    const int pos = pos_sh;
-    if (pos < -1) {  // left as it was
-        if (pos == -2 && tid == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
-        return;
-    }
-    const int n = pos < 0 ? 0 : (pos >> a.shift) + 1;
-    int32_t* out = a.blocks + (int64_t)blockIdx.x * a.nsel;
-    if (tid == 0)
-        a.len[blockIdx.x] = n == 0 ? 0 : ((min(n, a.nsel) - 1) << a.shift) + (pos & ((1 << a.shift) - 1)) + 1;
-    if (n <= a.nsel) {  // all of them
-        for (int i = tid; i < a.nsel; i += kPickThreads) out[i] = i < n ? i : -1;
-        return;
-    }
-    // [0, first) and [hi, n) for sure, `want` of [first, hi)
+    const int lane = threadIdx.x & 31;
+    const int64_t r = (int64_t)blockIdx.x * kRowsPerCta + (threadIdx.x >> 5);
+    if (r >= (int64_t)a.num_q * a.hkv) return;
+    const int t = (int)(r / a.hkv);
+    const int pos = __ldg(a.s.q_pos + t);  // checked beside the scores' loads
+    const int n = min(a.ld, pos < 0 ? 0 : (pos >> a.shift) + 1);
+    const bool choose = n > a.nsel;
     const int hi = n - a.local;
     int want = a.nsel - a.first - a.local;
-    const float* row = a.scores + (int64_t)blockIdx.x * a.ld;
-    uint32_t least = 0xFFFFFFFFu, best = 0u;
-    for (int i = a.first + tid; i < hi; i += kPickThreads) {
-        const float s = row[i];
-        const uint32_t u = __float_as_uint(s == 0.f ? 0.f : s);
-        const uint32_t k = u & 0x80000000u ? ~u : u | 0x80000000u;
-        key[i] = k;
-        least = min(least, k);
-        best = max(best, k);
+    uint32_t key[K];
+    if (choose) {
+        const float* row = a.scores + r * a.ld;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int i = k * 32 + lane;
+            key[k] = 0;  // below any score's code
+            if (i >= a.first && i < hi) {
+                key[k] = score_code(row[i]);
+            }
+        }
     }
-    least = __reduce_min_sync(0xffffffffu, least);
-    best = __reduce_max_sync(0xffffffffu, best);
-    if (lane == 0) {
-        atomicMin(&range[0], least);
-        atomicMax(&range[1], best);
+    const int b = warp_seq_of(a.s.q_start, a.s.num_seqs, t);
+    const Seq sq = load_seq(a.s, b, a.num_q);
+    if (t >= sq.q0 + sq.nq || t < sq.q0) return;  // behind the last sequence: left as it was
+    if (!sq.ok || pos < -1 || pos >= sq.ctx) {
+        if (lane == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
+        return;
+    }
+    int32_t* out = a.blocks + r * a.nsel;
+    if (lane == 0)
+        a.len[r] = seen_keys(pos, min(n, a.nsel), a.shift);
+    if (!choose) {
+        for (int i = lane; i < a.nsel; i += 32) out[i] = i < n ? i : -1;
+        return;
+    }
+    // the largest `cut` with at least `want` keys at or above it, until exactly `want` are, or few enough
+    // for four a lane
+    uint32_t cut = 0xFFFFFFFFu;
+    int ties = 0;
+    const uint32_t under = (1u << lane) - 1;
+    if (want > 0) {
+        uint32_t least = 0xFFFFFFFFu, best = 0u;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            least = min(least, key[k] ? key[k] : 0xFFFFFFFFu);
+            best = max(best, key[k]);
+        }
+        least = __reduce_min_sync(0xffffffffu, least);
+        best = __reduce_max_sync(0xffffffffu, best);
+        int have = hi - a.first;  // keys at or above `least`
+        while (least < best && have != want && have > kKept) {
+            const uint32_t mid = least + (best - least + 1) / 2;
+            int c = 0;
+#pragma unroll
+            for (int k = 0; k < K; ++k) c += key[k] >= mid;
+            c = __reduce_add_sync(0xffffffffu, c);
+            if (c >= want) least = mid, have = c; else best = mid - 1;
+        }
+        if (have <= kKept) {
+            // those, in order, with their blocks: the rest of the search is theirs alone
+            uint32_t* codes = kept[threadIdx.x >> 5][0];
+            uint32_t* names = kept[threadIdx.x >> 5][1];
+            int at = 0;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const bool in = key[k] >= least;
+                const uint32_t y = __ballot_sync(0xffffffffu, in);
+                if (in) {
+                    codes[at + __popc(y & under)] = key[k];
+                    names[at + __popc(y & under)] = k * 32 + lane;
+                }
+                at += __popc(y);
+            }
+            __syncwarp();
+            uint32_t c4[kKept / 32];
+#pragma unroll
+            for (int y = 0; y < kKept / 32; ++y) c4[y] = y * 32 + lane < have ? codes[y * 32 + lane] : 0u;
+            int left = have;
+            while (least < best && left != want) {
+                const uint32_t mid = least + (best - least + 1) / 2;
+                int c = 0;
+#pragma unroll
+                for (int y = 0; y < kKept / 32; ++y) c += __popc(__ballot_sync(0xffffffffu, c4[y] >= mid));
+                if (c >= want) least = mid, left = c; else best = mid - 1;
+            }
+            int over = 0;
+#pragma unroll
+            for (int y = 0; y < kKept / 32; ++y) over += __popc(__ballot_sync(0xffffffffu, c4[y] > least));
+            int eq = 0, to = a.first;
+#pragma unroll
+            for (int y = 0; y < kKept / 32; ++y) {
+                const bool yes = c4[y] > least, tie = c4[y] == least;  // (0, none, is below any)
+                const uint32_t e = __ballot_sync(0xffffffffu, tie);
+                const int rank = eq + __popc(e & under);
+                const uint32_t in = __ballot_sync(0xffffffffu, yes || (tie && rank < want - over));
+                if ((in >> lane) & 1) out[to + __popc(in & under)] = names[y * 32 + lane];
+                to += __popc(in);
+                eq += __popc(e);
+            }
+            for (int i = lane; i < a.first; i += 32) out[i] = i;
+            for (int i = lane; i < a.local; i += 32) out[a.nsel - a.local + i] = hi + i;
+            return;
+        }
+        cut = least;
+        if (have == want) {
+            --cut;
+        } else {
+            int c = 0;
+#pragma unroll
+            for (int k = 0; k < K; ++k) c += key[k] > cut;
+            ties = want - __reduce_add_sync(0xffffffffu, c);
+        }
+    }
+    int at = 0, eq = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (k * 32 >= n) break;
+        const int i = k * 32 + lane;
+        const bool fix = i < n && (i < a.first || i >= hi);
+        const bool yes = fix || key[k] > cut, tie = !fix && key[k] == cut && ties > 0;
+        const uint32_t y = __ballot_sync(0xffffffffu, yes), e = __ballot_sync(0xffffffffu, tie);
+        const int rank = eq + __popc(e & under);
+        const int place = at + __popc(y & under) + min(rank, ties);
+        if ((yes || (tie && rank < ties)) && place < a.nsel) out[place] = i;
+        at += __popc(y);
+        eq += __popc(e);
+    }
+}
+
+template <int T>
+__global__ void __launch_bounds__(T) block_pick_kernel(const __grid_constant__ PickArgs a) {
+    extern __shared__ uint32_t key[];
+    __shared__ PickShared<T> sh;
+    __shared__ int bad_sh;
+    pdl_enter();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int t = blockIdx.x / a.hkv;
+    const int pos = __ldg(a.s.q_pos + t);  // checked beside the scores' loads
+    const int n = min(a.ld, pos < 0 ? 0 : (pos >> a.shift) + 1);
+    if (warp == 0) {
+        const int b = warp_seq_of(a.s.q_start, a.s.num_seqs, t);
+        const Seq sq = load_seq(a.s, b, a.num_q);
+        // 1: behind the last sequence, 2: bad
+        if (lane == 0)
+            bad_sh = t >= sq.q0 + sq.nq || t < sq.q0 ? 1 : !sq.ok || pos < -1 || pos >= sq.ctx ? 2 : 0;
+    }
+    const bool choose = n > a.nsel;
+    const int hi = n - a.local;
+    if (choose) {
+        uint32_t least = 0xFFFFFFFFu, best = 0u;
+        const float* row = a.scores + (int64_t)blockIdx.x * a.ld;
+        for (int i = a.first + tid; i < hi; i += T) {
+            const uint32_t k = score_code(row[i]);
+            key[i] = k;
+            least = min(least, k);
+            best = max(best, k);
+        }
+        least = __reduce_min_sync(0xffffffffu, least);
+        best = __reduce_max_sync(0xffffffffu, best);
+        if (lane == 0) sh.ends[0][warp] = least, sh.ends[1][warp] = best;
+        for (int i = tid; i < kBins; i += T) sh.hist[i] = 0;
+        if (tid == 0) sh.count = 0;
     }
     __syncthreads();
-    // the want-th largest key: bins over the range that is left, until a bin is one key or is taken whole
-    uint32_t low = range[0], width = range[1] - range[0];
-    uint32_t cut = 0xFFFFFFFFu;  // keys above are taken, and `ties` of those equal
-    int ties = 0;
-    while (want > 0) {
-        const int sh = max(0, 22 - __clz(width | 1));  // width >> sh < 1024
-        for (int i = tid; i < kBins; i += kPickThreads) hist[i] = 0;
-        __syncthreads();
-        for (int i = a.first + tid; i < hi; i += kPickThreads) {
-            const uint32_t d = key[i] - low;
-            if (key[i] >= low && d <= width) atomicAdd(&hist[d >> sh], 1);
-        }
-        __syncthreads();
-        // from the top: the thread with the bin where the count passes `want`
-        const int b0 = kBins - 1 - 4 * tid;
-        const int h0 = hist[b0], h1 = hist[b0 - 1], h2 = hist[b0 - 2], h3 = hist[b0 - 3];
-        int all;
-        const int above = cta_scan<kPickThreads>(h0 + h1 + h2 + h3, red, all);
-        if (above < want && above + h0 + h1 + h2 + h3 >= want) {
-            int c = above, z = 0;
-            if (c + h0 < want) {
-                c += h0, z = 1;
-                if (c + h1 < want) {
-                    c += h1, z = 2;
-                    if (c + h2 < want) c += h2, z = 3;
-                }
-            }
-            found[0] = b0 - z;
-            found[1] = want - c;
-        }
-        __syncthreads();
-        const int bin = found[0], need = found[1], has = hist[bin];
-        low += (uint32_t)bin << sh;
-        __syncthreads();
-        if (sh == 0 || (need == has && low > 0)) {
-            cut = sh == 0 ? low : low - 1;
-            ties = sh == 0 ? need : 0;
-            break;
-        }
-        want = need;
-        width = (1u << sh) - 1;
+    if (bad_sh) {  // left as it was
+        if (bad_sh == 2 && tid == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
+        return;
     }
-    // in order: a run of blocks per thread
-    const int per = (n + kPickThreads - 1) / kPickThreads;
-    const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
-    int sure = 0, equal = 0;
-    for (int i = i0; i < i1; ++i) {
-        if (i < a.first || i >= hi || key[i] > cut) ++sure;
-        else if (key[i] == cut) ++equal;
+    int32_t* out = a.blocks + (int64_t)blockIdx.x * a.nsel;
+    if (tid == 0) a.len[blockIdx.x] = seen_keys(pos, min(n, a.nsel), a.shift);
+    if (!choose) {  // all of them
+        for (int i = tid; i < a.nsel; i += T) out[i] = i < n ? i : -1;
+        return;
     }
-    uint32_t total;
-    uint32_t* ured = reinterpret_cast<uint32_t*>(red);
-    const uint32_t before = cta_scan<kPickThreads, uint32_t>((uint32_t)sure | (uint32_t)equal << 16, ured, total);
-    int eq = (int)(before >> 16);
-    int at = (int)(before & 0xFFFFu) + min(eq, ties);
-    for (int i = i0; i < i1; ++i) {
-        bool take = i < a.first || i >= hi || key[i] > cut;
-        if (!take && key[i] == cut) take = eq++ < ties;
-        if (take && at < a.nsel) out[at++] = i;
-    }
+    pick<T>(sh, key, n, a.first, hi, a.nsel - a.first - a.local, a.nsel, out);
 }
 
 }  // namespace
@@ -522,9 +1093,10 @@ cudaError_t launch_bounds(const dsa_gqa_shape& sh, const void* k, const float* k
     a.hkv = sh.num_kv_heads;
     a.shift = 31 - __builtin_clz((unsigned)block);
     a.scale_shift = scale_shift(sh);
+    a.page_shift = page_shift_of(s);
     const int64_t blocks = std::min<int64_t>(num_q, (num_q >> a.shift) + 2 * (int64_t)s.num_seqs);
-    const int64_t ctas = (blocks * sh.num_kv_heads + kBoundThreads / 32 - 1) / (kBoundThreads / 32);
-    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(ctas, kPlanSms * 6));
+    const int64_t ctas = blocks * ((sh.num_kv_heads + 1) / 2);  // two heads of a block at a time
+    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(ctas, kPlanSms * 8));
     auto go = [&](auto kern) { return launch_pdl(kern, dim3(grid), dim3(kBoundThreads), 0, stream, 1, a); };
     if (sh.head_dim == 64)
         return sh.kv_dtype == DSA_BF16 ? go(block_bounds_kernel<64, false>) : go(block_bounds_kernel<64, true>);
@@ -547,29 +1119,12 @@ cudaError_t launch_select(const dsa_gqa_shape& sh, const void* q, const void* bo
     a.group = sh.num_heads / sh.num_kv_heads;
     a.hkv = sh.num_kv_heads;
     a.shift = shift;
+    a.page_shift = page_shift_of(s);
     a.ld = (int32_t)select_ld(s, block);
     a.pad = 1;
     while (a.pad < a.group && a.pad < 8) a.pad *= 2;
     a.npt = (a.group + 7) / 8;
     const int tpt = 8 / a.pad;
-    a.tokens = std::min(s.max_q_per_seq, kScoreTiles / a.npt * tpt);
-    a.direct = s.max_q_per_seq <= a.tokens;
-    a.xt = (a.ld + kScoreBlocks - 1) / kScoreBlocks;
-    const int64_t slots = a.direct ? s.num_seqs : std::min<int64_t>(num_q, num_q / a.tokens + s.num_seqs);
-    const int64_t grid = slots * a.hkv * a.xt;
-    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-    const size_t smem = (size_t)((a.tokens + tpt - 1) / tpt) * a.npt * (sh.head_dim / 32) * 512;
-    auto go = [&](auto d) {
-        auto kern = block_score_kernel<decltype(d)::value>;
-        static OncePerDevice once;
-        const cudaError_t e = once.run([&] {
-            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kScoreTiles * (decltype(d)::value / 32) * 512);
-        });
-        return e != cudaSuccess ? e : launch_pdl(kern, dim3((unsigned)grid), dim3(kScoreThreads), smem, stream, 1, a);
-    };
-    cudaError_t e = sh.head_dim == 64 ? go(std::integral_constant<int, 64>()) : go(std::integral_constant<int, 128>());
-    if (e != cudaSuccess) return e;
     PickArgs p;
     p.scores = a.scores;
     p.blocks = blocks;
@@ -577,20 +1132,85 @@ cudaError_t launch_select(const dsa_gqa_shape& sh, const void* q, const void* bo
     p.s = s;
     p.d_status = d_status;
     p.num_q = num_q;
-    p.hkv = a.hkv;
+    p.hkv = sh.num_kv_heads;
     p.shift = shift;
     p.ld = a.ld;
     p.nsel = nsel;
     p.first = first;
     p.local = local;
-    static OncePerDevice once;
-    e = once.run([] {
-        return cudaFuncSetAttribute(block_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    DSA_GQA_MAX_BLOCKS * 4);
-    });
+    // up to four tiles of query rows per sequence and head: as many CTAs as fit at once, in shares of
+    // the blocks (four tiles of 16 at least)
+    const int64_t tiles = ((int64_t)s.max_q_per_seq + tpt - 1) / tpt * a.npt;
+    cudaError_t e;
+    if (s.max_q_per_seq <= kFewTiles * tpt && tiles <= kFewTiles) {
+        a.tokens = s.max_q_per_seq;
+        a.direct = 1;
+        const int64_t pairs = (int64_t)s.num_seqs * a.hkv, most = (a.ld + 16 * kFewWarps - 1) / (16 * kFewWarps);
+        // (sequence, key head)s that make two CTAs an SM choose for themselves; 64 sequences of 512
+        // blocks and 8 heads @@
+        const bool own = pairs >= 2 * kPlanSms && (int64_t)s.max_q_per_seq * a.ld <= kFewScores;
+        a.xt = own ? 1 : (int32_t)std::max<int64_t>(1, std::min<int64_t>(most, kPlanSms * 5 / pairs));
+        const int64_t grid = pairs * a.xt;
+        if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+        const size_t smem = own ? (size_t)s.max_q_per_seq * a.ld * 4 : 0;
+        auto go = [&](auto kern) {
+            return launch_pdl(kern, dim3((unsigned)grid), dim3(kFewThreads), smem, stream, 1, a, p);
+        };
+        auto by_tiles = [&](auto d, auto o) {
+            constexpr int D = decltype(d)::value;
+            constexpr bool O = decltype(o)::value;
+            return tiles == 1   ? go(block_score_few_kernel<D, 1, O>)
+                   : tiles == 2 ? go(block_score_few_kernel<D, 2, O>)
+                                : go(block_score_few_kernel<D, 4, O>);
+        };
+        using std::integral_constant;
+        if (sh.head_dim == 64)
+            e = own ? by_tiles(integral_constant<int, 64>(), std::true_type())
+                    : by_tiles(integral_constant<int, 64>(), std::false_type());
+        else
+            e = own ? by_tiles(integral_constant<int, 128>(), std::true_type())
+                    : by_tiles(integral_constant<int, 128>(), std::false_type());
+        if (e != cudaSuccess || own) return e;
+    } else {
+        a.tokens = std::min(s.max_q_per_seq, kScoreTiles / a.npt * tpt);
+        a.direct = s.max_q_per_seq <= a.tokens;
+        a.xt = (a.ld + kScoreBlocks - 1) / kScoreBlocks;
+        const int64_t slots = a.direct ? s.num_seqs : std::min<int64_t>(num_q, num_q / a.tokens + s.num_seqs);
+        const int64_t grid = slots * a.hkv * a.xt;
+        if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+        const size_t smem = (size_t)((a.tokens + tpt - 1) / tpt) * a.npt * (sh.head_dim / 32) * 512;
+        auto go = [&](auto d) {
+            auto kern = block_score_kernel<decltype(d)::value>;
+            static OncePerDevice once;
+            const cudaError_t r = once.run([&] {
+                return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            kScoreTiles * (decltype(d)::value / 32) * 512);
+            });
+            return r != cudaSuccess ? r : launch_pdl(kern, dim3((unsigned)grid), dim3(kScoreThreads), smem, stream, 1, a);
+        };
+        e = sh.head_dim == 64 ? go(std::integral_constant<int, 64>()) : go(std::integral_constant<int, 128>());
+    }
     if (e != cudaSuccess) return e;
-    return launch_pdl(block_pick_kernel, dim3((unsigned)(num_q * a.hkv)), dim3(kPickThreads), (size_t)a.ld * 4, stream,
-                      1, p);
+    // a row's keys by 128 threads (many rows at once), or 512 where they are many
+    auto go = [&](auto threads) {
+        constexpr int T = decltype(threads)::value;
+        static OncePerDevice once;
+        const cudaError_t r = once.run([] {
+            return cudaFuncSetAttribute(block_pick_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        DSA_GQA_MAX_BLOCKS * 4);
+        });
+        if (r != cudaSuccess) return r;
+        return launch_pdl(block_pick_kernel<T>, dim3((unsigned)(num_q * a.hkv)), dim3(T), (size_t)a.ld * 4, stream, 1,
+                          p);
+    };
+    const unsigned ctas = (unsigned)(((int64_t)num_q * a.hkv + kRowsPerCta - 1) / kRowsPerCta);
+    auto rows = [&](auto kern) { return launch_pdl(kern, dim3(ctas), dim3(32 * kRowsPerCta), 0, stream, 1, p); };
+    if ((int64_t)num_q * a.hkv >= 8 * kPlanSms * kRowsPerCta) {
+        if (a.ld <= 256) return rows(block_pick_row_kernel<8>);
+        if (a.ld <= 512) return rows(block_pick_row_kernel<16>);
+        if (a.ld <= 1024) return rows(block_pick_row_kernel<32>);
+    }
+    return a.ld <= 4096 ? go(std::integral_constant<int, 128>()) : go(std::integral_constant<int, 512>());
 }
 
 }  // namespace gqa

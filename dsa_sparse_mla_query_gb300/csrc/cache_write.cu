@@ -685,7 +685,7 @@ cudaError_t launch_kv_insert(const dsa_gqa_shape& sh, const void* k, int64_t k_i
 // once for all heads; then eight warps of 16 rows each take the heads one after
 // the other (a head's rows in as many warps as it needs), so that a block's
 // maximum is met on the way and every value is read once, held in registers
-// between the maximum and its code.  Few blocks: blockIdx.y shares the heads.
+// as it came between the maximum and its code.  Few blocks: blockIdx.y shares the heads.
 namespace {
 
 constexpr float kLeastScale = 0x1p-60f;
@@ -701,41 +701,55 @@ struct KvBlockInsert {
     int64_t k_stride, v_stride, q_stride;
     dsa_seqs s;
     int32_t* d_status;
-    int32_t num_q, hq, hkv, rot, shift;  // hq: 0 without queries; 2^shift tokens per scale
+    int32_t num_q, hq, hkv, rot, shift, page_shift;  // hq: 0 without queries; 2^shift tokens per scale
+    int32_t units;  // 16 heads of a token's queries
 };
 
-// a row's 8 dims of lane li, rotated: `o` holds the partner dims (HALVES) or the same (PAIRS)
+// The cosines and sines of a token as its row's lanes take them, 16 bytes (two
+// frequencies) at a time: [j][lane][2], lanes side by side, so that a warp's
+// loads meet no bank twice (frequencies in their own order did, four times: 630
+// us for 49,000 tokens of 64/8 heads, 420 so).
 template <bool HALVES>
-__device__ __forceinline__ void turn8(float (&v)[8], const uint4& x, const uint4& o, bool turned, bool upper,
-                                      const float2* cs) {
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, os[4] = {o.x, o.y, o.z, o.w};
-    if (!turned) {
-        unpack_bf16x8(x, v);
-        return;
-    }
+struct Turn {
+    static constexpr int kUnits = HALVES ? 4 : 2;  // a lane's 16-byte units
+    float4 c[kUnits];
+    __device__ __forceinline__ void load(const float2* token, int lanes, int l) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float a = bf16_lo(xs[e]), b = bf16_hi(xs[e]);
-        if (HALVES) {
-            const float2 c0 = cs[2 * e], c1 = cs[2 * e + 1];
-            const float s0 = upper ? c0.y : -c0.y, s1 = upper ? c1.y : -c1.y;
-            v[2 * e] = fmaf(bf16_lo(os[e]), s0, a * c0.x);
-            v[2 * e + 1] = fmaf(bf16_hi(os[e]), s1, b * c1.x);
-        } else {
-            const float2 c = cs[e];
-            v[2 * e] = fmaf(b, -c.y, a * c.x);
-            v[2 * e + 1] = fmaf(a, c.y, b * c.x);
+        for (int j = 0; j < kUnits; ++j) c[j] = reinterpret_cast<const float4*>(token)[j * lanes + l];
+    }
+    static __device__ __forceinline__ int place(int f, int lanes) {
+        const int l = f / (2 * kUnits), j = f % (2 * kUnits) / 2;
+        return (j * lanes + l) * 2 + (f & 1);
+    }
+    // a row's 8 dims: `o` holds the partner dims (HALVES)
+    __device__ __forceinline__ void turn8(float (&v)[8], const uint4& x, const uint4& o, bool upper) const {
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, os[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float a = bf16_lo(xs[e]), b = bf16_hi(xs[e]);
+            if (HALVES) {
+                const float4 f = c[e];
+                v[2 * e] = fmaf(bf16_lo(os[e]), upper ? f.y : -f.y, a * f.x);
+                v[2 * e + 1] = fmaf(bf16_hi(os[e]), upper ? f.w : -f.w, b * f.z);
+            } else {
+                const float4 f = c[e / 2];
+                const float co = e & 1 ? f.z : f.x, si = e & 1 ? f.w : f.y;
+                v[2 * e] = fmaf(b, -si, a * co);
+                v[2 * e + 1] = fmaf(a, si, b * co);
+            }
         }
     }
-}
+};
 
 template <int D, bool HALVES>
 __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const __grid_constant__ KvBlockInsert a) {
     constexpr int kLanes = D / 8;        // lanes per row
     constexpr int kGroup = 32 / kLanes;  // rows per warp access
     constexpr int kAcc = 16 / kGroup;    // accesses of a warp's 16 rows
+    constexpr int kChunk = Pieces<kBlkThreads>::kChunk;
     extern __shared__ __align__(16) float2 table[];  // [token][rot / 2]: cos, sin
     __shared__ Pieces<kBlkThreads> pieces;
+    __shared__ int4 seq_sh[kChunk];  // first row, tokens, first position, context
     __shared__ float top[2][kBlkWarps];
     __shared__ bool good[128];
     pdl_enter();
@@ -746,33 +760,81 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
     const int step = a.rot / 16;  // HALVES: lanes between a pair's dims
     const bool upper = turned && HALVES && li >= step;
     const int from = !turned || !HALVES ? lane : upper ? lane - step : lane + step;
-    const int f0 = !turned ? 0 : HALVES ? 8 * (upper ? li - step : li) : 4 * li;  // the lane's first frequency
+    const int tl = HALVES ? step : 2 * step;         // lanes of the table
+    const int ti = upper ? li - step : li;           // this lane's place among them
     const bool lead = blockIdx.y == 0;
+    auto partner = [&](const uint4& x) {
+        uint4 o = x;
+        if (HALVES && a.rot) {
+            o.x = __shfl_sync(0xffffffffu, o.x, from);
+            o.y = __shfl_sync(0xffffffffu, o.y, from);
+            o.z = __shfl_sync(0xffffffffu, o.z, from);
+            o.w = __shfl_sync(0xffffffffu, o.w, from);
+        }
+        return o;
+    };
     int64_t before = 0;
     int turn = 0;
-    for (int c0 = 0; c0 < a.s.num_seqs; c0 += Pieces<kBlkThreads>::kChunk) {
-        const int left = min(Pieces<kBlkThreads>::kChunk, a.s.num_seqs - c0);
+    for (int c0 = 0; c0 < a.s.num_seqs; c0 += kChunk) {
+        const int left = min(kChunk, a.s.num_seqs - c0);
         const int total = pieces.scan(c0, a.s.num_seqs, [&](int b) {
             const NewTokens n = new_tokens(a.s, b, a.num_q);
             if (n.bad && blockIdx.x == 0 && lead) report(a.d_status, DSA_ERR_BAD_INPUT);
+            seq_sh[b - c0] = make_int4(n.q0, n.nq, n.p0, n.ctx);
             return blocks_touched(n, a.shift);
         });
         for (int x = (int)((gridDim.x + blockIdx.x - before % gridDim.x) % gridDim.x); x < total; x += gridDim.x) {
             const int i = pieces.find(x, left), b = c0 + i;
-            const NewTokens nt = new_tokens(a.s, b, a.num_q);
-            const int blk = (nt.p0 >> a.shift) + (x - pieces.first[i]);
+            const int4 sq = seq_sh[i];
+            const int blk = (sq.z >> a.shift) + (x - pieces.first[i]);
             const int64_t lo = (int64_t)blk << a.shift;
-            const int pos0 = (int)max(lo, (int64_t)nt.p0);                    // the piece's first new token
-            const int t0 = nt.q0 + (pos0 - nt.p0);
-            const int n = (int)min(lo + (1 << a.shift), (int64_t)nt.p0 + nt.nq) - pos0;
+            const int pos0 = (int)max(lo, (int64_t)sq.z);                     // the piece's first new token
+            const int t0 = sq.x + (pos0 - sq.z);
+            const int n = (int)min(lo + (1 << a.shift), (int64_t)sq.z + sq.y) - pos0;
             const int old = pos0 - (int)lo;                                   // older tokens of the block
-            const int64_t row0 = phys_row(a.s, b, lo);                        // the block's first row
+
+            // keys and values: a head's rows in `per` warps, `heads` heads a round; then the
+            // queries, 16 heads of a token a warp
+            const int per = n <= 16 ? 1 : n <= 32 ? 2 : n <= 64 ? 4 : 8;
+            const int heads = kBlkWarps / per, part = warp % per;
+            const int rounds = (2 * a.hkv + heads - 1) / heads;
+            const int q_units = n * a.units;
+            const int all = rounds + (q_units + kBlkWarps - 1) / kBlkWarps;
+            // a round's 16 rows of this warp, whatever becomes of them
+            auto load = [&](int r, uint4 (&raw)[kAcc]) {
+                if (r < rounds) {
+                    const int task = r * heads + warp / per;
+                    const int h = task < a.hkv ? task : task - a.hkv;
+                    const __nv_bfloat16* src = task < a.hkv ? a.k : a.v;
+                    const int64_t in = task < a.hkv ? a.k_in : a.v_in;
+#pragma unroll
+                    for (int u = 0; u < kAcc; ++u) {
+                        const int tok = part * 16 + u * kGroup + sub;
+                        raw[u] = make_uint4(0u, 0u, 0u, 0u);
+                        if (task < 2 * a.hkv && tok < n)
+                            raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + (int64_t)(t0 + tok) * in + h * D + 8 * li));
+                    }
+                } else {
+                    const int y = (r - rounds) * kBlkWarps + warp, tok = y / max(1, a.units), h0 = (y - tok * a.units) * 16;
+#pragma unroll
+                    for (int u = 0; u < kAcc; ++u) {
+                        const int h = h0 + u * kGroup + sub;
+                        raw[u] = make_uint4(0u, 0u, 0u, 0u);
+                        if (y < q_units && h < a.hq)
+                            raw[u] = __ldcs(reinterpret_cast<const uint4*>(a.q + (int64_t)(t0 + tok) * a.q_in + h * D +
+                                                                           8 * li));
+                    }
+                }
+            };
+            uint4 raw[kAcc];
+            if ((int)blockIdx.y < all) load(blockIdx.y, raw);  // on their way beside the tokens' checks
+            const int64_t row0 = row_at(a.s, a.page_shift, b, lo);  // the block's first row
             const bool there = row0 >= 0 && (row0 & ((1 << a.shift) - 1)) == 0;
             __syncthreads();  // the last piece's table and tokens are no longer read
             bool some = false;
             if ((int)threadIdx.x < n) {
                 const int p = __ldg(a.s.q_pos + t0 + threadIdx.x);
-                const bool ok = p == pos0 + (int)threadIdx.x && p < nt.ctx && there &&
+                const bool ok = p == pos0 + (int)threadIdx.x && p < sq.w && there &&
                                 row0 + old + (int)threadIdx.x < a.s.num_rows;
                 if (!ok && p != -1 && lead) report(a.d_status, DSA_ERR_BAD_INPUT);
                 good[threadIdx.x] = ok;
@@ -782,59 +844,80 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
                 const int tok = y / half, f = y - tok * half;
                 float c, sn;
                 rope_cs(pos0 + tok, __ldg(a.inv_freq + f), c, sn);
-                table[y] = make_float2(c, sn);
+                table[tok * half + Turn<HALVES>::place(f, tl)] = make_float2(c, sn);
             }
             if (!__syncthreads_or(some)) continue;
 
-            // ---- keys and values: a head's rows in `per` warps
-            const int per = n <= 16 ? 1 : n <= 32 ? 2 : n <= 64 ? 4 : 8;
-            const int heads = kBlkWarps / per;
-            const int rounds = (2 * a.hkv + heads - 1) / heads;
-            for (int r = blockIdx.y; r < rounds; r += gridDim.y) {
-                const int task = r * heads + warp / per, part = warp % per;
+            for (int r = blockIdx.y; r < all; r += gridDim.y) {
+                if (r != (int)blockIdx.y) load(r, raw);
+                if (r >= rounds) {
+                    const int y = (r - rounds) * kBlkWarps + warp, tok = y / a.units, h0 = (y - tok * a.units) * 16;
+                    if (y >= q_units || !good[tok]) continue;
+                    Turn<HALVES> t;
+                    if (turned) t.load(table + tok * half, tl, ti);
+                    __nv_bfloat16* dst = a.q_out + (int64_t)(t0 + tok) * a.q_stride + 8 * li;
+#pragma unroll
+                    for (int u = 0; u < kAcc; ++u) {
+                        if (h0 + u * kGroup >= a.hq) break;  // the same for the warp
+                        const uint4 o = partner(raw[u]);
+                        uint4 z = raw[u];
+                        if (turned) {
+                            float v[8];
+                            t.turn8(v, raw[u], o, upper);
+                            z = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                           pack_bf16x2(v[6], v[7]));
+                        }
+                        const int h = h0 + u * kGroup + sub;
+                        if (h < a.hq) *reinterpret_cast<uint4*>(dst + h * D) = z;
+                    }
+                    continue;
+                }
+                const int task = r * heads + warp / per;
                 const bool live = task < 2 * a.hkv;
                 const bool is_k = task < a.hkv;
                 const int h = is_k ? task : task - a.hkv;
-                const __nv_bfloat16* src = is_k ? a.k : a.v;
-                const int64_t in = is_k ? a.k_in : a.v_in;
                 uint8_t* cache = is_k ? a.k_cache : a.v_cache;
                 float* scales = is_k ? a.k_scale : a.v_scale;
                 const int64_t stride = is_k ? a.k_stride : a.v_stride;
                 const int64_t at_scale = (row0 >> a.shift) * a.hkv + h;
                 const float held = live && old ? scales[at_scale] : 0.f;
-                uint4 raw[kAcc];
-#pragma unroll
-                for (int u = 0; u < kAcc; ++u) {
-                    const int tok = part * 16 + u * kGroup + sub;
-                    raw[u] = make_uint4(0u, 0u, 0u, 0u);
-                    if (live && tok < n && good[tok])
-                        raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + (int64_t)(t0 + tok) * in + h * D + 8 * li));
-                }
-                float v[kAcc][8];
+                // the values are turned twice, for their maximum and for their codes: a table read
+                // and a few products less dear than the registers (three CTAs an SM for two)
+                auto values = [&](int u, float (&v)[8]) {
+                    if (!is_k) {  // the same for the warp
+                        unpack_bf16x8(raw[u], v);
+                        return;
+                    }
+                    const uint4 o = partner(raw[u]);
+                    if (turned) {
+                        Turn<HALVES> t;
+                        t.load(table + min(part * 16 + u * kGroup + sub, n - 1) * half, tl, ti);
+                        t.turn8(v, raw[u], o, upper);
+                    } else {
+                        unpack_bf16x8(raw[u], v);
+                    }
+                };
                 float m = 0.f;
 #pragma unroll
                 for (int u = 0; u < kAcc; ++u) {
-                    const int tok = min(part * 16 + u * kGroup + sub, n - 1);
-                    uint4 o = raw[u];
-                    if (HALVES && a.rot) {
-                        o.x = __shfl_sync(0xffffffffu, o.x, from);
-                        o.y = __shfl_sync(0xffffffffu, o.y, from);
-                        o.z = __shfl_sync(0xffffffffu, o.z, from);
-                        o.w = __shfl_sync(0xffffffffu, o.w, from);
-                    }
-                    turn8<HALVES>(v[u], raw[u], o, turned && is_k, upper, table + tok * half + f0);
+                    if (part * 16 + u * kGroup >= n) break;  // the same for the warp
+                    float v[8];
+                    values(u, v);
+                    const int tok = part * 16 + u * kGroup + sub;
+                    const bool in = tok < n && good[min(tok, n - 1)];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float y = fabsf(v[u][e]);
-                        m = fmaxf(m, y < INFINITY ? y : 0.f);  // what is not finite has no say
+                        const float y = fabsf(v[e]);
+                        m = fmaxf(m, in && y < INFINITY ? y : 0.f);  // what is not finite has no say
                     }
                 }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                if (lane == 0) top[turn][warp] = m;
-                __syncthreads();
-                for (int w = warp - part; w < warp - part + per; ++w) m = fmaxf(m, top[turn][w]);
-                turn ^= 1;  // (the next round's barrier lies between this reading and the next writing)
+                m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+                if (per > 1) {  // (the same for the CTA)
+                    if (lane == 0) top[turn][warp] = m;
+                    __syncthreads();
+                    for (int w = warp - part; w < warp - part + per; ++w) m = fmaxf(m, top[turn][w]);
+                    turn ^= 1;  // (the next round's barrier lies between this reading and the next writing)
+                }
                 if (!live) continue;
                 float scale = m > 0.f ? fmaxf(two_to(scale_exponent(m, 8, 0x600000u)), kLeastScale) : kLeastScale;
                 if (old) {
@@ -864,44 +947,16 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
                 const float rs = 1.f / scale;
 #pragma unroll
                 for (int u = 0; u < kAcc; ++u) {
+                    if (part * 16 + u * kGroup >= n) break;
+                    float v[8];
+                    values(u, v);
                     const int tok = part * 16 + u * kGroup + sub;
                     if (tok < n && good[tok])
                         *reinterpret_cast<uint2*>(cache + (row0 + old + tok) * stride + h * D + 8 * li) =
-                            make_uint2(pack_e4m3x4(v[u][0] * rs, v[u][1] * rs, v[u][2] * rs, v[u][3] * rs),
-                                       pack_e4m3x4(v[u][4] * rs, v[u][5] * rs, v[u][6] * rs, v[u][7] * rs));
+                            make_uint2(pack_e4m3x4(v[0] * rs, v[1] * rs, v[2] * rs, v[3] * rs),
+                                       pack_e4m3x4(v[4] * rs, v[5] * rs, v[6] * rs, v[7] * rs));
                 }
                 if (part == 0 && lane == 0 && scale != held) scales[at_scale] = scale;
-            }
-
-            // ---- queries: 16 (token, head) rows a warp
-            const int rows = n * a.hq;
-            for (int r = ((int)blockIdx.y * kBlkWarps + warp) * 16; r < rows; r += gridDim.y * kBlkWarps * 16) {
-                uint4 raw[kAcc];
-                int tok[kAcc], head[kAcc];
-#pragma unroll
-                for (int u = 0; u < kAcc; ++u) {
-                    const int y = min(r + u * kGroup + sub, rows - 1);
-                    tok[u] = y / a.hq;
-                    head[u] = y - tok[u] * a.hq;
-                    raw[u] = __ldcs(reinterpret_cast<const uint4*>(a.q + (int64_t)(t0 + tok[u]) * a.q_in + head[u] * D +
-                                                                   8 * li));
-                }
-#pragma unroll
-                for (int u = 0; u < kAcc; ++u) {
-                    uint4 o = raw[u];
-                    if (HALVES && a.rot) {
-                        o.x = __shfl_sync(0xffffffffu, o.x, from);
-                        o.y = __shfl_sync(0xffffffffu, o.y, from);
-                        o.z = __shfl_sync(0xffffffffu, o.z, from);
-                        o.w = __shfl_sync(0xffffffffu, o.w, from);
-                    }
-                    float v[8];
-                    turn8<HALVES>(v, raw[u], o, turned, upper, table + tok[u] * half + f0);
-                    if (r + u * kGroup + sub < rows && good[tok[u]])
-                        *reinterpret_cast<uint4*>(a.q_out + (int64_t)(t0 + tok[u]) * a.q_stride + head[u] * D + 8 * li) =
-                            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                       pack_bf16x2(v[6], v[7]));
-                }
             }
         }
         before += total;
@@ -939,12 +994,14 @@ cudaError_t launch_kv_block_insert(const dsa_gqa_shape& sh, const void* k, int64
     a.hkv = sh.num_kv_heads;
     a.rot = inv_freq ? rot : 0;
     a.shift = 31 - __builtin_clz((unsigned)sh.scale_block);
+    a.page_shift = page_shift_of(s);
+    a.units = (a.hq + 15) / 16;
     // pieces: at most a block per token, and two more than whole blocks per sequence; the heads
     // are shared where they do not fill the GPU (eight CTAs per SM in all)
     const int64_t blocks = std::min<int64_t>(num_q, (num_q >> a.shift) + 2 * (int64_t)s.num_seqs);
     const int64_t longest = std::min<int64_t>(sh.scale_block, s.max_q_per_seq);
     const int64_t per = longest <= 16 ? 1 : longest <= 32 ? 2 : longest <= 64 ? 4 : 8;
-    const int64_t work = std::max<int64_t>((2 * sh.num_kv_heads * per + 7) / 8, (longest * a.hq + 127) / 128);
+    const int64_t work = (2 * sh.num_kv_heads * per + 7) / 8 + (longest * a.units + 7) / 8;
     const unsigned grid = (unsigned)std::min<int64_t>(blocks, 152 * 8);
     const unsigned share = (unsigned)std::max<int64_t>(1, std::min<int64_t>(work, 152 * 8 / grid));
     const size_t smem = (size_t)sh.scale_block * (a.rot / 2) * sizeof(float2);  // up to 64 KB

@@ -101,6 +101,20 @@ __device__ __forceinline__ NewTokens new_tokens(const dsa_seqs& s, int b, int nu
     return r;
 }
 
+// phys_row with the page size as a power of two: a 64-bit division takes as long as a tile's products
+__device__ __forceinline__ int64_t row_at(const dsa_seqs& s, int page_shift, int b, int64_t j) {
+    if (!s.page_table) {
+        const int64_t row = __ldg(s.seq_base + b) + j;
+        return row >= 0 && row < s.num_rows ? row : -1;
+    }
+    const int64_t p = j >> page_shift;
+    if (p >= s.max_pages) return -1;
+    const int64_t page = __ldg(s.page_table + (int64_t)b * s.max_pages + p);
+    const int64_t row = (page << page_shift) + (j & ((1 << page_shift) - 1));
+    return page >= 0 && row < s.num_rows ? row : -1;
+}
+inline int page_shift_of(const dsa_seqs& s) { return s.page_table ? 31 - __builtin_clz((unsigned)s.page_size) : 0; }
+
 // the blocks of 2^shift tokens that they lie in
 __device__ __forceinline__ int blocks_touched(const NewTokens& n, int shift) {
     return n.nq ? (int)((((int64_t)n.p0 + n.nq - 1) >> shift) - (n.p0 >> shift)) + 1 : 0;
