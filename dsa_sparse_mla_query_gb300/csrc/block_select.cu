@@ -11,16 +11,16 @@
 //
 // - block_bounds_kernel: minimum and maximum over the keys of the blocks that new
 //   tokens touch, four warps per block and head, keys read once.
-// - block_score_kernel: the sums on the warp-level matrix instruction, 16 blocks
-//   by 8 query rows, k-steps over lo with min(q, 0), then over hi with max(q, 0).
-//   A warp holds 16 blocks' bounds as f16 fragments straight from global memory
-//   (the order of the dims within a k-step is the same for both operands and free
-//   otherwise, so a thread's 16 bytes make whole fragments) and walks the query
-//   rows, which lie in shared memory as fragments.  With one token a sequence it
-//   reads 2 D bytes a block once: HBM.  With a prompt's tokens a product of
-//   [tokens heads] x [blocks]: the matrix instruction.
-// - block_pick_kernel: the nsel best of a row by a histogram over the keys' range
-//   (order-preserving codes), one CTA per query and key head.
+// - block_score_few_kernel: few tokens a sequence read 2 D bytes a block once:
+//   HBM.  The sums on the warp-level 8-bit matrix instruction, 16 blocks by 8
+//   query rows, straight from global memory (the order of the dims within a
+//   k-step is the same for both operands and free otherwise, so a thread's 16
+//   bytes make whole fragments).
+// - block_score_wide_kernel: a prompt's tokens, a product of [blocks] x [tokens
+//   heads] on tcgen05.
+// - block_pick_kernel, block_pick_row_kernel: the nsel best of a row by a
+//   histogram over the keys' range (order-preserving codes) or, many rows, by
+//   halving it, a warp a row.
 #include <algorithm>
 
 #include "gqa_common.cuh"
@@ -417,10 +417,6 @@ __device__ __forceinline__ void pick(PickShared<T>& sh, uint32_t* key, int n, in
 
 // ---------------------------------------------------------------------------
 // scores
-constexpr int kScoreThreads = 256, kScoreWarps = kScoreThreads / 32;
-constexpr int kScoreBlocks = 16 * kScoreWarps;  // blocks per CTA
-constexpr int kScoreTiles = 32;                 // 8-row query tiles per CTA
-
 struct ScoreArgs {
     const __nv_bfloat16* q;
     const int8_t* bounds;
@@ -430,33 +426,20 @@ struct ScoreArgs {
     int64_t q_stride;
     int32_t* d_status;
     int32_t num_q, group, hkv, shift, ld, page_shift;
-    int32_t pad;     // a token's rows: a power of two of them in one tile, or 8
-    int32_t npt;     // tiles per token (1 where pad < 8)
+    int32_t pad;     // a token's rows, a power of two of them (up to 8 in the 8-row tiles of few rows)
+    int32_t npt;     // tiles per token there (1 where pad < 8)
     int32_t tokens;  // per CTA
-    int32_t xt;      // CTAs along the blocks
+    int32_t xt;      // CTAs (items) that share the blocks
+    int32_t items;   // of the CTAs that take them in turn
     int32_t direct;  // slot = sequence
 };
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&x)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t below0(uint32_t x) {  // two f16
-    const __half2 v = __hmin2(*reinterpret_cast<__half2*>(&x), __half2half2(__ushort_as_half(0)));
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ uint32_t above0(uint32_t x) {
-    const __half2 v = __hmax2(*reinterpret_cast<__half2*>(&x), __half2half2(__ushort_as_half(0)));
-    return *reinterpret_cast<const uint32_t*>(&v);
 }
 // four signed bytes as f16: a byte + 128 under the exponent of 1024, less 1152
 __device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -469,89 +452,18 @@ __device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
     hi = *reinterpret_cast<const uint32_t*>(&yh);
 }
 
-// a thread's 16 dims, chunk c of its query row: tile j of token tok, column lane / 4
-template <int D>
-__device__ __forceinline__ void load_query(const ScoreArgs& a, int t0, int tok, int n, int kvh, int j, int c, uint4 (&x)[2]) {
-    const int lane = threadIdx.x & 31, col = lane >> 2, t = lane & 3;
-    const int head = min(j * 8 + col % a.pad, a.group - 1);  // a group's last head again behind it
-    const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(t0 + tok) * a.q_stride +
-                                                      (int64_t)(kvh * a.group + head) * D + c * 64 + t * 16);
-    x[0] = tok < n ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);
-    x[1] = tok < n ? __ldg(src + 1) : make_uint4(0u, 0u, 0u, 0u);
-}
-// one over the step of a token's group, for the lanes that hold its rows
-template <int D>
-__device__ __forceinline__ float query_step(const ScoreArgs& a, int t0, int tok, int n, int kvh) {
-    float top = 0.f;
-    for (int j = 0; j < a.npt; ++j)
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-            uint4 x[2];
-            load_query<D>(a, t0, tok, n, kvh, j, c, x);
-            const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float u = fabsf(__uint_as_float(w[e] << 16)), v = fabsf(__uint_as_float(w[e] & 0xFFFF0000u));
-                top = fmaxf(top, fmaxf(u < INFINITY ? u : 0.f, v < INFINITY ? v : 0.f));
-            }
-        }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    for (int o = 1; o < a.pad; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4 * o));
-    return two_to(top > 0.f ? -scale_exponent(top, 6, 0x7E0000u) : 0);
+// 16 bytes to shared memory, asynchronously, or zeros
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool copy) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(copy ? 16 : 0)
+                 : "memory");
 }
 __device__ __forceinline__ float whole_steps(float v, float up) {
     return v == v ? fmaxf(-127.f, fminf(127.f, rintf(v * up))) : 0.f;
 }
 
-// Queries of n tokens from row t0 in whole steps, as fragments: a token's tiles
-// (a tile's tokens where they are several) by one warp, [tile][KS / 2][lane]
-template <int D>
-__device__ __forceinline__ void quantise(const ScoreArgs& a, int t0, int n, int kvh, int warp, int warps, uint4* q_sh) {
-    const int lane = threadIdx.x & 31, col = lane >> 2;
-    const int tpt = 8 / a.pad;  // tokens per tile (npt = 1)
-    const int groups = (n + tpt - 1) / tpt;
-    for (int gu = warp; gu < groups; gu += warps) {
-        const int tok = gu * tpt + col / a.pad;
-        const float up = query_step<D>(a, t0, tok, n, kvh);
-        auto two = [&](uint32_t w) {
-            return pack_f16(whole_steps(__uint_as_float(w << 16), up), whole_steps(__uint_as_float(w & 0xFFFF0000u), up));
-        };
-        for (int j = 0; j < a.npt; ++j)
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                uint4 x[2];
-                load_query<D>(a, t0, tok, n, kvh, j, c, x);
-                uint4* dst = q_sh + ((gu * a.npt + j) * (D / 32) + 2 * c) * 32 + lane;
-                dst[0] = make_uint4(two(x[0].x), two(x[0].y), two(x[0].z), two(x[0].w));
-                dst[32] = make_uint4(two(x[1].x), two(x[1].y), two(x[1].z), two(x[1].w));
-            }
-    }
-}
-
-// the best of a token's heads (columns 2t, 2t + 1 of rows blk and blk + 8) into its rows of scores
-__device__ __forceinline__ void store_scores(const ScoreArgs& a, float (&m)[4], int t0, int n, int kvh, int gu, int blk,
-                                             float step0, float step1) {
-    const int t = threadIdx.x & 3, tpt = 8 / a.pad;
-    if (a.pad >= 2) m[0] = m[1] = fmaxf(m[0], m[1]), m[2] = m[3] = fmaxf(m[2], m[3]);
-    for (int o = 2; o < a.pad; o <<= 1)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], o / 2));
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int c = 2 * t + e;
-        const int tok = gu * tpt + c / a.pad;
-        if (c % a.pad || tok >= n) continue;
-        float* dst = a.scores + ((int64_t)(t0 + tok) * a.hkv + kvh) * a.ld + blk;
-        // (a step above 2^105 overflows to equal scores)
-        if (blk < a.ld) dst[0] = m[e] * step0;
-        if (blk + 8 < a.ld) dst[8] = m[2 + e] * step1;
-    }
-}
-
 // A few query rows a sequence (up to 4 tiles): a CTA of four warps takes a
 // (sequence, key head), or a share of its blocks.  Every warp keeps two tiles of
-// 16 blocks on their way, and the page of a third; bounds are fragments of the
+// 16 blocks on their way, and the pages of two more; bounds are fragments of the
 // 8-bit matrix instruction as they lie in memory, so that a tile of 4 KB takes
 // eight products and few other instructions.  Where (sequence, key head)s alone
 // fill the GPU (PICK) their scores stay in shared memory, and the CTA chooses
@@ -582,10 +494,15 @@ __global__ void __launch_bounds__(kFewThreads, PICK ? 4 : 5)
     if (n == 0) return;
     // places of tile i's blocks (lanes 0 .. 15) among the cache's, by the context; those that no query
     // sees may lie anywhere
-    auto place = [&](int i) -> int {
+    const int64_t base = first_row(a.s, b);
+    auto page_of = [&](int i) {
+        const int64_t tok = (int64_t)(i * 16 + (lane & 15)) << a.shift;
+        return tok < sq.ctx ? page_at(a.s, a.page_shift, b, tok) : 0;
+    };
+    auto place = [&](int i, int page) -> int {
         const int64_t tok = (int64_t)(i * 16 + (lane & 15)) << a.shift;
         if (tok >= sq.ctx) return -1;
-        const int64_t row = row_at(a.s, a.page_shift, b, tok);
+        const int64_t row = row_in(a.s, a.page_shift, page, base, tok);
         return row < 0 || (row & ((1 << a.shift) - 1)) ? -2 : (int)(row >> a.shift);
     };
     struct Tile {
@@ -605,7 +522,7 @@ __global__ void __launch_bounds__(kFewThreads, PICK ? 4 : 5)
     };
     const int stride = a.xt * kFewWarps;
     int i = share * kFewWarps + warp;
-    int at = place(i), next = place(i + stride);
+    int page = page_of(i), then_page = page_of(i + stride);
     if (tid < n) pos_sh[tid] = __ldg(a.s.q_pos + sq.q0 + tid);
     // ---- the queries in whole steps: a thread's 16 dims of a row, twice for more than two tiles
     constexpr int kSets = (NT * 8 * (D / 16) + kFewThreads - 1) / kFewThreads;
@@ -623,7 +540,10 @@ __global__ void __launch_bounds__(kFewThreads, PICK ? 4 : 5)
         if (j < NT && tok < n) raw[y][0] = __ldg(src), raw[y][1] = __ldg(src + 1);
     }
     Tile cur;
+    int at = place(i, page);
     fetch(at, cur);
+    page = then_page;
+    then_page = page_of(i + 2 * stride);
     __syncthreads();
     auto token = [&](int y) {
         const int row = (y * kFewThreads + tid) / (D / 16);
@@ -680,9 +600,10 @@ __global__ void __launch_bounds__(kFewThreads, PICK ? 4 : 5)
     for (; i * 16 <= most; i += stride) {
         lost = lost || (at == -2 && i * 16 + (lane & 15) <= most);
         Tile then;
-        fetch(next, then);
-        at = next;
-        next = place(i + 2 * stride);
+        at = place(i + stride, page);
+        fetch(at, then);
+        page = then_page;
+        then_page = page_of(i + 3 * stride);
         int acc[NT][4], odd[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0;
@@ -768,123 +689,427 @@ __global__ void __launch_bounds__(kFewThreads, PICK ? 4 : 5)
     }
 }
 
+// Many query rows a sequence: [128 blocks] x [256 (token, head) columns] on the
+// tensor cores, K = 2 D: min(q, 0) beside lo, max(q, 0) beside hi, whole numbers
+// in f16 (sums below 2^22: exact).  Blocks are the rows, so that a token's heads
+// are columns, and their maximum one thread's, and a warp stores 32 neighbouring
+// scores of a token.  A CTA an SM takes items in turn, a head of up to 256 / pad
+// tokens each: its columns are laid out in shared memory once (a warp owns a
+// token, so its step is a warp's maximum), then it walks over tiles of blocks.
+// Eight warps turn the bounds into f16, 64 dims at a time, ahead of the products,
+// which one thread issues, and eight warps take the maxima of the last tile out
+// of TMEM.  The bounds on their way are asynchronous copies, each lane's its own:
+// loads into registers are waited for by the fence behind every chunk (1,250
+// cycles a chunk, 500 so).  As an operand in TMEM they bound the products at some
+// 150 cycles each, whatever their columns, and leave no second accumulator.
+constexpr int kWideCols = 256, kWideHalf = 128, kWideRows = 128;  // a warp's maxima: half of the columns
+constexpr int kWideRing = 3;
+constexpr int kWideLay = 512, kWideThreads = kWideLay + 32;
+constexpr int kTagSelect = 8;
+
 template <int D>
-__global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __grid_constant__ ScoreArgs a) {
-    constexpr int KS = D / 16;  // k-steps over lo, and over hi
-    extern __shared__ __align__(16) uint4 q_sh[];  // [tile][KS / 2][lane]: two k-steps' fragments
-    __shared__ Pieces<kScoreThreads> pieces;
-    __shared__ int own_sh[kScoreWarps];  // the last block that a query sees
+struct Wide {
+    static constexpr int kChunks = D / 32;              // of 64 dims: lo's, then hi's
+    static constexpr int kB = kChunks * kWideCols * 128, kA = kWideRing * kWideRows * 128;
+    static constexpr int kStage = kWideRows * 2 * D;    // bounds of the next tile
+    static constexpr int kSmem = kB + kA + kStage + 1024 + 64 + 256;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const __grid_constant__ ScoreArgs a) {
+    using C = Wide<D>;
+    extern __shared__ uint8_t wide_sh[];
+    uint8_t* bsh = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(wide_sh) + 1023) & ~(uintptr_t)1023);
+    uint8_t* ash = bsh + C::kB;
+    uint8_t* stage = ash + C::kA;
+    int* most_sh = reinterpret_cast<int*>(stage + C::kStage);  // [warps] last block that a token sees
+    uint64_t* afull = reinterpret_cast<uint64_t*>(most_sh + 16);
+    uint64_t *aempty = afull + kWideRing, *tfull = aempty + kWideRing, *tempty = tfull + 2;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tempty + 2);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 3);
+    __shared__ Pieces<kWideThreads> pieces;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < kWideRing; ++i) {
+            ptx::mbar_init(afull + i, 8);
+            ptx::mbar_init(aempty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(tfull + i, 1);
+            ptx::mbar_init(tempty + i, 8);
+        }
+        abort_flag[0] = 0;
+        abort_flag[1] = kTagSelect;
+        ptx::fence_mbar_init();
+    }
+    if (warp == kWideLay / 32) {
+        ptx::tmem_alloc(tmem_slot, 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
     pdl_enter();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = lane >> 2, t = lane & 3;
-    const int xtile = blockIdx.x % a.xt;
-    const int rest = blockIdx.x / a.xt;
-    const int kvh = rest % a.hkv, slot = rest / a.hkv;
-    // ---- the CTA's tokens: [t0, t0 + n) of sequence b
-    int b = slot, skip = 0;
-    if (!a.direct) {
-        int before = 0;
-        b = -1;
-        for (int c0 = 0; c0 < a.s.num_seqs; c0 += Pieces<kScoreThreads>::kChunk) {
-            const int total = pieces.scan(c0, a.s.num_seqs, [&](int i) {
+
+    bool ok = true;
+    int tile = 0;            // tiles so far
+    Cursor<kWideRing> ring;  // the products' and the bounds' place among the chunks
+    bool lap = false;        // every place has been used
+    const int quarter = warp & 3, part = (warp >> 2) & 1;  // rows, and maxima: half; bounds: lo or hi
+    for (int item = blockIdx.x; item < a.items && __syncthreads_and(ok); item += gridDim.x) {
+        const int share = item % a.xt, rest = item / a.xt;
+        const int kvh = rest % a.hkv, slot = rest / a.hkv;
+        // ---- the CTA's tokens: [t0, t0 + n) of sequence b
+        int b = slot, skip = 0;
+        if (!a.direct) {
+            auto tiles_of_seq = [&](int i) {
                 const Seq q = load_seq(a.s, i, a.num_q);
-                if (!q.ok && blockIdx.x == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
+                if (!q.ok && item == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
                 return q.ok ? (q.nq + a.tokens - 1) / a.tokens : 0;
-            });
-            if (slot < before + total) {
-                const int i = pieces.find(slot - before, min(Pieces<kScoreThreads>::kChunk, a.s.num_seqs - c0));
-                b = c0 + i;
-                skip = (slot - before - pieces.first[i]) * a.tokens;
-                break;
-            }
-            before += total;
-            __syncthreads();
-        }
-        if (b < 0) return;
-    }
-    const Seq sq = load_seq(a.s, b, a.num_q);
-    if (!sq.ok) {
-        if (threadIdx.x == 0 && xtile == 0 && kvh == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
-        return;
-    }
-    const int n = min(a.tokens, sq.nq - skip);
-    if (n <= 0) return;
-    const int t0 = sq.q0 + skip;
-    int most = -1;
-    for (int i = threadIdx.x; i < n; i += kScoreThreads) {
-        const int p = __ldg(a.s.q_pos + t0 + i);
-        const int o = p >= 0 && p < sq.ctx ? p >> a.shift : -1;
-        most = max(most, o);
-    }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) own_sh[warp] = most;
-    __syncthreads();
+            };
+            b = -1;
+            if (a.s.num_seqs <= 32) {  // a warp's sums: no barrier
+                const int mine = lane < a.s.num_seqs ? tiles_of_seq(lane) : 0;
+                int incl = mine;
 #pragma unroll
-    for (int w = 0; w < kScoreWarps; ++w) most = max(most, own_sh[w]);
-    if (xtile * kScoreBlocks > most) return;  // no query sees these blocks
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += y;
+                }
+                const uint32_t hit = __ballot_sync(0xffffffffu, slot >= incl - mine && slot < incl);
+                if (hit) {
+                    b = __ffs(hit) - 1;
+                    skip = (slot - __shfl_sync(0xffffffffu, incl - mine, b)) * a.tokens;
+                }
+            } else {
+                int before = 0;
+                for (int c0 = 0; c0 < a.s.num_seqs; c0 += Pieces<kWideThreads>::kChunk) {
+                    const int total = pieces.scan(c0, a.s.num_seqs, tiles_of_seq);
+                    if (slot < before + total) {
+                        const int i = pieces.find(slot - before, min(Pieces<kWideThreads>::kChunk, a.s.num_seqs - c0));
+                        b = c0 + i;
+                        skip = (slot - before - pieces.first[i]) * a.tokens;
+                        break;
+                    }
+                    before += total;
+                    __syncthreads();
+                }
+            }
+        }
+        Seq sq{0, 0, 0, false};
+        if (b >= 0) sq = load_seq(a.s, b, a.num_q);
+        if (a.direct && !sq.ok && tid == 0 && share == 0 && kvh == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
+        const int n = sq.ok ? min(a.tokens, sq.nq - skip) : 0;
+        const int t0 = sq.q0 + skip;
+        // ---- the bounds' warps: a lane's 16 bytes of a chunk's row, four lanes a row, 16 rows a warp; on
+        // their way beside the queries
+        const bool bounds_warp = warp >= 8 && warp < 16;
+        const int li = lane & 3, row0 = (warp - 8) * 16 + (lane >> 2);
+        // block of row (warp - 8) 16 + lane, by the context (-1 none, -2 lost), from its page
+        auto token_of = [&](int x) { return (int64_t)(x * kWideRows + (warp & 7) * 16 + (lane & 15)) << a.shift; };
+        const int64_t base = n > 0 ? first_row(a.s, b) : 0;
+        auto page_of_tile = [&](int x) {
+            return token_of(x) < sq.ctx ? page_at(a.s, a.page_shift, b, token_of(x)) : 0;
+        };
+        auto place = [&](int x, int page) -> int {
+            if (token_of(x) >= sq.ctx) return -1;
+            const int64_t r = row_in(a.s, a.page_shift, page, base, token_of(x));
+            return r < 0 || (r & ((1 << a.shift) - 1)) ? -2 : (int)(r >> a.shift);
+        };
+        const uint4* bounds = reinterpret_cast<const uint4*>(a.bounds + (int64_t)kvh * (2 * D)) + li;
+        // a lane's copies are its own: nobody else waits for them
+        uint8_t* mine = stage + (warp & 7) * (C::kStage / 8) + lane * 16;
+        auto fetch = [&](int at, int c) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int p = __shfl_sync(0xffffffffu, at, u * 8 + (lane >> 2));
+                copy16(mine + (2 * c + u) * 512, bounds + (int64_t)max(p, 0) * (a.hkv * (D / 8)) + 4 * c, p >= 0);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        int at = -1;
+        int page = 0;  // of the next tile
+        if (bounds_warp && n > 0) {
+            at = place(share, page_of_tile(share));
+            page = page_of_tile(share + a.xt);
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c) fetch(at, c);
+        }
+        // ---- the queries in whole steps: a warp takes a token's columns (of 8 columns' tokens, where they
+        // are several), four columns at a time, 16 dims a lane (D = 64: eight columns)
+        if (tid < kWideLay) {
+            constexpr int kLanes = D / 16, kSet = 32 / kLanes;  // lanes per column, columns per set
+            const int pad = a.pad, sh = 31 - __clz(pad);
+            const int unit = max(pad, 8);       // columns a warp takes at a time
+            // (eight lanes next to each other: four of two columns, so that their stores meet no bank twice)
+            const int c = (lane & 3) | (D == 128 ? lane >> 4 << 2 : 0), lane_col = (lane >> 2) & (kSet - 1);
+            auto query = [&](int col, uint32_t (&w)[8]) {
+                const int tok = col >> sh, head = min(col & (pad - 1), a.group - 1);  // the last again behind it
+                const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(t0 + tok) * a.q_stride +
+                                                                  (int64_t)(kvh * a.group + head) * D + 16 * c);
+                uint4 u = make_uint4(0u, 0u, 0u, 0u), v = u;
+                if (tok < n) u = __ldg(src), v = __ldg(src + 1);
+                w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w, w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
+            };
+            // largest magnitude, as it is; what is not finite leaves by hand
+            auto top_of = [&](const uint32_t (&w)[8]) {
+                uint32_t m = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+                for (int e = 1; e < 8; ++e) m = packed_max<false>(m, w[e] & 0x7FFF7FFFu);
+                const float2 m2 = packed_floats<false>(m);
+                float top = fmaxf(m2.x, m2.y);
+                if (!(m2.x < INFINITY && m2.y < INFINITY)) {
+                    top = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float u = fabsf(__uint_as_float(w[e] << 16)), v = fabsf(__uint_as_float(w[e] & 0xFFFF0000u));
+                        top = fmaxf(top, fmaxf(u < INFINITY ? u : 0.f, v < INFINITY ? v : 0.f));
+                    }
+                }
+                return top;
+            };
+            // over a column's lanes, and over the columns of its token among the set's
+            auto over_token = [&](float top) {
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                if (D == 128) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+#pragma unroll
+                for (int o = 1; o < kSet; o <<= 1) {
+                    const float y = __shfl_xor_sync(0xffffffffu, top, 4 * o);
+                    if (o < pad) top = fmaxf(top, y);
+                }
+                return top;
+            };
+            auto lay = [&](int col, const uint32_t (&w)[8], float top) {
+                float step;
+                const float up = step_up(top, step);
+                // rounded by adding 1.5 2^23 (a value times a power of two is exact); what is not finite by hand
+                uint32_t m = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m = packed_max<false>(m, w[e] & 0x7FFF7FFFu);
+                const float2 m2 = packed_floats<false>(m);
+                const bool plain = m2.x < INFINITY && m2.y < INFINITY;
+                const uint64_t up2 = f32x2(up, up), magic = f32x2(0x1.8p23f, 0x1.8p23f), back = f32x2(-0x1.8p23f, -0x1.8p23f);
+                const __half2 zero = __half2half2(__ushort_as_half(0));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t lo[4], hi[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t q2 = w[4 * h + e];
+                        float u = __uint_as_float(q2 << 16), v = __uint_as_float(q2 & 0xFFFF0000u);
+                        if (plain) {
+                            unpack2(add2(fma2(f32x2(u, v), up2, magic), back), u, v);
+                        } else {
+                            u = whole_steps(u, up);
+                            v = whole_steps(v, up);
+                        }
+                        uint32_t z2 = pack_f16(u, v);
+                        const __half2 l2 = __hmin2(*reinterpret_cast<__half2*>(&z2), zero);
+                        const __half2 h2 = __hmax2(*reinterpret_cast<__half2*>(&z2), zero);
+                        lo[e] = *reinterpret_cast<const uint32_t*>(&l2);
+                        hi[e] = *reinterpret_cast<const uint32_t*>(&h2);
+                    }
+                    uint8_t* dst = bsh + (c / 4) * (kWideCols * 128) + col * 128 + (((c % 4 * 2 + h) ^ (col & 7)) << 4);
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *reinterpret_cast<uint4*>(dst + C::kChunks / 2 * (kWideCols * 128)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                }
+            };
+            if (unit == 8) {  // all of the warp's columns on their way at once
+                constexpr int kSets = kWideCols / (kWideLay / 32) / kSet;
+                uint32_t w[kSets][8];
+                float top[kSets];
+                const int c0 = warp * (kWideCols / (kWideLay / 32)) + lane_col;
+#pragma unroll
+                for (int y = 0; y < kSets; ++y) query(c0 + y * kSet, w[y]);
+#pragma unroll
+                for (int y = 0; y < kSets; ++y) top[y] = over_token(top_of(w[y]));
+#pragma unroll
+                for (int y = 0; y < kSets; ++y)
+                    lay(c0 + y * kSet, w[y], kSet == 4 && pad == 8 ? fmaxf(top[y], top[y ^ 1]) : top[y]);
+            } else {
+                // tokens of 16 columns or more: read twice
+                for (int c0 = warp * unit; c0 < kWideCols; c0 += kWideLay / 32 * unit) {
+                    float top = 0.f;
+                    for (int y = 0; y < unit; y += kSet) {
+                        uint32_t w[8];
+                        query(c0 + y + lane_col, w);
+                        top = fmaxf(top, top_of(w));
+                    }
+                    top = over_token(top);
+                    for (int y = 0; y < unit; y += kSet) {
+                        uint32_t w[8];
+                        query(c0 + y + lane_col, w);
+                        lay(c0 + y + lane_col, w, top);
+                    }
+                }
+            }
+            int most = -1;
+            for (int i = tid; i < n; i += kWideLay) {
+                const int p = __ldg(a.s.q_pos + t0 + i);
+                if (p >= 0 && p < sq.ctx) most = max(most, p >> a.shift);
+            }
+            most = __reduce_max_sync(0xffffffffu, most);
+            if (lane == 0) most_sh[warp] = most;
+            ptx::fence_proxy_async_smem();
+        }
+        __syncthreads();
+        int most = -1;
+#pragma unroll
+        for (int w = 0; w < kWideLay / 32; ++w) most = max(most, most_sh[w]);
+        const int cols = (n * a.pad + 15) & ~15;
+        const int tiles = (most + kWideRows) / kWideRows;  // 0 where no query sees a block
 
-    // ---- this warp's bounds: rows col and col + 8 of its 16 blocks
-    const int blk0 = xtile * kScoreBlocks + warp * 16;
-    int64_t at = -1;  // the lane's block (lanes 0 .. 15)
-    if (blk0 + (lane & 15) <= most) {
-        const int64_t row = row_at(a.s, a.page_shift, b, (int64_t)(blk0 + (lane & 15)) << a.shift);
-        if (row < 0 || (row & ((1 << a.shift) - 1))) {
-            if (kvh == 0 && lane < 16) report(a.d_status, DSA_ERR_BAD_INPUT);
+        if (warp == kWideLay / 32) {
+            // ---- the products
+            if (lane == 0) {
+                const uint32_t idesc = ptx::idesc_f16_m128(cols, false);
+                for (int x = share; x < tiles && ok; x += a.xt, ++tile) {
+                    const int buf = tile & 1;
+                    if (tile >= 2) ok = quick_wait(tempty + buf, ((tile >> 1) - 1) & 1, abort_flag, a.d_status);
+                    for (int c = 0; c < C::kChunks && ok; ++c, ring.move(1)) {
+                        ok = quick_wait(afull + ring.st, ring.ph, abort_flag, a.d_status);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            ptx::mma_ss(tmem + buf * kWideCols,
+                                        ptx::sdesc_sw128(smem_u32(ash) + ring.st * (kWideRows * 128) + k * 32),
+                                        ptx::sdesc_sw128(smem_u32(bsh) + c * (kWideCols * 128) + k * 32), idesc,
+                                        c > 0 || k > 0 ? 1u : 0u);
+                        ptx::mma_commit(aempty + ring.st);
+                        if (c == C::kChunks - 1) ptx::mma_commit(tfull + buf);
+                    }
+                }
+            }
+            __syncwarp();
+        } else if (bounds_warp) {
+            // ---- bounds to f16
+            for (int x = share; x < tiles && ok; x += a.xt) {
+                if (at == -2 && lane < 16 && x * kWideRows + (warp - 8) * 16 + lane <= most && kvh == 0)
+                    report(a.d_status, DSA_ERR_BAD_INPUT);
+                at = place(x + a.xt, page);
+                page = page_of_tile(x + 2 * a.xt);
+#pragma unroll
+                for (int c = 0; c < C::kChunks; ++c) {
+                    if (lap) ok = ok && quick_wait(aempty + ring.st, ring.ph ^ 1u, abort_flag, a.d_status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    // (the oldest group: as many are on their way as a tile has chunks)
+                    asm volatile("cp.async.wait_group %0;" ::"n"(C::kChunks - 1) : "memory");
+                    uint4 z[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) z[u] = *reinterpret_cast<const uint4*>(mine + (2 * c + u) * 512);
+                    fetch(at, c);  // the next tile's, beside this one's products
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int row = row0 + u * 8;
+                        uint32_t f[8];
+                        bytes_to_f16(z[u].x, f[0], f[1]);
+                        bytes_to_f16(z[u].y, f[2], f[3]);
+                        bytes_to_f16(z[u].z, f[4], f[5]);
+                        bytes_to_f16(z[u].w, f[6], f[7]);
+                        uint8_t* dst = ash + ring.st * (kWideRows * 128) + row * 128;
+                        *reinterpret_cast<uint4*>(dst + (((li * 2) ^ (row & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+                        *reinterpret_cast<uint4*>(dst + (((li * 2 + 1) ^ (row & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(afull + ring.st);
+                    ring.move(1);
+                    lap = lap || ring.st == 0;
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");  // the next item's take the same places
         } else {
-            at = (row >> a.shift) * a.hkv + kvh;
+            // ---- maxima: this thread's block, 32 of its half of the columns at a time
+            const int from = part * kWideHalf, to = min(cols, from + kWideHalf);
+            // the step of its block: the page's load two tiles ahead, the step's one
+            auto page_of = [&](int x) {
+                const int blk = x * kWideRows + quarter * 32 + lane;
+                return blk <= most ? page_at(a.s, a.page_shift, b, (int64_t)blk << a.shift) : -1;
+            };
+            auto step_at = [&](int x, int page) {
+                const int blk = x * kWideRows + quarter * 32 + lane;
+                const int64_t r = blk <= most ? row_in(a.s, a.page_shift, page, base, (int64_t)blk << a.shift) : -1;
+                return r >= 0 && (r & ((1 << a.shift) - 1)) == 0 ? __ldg(a.steps + (r >> a.shift) * a.hkv + kvh) : 0.f;
+            };
+            const int64_t next = (int64_t)a.hkv * a.ld;  // to the next token's row
+            float ahead = step_at(share, page_of(share));
+            int far = page_of(share + a.xt);
+            for (int x = share; x < tiles && ok; x += a.xt, ++tile) {
+                const int buf = tile & 1, blk = x * kWideRows + quarter * 32 + lane;
+                const float step = ahead;
+                ahead = step_at(x + a.xt, far);
+                far = page_of(x + 2 * a.xt);
+                ok = __all_sync(0xffffffffu, quick_wait(tfull + buf, (tile >> 1) & 1, abort_flag, a.d_status));
+                if (!ok) break;
+                ptx::tc_fence_after();
+                auto give_back = [&] {  // every column is read
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(tempty + buf);
+                };
+                if (from >= to) give_back();
+                const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kWideCols;
+                const int lim = blk <= most ? n : 0;  // tokens that this thread stores
+                int tok = from / a.pad;
+                float* dst = a.scores + ((int64_t)(t0 + tok) * a.hkv + kvh) * a.ld + blk;
+                float last = -INFINITY;  // pad 64: of the first half of a token's columns
+                auto store = [&](float m) {
+                    // (a step above 2^105 overflows to equal scores)
+                    if (tok < lim) *dst = m * step;
+                    ++tok;
+                    dst += next;
+                };
+                auto put = [&](auto pad, const uint32_t (&v)[32], int c) {
+                    constexpr int P = decltype(pad)::value;
+                    if constexpr (P <= 32) {
+#pragma unroll
+                        for (int y = 0; y < 32; y += P) {
+                            float m = __uint_as_float(v[y]);
+#pragma unroll
+                            for (int e = 1; e + 1 < P; e += 2)
+                                m = fmaxf(fmaxf(m, __uint_as_float(v[y + e])), __uint_as_float(v[y + e + 1]));
+                            if (P > 1) m = fmaxf(m, __uint_as_float(v[y + P - 1]));
+                            store(m);
+                        }
+                    } else {
+                        float m = __uint_as_float(v[0]);
+#pragma unroll
+                        for (int e = 1; e < 32; ++e) m = fmaxf(m, __uint_as_float(v[e]));
+                        if (c & 32) store(fmaxf(m, last));
+                        else last = m;
+                    }
+                };
+                auto walk = [&](auto pad) {
+#pragma unroll 1
+                    for (int c = from; c < to; c += 32) {
+                        uint32_t v[32];
+                        ptx::tmem_ld32_async(src + c, v);
+                        ptx::tmem_wait_ld32(v);
+                        if (c + 32 >= to) give_back();
+                        put(pad, v, c);
+                    }
+                };
+                using std::integral_constant;
+                if (a.pad == 8) walk(integral_constant<int, 8>());
+                else if (a.pad == 4) walk(integral_constant<int, 4>());
+                else if (a.pad == 16) walk(integral_constant<int, 16>());
+                else if (a.pad == 1) walk(integral_constant<int, 1>());
+                else if (a.pad == 2) walk(integral_constant<int, 2>());
+                else if (a.pad == 32) walk(integral_constant<int, 32>());
+                else walk(integral_constant<int, 64>());
+            }
         }
     }
-    const int64_t at0 = __shfl_sync(0xffffffffu, at, col), at1 = __shfl_sync(0xffffffffu, at, col + 8);
-    uint4 raw[2][D / 32];  // [row][lo's chunks, hi's]
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-        raw[0][c] = raw[1][c] = make_uint4(0u, 0u, 0u, 0u);
-        if (at0 >= 0) raw[0][c] = __ldg(reinterpret_cast<const uint4*>(a.bounds + at0 * (2 * D) + c * 64) + t);
-        if (at1 >= 0) raw[1][c] = __ldg(reinterpret_cast<const uint4*>(a.bounds + at1 * (2 * D) + c * 64) + t);
-    }
-    const float step0 = at0 >= 0 ? __ldg(a.steps + at0) : 0.f, step1 = at1 >= 0 ? __ldg(a.steps + at1) : 0.f;
-
-    // ---- the queries in whole steps, as fragments
-    const int tpt = 8 / a.pad, groups = (n + tpt - 1) / tpt;
-    quantise<D>(a, t0, n, kvh, warp, kScoreWarps, q_sh);
+    ptx::tc_fence_before();
     __syncthreads();
-    if (blk0 > most) return;
-
-    uint32_t lo[KS][4], hi[KS][4];
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const uint32_t w[4] = {raw[r][c].x, raw[r][c].y, raw[r][c].z, raw[r][c].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                auto& f = c < D / 64 ? lo : hi;
-                const int k = (c % (D / 64)) * 4 + e;
-                bytes_to_f16(w[e], f[k][r], f[k][2 + r]);
-            }
-        }
-    for (int gu = 0; gu < groups; ++gu) {
-        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        for (int j = 0; j < a.npt; ++j) {
-            float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-            const uint4* src = q_sh + (gu * a.npt + j) * (KS / 2) * 32 + lane;
-#pragma unroll
-            for (int k = 0; k < KS; k += 2) {
-                const uint4 z = src[(k / 2) * 32];
-                mma_f16(x, lo[k], below0(z.x), below0(z.y));
-                mma_f16(y, hi[k], above0(z.x), above0(z.y));
-                mma_f16(x, lo[k + 1], below0(z.z), below0(z.w));
-                mma_f16(y, hi[k + 1], above0(z.z), above0(z.w));
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], x[e] + y[e]);
-        }
-        store_scores(a, m, t0, n, kvh, gu, blk0 + col, step0, step1);
-    }
+    ptx::tc_fence_after();
+    if (warp == kWideLay / 32) ptx::tmem_dealloc(tmem, 512);
 }
 
-// ---------------------------------------------------------------------------
-// the best blocks of a row
 // A warp per row of up to 32 K blocks: the keys stay in registers, and the cut
 // is found by halving their range (counts by a warp's sums, no barrier; it ends
 // when exactly `want` lie above).
@@ -1172,21 +1397,31 @@ cudaError_t launch_select(const dsa_gqa_shape& sh, const void* q, const void* bo
                     : by_tiles(integral_constant<int, 128>(), std::false_type());
         if (e != cudaSuccess || own) return e;
     } else {
-        a.tokens = std::min(s.max_q_per_seq, kScoreTiles / a.npt * tpt);
+        a.pad = 1;
+        while (a.pad < a.group) a.pad *= 2;
+        a.tokens = std::min(s.max_q_per_seq, kWideCols / a.pad);
         a.direct = s.max_q_per_seq <= a.tokens;
-        a.xt = (a.ld + kScoreBlocks - 1) / kScoreBlocks;
         const int64_t slots = a.direct ? s.num_seqs : std::min<int64_t>(num_q, num_q / a.tokens + s.num_seqs);
-        const int64_t grid = slots * a.hkv * a.xt;
-        if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-        const size_t smem = (size_t)((a.tokens + tpt - 1) / tpt) * a.npt * (sh.head_dim / 32) * 512;
+        const int64_t items = slots * a.hkv, most = (a.ld + kWideRows - 1) / kWideRows;
+        // items that share a head's tiles each lay its columns out, which takes some two tiles' time: the
+        // fewest rounds times what one takes (512 heads of eight tiles: one each)
+        a.xt = 1;
+        int64_t best = INT64_MAX;
+        for (int64_t x = 1; x <= std::min<int64_t>(most, 64); ++x) {
+            const int64_t t = (items * x + kPlanSms - 1) / kPlanSms * (2 + (most + x - 1) / x);
+            if (t < best) best = t, a.xt = (int32_t)x;
+        }
+        if (items * a.xt > INT32_MAX) return cudaErrorInvalidConfiguration;
+        a.items = (int32_t)(items * a.xt);
+        const unsigned grid = (unsigned)std::min<int64_t>(a.items, num_sms());
         auto go = [&](auto d) {
-            auto kern = block_score_kernel<decltype(d)::value>;
+            constexpr int D = decltype(d)::value;
+            auto kern = block_score_wide_kernel<D>;
             static OncePerDevice once;
-            const cudaError_t r = once.run([&] {
-                return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                            kScoreTiles * (decltype(d)::value / 32) * 512);
-            });
-            return r != cudaSuccess ? r : launch_pdl(kern, dim3((unsigned)grid), dim3(kScoreThreads), smem, stream, 1, a);
+            const cudaError_t r = once.run(
+                [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide<D>::kSmem); });
+            if (r != cudaSuccess) return r;
+            return launch_pdl(kern, dim3(grid), dim3(kWideThreads), Wide<D>::kSmem, stream, 1, a);
         };
         e = sh.head_dim == 64 ? go(std::integral_constant<int, 64>()) : go(std::integral_constant<int, 128>());
     }

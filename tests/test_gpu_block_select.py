@@ -232,6 +232,17 @@ STEPS = {
     "prompt": ([300], [300], 8, 2, 128, 16, dict(page=64, nsel=6, first=1, local=2, sb=64)),
     "ragged prompts": ([150, 20, 400, 7], [150, 3, 61, 0], 8, 2, 64, 32, dict(page=64, nsel=4, sb=64)),
     "many blocks": ([60000], [1], 8, 1, 64, 16, dict(kv="bf16", page=64, nsel=64, first=1, local=2)),
+    "prompt of group 20": ([260], [200], 20, 1, 128, 32, dict(page=64, nsel=4, sb=64)),
+    "prompt of group 33": ([260], [130], 33, 1, 64, 16, dict(kv="bf16", page=64, nsel=4)),
+    "ungrouped prompt": ([1500], [700], 3, 3, 64, 16, dict(kv="bf16", page=64, nsel=7, first=1)),
+    "prompt of many tiles": ([9000], [37], 8, 1, 128, 16, dict(kv="bf16", page=64, nsel=40, first=1, local=2)),
+    "many sequences": ([900 - 5 * i for i in range(160)], [1 + i % 3 for i in range(160)], 8, 2, 128, 16,
+                       dict(kv="bf16", page=64, nsel=9, first=1, local=2)),
+    "many sequences of drafts": ([300 + 3 * i for i in range(80)], [4] * 80, 20, 4, 64, 16,
+                                 dict(kv="bf16", page=16, nsel=7)),
+    "many rows": ([1500], [1400], 8, 4, 64, 16, dict(kv="bf16", page=64, nsel=9, first=1, local=2)),
+    "many rows, more blocks": ([8000], [1300], 4, 4, 64, 16, dict(kv="bf16", page=64, nsel=33)),
+    "many rows, most blocks": ([16000], [1250], 4, 4, 64, 16, dict(kv="bf16", page=64, nsel=200, first=2, local=3)),
     "a list of one": ([400, 16], [2, 1], 8, 2, 64, 16, dict(page=16, nsel=1)),
     "nothing but sure ones": ([400], [2], 8, 2, 64, 16, dict(page=16, nsel=5, first=2, local=3)),
     "a list of 200": ([9000], [2], 8, 1, 64, 16, dict(page=16, nsel=200)),
@@ -318,6 +329,19 @@ def test_equal_scores_go_to_the_smaller_block():
         s.steps[:] = 1.0
         s.device()
         s.run_select().check_select()
+
+
+@pytest.mark.parametrize("nsel", [6, 100, 300])
+@pytest.mark.parametrize("new, levels", [(1300, 1), (1300, 2), (1300, 40), (40, 2)])
+def test_equal_scores_in_many_rows(new, levels, nsel):
+    """The cut inside ties for rows that a warp chooses, with few keys left and with many."""
+    s = Step([12000], [new], 4, 4, 64, 16, kv="bf16", page=64, nsel=nsel, first=1, local=2, seed=levels)
+    s.bounds[:] = 0
+    g = torch.Generator().manual_seed(levels)
+    s.bounds[:, :, 1, :] = torch.randint(0, levels, s.steps.shape, generator=g).to(torch.int8)[..., None]
+    s.steps[:] = 1.0
+    s.device()
+    s.run_select().check_select(_few(s, 10))
 
 
 def test_steps_far_apart():
