@@ -13,7 +13,7 @@ cudaError_t launch_attend(const dsa_gqa_shape& sh, const void* q, const void* k,
     each.num_seqs = num_q;
     each.max_q_per_seq = 1;
     each.max_ctx = nsel * block;
-    const Plan p = make_plan(sh, each);
+    const Plan p = make_plan(sh, each, sh.kv_dtype == DSA_BF16 ? 2 : 3);
     return launch_all<true>(p, sh, q, k, v, k_scale, v_scale, s, num_q, sm_scale, out, lse, workspace, d_status,
                             stream, std::min(block, p.tile), blocks, len, nsel, block);
 }

@@ -60,13 +60,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -3e38f;  // the reference of a row that has seen no key (its sum is 0)
 
 // NT: 8-row tiles of query rows; KS: computing warps, 16 keys of a tile each
-template <int D, bool FP8, int NT, int KS>
+template <int D, bool FP8, int NT, int KS, bool LISTED>
 struct Cfg {
     static constexpr int kRows = 8 * NT;     // query rows per chunk
     static constexpr int kTile = 16 * KS;    // keys per tile
     static constexpr bool kSplitRegs = KS == 8;  // three warpgroups, the registers given to the computing two
     static constexpr int kThreads = kSplitRegs ? 384 : 32 * (KS + 1);
-    static constexpr int kOcc = KS == 8 ? 1 : 2;  // CTAs per SM
+    static constexpr int kOcc = KS == 8 ? 1 : LISTED && FP8 ? 3 : 2;  // CTAs per SM
     static constexpr int kHeadBytes = D * (FP8 ? 1 : 2);
     static constexpr int kHalf = kTile * kHeadBytes;  // K or V of a stage
     static constexpr int kStage = 2 * kHalf;
@@ -80,7 +80,7 @@ struct Cfg {
     static constexpr int kQBytes = kQShared ? (D / 16) * NT * 32 * 8 : 0;
     static constexpr int kMisc = 256 + kRows * 24;
     static constexpr int kFixed = kScratch + kMl + kQBytes + kMisc;
-    static constexpr int kBudget = (kOcc == 2 ? 115712 : 232448) - kFixed;
+    static constexpr int kBudget = (kOcc == 3 ? 76800 : kOcc == 2 ? 115712 : 232448) - kFixed;
     static constexpr int kFit = kBudget / (kStage + kScaleBytes);
     static constexpr int kStages = kFit < 8 ? kFit : 8;
     static constexpr int kSmem = kStages * (kStage + kScaleBytes) + kFixed;
@@ -420,10 +420,10 @@ struct Walk {
 };
 
 template <int D, bool FP8, int NT, int KS, bool LISTED>
-__global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT, KS>::kOcc)
+__global__ void __launch_bounds__(Cfg<D, FP8, NT, KS, LISTED>::kThreads, Cfg<D, FP8, NT, KS, LISTED>::kOcc)
     gqa_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ Args a) {
-    using C = Cfg<D, FP8, NT, KS>;
+    using C = Cfg<D, FP8, NT, KS, LISTED>;
     constexpr int HB = C::kHeadBytes, kTile = C::kTile;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem;
@@ -1170,11 +1170,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS>::kThreads, Cfg<D, FP8, NT,
 
 // Joins the partials of one cut (lane, sequence), a CTA per row: its four
 // warps take every fourth part.  Weights 2^(m_i - M), in the parts' order.
-constexpr int kJoinParts = 2 * kPlanSms + 8;  // parts of one sequence: at most the CTAs of a lane column
+template <int OCC>
+constexpr int kJoinParts = OCC * kPlanSms + 8;  // parts of one sequence: at most the CTAs of a lane column
 
-template <int D>
+template <int D, int OCC>
 __global__ void __launch_bounds__(128) gqa_join_kernel(const __grid_constant__ Args a, int rows) {
-    __shared__ float weight[kJoinParts];
+    __shared__ float weight[kJoinParts<OCC>];
     __shared__ float red[4][D];
     __shared__ float sums[4], tops[4];
     pdl_enter();
@@ -1207,9 +1208,9 @@ __global__ void __launch_bounds__(128) gqa_join_kernel(const __grid_constant__ A
             }
         }
     };
-    float2 v[(kJoinParts + 127) / 128];
+    float2 v[(kJoinParts<OCC> + 127) / 128];
 #pragma unroll
-    for (int k = 0; k < (kJoinParts + 127) / 128; ++k) {
+    for (int k = 0; k < (kJoinParts<OCC> + 127) / 128; ++k) {
         const int i = k * 128 + threadIdx.x;
         v[k] = i < n ? a.part_ml[slot(i) * rows + r] : make_float2(kNone, 0.f);
     }
@@ -1218,7 +1219,7 @@ __global__ void __launch_bounds__(128) gqa_join_kernel(const __grid_constant__ A
     float top = kNone;
     bool skip = false;
 #pragma unroll
-    for (int k = 0; k < (kJoinParts + 127) / 128; ++k) {
+    for (int k = 0; k < (kJoinParts<OCC> + 127) / 128; ++k) {
         skip = skip || v[k].y == -1.f;
         top = fmaxf(top, v[k].x);
     }
@@ -1229,7 +1230,7 @@ __global__ void __launch_bounds__(128) gqa_join_kernel(const __grid_constant__ A
     top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     float sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < (kJoinParts + 127) / 128; ++k) {
+    for (int k = 0; k < (kJoinParts<OCC> + 127) / 128; ++k) {
         const int i = k * 128 + threadIdx.x;
         const float w = fast_exp2(v[k].x - top);
         if (i < n) weight[i] = w;
@@ -1280,7 +1281,8 @@ struct Plan {
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s) {
+// occ: CTAs per SM of up to 8 rows
+Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s, int occ) {
     Plan p;
     const int group = sh.num_heads / sh.num_kv_heads;
     const int64_t rows = (int64_t)s.max_q_per_seq * group;
@@ -1291,7 +1293,7 @@ Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s) {
     p.tile = p.nt == 1 ? 64 : 128;
     p.chunks = (int)((rows + p.rows - 1) / p.rows);
     p.lanes = sh.num_kv_heads * p.chunks;
-    const int n = kPlanSms * (p.nt == 1 ? 2 : 1);
+    const int n = kPlanSms * (p.nt == 1 ? occ : 1);
     const int64_t tiles = std::max<int64_t>(1, ((int64_t)s.max_ctx + p.tile - 1) / p.tile);
     // Clusters where all (lane, sequence)s fit at once and an estimate from the
     // longest sequence says that they are faster: a CTA takes at least tile_ns a
@@ -1343,7 +1345,7 @@ Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s) {
 
 template <int D, bool FP8, int NT, int KS, bool LISTED>
 cudaError_t launch_one(const CUtensorMap& km, const CUtensorMap& vm, const Args& a, int grid, cudaStream_t stream) {
-    using C = Cfg<D, FP8, NT, KS>;
+    using C = Cfg<D, FP8, NT, KS, LISTED>;
     auto kern = gqa_decode_kernel<D, FP8, NT, KS, LISTED>;
     static OncePerDevice once;
     const cudaError_t e = once.run([&] {
@@ -1408,7 +1410,8 @@ cudaError_t launch_all(const Plan& p, const dsa_gqa_shape& sh, const void* q, co
         e = fp8 ? by_rows(integral_constant<int, 128>(), std::true_type())
                 : by_rows(integral_constant<int, 128>(), std::false_type());
     if (e != cudaSuccess || p.cluster || p.parts == 1) return e;
-    auto join = sh.head_dim == 64 ? gqa_join_kernel<64> : gqa_join_kernel<128>;
+    constexpr int OCC = LISTED ? 3 : 2;
+    auto join = sh.head_dim == 64 ? gqa_join_kernel<64, OCC> : gqa_join_kernel<128, OCC>;
     return launch_pdl(join, dim3(p.grid, p.rows), dim3(128), 0, stream, 1, a, p.rows);
 }
 
