@@ -184,6 +184,7 @@ size_t select_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s, int num_q, i
 cudaError_t launch_select(const dsa_gqa_shape& sh, const void* q, const void* bounds, const float* steps,
                           const dsa_seqs& s, int num_q, int block, int nsel, int first, int local, int32_t* blocks,
                           int32_t* len, void* workspace, int32_t* d_status, cudaStream_t stream);
+size_t attend_workspace(const dsa_gqa_shape& sh);
 cudaError_t launch_attend(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v, const float* k_scale,
                           const float* v_scale, const dsa_seqs& s, int num_q, const int32_t* blocks,
                           const int32_t* len, int block, int nsel, float sm_scale, void* out, float* lse,
@@ -650,7 +651,7 @@ static void check_nsel(Check& c, int32_t nsel) {
 }
 
 static size_t block_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s, int32_t num_q, int32_t block) {
-    return std::max(gqa::decode_workspace(sh), gqa::select_workspace(sh, s, num_q, block));
+    return std::max(gqa::attend_workspace(sh), gqa::select_workspace(sh, s, num_q, block));
 }
 
 static void check_block_workspace(Check& c, const dsa_gqa_shape& sh, const dsa_seqs* s, int32_t num_q, int32_t block,

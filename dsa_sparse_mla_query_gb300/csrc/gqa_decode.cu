@@ -5,19 +5,17 @@
 namespace dsa {
 namespace gqa {
 
-// For any call: two partials of 8, 16 or 32 rows per CTA, of two CTAs per SM with 8.
-size_t decode_workspace(const dsa_gqa_shape& sh) {
-    const size_t rows = (size_t)2 * kPlanSms * 32;
-    return up256(rows * sh.head_dim * 4) + up256(rows * 8) + up256((size_t)2 * kPlanSms * 16);
-}
+constexpr int kDecodeOcc = 2;
+
+size_t decode_workspace(const dsa_gqa_shape& sh) { return plan_workspace(sh, kDecodeOcc); }
 
 cudaError_t launch_decode(const dsa_gqa_shape& sh, const void* q, const void* k, const void* v, const float* k_scale,
                           const float* v_scale, const dsa_seqs& s, int num_q, float sm_scale, void* out, float* lse,
                           void* workspace, int32_t* d_status, cudaStream_t stream) {
-    const Plan p = make_plan(sh, s, 2);
+    const Plan p = make_plan(sh, s, kDecodeOcc);
     const int box = s.page_table ? std::min(s.page_size, p.tile) : p.tile;
     return launch_all<false>(p, sh, q, k, v, k_scale, v_scale, s, num_q, sm_scale, out, lse, workspace, d_status,
-                             stream, box, nullptr, nullptr, 0, 0);
+                             stream, kDecodeOcc, box, nullptr, nullptr, 0, 0);
 }
 
 }  // namespace gqa

@@ -55,6 +55,7 @@ namespace {
 
 constexpr int kTagDecode = 6;
 constexpr int kMaxCluster = 16;
+constexpr int kListedOcc = 3;  // CTAs per SM of up to 8 rows over listed blocks, e4m3
 constexpr float kLazy = 8.f;  // a row's reference moves when its maximum passes it by 2^8
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -3e38f;  // the reference of a row that has seen no key (its sum is 0)
@@ -66,7 +67,7 @@ struct Cfg {
     static constexpr int kTile = 16 * KS;    // keys per tile
     static constexpr bool kSplitRegs = KS == 8;  // three warpgroups, the registers given to the computing two
     static constexpr int kThreads = kSplitRegs ? 384 : 32 * (KS + 1);
-    static constexpr int kOcc = KS == 8 ? 1 : LISTED && FP8 ? 3 : 2;  // CTAs per SM
+    static constexpr int kOcc = KS == 8 ? 1 : LISTED && FP8 ? kListedOcc : 2;  // CTAs per SM
     static constexpr int kHeadBytes = D * (FP8 ? 1 : 2);
     static constexpr int kHalf = kTile * kHeadBytes;  // K or V of a stage
     static constexpr int kStage = 2 * kHalf;
@@ -1357,13 +1358,21 @@ cudaError_t launch_one(const CUtensorMap& km, const CUtensorMap& vm, const Args&
 }
 
 
+// Workspace of any call with `occ` CTAs per SM of up to 8 rows, one with more: two partial results and
+// one note a CTA.
+size_t plan_workspace(const dsa_gqa_shape& sh, int occ) {
+    const size_t rows = std::max<size_t>((size_t)2 * kPlanSms * 32, (size_t)2 * kPlanSms * occ * 8);
+    return up256(rows * sh.head_dim * 4) + up256(rows * 8) + up256((size_t)kPlanSms * occ * 16);
+}
+
 // The maps, the arguments and the launches, with `box` rows per TMA box.
 template <bool LISTED>
 cudaError_t launch_all(const Plan& p, const dsa_gqa_shape& sh, const void* q, const void* k, const void* v,
                        const float* k_scale, const float* v_scale, const dsa_seqs& s, int num_q, float sm_scale,
-                       void* out, float* lse, void* workspace, int32_t* d_status, cudaStream_t stream, int box,
+                       void* out, float* lse, void* workspace, int32_t* d_status, cudaStream_t stream, int occ, int box,
                        const int32_t* blocks, const int32_t* len, int nsel, int block) {
     const bool fp8 = sh.kv_dtype != DSA_BF16;
+    if (p.o_bytes + p.ml_bytes + p.desc_bytes > plan_workspace(sh, occ)) return cudaErrorInvalidValue;
     CUtensorMap km, vm;
     cudaError_t e = cache_map(&km, fp8, k, sh.num_kv_heads, sh.head_dim, sh.k_stride, s.num_rows, box, box == p.tile);
     if (e == cudaSuccess)
@@ -1410,7 +1419,7 @@ cudaError_t launch_all(const Plan& p, const dsa_gqa_shape& sh, const void* q, co
         e = fp8 ? by_rows(integral_constant<int, 128>(), std::true_type())
                 : by_rows(integral_constant<int, 128>(), std::false_type());
     if (e != cudaSuccess || p.cluster || p.parts == 1) return e;
-    constexpr int OCC = LISTED ? 3 : 2;
+    constexpr int OCC = LISTED ? kListedOcc : 2;
     auto join = sh.head_dim == 64 ? gqa_join_kernel<64, OCC> : gqa_join_kernel<128, OCC>;
     return launch_pdl(join, dim3(p.grid, p.rows), dim3(128), 0, stream, 1, a, p.rows);
 }
