@@ -705,41 +705,59 @@ struct KvBlockInsert {
     int32_t units;  // 16 heads of a token's queries
 };
 
-// The cosines and sines of a token as its row's lanes take them, 16 bytes (two
-// frequencies) at a time: [j][lane][2], lanes side by side, so that a warp's
-// loads meet no bank twice (frequencies in their own order did, four times: 630
-// us for 49,000 tokens of 64/8 heads, 420 so).
-template <bool HALVES>
+// A lane's 8 dims of a row, as two chunks of four: with DSA_ROPE_HALVES a rotated
+// chunk and its partners, so that a pair's dims are one lane's (no shuffles, and
+// every value is unpacked once); eight in a row otherwise.  Its four cosines and
+// sines lie in the token's table as {c, c, s, s} of two frequencies, the lanes'
+// 16 bytes side by side, so that a warp's loads meet no bank twice.
 struct Turn {
-    static constexpr int kUnits = HALVES ? 4 : 2;  // a lane's 16-byte units
-    float4 c[kUnits];
-    __device__ __forceinline__ void load(const float2* token, int lanes, int l) {
+    uint64_t c[2], s[2], ns[2];  // of two frequencies each
+    __device__ __forceinline__ void load(const float4* token, int lanes, int l) {
 #pragma unroll
-        for (int j = 0; j < kUnits; ++j) c[j] = reinterpret_cast<const float4*>(token)[j * lanes + l];
-    }
-    static __device__ __forceinline__ int place(int f, int lanes) {
-        const int l = f / (2 * kUnits), j = f % (2 * kUnits) / 2;
-        return (j * lanes + l) * 2 + (f & 1);
-    }
-    // a row's 8 dims: `o` holds the partner dims (HALVES)
-    __device__ __forceinline__ void turn8(float (&v)[8], const uint4& x, const uint4& o, bool upper) const {
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, os[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float a = bf16_lo(xs[e]), b = bf16_hi(xs[e]);
-            if (HALVES) {
-                const float4 f = c[e];
-                v[2 * e] = fmaf(bf16_lo(os[e]), upper ? f.y : -f.y, a * f.x);
-                v[2 * e + 1] = fmaf(bf16_hi(os[e]), upper ? f.w : -f.w, b * f.z);
-            } else {
-                const float4 f = c[e / 2];
-                const float co = e & 1 ? f.z : f.x, si = e & 1 ? f.w : f.y;
-                v[2 * e] = fmaf(b, -si, a * co);
-                v[2 * e + 1] = fmaf(a, si, b * co);
-            }
+        for (int j = 0; j < 2; ++j) {
+            const float4 f = token[j * lanes + l];
+            c[j] = f32x2(f.x, f.y);
+            s[j] = f32x2(f.z, f.w);
+            ns[j] = f32x2(-f.z, -f.w);
         }
     }
+    // place of frequency f's cosine among a token's floats; its sine two behind
+    static __device__ __forceinline__ int place(int f, int lanes) {
+        return ((f % 4 / 2) * lanes + f / 4) * 4 + (f & 1);
+    }
 };
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float2 floats(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+// words {chunk a: x, y; chunk b: z, w} -> values in the chunks' order
+template <bool HALVES>
+__device__ __forceinline__ void turn8(float (&v)[8], const uint4& x, const Turn& t) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        // two pairs: HALVES (a, b) of dims 2j, 2j + 1; PAIRS words 2j, 2j + 1
+        const uint32_t p = HALVES ? (j ? x.y : x.x) : (j ? x.z : x.x), q = HALVES ? (j ? x.w : x.z) : (j ? x.w : x.y);
+        const uint64_t x0 = HALVES ? f32x2(bf16_lo(p), bf16_hi(p)) : f32x2(bf16_lo(p), bf16_lo(q));
+        const uint64_t x1 = HALVES ? f32x2(bf16_lo(q), bf16_hi(q)) : f32x2(bf16_hi(p), bf16_hi(q));
+        const float2 y0 = floats(fma2(x1, t.ns[j], mul2(x0, t.c[j]))), y1 = floats(fma2(x0, t.s[j], mul2(x1, t.c[j])));
+        if (HALVES) {
+            v[2 * j] = y0.x, v[2 * j + 1] = y0.y, v[4 + 2 * j] = y1.x, v[4 + 2 * j + 1] = y1.y;
+        } else {
+            v[4 * j] = y0.x, v[4 * j + 1] = y1.x, v[4 * j + 2] = y0.y, v[4 * j + 3] = y1.y;
+        }
+    }
+}
 
 template <int D, bool HALVES>
 __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const __grid_constant__ KvBlockInsert a) {
@@ -747,7 +765,7 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
     constexpr int kGroup = 32 / kLanes;  // rows per warp access
     constexpr int kAcc = 16 / kGroup;    // accesses of a warp's 16 rows
     constexpr int kChunk = Pieces<kBlkThreads>::kChunk;
-    extern __shared__ __align__(16) float2 table[];  // [token][rot / 2]: cos, sin
+    extern __shared__ __align__(16) float table[];  // [token][rot]: Turn's
     __shared__ Pieces<kBlkThreads> pieces;
     __shared__ int4 seq_sh[kChunk];  // first row, tokens, first position, context
     __shared__ float top[2][kBlkWarps];
@@ -757,21 +775,14 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
     const int half = a.rot / 2;
     const int li = lane % kLanes, sub = lane / kLanes;
     const bool turned = 8 * li < a.rot;
-    const int step = a.rot / 16;  // HALVES: lanes between a pair's dims
-    const bool upper = turned && HALVES && li >= step;
-    const int from = !turned || !HALVES ? lane : upper ? lane - step : lane + step;
-    const int tl = HALVES ? step : 2 * step;         // lanes of the table
-    const int ti = upper ? li - step : li;           // this lane's place among them
+    const int tl = a.rot / 8;  // lanes of the table
+    // the lane's chunks of four dims: of keys and queries, and of values
+    const int ca = HALVES && turned ? 4 * li : 8 * li, cb = HALVES && turned ? 4 * li + half : 8 * li + 4;
     const bool lead = blockIdx.y == 0;
-    auto partner = [&](const uint4& x) {
-        uint4 o = x;
-        if (HALVES && a.rot) {
-            o.x = __shfl_sync(0xffffffffu, o.x, from);
-            o.y = __shfl_sync(0xffffffffu, o.y, from);
-            o.z = __shfl_sync(0xffffffffu, o.z, from);
-            o.w = __shfl_sync(0xffffffffu, o.w, from);
-        }
-        return o;
+    auto row8 = [&](const __nv_bfloat16* row, bool split) {
+        if (!HALVES || !split) return __ldcs(reinterpret_cast<const uint4*>(row + 8 * li));
+        const uint2 x = __ldcs(reinterpret_cast<const uint2*>(row + ca)), y = __ldcs(reinterpret_cast<const uint2*>(row + cb));
+        return make_uint4(x.x, x.y, y.x, y.y);
     };
     int64_t before = 0;
     int turn = 0;
@@ -812,7 +823,7 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
                         const int tok = part * 16 + u * kGroup + sub;
                         raw[u] = make_uint4(0u, 0u, 0u, 0u);
                         if (task < 2 * a.hkv && tok < n)
-                            raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + (int64_t)(t0 + tok) * in + h * D + 8 * li));
+                            raw[u] = row8(src + (int64_t)(t0 + tok) * in + h * D, task < a.hkv);
                     }
                 } else {
                     const int y = (r - rounds) * kBlkWarps + warp, tok = y / max(1, a.units), h0 = (y - tok * a.units) * 16;
@@ -821,8 +832,7 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
                         const int h = h0 + u * kGroup + sub;
                         raw[u] = make_uint4(0u, 0u, 0u, 0u);
                         if (y < q_units && h < a.hq)
-                            raw[u] = __ldcs(reinterpret_cast<const uint4*>(a.q + (int64_t)(t0 + tok) * a.q_in + h * D +
-                                                                           8 * li));
+                            raw[u] = row8(a.q + (int64_t)(t0 + tok) * a.q_in + h * D, true);
                     }
                 }
             };
@@ -844,7 +854,9 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
                 const int tok = y / half, f = y - tok * half;
                 float c, sn;
                 rope_cs(pos0 + tok, __ldg(a.inv_freq + f), c, sn);
-                table[tok * half + Turn<HALVES>::place(f, tl)] = make_float2(c, sn);
+                float* at = table + tok * a.rot + Turn::place(f, tl);
+                at[0] = c;
+                at[2] = sn;
             }
             if (!__syncthreads_or(some)) continue;
 
@@ -853,22 +865,27 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
                 if (r >= rounds) {
                     const int y = (r - rounds) * kBlkWarps + warp, tok = y / a.units, h0 = (y - tok * a.units) * 16;
                     if (y >= q_units || !good[tok]) continue;
-                    Turn<HALVES> t;
-                    if (turned) t.load(table + tok * half, tl, ti);
-                    __nv_bfloat16* dst = a.q_out + (int64_t)(t0 + tok) * a.q_stride + 8 * li;
+                    Turn t;
+                    if (turned) t.load(reinterpret_cast<const float4*>(table + tok * a.rot), tl, li);
+                    __nv_bfloat16* dst = a.q_out + (int64_t)(t0 + tok) * a.q_stride;
 #pragma unroll
                     for (int u = 0; u < kAcc; ++u) {
                         if (h0 + u * kGroup >= a.hq) break;  // the same for the warp
-                        const uint4 o = partner(raw[u]);
                         uint4 z = raw[u];
                         if (turned) {
                             float v[8];
-                            t.turn8(v, raw[u], o, upper);
+                            turn8<HALVES>(v, raw[u], t);
                             z = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                            pack_bf16x2(v[6], v[7]));
                         }
                         const int h = h0 + u * kGroup + sub;
-                        if (h < a.hq) *reinterpret_cast<uint4*>(dst + h * D) = z;
+                        if (h >= a.hq) continue;
+                        if (HALVES) {
+                            *reinterpret_cast<uint2*>(dst + h * D + ca) = make_uint2(z.x, z.y);
+                            *reinterpret_cast<uint2*>(dst + h * D + cb) = make_uint2(z.z, z.w);
+                        } else {
+                            *reinterpret_cast<uint4*>(dst + h * D + 8 * li) = z;
+                        }
                     }
                     continue;
                 }
@@ -884,15 +901,11 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
                 // the values are turned twice, for their maximum and for their codes: a table read
                 // and a few products less dear than the registers (three CTAs an SM for two)
                 auto values = [&](int u, float (&v)[8]) {
-                    if (!is_k) {  // the same for the warp
-                        unpack_bf16x8(raw[u], v);
-                        return;
-                    }
-                    const uint4 o = partner(raw[u]);
-                    if (turned) {
-                        Turn<HALVES> t;
-                        t.load(table + min(part * 16 + u * kGroup + sub, n - 1) * half, tl, ti);
-                        t.turn8(v, raw[u], o, upper);
+                    if (is_k && turned) {
+                        Turn t;
+                        t.load(reinterpret_cast<const float4*>(table + min(part * 16 + u * kGroup + sub, n - 1) * a.rot),
+                               tl, li);
+                        turn8<HALVES>(v, raw[u], t);
                     } else {
                         unpack_bf16x8(raw[u], v);
                     }
@@ -904,12 +917,16 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
                     float v[8];
                     values(u, v);
                     const int tok = part * 16 + u * kGroup + sub;
-                    const bool in = tok < n && good[min(tok, n - 1)];
+                    // what is not finite has no say (fmaxf leaves NaN out; infinities are rare)
+                    float y = fabsf(v[0]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float y = fabsf(v[e]);
-                        m = fmaxf(m, in && y < INFINITY ? y : 0.f);  // what is not finite has no say
+                    for (int e = 1; e < 8; ++e) y = fmaxf(y, fabsf(v[e]));
+                    if (!(y < INFINITY)) {
+                        y = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y = fmaxf(y, fabsf(v[e]) < INFINITY ? fabsf(v[e]) : 0.f);
                     }
+                    m = fmaxf(m, tok < n && good[min(tok, n - 1)] ? y : 0.f);
                 }
                 m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
                 if (per > 1) {  // (the same for the CTA)
@@ -951,10 +968,17 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
                     float v[8];
                     values(u, v);
                     const int tok = part * 16 + u * kGroup + sub;
-                    if (tok < n && good[tok])
-                        *reinterpret_cast<uint2*>(cache + (row0 + old + tok) * stride + h * D + 8 * li) =
-                            make_uint2(pack_e4m3x4(v[0] * rs, v[1] * rs, v[2] * rs, v[3] * rs),
-                                       pack_e4m3x4(v[4] * rs, v[5] * rs, v[6] * rs, v[7] * rs));
+                    if (tok < n && good[tok]) {
+                        uint8_t* dst = cache + (row0 + old + tok) * stride + h * D;
+                        const uint32_t x = pack_e4m3x4(v[0] * rs, v[1] * rs, v[2] * rs, v[3] * rs);
+                        const uint32_t y = pack_e4m3x4(v[4] * rs, v[5] * rs, v[6] * rs, v[7] * rs);
+                        if (HALVES && is_k) {
+                            *reinterpret_cast<uint32_t*>(dst + ca) = x;
+                            *reinterpret_cast<uint32_t*>(dst + cb) = y;
+                        } else {
+                            *reinterpret_cast<uint2*>(dst + 8 * li) = make_uint2(x, y);
+                        }
+                    }
                 }
                 if (part == 0 && lane == 0 && scale != held) scales[at_scale] = scale;
             }
@@ -1004,7 +1028,7 @@ cudaError_t launch_kv_block_insert(const dsa_gqa_shape& sh, const void* k, int64
     const int64_t work = (2 * sh.num_kv_heads * per + 7) / 8 + (longest * a.units + 7) / 8;
     const unsigned grid = (unsigned)std::min<int64_t>(blocks, 152 * 8);
     const unsigned share = (unsigned)std::max<int64_t>(1, std::min<int64_t>(work, 152 * 8 / grid));
-    const size_t smem = (size_t)sh.scale_block * (a.rot / 2) * sizeof(float2);  // up to 64 KB
+    const size_t smem = (size_t)sh.scale_block * a.rot * sizeof(float);  // up to 64 KB
     auto go = [&](auto d, auto h) {
         auto kern = kv_block_insert_kernel<decltype(d)::value, decltype(h)::value>;
         static OncePerDevice once;

@@ -75,6 +75,23 @@ struct Pieces {
     }
 };
 
+// phys_row with the page size as a power of two (a 64-bit division takes as long as a tile's products),
+// and in two steps, so that the page's load can be under way while other work is done: its result must
+// not be touched before, not even widened.
+__device__ __forceinline__ int page_at(const dsa_seqs& s, int page_shift, int b, int64_t j) {
+    const int64_t p = j >> page_shift;
+    return s.page_table && p < s.max_pages ? __ldg(s.page_table + (int64_t)b * s.max_pages + p) : -1;
+}
+__device__ __forceinline__ int64_t first_row(const dsa_seqs& s, int b) { return s.page_table ? 0 : __ldg(s.seq_base + b); }
+__device__ __forceinline__ int64_t row_in(const dsa_seqs& s, int page_shift, int page, int64_t first, int64_t j) {
+    const int64_t row = s.page_table ? ((int64_t)page << page_shift) + (j & ((1 << page_shift) - 1)) : first + j;
+    return (page >= 0 || !s.page_table) && row >= 0 && row < s.num_rows ? row : -1;
+}
+__device__ __forceinline__ int64_t row_at(const dsa_seqs& s, int page_shift, int b, int64_t j) {
+    return row_in(s, page_shift, page_at(s, page_shift, b, j), first_row(s, b), j);
+}
+inline int page_shift_of(const dsa_seqs& s) { return s.page_table ? 31 - __builtin_clz((unsigned)s.page_size) : 0; }
+
 // Sequence b's new tokens: rows [q0, q0 + nq) at positions p0, p0 + 1, ..;
 // nq = 0 where there is nothing to do (p0 = -1: refused tokens).
 struct NewTokens {
@@ -100,23 +117,6 @@ __device__ __forceinline__ NewTokens new_tokens(const dsa_seqs& s, int b, int nu
     }
     return r;
 }
-
-// phys_row with the page size as a power of two (a 64-bit division takes as long as a tile's products),
-// and in two steps, so that the page's load can be under way while other work is done: its result must
-// not be touched before, not even widened.
-__device__ __forceinline__ int page_at(const dsa_seqs& s, int page_shift, int b, int64_t j) {
-    const int64_t p = j >> page_shift;
-    return s.page_table && p < s.max_pages ? __ldg(s.page_table + (int64_t)b * s.max_pages + p) : -1;
-}
-__device__ __forceinline__ int64_t first_row(const dsa_seqs& s, int b) { return s.page_table ? 0 : __ldg(s.seq_base + b); }
-__device__ __forceinline__ int64_t row_in(const dsa_seqs& s, int page_shift, int page, int64_t first, int64_t j) {
-    const int64_t row = s.page_table ? ((int64_t)page << page_shift) + (j & ((1 << page_shift) - 1)) : first + j;
-    return (page >= 0 || !s.page_table) && row >= 0 && row < s.num_rows ? row : -1;
-}
-__device__ __forceinline__ int64_t row_at(const dsa_seqs& s, int page_shift, int b, int64_t j) {
-    return row_in(s, page_shift, page_at(s, page_shift, b, j), first_row(s, b), j);
-}
-inline int page_shift_of(const dsa_seqs& s) { return s.page_table ? 31 - __builtin_clz((unsigned)s.page_size) : 0; }
 
 // the blocks of 2^shift tokens that they lie in
 __device__ __forceinline__ int blocks_touched(const NewTokens& n, int shift) {
