@@ -12,10 +12,10 @@
 // - block_bounds_kernel: minimum and maximum over the keys of the blocks that new
 //   tokens touch, four warps per block and head, keys read once.
 // - block_score_few_kernel: few tokens a sequence read 2 D bytes a block once:
-//   HBM.  The sums on the warp-level 8-bit matrix instruction, 16 blocks by 8
-//   query rows, straight from global memory (the order of the dims within a
-//   k-step is the same for both operands and free otherwise, so a thread's 16
-//   bytes make whole fragments).
+//   HBM.  The sums on the warp-level matrix instruction, 16 blocks by 8 query
+//   rows, straight from global memory (the order of the dims within a k-step is
+//   the same for both operands and free otherwise, so a thread's 16 bytes make
+//   whole fragments).
 // - block_score_wide_kernel: a prompt's tokens, a product of [blocks] x [tokens
 //   heads] on tcgen05.
 // - block_pick_kernel, block_pick_row_kernel: the nsel best of a row by a
@@ -434,12 +434,11 @@ struct ScoreArgs {
     int32_t direct;  // slot = sequence
 };
 
-__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                       uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&x)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
 }
 // four signed bytes as f16: a byte + 128 under the exponent of 1024, less 1152
 __device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -463,19 +462,21 @@ __device__ __forceinline__ float whole_steps(float v, float up) {
 
 // A few query rows a sequence (up to 4 tiles): a CTA of four warps takes a
 // (sequence, key head), or a share of its blocks.  Every warp keeps two tiles of
-// 16 blocks on their way, and the pages of two more; bounds are fragments of the
-// 8-bit matrix instruction as they lie in memory, so that a tile of 4 KB takes
-// eight products and few other instructions.  Where (sequence, key head)s alone
-// fill the GPU (PICK) their scores stay in shared memory, and the CTA chooses
-// among them: no second launch.
+// 16 blocks on their way, and the pages of two more; a thread's 16 bytes of a
+// block become fragments of whole k-steps as they meet the products (f16: 8
+// cycles a product; as 8-bit integers, which need no conversion, half as many
+// products took some 64 each: 64 x 512 blocks of 8 heads 30 us as they did, 3 x
+// 8,192 39.4 and 30.2 so).  Where
+// (sequence, key head)s alone fill the GPU (PICK) their scores stay in shared
+// memory, and the CTA chooses among them: no second launch.
 constexpr int kFewThreads = 128, kFewWarps = kFewThreads / 32, kFewTiles = 4;
-constexpr int kFewScores = 8192;  // of a CTA's tokens, in shared memory
+constexpr int kFewScores = 6144;  // of a CTA's tokens, in shared memory
 
 template <int D, int NT, bool PICK>
 __global__ void __launch_bounds__(kFewThreads, PICK ? 4 : 5)
     block_score_few_kernel(const __grid_constant__ ScoreArgs a, const __grid_constant__ PickArgs k) {
     extern __shared__ uint32_t keys[];  // PICK: [token][ld]
-    __shared__ __align__(16) uint32_t q_sh[NT * (D / 32) * 32 * 4];  // [tile][lo, hi][D / 64][lane][4]
+    __shared__ __align__(16) uint4 q_sh[NT * (D / 32) * 64];  // [tile][lo, hi][D / 64][2][lane]: two k-steps each
     __shared__ uint32_t top_sh[8 * kFewTiles];                    // largest of a token's queries
     __shared__ int pos_sh[8 * kFewTiles];
     __shared__ PickShared<kFewThreads> pick_sh;
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(kFewThreads, PICK ? 4 : 5)
     if (tid < n) pos_sh[tid] = __ldg(a.s.q_pos + sq.q0 + tid);
     // ---- the queries in whole steps: a thread's 16 dims of a row, twice for more than two tiles
     constexpr int kSets = (NT * 8 * (D / 16) + kFewThreads - 1) / kFewThreads;
-    const int tpt = 8 / a.pad;
+    const int tpt = 8 >> (31 - __clz(a.pad));
     uint4 raw[kSets][2];
 #pragma unroll
     for (int y = 0; y < kSets; ++y) {
@@ -576,26 +577,36 @@ __global__ void __launch_bounds__(kFewThreads, PICK ? 4 : 5)
         const float up = step_up(top, step);
         const uint32_t w[8] = {raw[y][0].x, raw[y][0].y, raw[y][0].z, raw[y][0].w,
                                raw[y][1].x, raw[y][1].y, raw[y][1].z, raw[y][1].w};
-        uint32_t lo[4], hi[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            lo[e] = hi[e] = 0;
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                const uint32_t u = w[2 * e + z / 2];
-                const int v = (int)whole_steps(__uint_as_float(z & 1 ? u & 0xFFFF0000u : u << 16), up);
-                lo[e] |= (uint32_t)(min(v, 0) & 0xFF) << (8 * z);
-                hi[e] |= (uint32_t)max(v, 0) << (8 * z);
-            }
-        }
         // dims 16 c ..: chunk c / 4, thread c % 4 of the row's four
-        uint4* dst = reinterpret_cast<uint4*>(q_sh) + ((row >> 3) * (D / 32) + c / 4) * 32 + (row & 7) * 4 + c % 4;
-        dst[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        dst[(D / 64) * 32] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        uint4* dst = q_sh + ((row >> 3) * (D / 32) + c / 4) * 64 + (row & 7) * 4 + c % 4;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t lo[4], hi[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t z = w[4 * h + e];
+                const float u = whole_steps(__uint_as_float(z << 16), up), v = whole_steps(__uint_as_float(z & 0xFFFF0000u), up);
+                lo[e] = pack_f16(fminf(u, 0.f), fminf(v, 0.f));
+                hi[e] = pack_f16(fmaxf(u, 0.f), fmaxf(v, 0.f));
+            }
+            dst[32 * h] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            dst[(D / 64) * 64 + 32 * h] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        }
     }
     __syncthreads();
     const int groups = (n + tpt - 1) / tpt;
-    const uint4* qf = reinterpret_cast<const uint4*>(q_sh) + lane;
+    const uint4* qf = q_sh + lane;
+    // (divisions take longer than a tile's products: out of the loop)
+    const int sh = 31 - __clz(a.pad);
+    bool leads[NT];   // a token's first tile
+    int group_of[NT], put[2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        group_of[j] = j / a.npt;
+        leads[j] = group_of[j] * a.npt == j && group_of[j] < groups;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) put[e] = (2 * t + e) & (a.pad - 1) ? -1 : (2 * t + e) >> sh;  // token of the group
     bool lost = false;
     for (; i * 16 <= most; i += stride) {
         lost = lost || (at == -2 && i * 16 + (lane & 15) <= most);
@@ -604,17 +615,25 @@ __global__ void __launch_bounds__(kFewThreads, PICK ? 4 : 5)
         fetch(at, then);
         page = then_page;
         then_page = page_of(i + 3 * stride);
-        int acc[NT][4], odd[4] = {0, 0, 0, 0};
+        float acc[NT][4], odd[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0;
+        for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {  // lo's chunks, hi's
             const uint4 r0 = cur.x[0][c], r1 = cur.x[1][c];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const uint4 z = qf[(j * (D / 32) + c) * 32];
-                mma_s8(acc[j], r0.x, r1.x, r0.y, r1.y, z.x, z.y);
-                mma_s8(NT == 1 ? odd : acc[j], r0.z, r1.z, r0.w, r1.w, z.z, z.w);
+            for (int h = 0; h < 2; ++h) {
+                uint32_t f[2][4];
+                bytes_to_f16(h ? r0.z : r0.x, f[0][0], f[0][2]);
+                bytes_to_f16(h ? r1.z : r1.x, f[0][1], f[0][3]);
+                bytes_to_f16(h ? r0.w : r0.y, f[1][0], f[1][2]);
+                bytes_to_f16(h ? r1.w : r1.y, f[1][1], f[1][3]);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const uint4 z = qf[(j * (D / 32) + c) * 64 + 32 * h];
+                    mma_f16(acc[j], f[0], z.x, z.y);
+                    mma_f16(NT == 1 ? odd : acc[j], f[1], z.z, z.w);
+                }
             }
         }
         if (NT == 1)
@@ -624,24 +643,23 @@ __global__ void __launch_bounds__(kFewThreads, PICK ? 4 : 5)
         const int blk = i * 16 + col;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            if (j % a.npt) continue;
-            int m[4] = {acc[j][0], acc[j][1], acc[j][2], acc[j][3]};
+            if (!leads[j]) continue;
+            float m[4] = {acc[j][0], acc[j][1], acc[j][2], acc[j][3]};
 #pragma unroll
             for (int z = j + 1; z < NT; ++z)
                 if (z < j + a.npt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) m[e] = max(m[e], acc[z][e]);
-            if (a.pad >= 2) m[0] = m[1] = max(m[0], m[1]), m[2] = m[3] = max(m[2], m[3]);
+                    for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], acc[z][e]);
+            if (a.pad >= 2) m[0] = m[1] = fmaxf(m[0], m[1]), m[2] = m[3] = fmaxf(m[2], m[3]);
             for (int o = 2; o < a.pad; o <<= 1)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) m[e] = max(m[e], __shfl_xor_sync(0xffffffffu, m[e], o / 2));
-            if (j / a.npt >= groups) continue;
+                for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], o / 2));
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int c = 2 * t + e, tok = j / a.npt * tpt + c / a.pad;
-                if (c % a.pad || tok >= n) continue;
+                const int tok = group_of[j] * tpt + put[e];
+                if (put[e] < 0 || tok >= n) continue;
                 // (a step above 2^105 overflows to equal scores)
-                const float s0 = (float)m[e] * cur.step[0], s1 = (float)m[2 + e] * cur.step[1];
+                const float s0 = m[e] * cur.step[0], s1 = m[2 + e] * cur.step[1];
                 if (PICK) {
                     if (blk <= most) keys[tok * a.ld + blk] = score_code(s0);
                     if (blk + 8 <= most) keys[tok * a.ld + blk + 8] = score_code(s1);
@@ -1270,6 +1288,7 @@ __global__ void __launch_bounds__(T) block_pick_kernel(const __grid_constant__ P
     if (choose) {
         uint32_t least = 0xFFFFFFFFu, best = 0u;
         const float* row = a.scores + (int64_t)blockIdx.x * a.ld;
+#pragma unroll 8
         for (int i = a.first + tid; i < hi; i += T) {
             const uint32_t k = score_code(row[i]);
             key[i] = k;
@@ -1426,7 +1445,7 @@ cudaError_t launch_select(const dsa_gqa_shape& sh, const void* q, const void* bo
         e = sh.head_dim == 64 ? go(std::integral_constant<int, 64>()) : go(std::integral_constant<int, 128>());
     }
     if (e != cudaSuccess) return e;
-    // a row's keys by 128 threads (many rows at once), or 512 where they are many
+    // a row's keys by 128 threads (many rows at once), or 1,024 where they are many
     auto go = [&](auto threads) {
         constexpr int T = decltype(threads)::value;
         static OncePerDevice once;
@@ -1445,7 +1464,7 @@ cudaError_t launch_select(const dsa_gqa_shape& sh, const void* q, const void* bo
         if (a.ld <= 512) return rows(block_pick_row_kernel<16>);
         if (a.ld <= 1024) return rows(block_pick_row_kernel<32>);
     }
-    return a.ld <= 4096 ? go(std::integral_constant<int, 128>()) : go(std::integral_constant<int, 512>());
+    return a.ld <= 2048 ? go(std::integral_constant<int, 128>()) : go(std::integral_constant<int, 1024>());
 }
 
 }  // namespace gqa
