@@ -88,8 +88,8 @@ __device__ __forceinline__ uint32_t high_code(float v, float up) {
 
 // Four warps take a block and head, its rows among them: minima and maxima as
 // they lie in the cache (pairs of f16 or bf16: exact), converted at the end.
-// Rows with scales of their own, and blocks with values that are not finite,
-// take the long way in fp32, by one warp.
+// Rows with scales of their own, negative scales and blocks with values that are
+// not finite take the long way in fp32, by one warp.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kBoundThreads) block_bounds_kernel(const __grid_constant__ BoundArgs a) {
     constexpr int V = FP8 ? 16 : 8;    // dims per lane
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kBoundThreads) block_bounds_kernel(const __gri
                 if (part == 0 && live) {
                     // D / 64 pairs of dims a lane
                     float top = 0.f;
+                    odd = !(scale >= 0.f);  // (turned around by a negative one)
                     float2 l[D / 64], g[D / 64];
 #pragma unroll
                     for (int y = 0; y < D / 64; ++y) {
@@ -465,8 +466,7 @@ __device__ __forceinline__ float whole_steps(float v, float up) {
 // 16 blocks on their way, and the pages of two more; a thread's 16 bytes of a
 // block become fragments of whole k-steps as they meet the products (f16: 8
 // cycles a product; as 8-bit integers, which need no conversion, half as many
-// products took some 64 each: 64 x 512 blocks of 8 heads 30 us as they did, 3 x
-// 8,192 39.4 and 30.2 so).  Where
+// products took some 64 each: 3 x 8,192 blocks of 8 heads 39 us, 30 so).  Where
 // (sequence, key head)s alone fill the GPU (PICK) their scores stay in shared
 // memory, and the CTA chooses among them: no second launch.
 constexpr int kFewThreads = 128, kFewWarps = kFewThreads / 32, kFewTiles = 4;
@@ -1390,8 +1390,8 @@ cudaError_t launch_select(const dsa_gqa_shape& sh, const void* q, const void* bo
         a.tokens = s.max_q_per_seq;
         a.direct = 1;
         const int64_t pairs = (int64_t)s.num_seqs * a.hkv, most = (a.ld + 16 * kFewWarps - 1) / (16 * kFewWarps);
-        // (sequence, key head)s that make two CTAs an SM choose for themselves; 64 sequences of 512
-        // blocks and 8 heads @@
+        // (sequence, key head)s that make two CTAs an SM choose for themselves (64 sequences of 512 blocks
+        // and 8 heads: 33 us with the bounds, 52 with a second kernel)
         const bool own = pairs >= 2 * kPlanSms && (int64_t)s.max_q_per_seq * a.ld <= kFewScores;
         a.xt = own ? 1 : (int32_t)std::max<int64_t>(1, std::min<int64_t>(most, kPlanSms * 5 / pairs));
         const int64_t grid = pairs * a.xt;

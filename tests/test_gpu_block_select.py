@@ -309,6 +309,34 @@ def test_bounds_at_borders_and_of_values_that_are_not_finite():
     s.run_bounds().check_bounds()
 
 
+@pytest.mark.parametrize("kv", ["row", "block"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_bounds_of_codes_and_scales_of_any_kind(kv, d):
+    """NaN codes, and scales that are negative, zero or not finite."""
+    s = Step([16 * 8], [16 * 8], 3, 3, d, 16, kv=kv, page=16, seed=1)
+    rows = s.rows_of(0)
+    s.k[rows[5], 0, 3], s.k[rows[16 + 7], 1, d - 1] = 0x7F, 0xFF
+    at = rows if kv == "row" else rows // 16
+    for i, x in enumerate([-0.25, 0.0, math.inf, -math.inf, math.nan, 2.0 ** -126]):
+        s.ks[at[16 * (i + 2) + (3 if kv == "row" else 0)], 0] = x
+    s.kr = s.ks if kv == "row" else s.ks.repeat_interleave(16, 0)
+    s.device()
+    s.run_bounds().check_bounds()
+
+
+@pytest.mark.parametrize("tokens", [1, 700])
+def test_nothing_but_padding(tokens):
+    """Rows behind the last sequence alone: nothing is written."""
+    s = Step([400, 50], [tokens, 1], 8, 2, 64, 16, page=16, extra_q=3)
+    s.blocks.fill_(0)
+    s.len.fill_(16)
+    s.seqs.q_start = _i32([0, 0, 0])
+    s.run_bounds().run_select().run_attend()
+    assert s.stat() == 0
+    assert bool((s.out == 7).all()) and bool((s.lse == 7).all()) and bool((s.blocks == 0).all())
+    assert torch.equal(s.dbounds.cpu(), s.bounds)
+
+
 def test_queries_that_are_not_finite_or_zero():
     s = Step([500] * 4, [1] * 4, 8, 2, 64, 16, kv="bf16", page=16, nsel=5, seed=2)
     s.q[0] = 0
