@@ -17,7 +17,7 @@ cudaError_t launch_attend(const dsa_gqa_shape& sh, const void* q, const void* k,
     each.num_seqs = num_q;
     each.max_q_per_seq = 1;
     each.max_ctx = nsel * block;
-    const Plan p = make_plan(sh, each, listed_occ(sh));
+    const Plan p = make_plan(sh, each, listed_occ(sh), true);
     return launch_all<true>(p, sh, q, k, v, k_scale, v_scale, s, num_q, sm_scale, out, lse, workspace, d_status,
                             stream, listed_occ(sh), std::min(block, p.tile), blocks, len, nsel, block);
 }

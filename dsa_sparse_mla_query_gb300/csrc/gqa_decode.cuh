@@ -105,6 +105,7 @@ struct Args {
     int32_t scale_shift;  // e4m3: 2^scale_shift rows share a scale
     const int32_t *blocks, *len;  // LISTED: [num_q][hkv][nsel] blocks of 2^block_shift keys, [num_q][hkv] keys
     int32_t nsel, block_shift;
+    int32_t rounds;  // LISTED: whole (lane, token)s in turn, no deal
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -263,6 +264,13 @@ struct Walk {
         }
         const int c = blockIdx.x / a.hl;
         const int units = a.lanes / a.hl;
+        if (LISTED && a.rounds) {
+            // (lane, token)s x = blockIdx.x, + gridDim.x, ..: `left` of them
+            const int64_t all = (int64_t)a.lanes * B;
+            left = all > blockIdx.x ? (all - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+            r0 = blockIdx.x;
+            return;
+        }
         if (LISTED) {
             const int64_t each = ((((int64_t)a.nsel << a.block_shift) + TILE - 1) / TILE) + START;
             deal.set(B * each * units, a.parts);
@@ -366,6 +374,26 @@ struct Walk {
     }
     // the next piece, without its limit: `pos` is the lane's share of that
     __device__ __forceinline__ bool begin(const Args& a, Piece& p, int& pos) {
+        if (LISTED && a.rounds) {
+            if (left == 0) return false;
+            --left;
+            u = (int)((uint32_t)r0 / (uint32_t)seqs);  // below 2^31: (num_q, key head)s are below 2^30
+            b = (int)((uint32_t)r0 - (uint32_t)u * (uint32_t)seqs);
+            r0 += gridDim.x;
+            p.lane = u;
+            p.b = b;
+            p.q = seq(a);
+            p.front = p.back = false;
+            p.i0 = 0;
+            p.i1 = tiles_of<TILE>(p.q);
+            p.row0 = p.lane / a.hkv * ROWS;
+            p.tok0 = 0;
+            p.ntok = 1;
+            pos = -1;
+            if ((threadIdx.x & 31) == 0) pos = __ldg(a.len + (int64_t)p.b * a.hkv + p.lane % a.hkv) - 1;
+            p.base = 0;
+            return true;
+        }
         while (left > 0) {
             if (b == seqs) {
                 b = 0;
@@ -1276,14 +1304,14 @@ __global__ void __launch_bounds__(128) gqa_join_kernel(const __grid_constant__ A
 // ---------------------------------------------------------------------------
 // host side
 struct Plan {
-    int nt, tile, rows, chunks, lanes, hl, parts, grid, cluster;
+    int nt, tile, rows, chunks, lanes, hl, parts, grid, cluster, rounds;
     size_t o_bytes, ml_bytes, desc_bytes;
 };
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // occ: CTAs per SM of up to 8 rows
-Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s, int occ) {
+Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s, int occ, bool listed) {
     Plan p;
     const int group = sh.num_heads / sh.num_kv_heads;
     const int64_t rows = (int64_t)s.max_q_per_seq * group;
@@ -1306,8 +1334,19 @@ Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s, int occ) {
     // 92.7 and 100; four tokens over e4m3, 2 x 4,000 22.8 and 24.4, 19 x 4,000 50.5
     // and 57.5; level at 4 x 65,536, 165 and 164; and where the estimate chooses the
     // other: 3 x 30,000 70.8 and 66.7, 3 x up to 9,000 with 32/8 heads of 64 18.7 and 15.1.
-    p.cluster = 0;
+    p.cluster = p.rounds = 0;
     const int64_t segs = (int64_t)p.lanes * s.num_seqs;
+    // Listed blocks, many tokens: whole lists in turn, head by head, so that the CTAs read neighbouring
+    // tokens' blocks of one head at a time (they are mostly the same, and a head's cache fits the L2), and
+    // nothing is cut.  From eight lists a CTA on the last round costs less.
+    if (listed && segs >= 8 * n) {
+        p.rounds = 1;
+        p.grid = n;
+        p.hl = p.parts = 1;
+        p.o_bytes = p.ml_bytes = 0;
+        p.desc_bytes = up256((size_t)p.grid * 16);
+        return p;
+    }
     if (segs <= n) {
         int c = 1;
         auto room = [&](int size) { return size >= 16 ? n / 2 : size >= 8 ? n * 5 / 8 : n * 7 / 8; };
@@ -1399,6 +1438,7 @@ cudaError_t launch_all(const Plan& p, const dsa_gqa_shape& sh, const void* q, co
     a.hl = p.hl;
     a.parts = p.parts;
     a.cluster = p.cluster;
+    a.rounds = p.rounds;
     a.scale_shift = scale_shift(sh);
     a.blocks = blocks;
     a.len = len;

@@ -452,9 +452,9 @@ def test_any_lists(name):
 
 
 @pytest.mark.parametrize("kv", KINDS)
-@pytest.mark.parametrize("tokens, nsel", [(1, 32), (3, 40), (40, 32), (700, 8)])
+@pytest.mark.parametrize("tokens, nsel", [(1, 32), (3, 40), (40, 32), (700, 8), (2000, 3)])
 def test_splits_and_joins(kv, tokens, nsel):
-    """Clusters, cut lists and the joining kernel, by the number of tokens."""
+    """Clusters, cut lists and the joining kernel, whole lists in turn, by the number of tokens."""
     s = Step([4000] * tokens if tokens < 100 else [4000], [1] * tokens if tokens < 100 else [tokens], 8, 2, 128, 64,
              kv=kv, page=64, nsel=nsel, seed=tokens, extra_q=1)
     _random_lists(s, seed=tokens, empty=False)
