@@ -304,10 +304,11 @@ struct PickShared {
     int2 sums[W];
     int found[2], count;
 };
-// an order-preserving code of a score, 1 at least (NaN, of a step that was never written: last)
+// an order-preserving code of a score, 1 at least and infinity's at most (NaN, of a step that was never
+// written: last)
 __device__ __forceinline__ uint32_t score_code(float s) {
-    const uint32_t u = __float_as_uint(s == 0.f ? 0.f : s);
-    return s != s ? 1u : u & 0x80000000u ? ~u : u | 0x80000000u;
+    const uint32_t u = __float_as_uint(s + 0.f);  // (-0 as 0)
+    return s != s ? 1u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 // Of the n blocks of a row those in [0, first) and [hi, n), and the `want` with
@@ -1146,16 +1147,18 @@ __global__ void __launch_bounds__(32 * kRowsPerCta) block_pick_row_kernel(const 
     const bool choose = n > a.nsel;
     const int hi = n - a.local;
     int want = a.nsel - a.first - a.local;
+    const int i0 = lane * K;  // the lane's blocks: neighbours, so that the lanes' order is theirs
     uint32_t key[K];
     if (choose) {
         const float* row = a.scores + r * a.ld;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int i = k * 32 + lane;
-            key[k] = 0;  // below any score's code
-            if (i >= a.first && i < hi) {
-                key[k] = score_code(row[i]);
-            }
+        for (int k = 0; k < K; k += 4) {
+            const int i = i0 + k;
+            const float4 f = i < a.ld ? *reinterpret_cast<const float4*>(row + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)  // 0: none, below any score's code
+                key[k + e] = (uint32_t)(i + e - a.first) < (uint32_t)(hi - a.first) ? score_code(v[e]) : 0u;
         }
     }
     const int b = warp_seq_of(a.s.q_start, a.s.num_seqs, t);
@@ -1177,6 +1180,15 @@ __global__ void __launch_bounds__(32 * kRowsPerCta) block_pick_row_kernel(const 
     uint32_t cut = 0xFFFFFFFFu;
     int ties = 0;
     const uint32_t under = (1u << lane) - 1;
+    auto before = [&](int x) {  // sum over the lanes before
+        int incl = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        return incl - x;
+    };
     if (want > 0) {
         uint32_t least = 0xFFFFFFFFu, best = 0u;
 #pragma unroll
@@ -1199,17 +1211,16 @@ __global__ void __launch_bounds__(32 * kRowsPerCta) block_pick_row_kernel(const 
             // those, in order, with their blocks: the rest of the search is theirs alone
             uint32_t* codes = kept[threadIdx.x >> 5][0];
             uint32_t* names = kept[threadIdx.x >> 5][1];
-            int at = 0;
+            uint32_t mine = 0;  // the lane's keys that stay
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const bool in = key[k] >= least;
-                const uint32_t y = __ballot_sync(0xffffffffu, in);
-                if (in) {
-                    codes[at + __popc(y & under)] = key[k];
-                    names[at + __popc(y & under)] = k * 32 + lane;
+            for (int k = 0; k < K; ++k) mine |= key[k] >= least ? 1u << k : 0u;
+            int at = before(__popc(mine));
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if ((mine >> k) & 1) {
+                    codes[at] = key[k];
+                    names[at++] = i0 + k;
                 }
-                at += __popc(y);
-            }
             __syncwarp();
             uint32_t c4[kKept / 32];
 #pragma unroll
@@ -1250,19 +1261,24 @@ __global__ void __launch_bounds__(32 * kRowsPerCta) block_pick_row_kernel(const 
             ties = want - __reduce_add_sync(0xffffffffu, c);
         }
     }
-    int at = 0, eq = 0;
+    int sure = 0, same = 0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        if (k * 32 >= n) break;
-        const int i = k * 32 + lane;
+        const int i = i0 + k;
+        const bool fix = i < n && (i < a.first || i >= hi);
+        sure += fix || key[k] > cut;
+        same += !fix && key[k] == cut && ties > 0;
+    }
+    int at = before(sure), eq = before(same);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int i = i0 + k;
         const bool fix = i < n && (i < a.first || i >= hi);
         const bool yes = fix || key[k] > cut, tie = !fix && key[k] == cut && ties > 0;
-        const uint32_t y = __ballot_sync(0xffffffffu, yes), e = __ballot_sync(0xffffffffu, tie);
-        const int rank = eq + __popc(e & under);
-        const int place = at + __popc(y & under) + min(rank, ties);
-        if ((yes || (tie && rank < ties)) && place < a.nsel) out[place] = i;
-        at += __popc(y);
-        eq += __popc(e);
+        const int place = at + min(eq, ties);
+        if ((yes || (tie && eq < ties)) && place < a.nsel) out[place] = i;
+        at += yes;
+        eq += tie;
     }
 }
 
@@ -1317,7 +1333,8 @@ __global__ void __launch_bounds__(T) block_pick_kernel(const __grid_constant__ P
 
 }  // namespace
 
-size_t select_ld(const dsa_seqs& s, int block) { return ((size_t)s.max_ctx + block - 1) / block; }
+// scores of a row: whole 16 bytes
+size_t select_ld(const dsa_seqs& s, int block) { return (((size_t)s.max_ctx + block - 1) / block + 3) & ~(size_t)3; }
 
 size_t select_workspace(const dsa_gqa_shape& sh, const dsa_seqs& s, int num_q, int block) {
     return (size_t)num_q * sh.num_kv_heads * select_ld(s, block) * 4;

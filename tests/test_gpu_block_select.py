@@ -372,6 +372,24 @@ def test_equal_scores_in_many_rows(new, levels, nsel):
     s.run_select().check_select(_few(s, 10))
 
 
+def test_steps_that_were_never_written():
+    """NaN scores come last, whatever chooses (few rows, many rows, long rows): the lists are whole."""
+    for ctx, new, nsel in ((16 * 300, 1, 30), (16 * 300, 1300, 30), (16 * 300, 1300, 290), (16 * 5000, 1, 30)):
+        s = Step([ctx], [new], 4, 4, 64, 16, kv="bf16", page=16, nsel=nsel, first=1, seed=5)
+        s.steps[::3] = math.nan
+        s.device()
+        s.run_select()
+        assert s.stat() == 0
+        got = s.blocks[s.nq - 1].cpu()
+        rows = s.rows_of(0)
+        bad = {i for i in range(ctx // 16) if int(rows[16 * i]) // 16 % 3 == 0}
+        for g in range(4):
+            sel = got[g].tolist()
+            assert sel == sorted(set(sel)) and len(sel) == nsel and sel[0] == 0 and sel[-1] == ctx // 16 - 1
+            want = max(0, nsel - (ctx // 16 - len(bad)) - 2)
+            assert len(bad & set(sel)) <= want + 2
+
+
 def test_steps_far_apart():
     s = Step([16 * 300], [1], 8, 2, 64, 16, kv="bf16", page=16, nsel=30, seed=5)
     s.steps[:] = torch.exp2(torch.randint(-100, 80, s.steps.shape, generator=torch.Generator().manual_seed(1)).float())
