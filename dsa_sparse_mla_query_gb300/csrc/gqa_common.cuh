@@ -50,9 +50,10 @@ __device__ __forceinline__ int warp_seq_of(const int32_t* q_start, int B, int t)
 // apart: dimensions (128 bytes of a head's row, rows, the row's 128-byte
 // pieces, heads), so that a box of R rows lands in shared memory as one
 // [R][128 B] swizzled block per piece (all of a row's pieces, or one).  A
-// head row of 64 bytes (e4m3, d = 64) is one piece of 64 bytes.
+// head row of 64 bytes (e4m3, d = 64) is one piece of 64 bytes.  A miss brings
+// 256 bytes, the next head's row with a shorter one, or, `alone`, the row's own.
 inline cudaError_t cache_map(CUtensorMap* m, bool bytes, const void* base, int heads, int d, int64_t stride,
-                             int64_t rows, int box_rows, bool all_pieces) {
+                             int64_t rows, int box_rows, bool all_pieces, bool alone = false) {
     auto enc = tmap_encoder();
     if (!enc) return cudaErrorNotSupported;
     const uint64_t el = bytes ? 1 : 2;
@@ -65,7 +66,10 @@ inline cudaError_t cache_map(CUtensorMap* m, bool bytes, const void* base, int h
     const CUresult r = enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                            const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            piece == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                           !alone || d * el >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                           : d * el == 128         ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                   : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
