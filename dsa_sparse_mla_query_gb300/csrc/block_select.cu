@@ -21,6 +21,13 @@
 // - block_pick_kernel, block_pick_row_kernel: the nsel best of a row by a
 //   histogram over the keys' range (order-preserving codes) or, many rows, by
 //   halving it, a warp a row.
+//
+// Measured, 64/8 heads of 128, blocks of 64 keys, with the host's calls and the new
+// keys' bounds: 64 tokens over 32,768 keys 28.7 us, 3 over 524,288 30 us (HBM 36%
+// busy while the bounds are read: two or three rounds of loads a warp, then the
+// choice); 2,048 of 65,536 143 us: the scores 98 (the CTA's own warps turn the
+// bounds into f16 operands: the tensor cores are 35% busy), the choice 37 (69% of
+// the issue slots), the bounds 6.
 #include <algorithm>
 
 #include "gqa_common.cuh"

@@ -686,6 +686,11 @@ cudaError_t launch_kv_insert(const dsa_gqa_shape& sh, const void* k, int64_t k_i
 // the other (a head's rows in as many warps as it needs), so that a block's
 // maximum is met on the way and every value is read once, held in registers
 // as it came between the maximum and its code.  Few blocks: blockIdx.y shares the heads.
+//
+// Measured, 64/8 heads of 128, half of the dims rotated: 24 prompts of 61 to 4,096
+// tokens with their queries 393 us, 4.9 TB/s (HBM 60% and issue slots 48% busy:
+// latency of a block's rounds, two CTAs of 128 registers an SM; three of 80 spill
+// the raw rows); 64 x 1 token 4.8 us in a graph, 14.7 with the host's call.
 namespace {
 
 constexpr float kLeastScale = 0x1p-60f;
@@ -899,7 +904,7 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
                 const int64_t at_scale = (row0 >> a.shift) * a.hkv + h;
                 const float held = live && old ? scales[at_scale] : 0.f;
                 // the values are turned twice, for their maximum and for their codes: a table read
-                // and a few products less dear than the registers (three CTAs an SM for two)
+                // and a few products less dear than the registers that 64 fp32 values take
                 auto values = [&](int u, float (&v)[8]) {
                     if (is_k && turned) {
                         Turn t;

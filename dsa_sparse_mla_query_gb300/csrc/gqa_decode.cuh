@@ -36,13 +36,20 @@
 // listed blocks side by side.  Only where a box of rows lies differs: its block
 // from the token's list, then its page.  The lists are short and about as long
 // as each other, so tokens count alike in the deal, by the longest list, and no
-// CTA sums anything up before it starts.
+// CTA sums anything up before it starts.  Where there are many more lists than
+// CTAs (eight times), none is cut: CTAs take whole lists in turn, head by head, so
+// that the CTAs of a moment read one head's blocks (kept in L2), and nothing is
+// joined.  8 rows of e4m3 keys: three CTAs an SM (two leave the latency of random
+// 128-byte rows uncovered); a miss brings the row's own lines alone.
 //
 // Measured, 64/8 heads of 128: 64 x 32,768 bf16 1,230 us, 7.0 TB/s (a copy: 6.8);
 // 1 x 524,288 e4m3 170 to 173 us, 6.4 TB/s; 128 x 4 tokens over 61 to 16,381 e4m3 566 us,
 // 3.9 TB/s: there 32 rows make 64 products, 64 conversions and 480 instructions of
 // a warp's 16 keys, and two warps a scheduler leave 62% of its issue slots unused
 // (the rows split over 16 warps: 699, a key is then converted twice).
+// Listed, e4m3: 64 tokens x 32 blocks of 64 keys 66 us, 4.1 TB/s (start, random rows
+// and the join); 2,048 x 32 1,145 us: 8.6 GB, mostly from L2, 307 instructions a
+// warp for a tile's 16 keys, half of the issue slots in use.
 #pragma once
 
 #include <type_traits>

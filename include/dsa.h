@@ -49,7 +49,7 @@
  *     over NVFP4 latent rows, 5 indexer scan over NVFP4 keys) and bits
  *     16-30 the wait (its mbarrier's shared-memory offset / 8, or 0x7FFF for
  *     the attention's issue loop).  Kernel 6 is dense_gqa_decode or
- *     block_gqa_attend, 7 dense_gqa_prefill.
+ *     block_gqa_attend, 7 dense_gqa_prefill, 8 block_gqa_select.
  *   - Indices are logical token positions within a sequence.  The page table or
  *     seq_base maps them to physical cache rows.
  */
