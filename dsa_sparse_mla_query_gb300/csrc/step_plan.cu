@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const __grid_co
     pdl_enter();
     const int tid = threadIdx.x;
     const int page = 1 << a.shift;
-    const int64_t capacity = (int64_t)a.max_pages << a.shift;
+    const int64_t capacity = min((int64_t)a.max_pages << a.shift, (int64_t)1 << 30);  // positions stay below it
     const bool writer = blockIdx.x == 0;
     int f0 = __ldg(a.free_range), f1 = __ldg(a.free_range + 1);
     const bool bad_range = f0 < 0 || f1 < f0 || f1 > a.free_cap;

@@ -505,9 +505,9 @@ dsa_status dsa_kv_block_insert(const dsa_gqa_shape* shape, const void* k, int64_
  *   int64 [num_q].  page_size as in dsa_seqs; num_pages: pages in the cache.
  * No output may be an input's memory.
  * DSA_ERR_BAD_INPUT in *d_status: a request that cannot be served (a negative
- * length, more tokens than max_pages pages hold, rows past num_q, not enough
- * free pages for it and those before it): it takes no pages, ctx_len =
- * cached_len (0 if that is negative), q_pos = slot = -1 for its rows; a page
+ * length, more tokens than max_pages pages hold or than 2^30, rows past num_q,
+ * not enough free pages for it and those before it): it takes no pages, ctx_len
+ * = cached_len (0 if that is negative), q_pos = slot = -1 for its rows; a page
  * outside the cache (the rows in it: -1); a free_range that is not one of
  * free_pages (counts as empty). */
 dsa_status dsa_step_plan(const int32_t* cached_len, const int32_t* new_len, int32_t num_seqs,

@@ -69,7 +69,7 @@ def plan(cached, new, page, free, free_range, num_pages, table, num_q):
     for b, (p, n) in enumerate(zip(cached, new)):
         start.append(min(row, num_q))
         rows = max(n, 0)
-        ok = p >= 0 and n >= 0 and p + n <= width * page and row + rows <= num_q
+        ok = p >= 0 and n >= 0 and p + n <= min(width * page, 1 << 30) and row + rows <= num_q
         need = -(-(p + n) // page) - -(-p // page) if ok else 0
         if ok and need and want + need > hi - lo:
             ok = False

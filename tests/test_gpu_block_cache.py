@@ -104,6 +104,16 @@ def test_plan_refuses_requests(name):
     assert got == ref
 
 
+@pytest.mark.parametrize("past, new", [(2 ** 31 - 10, 20), (2 ** 31 - 21, 20), (2 ** 30 - 5, 6), (2 ** 30 - 5, 5)])
+def test_plan_stops_at_the_longest_context(past, new):
+    page, table = 1 << 20, [list(range(2100)), list(range(2100))]
+    args = ([past, 3], [new, 4], page, [2100], [0, 1], 2200)
+    ref, bad = BR.plan(*args, [list(r) for r in table], new + 4)
+    got, status = _plan(*args, table, new + 4)
+    assert bad == (past + new > 2 ** 30) and status == (BAD if bad else 0)
+    assert got == ref
+
+
 # ---------------------------------------------------------------------------
 # writes
 class Cache:
