@@ -460,11 +460,6 @@ __device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
     hi = *reinterpret_cast<const uint32_t*>(&yh);
 }
 
-// 16 bytes to shared memory, asynchronously, or zeros
-__device__ __forceinline__ void copy16(void* dst, const void* src, bool copy) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(copy ? 16 : 0)
-                 : "memory");
-}
 __device__ __forceinline__ float whole_steps(float v, float up) {
     return v == v ? fmaxf(-127.f, fminf(127.f, rintf(v * up))) : 0.f;
 }

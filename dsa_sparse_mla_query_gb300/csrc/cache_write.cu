@@ -769,9 +769,10 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
     constexpr int kLanes = D / 8;        // lanes per row
     constexpr int kGroup = 32 / kLanes;  // rows per warp access
     constexpr int kAcc = 16 / kGroup;    // accesses of a warp's 16 rows
-    constexpr int kChunk = Pieces<kBlkThreads>::kChunk;
-    extern __shared__ __align__(16) float table[];  // [token][rot]: Turn's
-    __shared__ Pieces<kBlkThreads> pieces;
+    using Sequences = Pieces<kBlkThreads, 2>;  // (two CTAs an SM beside 64 KB of angles and 32 of rows)
+    constexpr int kChunk = Sequences::kChunk;
+    extern __shared__ __align__(16) float table[];  // [token][rot]: Turn's; the warps' next 16 rows each
+    __shared__ Sequences pieces;
     __shared__ int4 seq_sh[kChunk];  // first row, tokens, first position, context
     __shared__ float top[2][kBlkWarps];
     __shared__ bool good[128];
@@ -784,9 +785,10 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
     // the lane's chunks of four dims: of keys and queries, and of values
     const int ca = HALVES && turned ? 4 * li : 8 * li, cb = HALVES && turned ? 4 * li + half : 8 * li + 4;
     const bool lead = blockIdx.y == 0;
+    __nv_bfloat16* const stage = reinterpret_cast<__nv_bfloat16*>(table + (a.rot << a.shift)) + warp * 16 * D;
     auto row8 = [&](const __nv_bfloat16* row, bool split) {
-        if (!HALVES || !split) return __ldcs(reinterpret_cast<const uint4*>(row + 8 * li));
-        const uint2 x = __ldcs(reinterpret_cast<const uint2*>(row + ca)), y = __ldcs(reinterpret_cast<const uint2*>(row + cb));
+        if (!HALVES || !split) return *reinterpret_cast<const uint4*>(row + 8 * li);
+        const uint2 x = *reinterpret_cast<const uint2*>(row + ca), y = *reinterpret_cast<const uint2*>(row + cb);
         return make_uint4(x.x, x.y, y.x, y.y);
     };
     int64_t before = 0;
@@ -816,8 +818,10 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
             const int rounds = (2 * a.hkv + heads - 1) / heads;
             const int q_units = n * a.units;
             const int all = rounds + (q_units + kBlkWarps - 1) / kBlkWarps;
-            // a round's 16 rows of this warp, whatever becomes of them
-            auto load = [&](int r, uint4 (&raw)[kAcc]) {
+            // a round's 16 rows of this warp, whatever becomes of them: on their way to shared memory while
+            // the round before is worked on
+            auto load = [&](int r) {
+                if (r >= all) return;
                 if (r < rounds) {
                     const int task = r * heads + warp / per;
                     const int h = task < a.hkv ? task : task - a.hkv;
@@ -826,23 +830,22 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
 #pragma unroll
                     for (int u = 0; u < kAcc; ++u) {
                         const int tok = part * 16 + u * kGroup + sub;
-                        raw[u] = make_uint4(0u, 0u, 0u, 0u);
-                        if (task < 2 * a.hkv && tok < n)
-                            raw[u] = row8(src + (int64_t)(t0 + tok) * in + h * D, task < a.hkv);
+                        const bool in_it = task < 2 * a.hkv && tok < n;
+                        copy16(stage + (u * kGroup + sub) * D + 8 * li,
+                               src + (in_it ? (int64_t)(t0 + tok) * in + h * D + 8 * li : 0), in_it);
                     }
                 } else {
                     const int y = (r - rounds) * kBlkWarps + warp, tok = y / max(1, a.units), h0 = (y - tok * a.units) * 16;
 #pragma unroll
                     for (int u = 0; u < kAcc; ++u) {
                         const int h = h0 + u * kGroup + sub;
-                        raw[u] = make_uint4(0u, 0u, 0u, 0u);
-                        if (y < q_units && h < a.hq)
-                            raw[u] = row8(a.q + (int64_t)(t0 + tok) * a.q_in + h * D, true);
+                        const bool in_it = y < q_units && h < a.hq;
+                        copy16(stage + (u * kGroup + sub) * D + 8 * li,
+                               a.q + (in_it ? (int64_t)(t0 + tok) * a.q_in + h * D + 8 * li : 0), in_it);
                     }
                 }
             };
-            uint4 raw[kAcc];
-            if ((int)blockIdx.y < all) load(blockIdx.y, raw);  // on their way beside the tokens' checks
+            load(blockIdx.y);  // beside the tokens' checks
             const int64_t row0 = row_at(a.s, a.page_shift, b, lo);  // the block's first row
             const bool there = row0 >= 0 && (row0 & ((1 << a.shift) - 1)) == 0;
             __syncthreads();  // the last piece's table and tokens are no longer read
@@ -863,10 +866,20 @@ __global__ void __launch_bounds__(kBlkThreads, 2) kv_block_insert_kernel(const _
                 at[0] = c;
                 at[2] = sn;
             }
-            if (!__syncthreads_or(some)) continue;
+            if (!__syncthreads_or(some)) {
+                copies_wait();  // the next piece's take the same places
+                continue;
+            }
 
             for (int r = blockIdx.y; r < all; r += gridDim.y) {
-                if (r != (int)blockIdx.y) load(r, raw);
+                uint4 raw[kAcc];
+                copies_wait();
+                __syncwarp();
+#pragma unroll
+                for (int u = 0; u < kAcc; ++u)
+                    raw[u] = row8(stage + (u * kGroup + sub) * D, r >= rounds || r * heads + warp / per < a.hkv);
+                __syncwarp();
+                load(r + gridDim.y);
                 if (r >= rounds) {
                     const int y = (r - rounds) * kBlkWarps + warp, tok = y / a.units, h0 = (y - tok * a.units) * 16;
                     if (y >= q_units || !good[tok]) continue;
@@ -1033,12 +1046,12 @@ cudaError_t launch_kv_block_insert(const dsa_gqa_shape& sh, const void* k, int64
     const int64_t work = (2 * sh.num_kv_heads * per + 7) / 8 + (longest * a.units + 7) / 8;
     const unsigned grid = (unsigned)std::min<int64_t>(blocks, 152 * 8);
     const unsigned share = (unsigned)std::max<int64_t>(1, std::min<int64_t>(work, 152 * 8 / grid));
-    const size_t smem = (size_t)sh.scale_block * a.rot * sizeof(float);  // up to 64 KB
+    const size_t smem = (size_t)sh.scale_block * a.rot * sizeof(float) + (size_t)kBlkWarps * 16 * sh.head_dim * 2;  // up to 96 KB
     auto go = [&](auto d, auto h) {
         auto kern = kv_block_insert_kernel<decltype(d)::value, decltype(h)::value>;
         static OncePerDevice once;
         const cudaError_t e = once.run(
-            [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 64 * 8); });
+            [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 64 * 8 + kBlkWarps * 16 * 128 * 2); });
         if (e != cudaSuccess) return e;
         return launch_pdl(kern, dim3(grid, share), dim3(kBlkThreads), smem, stream, 1, a);
     };

@@ -34,9 +34,9 @@ __device__ __forceinline__ T cta_scan(T mine, T* red, T& total) {
 
 // Sequences in pieces, a chunk of them at a time: first[i] pieces lie before
 // sequence i of the chunk.
-template <int THREADS>
+template <int THREADS, int PER = 4>
 struct Pieces {
-    static constexpr int kPer = 4, kChunk = THREADS * kPer;
+    static constexpr int kPer = PER, kChunk = THREADS * kPer;
     int first[kChunk + 1];
     int red[THREADS / 32 + 1];
     // counts of sequences c0 .. ; count(b) >= 0.  Returns the chunk's pieces.
@@ -122,6 +122,13 @@ __device__ __forceinline__ NewTokens new_tokens(const dsa_seqs& s, int b, int nu
 __device__ __forceinline__ int blocks_touched(const NewTokens& n, int shift) {
     return n.nq ? (int)((((int64_t)n.p0 + n.nq - 1) >> shift) - (n.p0 >> shift)) + 1 : 0;
 }
+
+// 16 bytes to shared memory, asynchronously, or zeros
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool copy) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(copy ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // the least e >= -126 with |x| <= 1.m 2^e max, for max = (1 + limit 2^-23) 2^top: x > 0 finite
 __device__ __forceinline__ int scale_exponent(float x, int top, uint32_t limit) {
