@@ -685,12 +685,13 @@ cudaError_t launch_kv_insert(const dsa_gqa_shape& sh, const void* k, int64_t k_i
 // once for all heads; then eight warps of 16 rows each take the heads one after
 // the other (a head's rows in as many warps as it needs), so that a block's
 // maximum is met on the way and every value is read once, held in registers
-// as it came between the maximum and its code.  Few blocks: blockIdx.y shares the heads.
+// as it came between the maximum and its code; the next rows come to shared memory
+// meanwhile.  Few blocks: blockIdx.y shares the heads.
 //
 // Measured, 64/8 heads of 128, half of the dims rotated: 24 prompts of 61 to 4,096
-// tokens with their queries 393 us, 4.9 TB/s (HBM 60% and issue slots 48% busy:
-// latency of a block's rounds, two CTAs of 128 registers an SM; three of 80 spill
-// the raw rows); 64 x 1 token 4.8 us in a graph, 14.7 with the host's call.
+// tokens with their queries 341 us, 5.6 TB/s (a copy: 6.8; two CTAs of 128 registers
+// an SM; three of 80 spill the raw rows: 417; rows loaded into registers when a
+// round begins: 393); 64 x 1 token 4.8 us in a graph, 15 with the host's call.
 namespace {
 
 constexpr float kLeastScale = 0x1p-60f;
@@ -1039,13 +1040,14 @@ cudaError_t launch_kv_block_insert(const dsa_gqa_shape& sh, const void* k, int64
     a.page_shift = page_shift_of(s);
     a.units = (a.hq + 15) / 16;
     // pieces: at most a block per token, and two more than whole blocks per sequence; the heads
-    // are shared where they do not fill the GPU (eight CTAs per SM in all)
+    // are shared where that makes no more than 16 CTAs per SM, of which two run at once (824 pieces of 64
+    // tokens: whole 354 us, in two shares 341, in four 366: a share needs the angles too)
     const int64_t blocks = std::min<int64_t>(num_q, (num_q >> a.shift) + 2 * (int64_t)s.num_seqs);
     const int64_t longest = std::min<int64_t>(sh.scale_block, s.max_q_per_seq);
     const int64_t per = longest <= 16 ? 1 : longest <= 32 ? 2 : longest <= 64 ? 4 : 8;
     const int64_t work = (2 * sh.num_kv_heads * per + 7) / 8 + (longest * a.units + 7) / 8;
     const unsigned grid = (unsigned)std::min<int64_t>(blocks, 152 * 8);
-    const unsigned share = (unsigned)std::max<int64_t>(1, std::min<int64_t>(work, 152 * 8 / grid));
+    const unsigned share = (unsigned)std::max<int64_t>(1, std::min<int64_t>(work, 152 * 16 / grid));
     const size_t smem = (size_t)sh.scale_block * a.rot * sizeof(float) + (size_t)kBlkWarps * 16 * sh.head_dim * 2;  // up to 96 KB
     auto go = [&](auto d, auto h) {
         auto kern = kv_block_insert_kernel<decltype(d)::value, decltype(h)::value>;
