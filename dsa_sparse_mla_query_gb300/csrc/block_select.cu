@@ -438,8 +438,8 @@ struct ScoreArgs {
     int32_t pad;     // a token's rows, a power of two of them (up to 8 in the 8-row tiles of few rows)
     int32_t npt;     // tiles per token there (1 where pad < 8)
     int32_t tokens;  // per CTA
-    int32_t xt;      // CTAs (items) that share the blocks
-    int32_t items;   // of the CTAs that take them in turn
+    int32_t xt;      // CTAs that share the blocks
+    int32_t items, tiles;  // many rows: (sequence's tokens, key head)s, and tiles of blocks of the longest context
     int32_t direct;  // slot = sequence
 };
 
@@ -714,9 +714,10 @@ __global__ void __launch_bounds__(kFewThreads, PICK ? 4 : 5)
 // tensor cores, K = 2 D: min(q, 0) beside lo, max(q, 0) beside hi, whole numbers
 // in f16 (sums below 2^22: exact).  Blocks are the rows, so that a token's heads
 // are columns, and their maximum one thread's, and a warp stores 32 neighbouring
-// scores of a token.  A CTA an SM takes items in turn, a head of up to 256 / pad
-// tokens each: its columns are laid out in shared memory once (a warp owns a
-// token, so its step is a warp's maximum), then it walks over tiles of blocks.
+// scores of a token.  An item is a head of up to 256 / pad tokens, and its tiles of
+// blocks behind a start that takes some two tiles' time: its columns are laid out
+// in shared memory (a warp owns a token, so its step is a warp's maximum).  A CTA
+// an SM has an even share of all items' tiles and starts, in a row.
 // Eight warps turn the bounds into f16, 64 dims at a time, ahead of the products,
 // which one thread issues, and eight warps take the maxima of the last tile out
 // of TMEM.  The bounds on their way are asynchronous copies, each lane's its own:
@@ -724,7 +725,7 @@ __global__ void __launch_bounds__(kFewThreads, PICK ? 4 : 5)
 // cycles a chunk, 500 so).  As an operand in TMEM they bound the products at some
 // 150 cycles each, whatever their columns, and leave no second accumulator.
 constexpr int kWideCols = 256, kWideHalf = 128, kWideRows = 128;  // a warp's maxima: half of the columns
-constexpr int kWideRing = 3;
+constexpr int kWideRing = 3, kWideStart = 2;
 constexpr int kWideLay = 512, kWideThreads = kWideLay + 32;
 constexpr int kTagSelect = 8;
 
@@ -778,9 +779,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const
     Cursor<kWideRing> ring;  // the products' and the bounds' place among the chunks
     bool lap = false;        // every place has been used
     const int quarter = warp & 3, part = (warp >> 2) & 1;  // rows, and maxima: half; bounds: lo or hi
-    for (int item = blockIdx.x; item < a.items && __syncthreads_and(ok); item += gridDim.x) {
-        const int share = item % a.xt, rest = item / a.xt;
-        const int kvh = rest % a.hkv, slot = rest / a.hkv;
+    const int units = kWideStart + a.tiles;
+    const int64_t all = (int64_t)a.items * units;
+    int64_t unit = all * blockIdx.x / gridDim.x;
+    const int64_t end = all * (blockIdx.x + 1) / gridDim.x;
+    while (unit < end && __syncthreads_and(ok)) {
+        const int item = (int)(unit / units), u0 = (int)(unit - (int64_t)item * units);
+        const int u1 = (int)min((int64_t)units, u0 + (end - unit));
+        unit += u1 - u0;
+        const int x0 = max(u0 - kWideStart, 0);  // the CTA's tiles of the item: [x0, x1)
+        if (u1 - kWideStart <= x0) continue;
+        const int kvh = item % a.hkv, slot = item / a.hkv;
         // ---- the CTA's tokens: [t0, t0 + n) of sequence b
         int b = slot, skip = 0;
         if (!a.direct) {
@@ -820,7 +829,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const
         }
         Seq sq{0, 0, 0, false};
         if (b >= 0) sq = load_seq(a.s, b, a.num_q);
-        if (a.direct && !sq.ok && tid == 0 && share == 0 && kvh == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
+        if (a.direct && !sq.ok && tid == 0 && x0 == 0 && kvh == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
         const int n = sq.ok ? min(a.tokens, sq.nq - skip) : 0;
         const int t0 = sq.q0 + skip;
         // ---- the bounds' warps: a lane's 16 bytes of a chunk's row, four lanes a row, 16 rows a warp; on
@@ -852,8 +861,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const
         int at = -1;
         int page = 0;  // of the next tile
         if (bounds_warp && n > 0) {
-            at = place(share, page_of_tile(share));
-            page = page_of_tile(share + a.xt);
+            at = place(x0, page_of_tile(x0));
+            page = page_of_tile(x0 + 1);
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c) fetch(at, c);
         }
@@ -980,13 +989,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const
 #pragma unroll
         for (int w = 0; w < kWideLay / 32; ++w) most = max(most, most_sh[w]);
         const int cols = (n * a.pad + 15) & ~15;
-        const int tiles = (most + kWideRows) / kWideRows;  // 0 where no query sees a block
+        const int x1 = min(u1 - kWideStart, (most + kWideRows) / kWideRows);  // (none where no query sees a block)
 
         if (warp == kWideLay / 32) {
             // ---- the products
             if (lane == 0) {
                 const uint32_t idesc = ptx::idesc_f16_m128(cols, false);
-                for (int x = share; x < tiles && ok; x += a.xt, ++tile) {
+                for (int x = x0; x < x1 && ok; ++x, ++tile) {
                     const int buf = tile & 1;
                     if (tile >= 2) ok = quick_wait(tempty + buf, ((tile >> 1) - 1) & 1, abort_flag, a.d_status);
                     for (int c = 0; c < C::kChunks && ok; ++c, ring.move(1)) {
@@ -1007,11 +1016,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const
             __syncwarp();
         } else if (bounds_warp) {
             // ---- bounds to f16
-            for (int x = share; x < tiles && ok; x += a.xt) {
+            for (int x = x0; x < x1 && ok; ++x) {
                 if (at == -2 && lane < 16 && x * kWideRows + (warp - 8) * 16 + lane <= most && kvh == 0)
                     report(a.d_status, DSA_ERR_BAD_INPUT);
-                at = place(x + a.xt, page);
-                page = page_of_tile(x + 2 * a.xt);
+                at = place(x + 1, page);
+                page = page_of_tile(x + 2);
 #pragma unroll
                 for (int c = 0; c < C::kChunks; ++c) {
                     if (lap) ok = ok && quick_wait(aempty + ring.st, ring.ph ^ 1u, abort_flag, a.d_status);
@@ -1057,13 +1066,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const
                 return r >= 0 && (r & ((1 << a.shift) - 1)) == 0 ? __ldg(a.steps + (r >> a.shift) * a.hkv + kvh) : 0.f;
             };
             const int64_t next = (int64_t)a.hkv * a.ld;  // to the next token's row
-            float ahead = step_at(share, page_of(share));
-            int far = page_of(share + a.xt);
-            for (int x = share; x < tiles && ok; x += a.xt, ++tile) {
+            float ahead = step_at(x0, page_of(x0));
+            int far = page_of(x0 + 1);
+            for (int x = x0; x < x1 && ok; ++x, ++tile) {
                 const int buf = tile & 1, blk = x * kWideRows + quarter * 32 + lane;
                 const float step = ahead;
-                ahead = step_at(x + a.xt, far);
-                far = page_of(x + 2 * a.xt);
+                ahead = step_at(x + 1, far);
+                far = page_of(x + 2);
                 ok = __all_sync(0xffffffffu, quick_wait(tfull + buf, (tile >> 1) & 1, abort_flag, a.d_status));
                 if (!ok) break;
                 ptx::tc_fence_after();
@@ -1440,18 +1449,11 @@ cudaError_t launch_select(const dsa_gqa_shape& sh, const void* q, const void* bo
         a.tokens = std::min(s.max_q_per_seq, kWideCols / a.pad);
         a.direct = s.max_q_per_seq <= a.tokens;
         const int64_t slots = a.direct ? s.num_seqs : std::min<int64_t>(num_q, num_q / a.tokens + s.num_seqs);
-        const int64_t items = slots * a.hkv, most = (a.ld + kWideRows - 1) / kWideRows;
-        // items that share a head's tiles each lay its columns out, which takes some two tiles' time: the
-        // fewest rounds times what one takes (512 heads of eight tiles: one each)
-        a.xt = 1;
-        int64_t best = INT64_MAX;
-        for (int64_t x = 1; x <= std::min<int64_t>(most, 64); ++x) {
-            const int64_t t = (items * x + kPlanSms - 1) / kPlanSms * (2 + (most + x - 1) / x);
-            if (t < best) best = t, a.xt = (int32_t)x;
-        }
-        if (items * a.xt > INT32_MAX) return cudaErrorInvalidConfiguration;
-        a.items = (int32_t)(items * a.xt);
-        const unsigned grid = (unsigned)std::min<int64_t>(a.items, num_sms());
+        const int64_t items = slots * a.hkv;
+        a.tiles = (a.ld + kWideRows - 1) / kWideRows;
+        if (items > INT32_MAX) return cudaErrorInvalidConfiguration;
+        a.items = (int32_t)items;
+        const unsigned grid = (unsigned)std::min<int64_t>(items * a.tiles, num_sms());
         auto go = [&](auto d) {
             constexpr int D = decltype(d)::value;
             auto kern = block_score_wide_kernel<D>;
