@@ -995,6 +995,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const
             // ---- the products
             if (lane == 0) {
                 const uint32_t idesc = ptx::idesc_f16_m128(cols, false);
+                const uint64_t da = ptx::sdesc_sw128(smem_u32(ash)), db = ptx::sdesc_sw128(smem_u32(bsh));
                 for (int x = x0; x < x1 && ok; ++x, ++tile) {
                     const int buf = tile & 1;
                     if (tile >= 2) ok = quick_wait(tempty + buf, ((tile >> 1) - 1) & 1, abort_flag, a.d_status);
@@ -1005,8 +1006,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             ptx::mma_ss(tmem + buf * kWideCols,
-                                        ptx::sdesc_sw128(smem_u32(ash) + ring.st * (kWideRows * 128) + k * 32),
-                                        ptx::sdesc_sw128(smem_u32(bsh) + c * (kWideCols * 128) + k * 32), idesc,
+                                        da + (uint32_t)(ring.st * (kWideRows * 128 / 16) + k * 2),
+                                        db + (uint32_t)(c * (kWideCols * 128 / 16) + k * 2), idesc,
                                         c > 0 || k > 0 ? 1u : 0u);
                         ptx::mma_commit(aempty + ring.st);
                         if (c == C::kChunks - 1) ptx::mma_commit(tfull + buf);
