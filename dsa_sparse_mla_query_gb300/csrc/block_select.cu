@@ -25,7 +25,7 @@
 // Measured, 64/8 heads of 128, blocks of 64 keys, with the host's calls and the new
 // keys' bounds: 64 tokens over 32,768 keys 28.7 us, 3 over 524,288 30 us (HBM 36%
 // busy while the bounds are read: two or three rounds of loads a warp, then the
-// choice); 2,048 of 65,536 143 us: the scores 98 (the CTA's own warps turn the
+// choice); 2,048 of 65,536 140 us: the scores 95 (the CTA's own warps turn the
 // bounds into f16 operands: the tensor cores are 35% busy), the choice 37 (69% of
 // the issue slots), the bounds 6.
 #include <algorithm>
@@ -467,9 +467,9 @@ __device__ __forceinline__ float whole_steps(float v, float up) {
 // A few query rows a sequence (up to 4 tiles): a CTA of four warps takes a
 // (sequence, key head), or a share of its blocks.  Every warp keeps two tiles of
 // 16 blocks on their way, and the pages of two more; a thread's 16 bytes of a
-// block become fragments of whole k-steps as they meet the products (f16: 8
-// cycles a product; as 8-bit integers, which need no conversion, half as many
-// products took some 64 each: 3 x 8,192 blocks of 8 heads 39 us, 30 so).  Where
+// block become fragments of whole k-steps as they meet the products (f16:
+// as 8-bit integers, which need no conversion and half as many products, 3 x 8,192
+// blocks of 8 heads took 39 us, 30 so).  Where
 // (sequence, key head)s alone fill the GPU (PICK) their scores stay in shared
 // memory, and the CTA chooses among them: no second launch.
 constexpr int kFewThreads = 128, kFewWarps = kFewThreads / 32, kFewTiles = 4;
@@ -715,17 +715,18 @@ __global__ void __launch_bounds__(kFewThreads, PICK ? 4 : 5)
 // in f16 (sums below 2^22: exact).  Blocks are the rows, so that a token's heads
 // are columns, and their maximum one thread's, and a warp stores 32 neighbouring
 // scores of a token.  An item is a head of up to 256 / pad tokens, and its tiles of
-// blocks behind a start that takes some two tiles' time: its columns are laid out
-// in shared memory (a warp owns a token, so its step is a warp's maximum).  A CTA
-// an SM has an even share of all items' tiles and starts, in a row.
+// blocks behind a start that takes some three tiles' time (15,000 cycles, the last
+// maxima among them, a tile 4,500): its columns are laid out in shared memory (a
+// warp owns a token, so its step is a warp's maximum).  A CTA an SM has an even
+// share of all items' tiles and starts, in a row.
 // Eight warps turn the bounds into f16, 64 dims at a time, ahead of the products,
 // which one thread issues, and eight warps take the maxima of the last tile out
 // of TMEM.  The bounds on their way are asynchronous copies, each lane's its own:
 // loads into registers are waited for by the fence behind every chunk (1,250
-// cycles a chunk, 500 so).  As an operand in TMEM they bound the products at some
+// cycles a chunk, 640 so).  As an operand in TMEM they bound the products at some
 // 150 cycles each, whatever their columns, and leave no second accumulator.
 constexpr int kWideCols = 256, kWideHalf = 128, kWideRows = 128;  // a warp's maxima: half of the columns
-constexpr int kWideRing = 3, kWideStart = 2;
+constexpr int kWideRing = 3, kWideStart = 3;
 constexpr int kWideLay = 512, kWideThreads = kWideLay + 32;
 constexpr int kTagSelect = 8;
 
