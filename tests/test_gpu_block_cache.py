@@ -267,6 +267,18 @@ def test_more_sequences_than_a_chunk_of_the_scan():
     c.run().check()
 
 
+def test_sequences_without_a_page_between_others():
+    """Pieces that are given up after their rows are on their way, the next ones of the same CTA behind them."""
+    n = 2600
+    c = Cache([i % 5 for i in range(n)], [1 + i % 3 for i in range(n)], 8, 2, 128, 16, page=16, rot=64, half=True, seed=6)
+    lost = set(range(1, n, 3)) | set(range(1216, 1500))
+    table = c.table.clone()
+    c.table[sorted(lost)] = -1
+    c.run(status=BAD)
+    c.table = table
+    c.check(skip=lost)
+
+
 @pytest.mark.parametrize("amp", [1e-30, 2.0 ** -50, 1e-3, 300.0, 1e30])
 def test_scales_of_any_size(amp):
     """Blocks' scales grow or stay, whichever the older tokens' scale asks for."""
