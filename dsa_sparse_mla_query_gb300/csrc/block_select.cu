@@ -833,6 +833,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const
         if (a.direct && !sq.ok && tid == 0 && x0 == 0 && kvh == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
         const int n = sq.ok ? min(a.tokens, sq.nq - skip) : 0;
         const int t0 = sq.q0 + skip;
+        // a context that ends before these tiles (max_ctx may be far longer): nothing to lay out
+        if (n <= 0 || ((int64_t)x0 * kWideRows << a.shift) >= sq.ctx) continue;
         // ---- the bounds' warps: a lane's 16 bytes of a chunk's row, four lanes a row, 16 rows a warp; on
         // their way beside the queries
         const bool bounds_warp = warp >= 8 && warp < 16;
