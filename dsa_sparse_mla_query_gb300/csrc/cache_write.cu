@@ -689,7 +689,7 @@ cudaError_t launch_kv_insert(const dsa_gqa_shape& sh, const void* k, int64_t k_i
 // meanwhile.  Few blocks: blockIdx.y shares the heads.
 //
 // Measured, 64/8 heads of 128, half of the dims rotated: 24 prompts of 61 to 4,096
-// tokens with their queries 341 us, 5.6 TB/s (a copy: 6.8; two CTAs of 128 registers
+// tokens with their queries 341 to 347 us, 5.6 TB/s (a copy: 6.8; two CTAs of 128 registers
 // an SM; three of 80 spill the raw rows: 417; rows loaded into registers when a
 // round begins: 393); 64 x 1 token 4.8 us in a graph, 15 with the host's call.
 namespace {

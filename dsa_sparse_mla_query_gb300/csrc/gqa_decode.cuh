@@ -47,7 +47,7 @@
 // 3.9 TB/s: there 32 rows make 64 products, 64 conversions and 480 instructions of
 // a warp's 16 keys, and two warps a scheduler leave 62% of its issue slots unused
 // (the rows split over 16 warps: 699, a key is then converted twice).
-// Listed, e4m3: 64 tokens x 32 blocks of 64 keys 66 us, 4.1 TB/s (start, random rows
+// Listed, e4m3: 64 tokens x 32 blocks of 64 keys 62 to 66 us, 4.2 TB/s (start, random rows
 // and the join); 2,048 x 32 1,145 us: 8.6 GB, mostly from L2, 307 instructions a
 // warp for a tile's 16 keys, half of the issue slots in use.
 #pragma once
