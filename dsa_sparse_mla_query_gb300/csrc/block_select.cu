@@ -10,7 +10,8 @@
 // inputs, and ties are ties.
 //
 // - block_bounds_kernel: minimum and maximum over the keys of the blocks that new
-//   tokens touch, four warps per block and head, keys read once.
+//   tokens touch, four warps per block and head, keys read once; and over older
+//   blocks whose codes the new tokens' scale changed.
 // - block_score_few_kernel: few tokens a sequence read 2 D bytes a block once:
 //   HBM.  The sums on the warp-level matrix instruction, 16 blocks by 8 query
 //   rows, straight from global memory (the order of the dims within a k-step is
@@ -93,6 +94,37 @@ __device__ __forceinline__ uint32_t high_code(float v, float up) {
     return (uint32_t)(int)fmaxf(-127.f, fminf(127.f, x == 0.f && v > 0.f ? 1.f : ceilf(x))) & 0xFFu;
 }
 
+// May a sequence's new tokens (from position p0) have raised the scale of the scale block that p0
+// lies in, so that its older tokens' codes are others than before?  A scale grows by a power of two
+// to the least one that holds the new tokens: afterwards one of their codes is 224 or more, and every
+// older one 224 or less.  (Where that holds and nothing grew, the older blocks get the bounds that they
+// have.)  A warp, over the codes of one head: src its row of the scale block's first token, `older`
+// of its `all` rows before p0.
+template <int D>
+__device__ __forceinline__ bool scale_raised(const uint8_t* src, int64_t stride, int older, int all) {
+    constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+    const int lane = threadIdx.x & 31;
+    uint32_t held = 0, fresh = 0;  // largest magnitudes of older and of new codes
+    for (int r = lane / kLanes; r < all; r += kRows) {
+        const uint4 z = __ldg(reinterpret_cast<const uint4*>(src + r * stride) + lane % kLanes);
+        const uint32_t w[4] = {z.x, z.y, z.z, z.w};
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t x = w[e] & 0x7F7F7F7Fu;
+            m = __vmaxu4(m, x & ~__vcmpeq4(x, 0x7F7F7F7Fu));  // NaN has no say
+        }
+        held = __vmaxu4(held, r < older ? m : 0u);
+        fresh = __vmaxu4(fresh, r < older ? 0u : m);
+    }
+    auto most = [](uint32_t y) {
+        const uint32_t x = __vmaxu2(y & 0x00FF00FFu, (y >> 8) & 0x00FF00FFu);
+        return __reduce_max_sync(0xffffffffu, max(x & 0xFFu, x >> 16));
+    };
+    constexpr uint32_t k224 = 0x76;  // 1.75 2^7
+    return most(held) <= k224 && most(fresh) >= k224;
+}
+
 // Four warps take a block and head, its rows among them: minima and maxima as
 // they lie in the cache (pairs of f16 or bf16: exact), converted at the end.
 // Rows with scales of their own, negative scales and blocks with values that are
@@ -112,14 +144,17 @@ __global__ void __launch_bounds__(kBoundThreads) block_bounds_kernel(const __gri
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int part = warp % kParts, slot = warp / kParts;
     const int li = lane % L, sub = lane / L;
+    const int big = max(a.shift, a.scale_shift);
     int64_t before = 0;
     for (int c0 = 0; c0 < a.s.num_seqs; c0 += kChunk) {
         const int left = min(kChunk, a.s.num_seqs - c0);
         const int total = pieces.scan(c0, a.s.num_seqs, [&](int b) {
             const NewTokens n = new_tokens(a.s, b, a.num_q);
             if (n.bad && blockIdx.x == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
-            seq_sh[b - c0] = make_int4(n.p0, n.nq, n.ctx, 0);
-            return blocks_touched(n, a.shift);
+            // scale blocks of more than a block: from the first new token's scale block on
+            const int start = n.nq ? n.p0 >> big << (big - a.shift) : 0;
+            seq_sh[b - c0] = make_int4(n.p0, n.nq, n.ctx, start);
+            return n.nq ? blocks_touched(n, a.shift) + (n.p0 >> a.shift) - start : 0;
         });
         // CTAs take kHeads heads of a block at a time
         const int per = (a.hkv + kHeads - 1) / kHeads;
@@ -129,15 +164,24 @@ __global__ void __launch_bounds__(kBoundThreads) block_bounds_kernel(const __gri
             const int h = (int)(x - (int64_t)piece * per) * kHeads + slot;
             const int i = pieces.find(piece, left);
             const int4 nt = seq_sh[i];
-            const int64_t first = (int64_t)((nt.x >> a.shift) + (piece - pieces.first[i])) << a.shift;
+            const int64_t first = (int64_t)(nt.w + (piece - pieces.first[i])) << a.shift;
             const int n = (int)min((int64_t)1 << a.shift, (int64_t)nt.x + nt.y - first);  // its keys
             const int64_t row0 = row_at(a.s, a.page_shift, c0 + i, first);
+            // a block of older tokens alone (what is wrong with the sequence is reported with the others)
+            const bool older = FP8 && first + n <= nt.x;
+            const int64_t big0 = older ? first & -((int64_t)1 << big) : 0;  // its scale block's first token
+            const int64_t big_row = row0 - (first - big0);
+            if (older && (row0 < 0 || (big_row & ((1 << big) - 1)) || row0 + n > a.s.num_rows || nt.x + (int64_t)nt.y > nt.z))
+                continue;
             if (row0 < 0 || (row0 & ((1 << a.shift) - 1)) || row0 + n > a.s.num_rows || nt.x + (int64_t)nt.y > nt.z) {
                 if (threadIdx.x == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
                 continue;
             }
-            const bool live = h < a.hkv;
+            bool live = h < a.hkv;
             const uint8_t* src = a.k + row0 * a.stride + (int64_t)(live ? h : 0) * (FP8 ? D : 2 * D) + 16 * li;
+            if (FP8 && older && live && part == 0)  // (the warp that writes)
+                live = scale_raised<D>(a.k + big_row * a.stride + (int64_t)h * D, a.stride, (int)(nt.x - big0),
+                                       (int)min((int64_t)1 << big, min((int64_t)nt.x + nt.y - big0, a.s.num_rows - big_row)));
             const int64_t at = (row0 >> a.shift) * a.hkv + h;
             const bool even = !FP8 || a.scale_shift >= a.shift;  // one scale for the block
             float scale = 1.f;
@@ -1370,7 +1414,9 @@ cudaError_t launch_bounds(const dsa_gqa_shape& sh, const void* k, const float* k
     a.shift = 31 - __builtin_clz((unsigned)block);
     a.scale_shift = scale_shift(sh);
     a.page_shift = page_shift_of(s);
-    const int64_t blocks = std::min<int64_t>(num_q, (num_q >> a.shift) + 2 * (int64_t)s.num_seqs);
+    int64_t blocks = std::min<int64_t>(num_q, (num_q >> a.shift) + 2 * (int64_t)s.num_seqs);
+    if (a.scale_shift > a.shift)  // and the older ones of a scale block, once per sequence
+        blocks += std::min<int64_t>(num_q, s.num_seqs) * ((1 << (a.scale_shift - a.shift)) - 1);
     const int64_t ctas = blocks * ((sh.num_kv_heads + 1) / 2);  // two heads of a block at a time
     const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(ctas, kPlanSms * 8));
     auto go = [&](auto kern) { return launch_pdl(kern, dim3(grid), dim3(kBoundThreads), 0, stream, 1, a); };

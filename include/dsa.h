@@ -588,7 +588,12 @@ dsa_status block_gqa_workspace_size(const dsa_gqa_shape* shape, const dsa_seqs* 
  * the sequence is skipped).
  *   bounds int8 [ceil(num_rows / block), num_kv_heads, 2, head_dim], by physical
  *   row: block i of the cache is rows [i, i + 1) block; steps fp32
- *   [ceil(num_rows / block), num_kv_heads].  Other blocks' are left as they were.
+ *   [ceil(num_rows / block), num_kv_heads].  Other blocks' are left as they were,
+ *   but for caches whose scale blocks are longer than `block`: a new token that raises
+ *   a scale has the older codes of its scale block encoded again
+ *   (dsa_kv_block_insert), and where the first new token's scale block may be such a
+ *   one (no older code in it above 224, a new one of 224 or more), the blocks of it
+ *   before that token get their bounds again too.
  * DSA_ERR_BAD_INPUT: a malformed sequence, a block outside the cache or not at a
  * multiple of `block` rows (seq_base), new tokens past ctx_len: their blocks
  * are left.  Alignment: k_cache and bounds 16 bytes. */
