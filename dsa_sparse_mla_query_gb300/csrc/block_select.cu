@@ -818,6 +818,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_enter();
+    // every malformed sequence is reported, whatever rows it has: a share per CTA, by the products' warp, which
+    // waits for the columns anyway
+    if (warp == kWideLay / 32)
+        for (int64_t i = (int64_t)blockIdx.x * 32 + lane; i < a.s.num_seqs; i += gridDim.x * 32)
+            if (!load_seq(a.s, (int)i, a.num_q).ok) report(a.d_status, DSA_ERR_BAD_INPUT);
 
     bool ok = true;
     int tile = 0;            // tiles so far
@@ -840,7 +845,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const
         if (!a.direct) {
             auto tiles_of_seq = [&](int i) {
                 const Seq q = load_seq(a.s, i, a.num_q);
-                if (!q.ok && item == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
                 return q.ok ? (q.nq + a.tokens - 1) / a.tokens : 0;
             };
             b = -1;
@@ -874,7 +878,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const
         }
         Seq sq{0, 0, 0, false};
         if (b >= 0) sq = load_seq(a.s, b, a.num_q);
-        if (a.direct && !sq.ok && tid == 0 && x0 == 0 && kvh == 0) report(a.d_status, DSA_ERR_BAD_INPUT);
         const int n = sq.ok ? min(a.tokens, sq.nq - skip) : 0;
         const int t0 = sq.q0 + skip;
         // a context that ends before these tiles (max_ctx may be far longer): nothing to lay out

@@ -1,0 +1,114 @@
+"""Paths of the block selection and of attention over listed blocks that long
+batches take: many sequences beside a prompt, whole lists in turn with tiles of
+16 and 32 query rows, malformed sequences."""
+
+from __future__ import annotations
+
+import pytest
+import torch
+
+import block_reference as BR
+import dsa_sparse_mla_query_gb300 as dsa
+from test_gpu_block_select import BAD, DEV, KINDS, Step, _few, _i32, _random_lists
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    dsa.load()
+    yield
+    torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------------------
+# many sequences, one of them a prompt: the scores of every sequence by the tensor cores' kernel
+def _mixed(n, prompt, at, *, step=3, hq=8, hkv=2, d=64, page=16, **kw):
+    """`n` sequences, most with one token or none, number `at` with `prompt` of them."""
+    new = [prompt if b == at else int(b % step == 0) for b in range(n)]
+    ctx = [prompt + 70 if b == at else 1 + b % 90 for b in range(n)]
+    return Step(ctx, new, hq, hkv, d, 16, kv="bf16", page=page, nsel=5, first=1, local=2, seed=n, extra_q=3, **kw)
+
+
+@pytest.mark.parametrize("n, at", [(33, 32), (40, 0), (100, 57), (2177, 2176), (2300, 2200), (4400, 4399)])
+def test_select_of_a_prompt_among_many_sequences(n, at):
+    s = _mixed(n, 300, at, step=50 if n > 1000 else 3).run_select()
+    some = _few(s, 25) or list(range(s.nq))
+    start = s.q_start[at]
+    s.check_select(sorted(set(some) | {start, start + 150, start + 299}))
+
+
+@pytest.mark.parametrize("n", [1025, 2100])
+def test_bounds_of_more_sequences_than_a_scan_holds(n):
+    """1,024 at a time."""
+    _mixed(n, 40, n - 2).run_bounds().check_bounds()
+
+
+def test_a_mixed_step():
+    """A prompt's chunk beside decoding sequences: bounds, selection, attention."""
+    s = _mixed(50, 300, 20, d=128, hq=16).run_bounds().run_select().run_attend()
+    s.check_select(_few(s))
+    s.check_attend(_few(s))
+
+
+# ---------------------------------------------------------------------------
+# whole lists in turn (eight lists or more a CTA), tiles of 16 and 32 rows, two chunks of heads
+@pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("hq, hkv, d, tokens", [(32, 2, 128, 650), (32, 2, 64, 650), (40, 2, 64, 620), (33, 1, 128, 640),
+                                                (64, 1, 64, 1300), (9, 1, 128, 1300)])
+def test_whole_lists_in_turn_with_many_rows(kv, hq, hkv, d, tokens):
+    s = Step([tokens + 60], [tokens], hq, hkv, d, 32, kv=kv, page=32, nsel=4, seed=hq, extra_q=1)
+    _random_lists(s, seed=tokens)
+    s.run_attend().check_attend(_few(s, 12))
+
+
+# ---------------------------------------------------------------------------
+# malformed sequences
+@pytest.mark.parametrize("n, at", [(3, 0), (40, 1), (2300, 5)])
+def test_a_malformed_sequence_without_rows_is_reported(n, at):
+    """Behind a prompt that fills the first places of the tensor cores' kernel: the last sequence's context."""
+    s = _mixed(n, 300, at, step=50)
+    assert s.new[-1] == 0
+    ctx = list(s.ctx)
+    ctx[-1] = -1
+    s.seqs.ctx_len = _i32(ctx)
+    s.run_select()
+    s.check_select(_few(s, 12), status=BAD)
+    s.status.zero_()
+    s.run_bounds().check_bounds(status=BAD)
+
+
+# ---------------------------------------------------------------------------
+# the score
+@pytest.mark.parametrize("new", [1, 700])
+def test_scores_up_to_the_largest_step_that_is_exact(new):
+    """Whole numbers below 2^21 times steps up to 2^107, apart by less than the sums' range."""
+    s = Step([16 * 300], [new], 4, 4, 128, 16, kv="bf16", page=16, nsel=30, first=1, seed=5)
+    g = torch.Generator().manual_seed(1)
+    s.steps[:] = torch.exp2(torch.randint(104, 108, s.steps.shape, generator=g).float())
+    s.device()
+    s.run_select().check_select(_few(s, 8))
+
+
+@pytest.mark.parametrize("large", [1.0, 300.0])
+def test_how_far_the_score_may_lie_below_a_querys(large):
+    """The score bounds q' . k for q' = q in whole steps; |q - q'| is at most half a step in every dim, so that
+    q . k <= step_q score + step_q / 2 sum_d |k_d|, with a few dims far above the others as well."""
+    s = Step([512], [512], 8, 2, 64, 16, kv="bf16", page=64, seed=3)
+    s.q[:, :, 5] *= large
+    s.device()
+    s.run_bounds()
+    assert s.stat() == 0
+    rows = s.rows_of(0)
+    k = s.values("k")[rows]
+    home = torch.tensor([int(rows[i * 16]) // 16 for i in range(32)])
+    for t in range(0, 512, 37):
+        for g in range(2):
+            q = s.q[t, 4 * g:4 * g + 4].double()
+            step = BR.step_of(float(q.abs().max()))
+            score = step * BR.scores(BR.whole(q), s.dbounds.cpu()[home, g], s.dsteps.cpu()[home, g])
+            slack = step / 2 * k[:, g].abs().sum(-1)
+            best = ((q @ k[:, g].T) - slack).amax(0).view(32, 16).amax(1)
+            assert bool((score >= best - 1e-9 * best.abs()).all())
