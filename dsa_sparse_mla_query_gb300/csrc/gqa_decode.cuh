@@ -516,6 +516,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT, KS, LISTED>::kThreads, Cfg<D, 
                     own = warp_seq_of(a.s.q_start, a.s.num_seqs, p.b);
                     own_seq = load_seq(a.s, own, a.num_q);
                     own_seq.ok = own_seq.ok && p.b >= own_seq.q0 && p.b < own_seq.q0 + own_seq.nq;
+                    if (!own_seq.ok && lane == 0) report(a.d_status, DSA_ERR_BAD_INPUT);  // (its list may be empty)
                 }
                 // physical row of a box's first token among the sequence's, num_rows: outside the
                 // cache, -1: none; its load goes out before the queries' positions have arrived

@@ -629,7 +629,7 @@ dsa_status block_gqa_select(const dsa_gqa_shape* shape, const void* q, const int
  * any number of tokens per sequence.  DSA_ERR_BAD_INPUT: sel_len outside
  * [0, nsel block] (its row is left unwritten), a listed block that is not one of
  * the sequence's ctx_len tokens', a block outside the cache, a malformed
- * sequence (their keys and values count as zeros). */
+ * sequence with rows (their keys and values count as zeros). */
 dsa_status block_gqa_attend(const dsa_gqa_shape* shape, const void* q, const void* k_cache, const void* v_cache,
                             const float* k_scale, const float* v_scale, const dsa_seqs* seqs, int32_t num_q,
                             const int32_t* blocks, const int32_t* sel_len, int32_t block, int32_t nsel,

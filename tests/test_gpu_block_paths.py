@@ -1,8 +1,10 @@
 """Paths of the block selection and of attention over listed blocks that long
 batches take: many sequences beside a prompt, whole lists in turn with tiles of
-16 and 32 query rows, malformed sequences."""
+16 and 32 query rows, malformed sequences call by call."""
 
 from __future__ import annotations
+
+import math
 
 import pytest
 import torch
@@ -66,6 +68,61 @@ def test_whole_lists_in_turn_with_many_rows(kv, hq, hkv, d, tokens):
 
 # ---------------------------------------------------------------------------
 # malformed sequences
+def _shapes():
+    """Few rows a sequence; many, so that the tensor cores score them and a warp chooses a row."""
+    yield "few", dict(ctx=[900, 500, 64], new=[2, 2, 1], hq=8, hkv=2)
+    yield "wide", dict(ctx=[900, 500, 1400], new=[2, 2, 1300], hq=8, hkv=4)
+
+
+SHAPES = dict(_shapes())
+
+
+@pytest.mark.parametrize("name", SHAPES)
+@pytest.mark.parametrize("what", ["a negative context", "a context past max_ctx", "more rows than max_q_per_seq"])
+def test_a_malformed_sequence_alone_is_left(name, what):
+    """Each call reports it, and the other sequences have what they would have without it."""
+    a = SHAPES[name]
+    s = Step(a["ctx"], a["new"], a["hq"], a["hkv"], 64, 32, page=32, seed=4)
+    bad = 1
+    if what == "more rows than max_q_per_seq":
+        bad = 2 if name == "wide" else 0
+        if name == "few":
+            s.seqs.max_q_per_seq = 1  # of two tokens: sequences 0 and 1
+    ctx = list(a["ctx"])
+    if what == "a negative context":
+        ctx[bad] = -1
+    elif what == "a context past max_ctx":
+        ctx[bad] = max(a["ctx"]) + 1
+    elif name == "wide":
+        s.seqs.max_q_per_seq = 1299
+    s.seqs.ctx_len = _i32(ctx)
+    lost = {0, 1} if what == "more rows than max_q_per_seq" and name == "few" else {bad}
+    rows = [t for t in range(s.nq) if s.seq[t] not in lost]
+    gone = [t for t in range(s.nq) if s.seq[t] in lost]
+    some = rows[::max(1, len(rows) // 12)]
+
+    def fresh():
+        torch.cuda.synchronize()
+        s.status.zero_()
+
+    s.run_bounds().check_bounds(skip=lost, status=BAD)
+    fresh()
+    s.run_select().check_select(some, status=BAD)
+    assert bool((s.blocks[gone] == 77).all()) and bool((s.len[gone] == 77).all())
+    fresh()
+    # listed attention: the malformed sequence's keys and values count as zeros
+    s.blocks[gone], s.len[gone] = -1, 5
+    s.blocks[gone, :, 0] = 0
+    s.run_attend().check_attend(some, status=BAD)
+    assert bool((s.out[gone] == 0).all())
+    assert bool(((s.lse[gone] - math.log(5)).abs() < 1e-6).all())
+    fresh()
+    # empty lists read no keys, and the sequence is as malformed
+    s.blocks[gone], s.len[gone] = -1, 0
+    s.run_attend().check_attend(some, status=BAD)
+    assert bool((s.out[gone] == 0).all()) and bool((s.lse[gone] == -math.inf).all())
+
+
 @pytest.mark.parametrize("n, at", [(3, 0), (40, 1), (2300, 5)])
 def test_a_malformed_sequence_without_rows_is_reported(n, at):
     """Behind a prompt that fills the first places of the tensor cores' kernel: the last sequence's context."""
