@@ -550,11 +550,26 @@ dsa_status dsa_step_plan(const int32_t* cached_len, const int32_t* new_len, int3
         c.ptr(slot, "slot", 8);
     }
     c.ptr(next_range, "next_range", 4);
-    // every CTA reads the lengths and the range: what they are must not become what they will be
-    const void* out[] = {ctx_len, q_start, q_pos, slot, next_range};
-    for (const void* p : out)
-        c.need(!p || (p != cached_len && p != new_len && p != free_range && p != free_pages && p != page_table),
-               DSA_ERR_INVALID_ARG, "an output is one of the inputs");
+    // every CTA reads the lengths, the range and the free pages: what they are must not become what they will be
+    const int64_t n = std::max(0, num_seqs), rows = std::max(0, num_q);
+    struct Part {
+        const void* p;
+        int64_t bytes;
+        bool overlaps(const Part& o) const {
+            const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(o.p);
+            return p && o.p && bytes > 0 && o.bytes > 0 && (x < y ? y - x < (uint64_t)bytes : x - y < (uint64_t)o.bytes);
+        }
+    };
+    const Part in[] = {{cached_len, 4 * n}, {new_len, 4 * n}, {free_pages, 4 * (int64_t)free_cap}, {free_range, 8}};
+    const Part out[] = {{page_table, 4 * n * std::max(0, max_pages)}, {ctx_len, 4 * n}, {q_start, 4 * (n + 1)},
+                        {q_pos, 4 * rows}, {slot, 8 * rows}, {next_range, 8}};
+    bool input = false, output = false;
+    for (const Part& o : out) {
+        for (const Part& i : in) input = input || o.overlaps(i);
+        for (const Part& i : out) output = output || (&i != &o && o.overlaps(i));
+    }
+    c.need(!input, DSA_ERR_INVALID_ARG, "an output is one of the inputs");
+    c.need(!output, DSA_ERR_INVALID_ARG, "two outputs overlap");
     dsa_status st = c.done();
     if (st != DSA_OK) return st;
     return cuda_status(launch_step_plan(cached_len, new_len, num_seqs, free_pages, free_cap, free_range, page_size,

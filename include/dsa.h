@@ -503,7 +503,7 @@ dsa_status dsa_kv_block_insert(const dsa_gqa_shape* shape, const void* k, int64_
  *   free_range, next_range int32 [2]; page_table int32 [num_seqs, max_pages];
  *   ctx_len int32 [num_seqs]; q_start int32 [num_seqs + 1]; q_pos int32, slot
  *   int64 [num_q].  page_size as in dsa_seqs; num_pages: pages in the cache.
- * No output may be an input's memory.
+ * No output may overlap an input or another output.
  * DSA_ERR_BAD_INPUT in *d_status: a request that cannot be served (a negative
  * length, more tokens than max_pages pages hold or than 2^30, rows past num_q,
  * not enough free pages for it and those before it): it takes no pages, ctx_len

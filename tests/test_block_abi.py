@@ -109,6 +109,21 @@ def test_plan_refuses(lib, kw, part, status):
     assert rc == status and part in msg, (rc, msg)
 
 
+@pytest.mark.parametrize("kw, part", [
+    (dict(table=0x100), "an output is one of the inputs"),          # the page table over the lengths
+    (dict(table=0x2F0), "an output is one of the inputs"),          # its end in the free list
+    (dict(pos=0x1F0, num_q=5), "an output is one of the inputs"),   # the positions' end in new_len
+    (dict(start=0x104), "an output is one of the inputs"),
+    (dict(ctx=0x608, start=0x600), "two outputs overlap"),
+    (dict(pos=0x900), "two outputs overlap"),
+    (dict(nxt=0x904), "two outputs overlap"),
+    (dict(ctx=0x100, pos=0x900), "an output is one of the inputs; two outputs overlap"),
+])
+def test_plan_refuses_memory_that_overlaps(lib, kw, part):
+    rc, msg = _plan(lib, **kw)
+    assert rc == B.DSA_ERR_INVALID_ARG and part in msg, (rc, msg)
+
+
 def test_names_are_public():
     import dsa_sparse_mla_query_gb300 as dsa
     assert dsa.DSA_FP8_E4M3_BLOCKSCALE == 4
