@@ -499,6 +499,12 @@ dsa_status dsa_kv_block_insert(const dsa_gqa_shape* shape, const void* k, int64_
  * Rows from the last request's end to num_q are padding: q_pos = slot = -1.
  * Other entries of page_table are left as they were.  The results are what
  * dsa_seqs, dsa_kv_insert and dsa_kv_block_insert take.
+ * Pages are counted from cached_len alone.  Where tokens are taken back (a rejected
+ * draft: the next cached_len is below this step's ctx_len), the pages that opened behind
+ * those that stay, page_table[b][c] for ceil(cached_len / page_size) <= c <
+ * ceil(ctx_len / page_size), are the caller's to put back into the free list before
+ * the next plan: the places of free_pages in front of next_range[0] are free for them.
+ * The next plan takes other pages for these columns; what is not put back is lost.
  *   cached_len, new_len int32 [num_seqs]; free_pages int32 [free_cap];
  *   free_range, next_range int32 [2]; page_table int32 [num_seqs, max_pages];
  *   ctx_len int32 [num_seqs]; q_start int32 [num_seqs + 1]; q_pos int32, slot

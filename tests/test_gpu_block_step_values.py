@@ -112,3 +112,33 @@ def test_steps_against_what_the_cache_holds(kw):
         assert int(s.status) == 0
         s.check_writes(old)
         s.check_rest()
+
+
+def test_drafts_that_are_taken_back_lose_no_page():
+    """Pages opened behind the tokens that stay are put back in front of the free list before the next plan, as its
+    description asks: after many steps the pages in use are those of the tokens."""
+    s = Checked(3, page=16, max_ctx=256, rows=30)
+    g = torch.Generator().manual_seed(3)
+    length = [0, 0, 0]
+    for step in range(25):
+        new = [int(torch.randint(1, 10, (1,), generator=g)) for _ in range(3)]
+        for b in range(3):
+            s.k[b], s.v[b] = s.k[b][:length[b]], s.v[b][:length[b]]
+        s.load(new, step)
+        s.enqueue()
+        torch.cuda.synchronize()
+        assert int(s.status) == 0
+        s.check_rest()
+        keep = [int(torch.randint(0, n + 1, (1,), generator=g)) for n in new]
+        table = s.table.cpu()
+        back = []
+        for b in range(3):
+            back += table[b, -(-(length[b] + keep[b]) // 16):-(-(length[b] + new[b]) // 16)].tolist()
+            length[b] += keep[b]
+        first = int(s.range[0][0]) - len(back)
+        s.free[first:first + len(back)] = torch.tensor(back, dtype=torch.int32, device=s.free.device)
+        s.range[0][0] = first
+        s.cached.copy_(torch.tensor(length, dtype=torch.int32))
+        assert first == sum(-(-n // 16) for n in length)
+        used = [p for b in range(3) for p in table[b, :-(-length[b] // 16)].tolist()]
+        assert sorted(used + s.free[first:].tolist()) == list(range(s.num_pages))
