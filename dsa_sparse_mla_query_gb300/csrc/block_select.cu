@@ -504,6 +504,10 @@ __device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
     hi = *reinterpret_cast<const uint32_t*>(&yh);
 }
 
+// Scores are kept 2^15 times smaller: a sum (below 2^21) times a step, 2^-126 to 2^122, is then a
+// multiple of 2^-141 below 2^128, exact in fp32 at either end (subnormal at the lower one).
+constexpr float kStepDown = 0x1p-15f;
+
 __device__ __forceinline__ float whole_steps(float v, float up) {
     return v == v ? fmaxf(-127.f, fminf(127.f, rintf(v * up))) : 0.f;
 }
@@ -688,6 +692,7 @@ __global__ void __launch_bounds__(kFewThreads, PICK ? 4 : 5)
             for (int e = 0; e < 4; ++e) acc[0][e] += odd[e];
         // the best of a token's heads, and its scores of blocks blk and blk + 8
         const int blk = i * 16 + col;
+        const float step0 = kStepDown * cur.step[0], step1 = kStepDown * cur.step[1];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             if (!leads[j]) continue;
@@ -705,8 +710,7 @@ __global__ void __launch_bounds__(kFewThreads, PICK ? 4 : 5)
             for (int e = 0; e < 2; ++e) {
                 const int tok = group_of[j] * tpt + put[e];
                 if (put[e] < 0 || tok >= n) continue;
-                // (a step above 2^105 overflows to equal scores)
-                const float s0 = m[e] * cur.step[0], s1 = m[2 + e] * cur.step[1];
+                const float s0 = m[e] * step0, s1 = m[2 + e] * step1;
                 if (PICK) {
                     if (blk <= most) keys[tok * a.ld + blk] = score_code(s0);
                     if (blk + 8 <= most) keys[tok * a.ld + blk + 8] = score_code(s1);
@@ -888,7 +892,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const
         const int li = lane & 3, row0 = (warp - 8) * 16 + (lane >> 2);
         // block of row (warp - 8) 16 + lane, by the context (-1 none, -2 lost), from its page
         auto token_of = [&](int x) { return (int64_t)(x * kWideRows + (warp & 7) * 16 + (lane & 15)) << a.shift; };
-        const int64_t base = n > 0 ? first_row(a.s, b) : 0;
+        const int64_t base = first_row(a.s, b);
         auto page_of_tile = [&](int x) {
             return token_of(x) < sq.ctx ? page_at(a.s, a.page_shift, b, token_of(x)) : 0;
         };
@@ -910,7 +914,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const
         };
         int at = -1;
         int page = 0;  // of the next tile
-        if (bounds_warp && n > 0) {
+        if (bounds_warp) {
             at = place(x0, page_of_tile(x0));
             page = page_of_tile(x0 + 1);
 #pragma unroll
@@ -1121,7 +1125,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const
             int far = page_of(x0 + 1);
             for (int x = x0; x < x1 && ok; ++x, ++tile) {
                 const int buf = tile & 1, blk = x * kWideRows + quarter * 32 + lane;
-                const float step = ahead;
+                const float step = kStepDown * ahead;
                 ahead = step_at(x + 1, far);
                 far = page_of(x + 2);
                 ok = __all_sync(0xffffffffu, quick_wait(tfull + buf, (tile >> 1) & 1, abort_flag, a.d_status));
@@ -1139,8 +1143,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) block_score_wide_kernel(const
                 float* dst = a.scores + ((int64_t)(t0 + tok) * a.hkv + kvh) * a.ld + blk;
                 float last = -INFINITY;  // pad 64: of the first half of a token's columns
                 auto store = [&](float m) {
-                    // (a step above 2^105 overflows to equal scores)
-                    if (tok < lim) *dst = m * step;
+                        if (tok < lim) *dst = m * step;
                     ++tok;
                     dst += next;
                 };

@@ -139,12 +139,14 @@ def test_a_malformed_sequence_without_rows_is_reported(n, at):
 
 # ---------------------------------------------------------------------------
 # the score
-@pytest.mark.parametrize("new", [1, 700])
-def test_scores_up_to_the_largest_step_that_is_exact(new):
-    """Whole numbers below 2^21 times steps up to 2^107, apart by less than the sums' range."""
-    s = Step([16 * 300], [new], 4, 4, 128, 16, kv="bf16", page=16, nsel=30, first=1, seed=5)
-    g = torch.Generator().manual_seed(1)
-    s.steps[:] = torch.exp2(torch.randint(104, 108, s.steps.shape, generator=g).float())
+@pytest.mark.parametrize("lo, hi", [(-126, 123), (116, 123), (-126, -119)])
+@pytest.mark.parametrize("n, ctx, new", [(1, 16 * 300, 1), (1, 16 * 300, 700), (1, 16 * 100, 200), (1, 16 * 3000, 2),
+                                         (80, 16 * 100, 1)])
+def test_scores_with_every_step_that_bounds_have(n, ctx, new, lo, hi):
+    """2^-126 to 2^122 (of the largest fp32 values): the order is that of the exact scores."""
+    s = Step([ctx] * n, [new] * n, 4, 4, 128, 16, kv="bf16", page=16, nsel=30, first=1, seed=5)
+    g = torch.Generator().manual_seed(2)
+    s.steps[:] = torch.exp2(torch.randint(lo, hi, s.steps.shape, generator=g).double()).float()
     s.device()
     s.run_select().check_select(_few(s, 8))
 
