@@ -5,7 +5,7 @@ the attention query's RoPE + SSMax) and one rank's compute steps of decode
 context parallelism (top-k candidates, their merge, compaction, LSE combine),
 and attention with grouped heads for the layers without an indexer (K/V cache
 writes with the rotation, with a scale per row or per block of tokens; dense
-decode and prompts; attention over blocks chosen by a bound of their scores),
+decode and prompts; attention over blocks chosen by bounds of their keys),
 with a step's page tables and slots built on the GPU.
 
 The Python names mirror the C entry points; they only marshal arguments.

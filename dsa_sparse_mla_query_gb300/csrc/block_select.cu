@@ -1,10 +1,11 @@
-// block_select.cu -- blocks of keys for every query and key head, chosen by an
-// upper bound of their scores (sm_103a).
+// block_select.cu -- blocks of keys for every query and key head, chosen by a
+// score from bounds of their keys (sm_103a).
 //
 // Per block and head the bounds lo_d <= k_d <= hi_d of its keys, in whole steps
 // of a power of two s (lo rounded down, hi up, -127 .. 127), say for any query
 //   q . k <= s sum_d max(q_d lo_d, q_d hi_d) = s (max(q, 0) . hi + min(q, 0) . lo).
-// With q in whole steps too (-127 .. 127, one step for a token's group of heads)
+// With q in whole steps too (-127 .. 127, one step for a token's group of heads: the
+// bound is then the rounded query's, and an estimate of the query's own)
 // the sums are whole numbers below 2^22: exact in fp32 in any order, in the
 // tensor cores as well, so the order of the blocks depends on nothing but the
 // inputs, and ties are ties.
@@ -1474,8 +1475,11 @@ cudaError_t launch_select(const dsa_gqa_shape& sh, const void* q, const void* bo
         a.tokens = s.max_q_per_seq;
         a.direct = 1;
         const int64_t pairs = (int64_t)s.num_seqs * a.hkv, most = (a.ld + 16 * kFewWarps - 1) / (16 * kFewWarps);
-        // (sequence, key head)s that make two CTAs an SM choose for themselves (64 sequences of 512 blocks
-        // and 8 heads: 33 us with the bounds, 52 with a second kernel)
+        // (sequence, key head)s that make two CTAs an SM choose for themselves: with fewer the scores take
+        // longer than the second kernel (one token, 8 key heads, L2 flushed, without the bounds, a second kernel
+        // and not: 8 sequences of 512 blocks 29.2 us and 32.2, of 2,048 41.7 and 71.4; 24 33.0 and 33.2, 61.8
+        // and 78.9; 38 37.0 and 34.6, 75.3 and 81.9; 48 43.8 and 36.4, 97.7 and 85.1; 150 71.4 and 66.1,
+        // 179 and 165; of 32 blocks 21 and 18 with any number up to 64)
         const bool own = pairs >= 2 * kPlanSms && (int64_t)s.max_q_per_seq * a.ld <= kFewScores;
         a.xt = own ? 1 : (int32_t)std::max<int64_t>(1, std::min<int64_t>(most, kPlanSms * 5 / pairs));
         const int64_t grid = pairs * a.xt;
@@ -1534,6 +1538,9 @@ cudaError_t launch_select(const dsa_gqa_shape& sh, const void* q, const void* bo
         return launch_pdl(block_pick_kernel<T>, dim3((unsigned)(num_q * a.hkv)), dim3(T), (size_t)a.ld * 4, stream, 1,
                           p);
     };
+    // or by a warp, where the rows are eight CTAs of four an SM (with the scores, L2 flushed, a CTA a row and a warp:
+    // 2,432 rows of 256 blocks 37.1 us and 35.6, of 1,024 51.1 and 47.5; 4,864 51.9 and 43.6, 74.9 and 64.5;
+    // 16,384 107 and 76, 185 and 142; level at 512, 31.0 and 30.6, 37.2 and 38.3)
     const unsigned ctas = (unsigned)(((int64_t)num_q * a.hkv + kRowsPerCta - 1) / kRowsPerCta);
     auto rows = [&](auto kern) { return launch_pdl(kern, dim3(ctas), dim3(32 * kRowsPerCta), 0, stream, 1, p); };
     if ((int64_t)num_q * a.hkv >= 8 * kPlanSms * kRowsPerCta) {

@@ -1346,7 +1346,10 @@ Plan make_plan(const dsa_gqa_shape& sh, const dsa_seqs& s, int occ, bool listed)
     const int64_t segs = (int64_t)p.lanes * s.num_seqs;
     // Listed blocks, many tokens: whole lists in turn, head by head, so that the CTAs read neighbouring
     // tokens' blocks of one head at a time (they are mostly the same, and a head's cache fits the L2), and
-    // nothing is cut.  From eight lists a CTA on the last round costs less.
+    // nothing is cut.  With few lists a CTA a last round that is mostly empty costs more than the cuts: 32
+    // blocks of 64 keys, deal and whole lists, 8 rows e4m3, 8 heads, 1.1 lists a CTA 67.8 us and 70.2, 4.1
+    // 161 and 156, 8.1 287 and 274, 32.1 1,038 and 1,023; 33 heads on one, 1.1 66.3 and 75.1, 4.1 151 and 161,
+    // 8 255 and 247, 8.1 263 and 274, 16.1 493 and 501, 32.1 948 and 954.
     if (listed && segs >= 8 * n) {
         p.rounds = 1;
         p.grid = n;

@@ -13,7 +13,8 @@
  * context parallelism (top-k candidates, their merge, compaction, LSE combine).
  * Beside it: attention with grouped heads for the layers without an indexer
  * (K/V cache writes; over all keys: decode, prompts; over blocks chosen by a
- * bound of their scores), and a step's page tables and slots built on the GPU.
+ * score from bounds of their keys), and a step's page tables and slots built on
+ * the GPU.
  *
  * Sources (web pages, cited by title and section):
  *   [vLLM-ML4] "Day 0 support for Mistral Large 4" (vLLM blog), Implementation
@@ -567,7 +568,7 @@ dsa_status dense_gqa_prefill(const dsa_gqa_shape* shape, const void* q, const vo
  * cheap score and attends over those alone.  shape and seqs as for the dense
  * calls, any cache dtype; q_rope_pos is not read.
  *
- * The score of a block is a bound of the scores of its keys: per block and head
+ * The score of a block comes from bounds of its keys: per block and head
  *   step = 2^ceil(log2(max |k| / 127)) over its keys and dims (1 if all are 0),
  *   bounds[0][d] = floor(min k_d / step), bounds[1][d] = ceil(max k_d / step),
  *   both in [-127, 127] (values that are not finite do not count for the step;
@@ -576,8 +577,14 @@ dsa_status dense_gqa_prefill(const dsa_gqa_shape* shape, const void* q, const vo
  * steps of their own, 2^ceil(log2(max |q| / 127)) for the group (rounded to
  * nearest even; NaN counts as 0, infinities as 127):
  *   score(i) = step_i max_h sum_d max(q_h[d] bounds_i[0][d], q_h[d] bounds_i[1][d]),
- * whole numbers times a power of two: exact, so that the order is the same
- * everywhere; equal scores go to the smaller block. */
+ * whole numbers times a power of two, 2^-126 to 2^122: exact, so that the order is the
+ * same everywhere; equal scores go to the smaller block.
+ * For finite values score(i) is no less than any q'.k of the block's keys and the group's
+ * heads, q' being the queries in whole steps.  Of the queries themselves it is an
+ * estimate: q.k may pass step_q score(i) by step_q / 2 sum_d |k_d| (step_q the group's),
+ * which is little beside the bounds' slack for dims of like sizes and heads of like
+ * sizes, and is not where a few are far above the others.  A block that is not chosen
+ * may hold the larger product. */
 #define DSA_GQA_MAX_NSEL 1024
 #define DSA_GQA_MAX_BLOCKS 51200 /* blocks of the longest context */
 
@@ -599,7 +606,8 @@ dsa_status block_gqa_workspace_size(const dsa_gqa_shape* shape, const dsa_seqs* 
  *   a scale has the older codes of its scale block encoded again
  *   (dsa_kv_block_insert), and where the first new token's scale block may be such a
  *   one (no older code in it above 224, a new one of 224 or more), the blocks of it
- *   before that token get their bounds again too.
+ *   before that token get their bounds again too.  (That is for scales so far that are
+ *   powers of two, as the write makes them.)
  * DSA_ERR_BAD_INPUT: a malformed sequence, a block outside the cache or not at a
  * multiple of `block` rows (seq_base), new tokens past ctx_len: their blocks
  * are left.  Alignment: k_cache and bounds 16 bytes. */
