@@ -171,3 +171,86 @@ def test_how_far_the_score_may_lie_below_a_querys(large):
             slack = step / 2 * k[:, g].abs().sum(-1)
             best = ((q @ k[:, g].T) - slack).amax(0).view(32, 16).amax(1)
             assert bool((score >= best - 1e-9 * best.abs()).all())
+
+
+# ---------------------------------------------------------------------------
+# layouts
+@pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("new", [1, 600])
+def test_keys_and_values_in_one_cache(kv, new):
+    """Rows [keys' heads, values' heads, something else] of one buffer, for the three calls."""
+    s = Step([700, 90], [new, 1], 8, 2, 128, 32, kv=kv, page=64, nsel=5, first=1, local=2, seed=new)
+    both = torch.zeros(s.rows, 5, 128, dtype=s.dk.dtype, device=DEV)
+    if kv == "bf16":
+        both[:, 4] = math.nan
+    else:
+        both[:, 4] = 0x7F
+    both[:, :2], both[:, 2:4] = s.dk, s.dv
+    s.dk, s.dv = both[:, :2], both[:, 2:]
+    s.shape = dsa.GqaShape(8, 2, 128, KINDS[kv], q_stride=s.dq.stride(0), k_stride=5 * 128, v_stride=5 * 128,
+                           scale_block=s.sb if kv == "block" else 0)
+    s.run_bounds().check_bounds()
+    s.run_select().run_attend()
+    s.check_select(_few(s, 12))
+    s.check_attend(_few(s, 12))
+
+
+@pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("block, ctx", [(64, 500), (16, 500), (128, 259)])
+@pytest.mark.parametrize("new", [1, 200])
+def test_a_cache_that_ends_inside_a_block(kv, block, ctx, new):
+    """Contiguous rows up to the cache's last one; bounds and scales of the last block are there, its other rows not."""
+    s = Step([ctx], [new], 16, 2, 64, block, kv=kv, sb=64 if kv == "block" else 0, nsel=3, seed=ctx)
+    s.seqs.num_rows = ctx
+    s.dk, s.dv = s.dk[:ctx].clone(), s.dv[:ctx].clone()
+    if kv == "row":
+        s.dks, s.dvs = s.dks[:ctx].clone(), s.dvs[:ctx].clone()
+    elif kv == "block":
+        s.dks, s.dvs = [x[:-(-ctx // 64)].clone() for x in (s.dks, s.dvs)]
+    n = -(-ctx // block)
+    left = s.dbounds[n:].clone(), s.dsteps[n:].clone()
+    s.run_bounds().check_bounds()
+    assert torch.equal(left[0], s.dbounds[n:]) and torch.equal(left[1], s.dsteps[n:])
+    s.run_select().run_attend()
+    s.check_select(_few(s, 12))
+    s.check_attend(_few(s, 12))
+
+
+@pytest.mark.parametrize("d, half", [(64, False), (128, True)])
+def test_writes_and_dense_calls_over_one_cache_that_ends_inside_a_block(d, half):
+    """The same bits as with a cache for keys and one for values, each whole blocks."""
+    hq, hkv, sb, rows, past, new = 8, 2, 64, 250, 70, 180
+    g = torch.Generator().manual_seed(d)
+    x = torch.randn(new, hq + 2 * hkv, d, generator=g).bfloat16().to(DEV)
+    code = torch.randint(0, 0x70, (256, 5, d), generator=g).to(torch.uint8).to(DEV)
+    inv = (10000.0 ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)).float().to(DEV)
+    got = []
+    for shared in (False, True):
+        both = code[:rows].clone() if shared else code.clone()
+        if shared:
+            k, v = both[:, :2], both[:, 2:4]
+            stride = 5 * d
+        else:
+            k, v, stride = both[:, :2].contiguous(), both[:, 2:4].contiguous(), 0
+        ks, vs = [torch.full((4, hkv), 2.0 ** -7, device=DEV) for _ in range(2)]
+        shape = dsa.GqaShape(hq, hkv, d, dsa.DSA_FP8_E4M3_BLOCKSCALE, k_stride=stride, v_stride=stride, scale_block=sb)
+        seqs = dsa.Seqs(_i32([past + new]), _i32([0, new]), _i32(list(range(past, past + new))), max_ctx=past + new,
+                        max_q_per_seq=new, num_rows=rows if shared else 256, seq_base=torch.zeros(1, dtype=torch.int64, device=DEV))
+        status, q = _i32([0]), torch.empty(new, hq, d, dtype=torch.bfloat16, device=DEV)
+        xq, xk, xv = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+        dsa.dsa_kv_block_insert(shape, xk, xv, xq, seqs, new, inv, d, int(half), k, v, ks, vs, q, k_stride=xk.stride(0),
+                                v_stride=xv.stride(0), q_stride=xq.stride(0), d_status=status)
+        res = [k[:rows].clone(), v[:rows].clone(), ks, vs, q]
+        n = dsa.dense_gqa_workspace_size(shape, seqs, new)
+        ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+        for call in (dsa.dense_gqa_decode, dsa.dense_gqa_prefill):
+            out, lse = torch.empty_like(q), torch.empty(new, hq, device=DEV)
+            call(shape, q, k, v, ks, vs, seqs, new, 0.1, out, lse, ws, n, d_status=status)
+            torch.cuda.synchronize()
+            res += [out, lse]
+        assert int(status) == 0
+        if shared:
+            assert torch.equal(both[:, 4], code[:rows, 4])
+        got.append(res)
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
