@@ -27,9 +27,9 @@
 // Measured, 64/8 heads of 128, blocks of 64 keys, with the host's calls and the new
 // keys' bounds: 64 tokens over 32,768 keys 28.7 us, 3 over 524,288 30 us (HBM 36%
 // busy while the bounds are read: two or three rounds of loads a warp, then the
-// choice); 2,048 of 65,536 139 us: the scores 97 (the CTA's own warps turn the
+// choice); 2,048 of 65,536 138 us: the scores 96 (the CTA's own warps turn the
 // bounds into f16 operands: the tensor cores are 33% busy), the choice 39 (69% of
-// the issue slots), the bounds 6.
+// the issue slots), the bounds 5.
 #include <algorithm>
 
 #include "gqa_common.cuh"
